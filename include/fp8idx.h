@@ -56,7 +56,9 @@ typedef enum {
 typedef enum {
   FP8IDX_U8 = 0,  /* e4m3 codes or raw bytes */
   FP8IDX_F32 = 1,
-  FP8IDX_I32 = 2
+  FP8IDX_I32 = 2,
+  FP8IDX_BF16 = 3,
+  FP8IDX_F16 = 4
 } fp8idx_dtype;
 
 /* A strided view of caller-owned device memory.  Strides are in elements.
@@ -368,6 +370,152 @@ fp8idx_status fp8_paged_mqa_topk_noalloc(const fp8idx_tensor* q_fp8,
                                          const fp8idx_tensor* indices,
                                          const fp8idx_options* opts,
                                          void* stream);
+
+/*
+ * The operators around the indexer in a serving step.  A step adds new tokens
+ * to a batch of requests: fp8idx_paged_step_tables makes the block tables,
+ * slots and windows, fp8_paged_store writes the new tokens' keys (and values)
+ * into the paged caches, the calls above score and select, and
+ * fp8_paged_sparse_attn / fp8_mqa_sparse_attn_paged attend to the selected
+ * positions.  The pages have no counterpart to them.
+ *
+ * The attention's key/value cache: kv_cache [num_blocks, kv_heads, page] U8,
+ * where a page holds one head's block_size tokens: block_size rows of 2*D
+ * bytes (the token's key row, then its value row, e4m3), then block_size
+ * pairs of f32 (the key row's scale, the value row's scale), padded to a
+ * multiple of 16 bytes (fp8idx_kv_page_bytes).  It shares block size and
+ * block tables with the index cache of the logits calls.
+ */
+
+/* Bytes of one head's page of a key/value cache: block_size*(2*head_dim + 8)
+ * rounded up to a multiple of 16 (0 for a block_size or head_dim that
+ * fp8_paged_store does not implement).  Pure host function. */
+int64_t fp8idx_kv_page_bytes(int32_t block_size, int32_t head_dim);
+
+/*
+ * Block tables, slots and windows of a serving step, from request lengths:
+ * fp8idx_paged_step_tables.
+ * Request b holds old_lens[b] tokens and gets new_lens[b] more (negative
+ * lengths count as 0).  With cap = max_blocks*block_size,
+ *   context_lens[b] = min(old_lens[b] + new_lens[b], cap),
+ *   cu_new_lens = the exclusive prefix sum of new_lens, with its total,
+ *   cu_seq_lens = the exclusive prefix sum of context_lens, with its total,
+ * and table entries ceil(old/block_size) .. ceil(context/block_size)-1 of
+ * request b are dealt from the free blocks: the j-th block dealt, counted
+ * over the requests in order, is free_blocks[free_count - 1 - j], or -1 once
+ * the free blocks run out.  Other entries are left as they are.  Row t with
+ * cu_new_lens[b] <= t < cu_new_lens[b+1] is the token at position
+ * p = old_lens[b] + t - cu_new_lens[b]:
+ *   slot_mapping[t] = block_tables[b][p / block_size]*block_size
+ *                     + p % block_size (-1 without a block, or past cap),
+ *   cu_seqlen_ks[t] = cu_seq_lens[b],
+ *   cu_seqlen_ke[t] = cu_seq_lens[b] + min(p + 1, context_lens[b]).
+ * Rows past the last request get slot -1 and the empty window [0, 0), so a
+ * padded step stores and scores nothing for them.
+ *   counts[0] = all new tokens (rows past the number of rows given get no
+ *   outputs), [1] = blocks dealt, [2] = free blocks left (the next step's
+ *   free_count), [3] = blocks wanted beyond them.
+ * Sums past 2^31-1 saturate.  The call reads old_lens, free_blocks and
+ * free_count and writes the rest, so it can be repeated: the caller takes
+ * context_lens and counts[2] as the next step's old_lens and free_count.
+ *
+ *  old_lens, new_lens, context_lens  [batch] I32, batch <= 4096.
+ *  free_blocks   [n] I32, contiguous; free_count [1] I32 (clamped to n).
+ *  block_size    1, 16, 32, 64 or 128.
+ *  block_tables  [batch, max_blocks] I32, rows contiguous.
+ *  cu_new_lens   [batch + 1] I32.   slot_mapping [rows] I32.   counts [4] I32.
+ *  cu_seq_lens [batch + 1], cu_seqlen_ks, cu_seqlen_ke [rows] I32: may be
+ *                NULL (a decode step needs none of them).
+ * Outputs must not overlap inputs.  One kernel on `stream`.
+ */
+fp8idx_status fp8idx_paged_step_tables(
+    const fp8idx_tensor* old_lens, const fp8idx_tensor* new_lens,
+    const fp8idx_tensor* free_blocks, const fp8idx_tensor* free_count,
+    int32_t block_size, const fp8idx_tensor* block_tables,
+    const fp8idx_tensor* context_lens, const fp8idx_tensor* cu_new_lens,
+    const fp8idx_tensor* slot_mapping, const fp8idx_tensor* counts,
+    const fp8idx_tensor* cu_seq_lens, const fp8idx_tensor* cu_seqlen_ks,
+    const fp8idx_tensor* cu_seqlen_ke, void* stream);
+
+/*
+ * The quantising write into a paged cache: fp8_paged_store.
+ * Each row x of head_dim values becomes scale = max|x| / 448 (f32) and codes
+ * e4m3(clamp(x / scale, -448, 448)), rounded to nearest even; a row of zeros
+ * has scale 0 and codes 0.  Token t goes to slot s = slot_mapping[t]: token
+ * s % block_size of block s / block_size.  A slot that is negative or past
+ * the cache is skipped.  The slots of one call must differ (otherwise which
+ * token's bytes remain is unspecified).
+ *
+ *  k             [tokens, head_dim] (index cache) or [tokens, kv_heads,
+ *                head_dim] (key/value cache), BF16, F16 or F32, unit inner
+ *                stride, rows 16-byte aligned; head_dim 64 or 128.
+ *  v             NULL (index cache), or like k, with its own strides.
+ *  slot_mapping  [tokens] I32, contiguous.
+ *  kv_cache      index cache [num_blocks, block_size*(head_dim+4)] U8 as the
+ *                logits calls read it, or key/value cache [num_blocks,
+ *                kv_heads, page] U8 as described above (any block and head
+ *                strides that are multiples of 16 bytes; pages contiguous);
+ *                16-byte aligned; block_size 1, 16, 32, 64 or 128;
+ *                num_blocks*block_size < 2^31.
+ * One kernel on `stream`.
+ */
+fp8idx_status fp8_paged_store(const fp8idx_tensor* k, const fp8idx_tensor* v,
+                              const fp8idx_tensor* slot_mapping,
+                              const fp8idx_tensor* kv_cache, void* stream);
+
+/*
+ * Attention over the selected positions of a paged key/value cache:
+ * fp8_paged_sparse_attn (decode rows) and fp8_mqa_sparse_attn_paged (prefill
+ * rows).  For row r, query head h and the key head g = h / (heads/kv_heads):
+ *   s_j = softmax_scale * <q[r,h], K[g, i_j]>   over the entries i_j of
+ *         indices[r] that are selected,
+ *   out[r,h] = sum_j exp(s_j) V[g, i_j] / sum_j exp(s_j),
+ *   lse[r,h] = ln sum_j exp(s_j),
+ * with K and V the dequantised rows (code * scale).  An entry is selected if
+ * it is not negative and names a token of its request's block table whose
+ * block is in the cache; an entry given twice counts twice.  A row without
+ * selected entries gets out 0 and lse -inf.
+ *  - decode: row b*next_n + n; entry i is position i of request b -- what
+ *    fp8_paged_topk and fp8_paged_mqa_topk return.
+ *  - prefill: entry i with cu_seq_lens[r] <= i < cu_seq_lens[r+1] is token
+ *    i - cu_seq_lens[r] of request r -- what fp8_mqa_topk returns on the
+ *    logits of fp8_mqa_logits_paged.
+ *
+ *  q             [batch, next_n, heads, head_dim] (decode) or [M, heads,
+ *                head_dim] (prefill) BF16, unit inner stride, other strides
+ *                multiples of 8, 16-byte aligned; head_dim 64 or 128.
+ *  kv_cache      as for fp8_paged_store with v.
+ *  block_tables  [batch or requests, max_blocks] I32, rows contiguous.
+ *  cu_seq_lens   [requests + 1] I32, contiguous, requests <= 4096.
+ *  indices       [rows, k] I32, unit inner stride, k 1 .. 2048.
+ *  out           shape and type of q, unit inner stride.
+ *  lse           [rows, heads] F32, contiguous, or NULL.
+ *  heads a multiple of kv_heads, heads/kv_heads <= 128.
+ *  opts          NULL or num_ctas: the CTAs per row and key head (0 =
+ *                heuristic; 1, 2, 4 or 8), other fields ignored.
+ * Scores, softmax statistics and sums are f32; the kernel splits each query
+ * and each probability into two e4m3 values for the tensor cores (8
+ * significant bits, those of bf16: queries lose nothing).  No workspace; one
+ * kernel on `stream`.
+ */
+fp8idx_status fp8_paged_sparse_attn(const fp8idx_tensor* q,
+                                    const fp8idx_tensor* kv_cache,
+                                    const fp8idx_tensor* indices,
+                                    const fp8idx_tensor* block_tables,
+                                    float softmax_scale,
+                                    const fp8idx_tensor* out,
+                                    const fp8idx_tensor* lse,
+                                    const fp8idx_options* opts, void* stream);
+fp8idx_status fp8_mqa_sparse_attn_paged(const fp8idx_tensor* q,
+                                        const fp8idx_tensor* kv_cache,
+                                        const fp8idx_tensor* block_tables,
+                                        const fp8idx_tensor* cu_seq_lens,
+                                        const fp8idx_tensor* indices,
+                                        float softmax_scale,
+                                        const fp8idx_tensor* out,
+                                        const fp8idx_tensor* lse,
+                                        const fp8idx_options* opts,
+                                        void* stream);
 
 /* Support gates, after the pages' is_supported(num_heads, head_dim,
  * kv_block_size) (aiter PR 5047, Technical Details) and is_supported(

@@ -21,6 +21,18 @@ Entry points (same names as the C ABI):
   fp8_mqa_topk(logits, cu_seqlen_ks, cu_seqlen_ke, k, indices, stream=None)
   fp8_paged_mqa_topk(q_fp8, kv_cache, weights, context_lens, block_tables,
                      max_model_len, k, indices, workspace=None, stream=None)
+
+The operators around them in a serving step:
+  paged_step_tables(old_lens, new_lens, free_blocks, free_count, block_size,
+                    block_tables, context_lens, cu_new_lens, slot_mapping,
+                    counts, cu_seq_lens=None, cu_seqlen_ks=None,
+                    cu_seqlen_ke=None, stream=None)
+  fp8_paged_store(k, v, slot_mapping, kv_cache, stream=None)
+  fp8_paged_sparse_attn(q, kv_cache, indices, block_tables, softmax_scale,
+                        out, lse=None, stream=None, options=None)
+  fp8_mqa_sparse_attn_paged(q, kv_cache, block_tables, cu_seq_lens, indices,
+                            softmax_scale, out, lse=None, stream=None,
+                            options=None)
 """
 from ._native import (  # noqa: F401
     FP8IDX_ERR_CUDA,
@@ -35,15 +47,20 @@ from ._native import (  # noqa: F401
     device_status_message,
     fp8_mqa_logits,
     fp8_mqa_logits_paged,
+    fp8_mqa_sparse_attn_paged,
     fp8_mqa_topk,
     fp8_paged_mqa_logits,
     fp8_paged_mqa_topk,
+    fp8_paged_sparse_attn,
+    fp8_paged_store,
     fp8_paged_topk,
     is_supported,
+    kv_page_bytes,
     library,
     library_path,
     paged_mqa_topk_workspace,
     paged_is_supported,
+    paged_step_tables,
     plan_paged,
     plan_prefill,
     prefill_is_supported,

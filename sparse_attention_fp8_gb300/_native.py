@@ -17,7 +17,7 @@ FP8IDX_ERR_CUDA = 3
 FP8IDX_ERR_TIMEOUT = 4
 _STATUS_NAMES = {0: "OK", 1: "INVALID", 2: "UNSUPPORTED", 3: "CUDA", 4: "TIMEOUT"}
 
-_U8, _F32, _I32 = 0, 1, 2
+_U8, _F32, _I32, _BF16, _F16 = 0, 1, 2, 3, 4
 
 
 class Fp8IdxError(RuntimeError):
@@ -117,6 +117,15 @@ def library():
             lib.fp8idx_paged_mqa_topk_workspace.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                                                             ctypes.c_int32]
             lib.fp8idx_paged_mqa_topk_workspace.restype = ctypes.c_size_t
+            lib.fp8idx_kv_page_bytes.argtypes = [ctypes.c_int32] * 2
+            lib.fp8idx_kv_page_bytes.restype = ctypes.c_int64
+            lib.fp8idx_paged_step_tables.argtypes = [T, T, T, T, ctypes.c_int32, T, T, T, T, T, T, T, T, V]
+            lib.fp8_paged_store.argtypes = [T, T, T, T, V]
+            lib.fp8_paged_sparse_attn.argtypes = [T, T, T, T, ctypes.c_float, T, T, P(_Options), V]
+            lib.fp8_mqa_sparse_attn_paged.argtypes = [T, T, T, T, T, ctypes.c_float, T, T, P(_Options), V]
+            for f in ("fp8idx_paged_step_tables", "fp8_paged_store", "fp8_paged_sparse_attn",
+                      "fp8_mqa_sparse_attn_paged"):
+                getattr(lib, f).restype = ctypes.c_int
             for f in ("fp8_paged_mqa_logits", "fp8_paged_mqa_logits_ex", "fp8_mqa_logits", "fp8_mqa_logits_ex",
                       "fp8_mqa_logits_paged", "fp8_paged_topk", "fp8_mqa_topk", "fp8_paged_topk_ex",
                       "fp8_mqa_topk_ex"):
@@ -175,7 +184,8 @@ def _pack(t, ptr: int) -> bytes:
     global _dtype_codes
     if _dtype_codes is None:
         import torch
-        _dtype_codes = {torch.uint8: _U8, torch.float8_e4m3fn: _U8, torch.float32: _F32, torch.int32: _I32}
+        _dtype_codes = {torch.uint8: _U8, torch.float8_e4m3fn: _U8, torch.float32: _F32, torch.int32: _I32,
+                        torch.bfloat16: _BF16, torch.float16: _F16}
     dt = _dtype_codes.get(t.dtype)
     if dt is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
@@ -314,6 +324,82 @@ def fp8_paged_mqa_topk(q_fp8, kv_cache, weights, context_lens, block_tables, max
                                 ctypes.byref(oc) if oc is not None else None, _stream(stream, q_fp8))
     _check(st)
     return indices
+
+
+def _on_current_device(*tensors):
+    """The library launches on the current device: every tensor has to be
+    there (a kernel cannot be sent after the data of another device)."""
+    import torch
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("inputs must be CUDA tensors")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def kv_page_bytes(block_size, head_dim) -> int:
+    """Bytes of one head's page of a key/value cache (0 if not implemented)."""
+    return int(library().fp8idx_kv_page_bytes(int(block_size), int(head_dim)))
+
+
+def paged_step_tables(old_lens, new_lens, free_blocks, free_count, block_size, block_tables, context_lens,
+                      cu_new_lens, slot_mapping, counts, cu_seq_lens=None, cu_seqlen_ks=None, cu_seqlen_ke=None,
+                      stream=None):
+    """A serving step's block tables (new blocks dealt from the free list),
+    context lengths, slots and prefill windows from the requests' lengths.
+    Returns slot_mapping; counts holds [new tokens, blocks dealt, free blocks
+    left, blocks missing]."""
+    ts = (old_lens, new_lens, free_blocks, free_count, block_tables, context_lens, cu_new_lens, slot_mapping, counts,
+          cu_seq_lens, cu_seqlen_ks, cu_seqlen_ke)
+    _on_current_device(*ts)
+    d = [None if t is None else _pack(t, t.data_ptr()) for t in ts]
+    _check(library().fp8idx_paged_step_tables(*d[:4], int(block_size), *d[4:], _stream(stream, old_lens)))
+    return slot_mapping
+
+
+def fp8_paged_store(k, v, slot_mapping, kv_cache, stream=None):
+    """Quantises rows to e4m3 with one f32 scale each (max|x| / 448) and
+    writes them at their slots (a negative slot is skipped): k [tokens, D]
+    into an index cache (v None), or k and v [tokens, kv_heads, D] into a
+    key/value cache."""
+    ts = (k, v, slot_mapping, kv_cache)
+    _on_current_device(*ts)
+    d = [None if t is None else _pack(t, t.data_ptr()) for t in ts]
+    _check(library().fp8_paged_store(*d, _stream(stream, k)))
+    return kv_cache
+
+
+def fp8_paged_sparse_attn(q, kv_cache, indices, block_tables, softmax_scale, out, lse=None, stream=None,
+                          options: Options | None = None):
+    """Decode attention of q [batch, next_n, heads, D] over the positions
+    indices [batch*next_n, k] of each request (-1: no position) into ``out``,
+    and the log-sum-exp of the scores into ``lse``."""
+    ts = (q, kv_cache, indices, block_tables, out, lse)
+    _on_current_device(*ts)
+    d = [None if t is None else _pack(t, t.data_ptr()) for t in ts]
+    oc = options._c() if options is not None else None
+    _check(library().fp8_paged_sparse_attn(*d[:4], float(softmax_scale), *d[4:],
+                                           ctypes.byref(oc) if oc is not None else None, _stream(stream, q)))
+    return out
+
+
+def fp8_mqa_sparse_attn_paged(q, kv_cache, block_tables, cu_seq_lens, indices, softmax_scale, out, lse=None,
+                              stream=None, options: Options | None = None):
+    """Prefill attention of q [M, heads, D] over the columns indices [M, k]
+    of the packed requests (column i with cu_seq_lens[r] <= i <
+    cu_seq_lens[r+1] is a token of request r; -1: no column)."""
+    ts = (q, kv_cache, block_tables, cu_seq_lens, indices, out, lse)
+    _on_current_device(*ts)
+    d = [None if t is None else _pack(t, t.data_ptr()) for t in ts]
+    oc = options._c() if options is not None else None
+    _check(library().fp8_mqa_sparse_attn_paged(*d[:5], float(softmax_scale), *d[5:],
+                                               ctypes.byref(oc) if oc is not None else None, _stream(stream, q)))
+    return out
 
 
 def paged_is_supported(heads, head_dim, block_size, next_n) -> bool:

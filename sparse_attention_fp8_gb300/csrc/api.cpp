@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -13,6 +14,7 @@
 
 #include "fp8idx.h"
 #include "kernels.h"
+#include "operators.h"
 
 namespace {
 
@@ -305,7 +307,8 @@ fp8idx_status paged_setup(const fp8idx_tensor* q, const fp8idx_tensor* kv, const
   if (!contiguous(w)) return fail(FP8IDX_ERR_INVALID, "weights must be contiguous");
   if (cl->shape[0] != B || (B > 1 && cl->stride[0] != 1)) return fail(FP8IDX_ERR_INVALID, "context_lens must be [batch] contiguous");
   if (w->shape[0] != B * next_n || w->shape[1] != H) return fail(FP8IDX_ERR_INVALID, "weights must be [batch*next_n, heads]");
-  if (bt->shape[0] != B || (bt->shape[1] > 1 && bt->stride[1] != 1) || (B > 1 && bt->stride[0] < bt->shape[1]))
+  if (bt->shape[0] != B || (B > 0 && bt->shape[1] > 1 && bt->stride[1] != 1) ||
+      (B > 1 && bt->stride[0] < bt->shape[1]))
     return fail(FP8IDX_ERR_INVALID, "block_tables must be [batch, max_blocks] with unit inner stride");
   if (D <= 0 || kv->shape[1] % (D + 4) != 0) return fail(FP8IDX_ERR_INVALID, "kv_cache row is not block_size*(head_dim+4) bytes");
   const int64_t blk = kv->shape[1] / (D + 4);
@@ -755,6 +758,289 @@ fp8idx_status topk_impl(int mode, const fp8idx_tensor* logits, const fp8idx_tens
   return ok();
 }
 
+// ------------------------------------------- the operators around the indexer
+bool block_size_ok(int64_t bs) { return bs == 1 || bs == 16 || bs == 32 || bs == 64 || bs == 128; }
+bool row_dim_ok(int64_t d) { return d == 64 || d == 128; }
+int64_t kv_page_bytes(int64_t bs, int64_t d) { return (bs * (2 * d + 8) + 15) / 16 * 16; }
+
+fp8idx_status check_vector(const fp8idx_tensor* t, const char* name, int64_t n) {
+  TRY(check_tensor(t, name, FP8IDX_I32, 1));
+  if (t->shape[0] != n || (n > 1 && t->stride[0] != 1))
+    return fail(FP8IDX_ERR_INVALID, "%s: expected contiguous [%lld]", name, (long long)n);
+  return FP8IDX_OK;
+}
+
+// Whether the bytes of two tensors (with non-negative strides) can overlap,
+// as ranges of addresses.
+bool ranges_overlap(const fp8idx_tensor* a, const fp8idx_tensor* b) {
+  const auto range = [](const fp8idx_tensor* t, uintptr_t* lo, uintptr_t* hi) {
+    const int64_t size = t->dtype == FP8IDX_U8 ? 1 : (t->dtype == FP8IDX_BF16 || t->dtype == FP8IDX_F16) ? 2 : 4;
+    int64_t last = 0;
+    for (int i = 0; i < t->ndim; ++i) {
+      if (t->shape[i] == 0) return false;
+      last += (t->shape[i] - 1) * t->stride[i];
+    }
+    *lo = reinterpret_cast<uintptr_t>(t->data);
+    *hi = *lo + static_cast<uintptr_t>((last + 1) * size);
+    return true;
+  };
+  uintptr_t al, ah, bl, bh;
+  return range(a, &al, &ah) && range(b, &bl, &bh) && al < bh && bl < ah;
+}
+
+fp8idx_status step_tables_impl(const fp8idx_tensor* old_lens, const fp8idx_tensor* new_lens,
+                               const fp8idx_tensor* free_blocks, const fp8idx_tensor* free_count, int32_t block_size,
+                               const fp8idx_tensor* bt, const fp8idx_tensor* ctx, const fp8idx_tensor* cu_new,
+                               const fp8idx_tensor* slots, const fp8idx_tensor* counts, const fp8idx_tensor* cu_seq,
+                               const fp8idx_tensor* ks, const fp8idx_tensor* ke, void* stream) {
+  g_last_error.clear();
+  TRY(check_tensor(old_lens, "old_lens", FP8IDX_I32, 1));
+  const int64_t B = old_lens->shape[0];
+  TRY(check_vector(old_lens, "old_lens", B));
+  TRY(check_vector(new_lens, "new_lens", B));
+  TRY(check_tensor(free_blocks, "free_blocks", FP8IDX_I32, 1));
+  TRY(check_vector(free_blocks, "free_blocks", free_blocks->shape[0]));
+  TRY(check_vector(free_count, "free_count", 1));
+  TRY(check_tensor(bt, "block_tables", FP8IDX_I32, 2));
+  if (bt->shape[0] != B || (B > 0 && bt->shape[1] > 1 && bt->stride[1] != 1) ||
+      (B > 1 && bt->stride[0] < bt->shape[1]))
+    return fail(FP8IDX_ERR_INVALID, "block_tables must be [batch, max_blocks] with contiguous rows");
+  TRY(check_vector(ctx, "context_lens", B));
+  TRY(check_vector(cu_new, "cu_new_lens", B + 1));
+  TRY(check_tensor(slots, "slot_mapping", FP8IDX_I32, 1));
+  const int64_t T = slots->shape[0];
+  TRY(check_vector(slots, "slot_mapping", T));
+  TRY(check_vector(counts, "counts", 4));
+  if (cu_seq) TRY(check_vector(cu_seq, "cu_seq_lens", B + 1));
+  if (ks) TRY(check_vector(ks, "cu_seqlen_ks", T));
+  if (ke) TRY(check_vector(ke, "cu_seqlen_ke", T));
+  if (!block_size_ok(block_size))
+    return fail(FP8IDX_ERR_UNSUPPORTED, "step tables: block_size %d not in {1, 16, 32, 64, 128}", block_size);
+  if (B > kMaxBatch) return fail(FP8IDX_ERR_UNSUPPORTED, "step tables: batch %lld > %d", (long long)B, kMaxBatch);
+  if (bt->shape[1] * block_size >= (1ll << 31) || T >= (1ll << 31))
+    return fail(FP8IDX_ERR_UNSUPPORTED, "step tables: positions and rows must stay below 2^31");
+  const fp8idx_tensor* ins[] = {old_lens, new_lens, free_blocks, free_count};
+  const fp8idx_tensor* outs[] = {bt, ctx, cu_new, slots, counts, cu_seq, ks, ke};
+  for (int i = 0; i < 8; ++i) {
+    if (!outs[i]) continue;
+    for (const fp8idx_tensor* in : ins)
+      if (ranges_overlap(in, outs[i]))
+        return fail(FP8IDX_ERR_INVALID, "step tables: an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (outs[j] && ranges_overlap(outs[j], outs[i]))
+        return fail(FP8IDX_ERR_INVALID, "step tables: two outputs overlap");
+  }
+  StepTablesParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.old_lens = static_cast<const int32_t*>(old_lens->data);
+  p.new_lens = static_cast<const int32_t*>(new_lens->data);
+  p.free_blocks = static_cast<const int32_t*>(free_blocks->data);
+  p.free_count = static_cast<const int32_t*>(free_count->data);
+  p.block_tables = static_cast<int32_t*>(bt->data);
+  p.context_lens = static_cast<int32_t*>(ctx->data);
+  p.cu_new = static_cast<int32_t*>(cu_new->data);
+  p.slots = static_cast<int32_t*>(slots->data);
+  p.counts = static_cast<int32_t*>(counts->data);
+  p.cu_seq = cu_seq ? static_cast<int32_t*>(cu_seq->data) : nullptr;
+  p.ks = ks ? static_cast<int32_t*>(ks->data) : nullptr;
+  p.ke = ke ? static_cast<int32_t*>(ke->data) : nullptr;
+  p.bt_stride = B > 1 ? bt->stride[0] : bt->shape[1];
+  p.rows = T;
+  p.free_cap = free_blocks->shape[0];
+  p.batch = (int32_t)B;
+  p.max_blocks = (int32_t)bt->shape[1];
+  p.block_size = block_size;
+  DeviceInfo dev;
+  TRY(device_info(&dev));
+  // a thread per row (and, for small blocks, about one per block dealt)
+  const int64_t ctas = (std::max<int64_t>(T, B) + kStepThreads - 1) / kStepThreads;
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(ctas, dev.sms));
+  cudaError_t e = launch_step_tables(p, grid, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(FP8IDX_ERR_CUDA, "step tables launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+// A key/value cache [num_blocks, kv_heads, page]: its strides, and the block
+// size that its page has for head_dim D.
+fp8idx_status check_kv_cache(const fp8idx_tensor* kv, int64_t D, int64_t* block_size) {
+  TRY(check_tensor(kv, "kv_cache", FP8IDX_U8, 3));
+  const int64_t page = kv->shape[2], bs = page / (2 * D + 8);
+  if (bs < 1 || kv_page_bytes(bs, D) != page)
+    return fail(FP8IDX_ERR_INVALID, "kv_cache: a page of %lld bytes is not fp8idx_kv_page_bytes(block_size, %lld)",
+                (long long)page, (long long)D);
+  if (!block_size_ok(bs))
+    return fail(FP8IDX_ERR_UNSUPPORTED, "kv_cache: block_size %lld not in {1, 16, 32, 64, 128}", (long long)bs);
+  if (kv->shape[0] < 1 || kv->shape[1] < 1) return fail(FP8IDX_ERR_INVALID, "kv_cache: empty");
+  if (kv->stride[2] != 1) return fail(FP8IDX_ERR_INVALID, "kv_cache: pages must be contiguous");
+  const bool one_block = kv->shape[0] == 1, one_head = kv->shape[1] == 1;
+  if ((!one_block && (kv->stride[0] % 16 != 0 || kv->stride[0] < page)) ||
+      (!one_head && (kv->stride[1] % 16 != 0 || kv->stride[1] < page)))
+    return fail(FP8IDX_ERR_INVALID, "kv_cache: block and head strides must be multiples of 16 bytes, at least a page");
+  if (!one_block && !one_head && kv->stride[0] < kv->shape[1] * kv->stride[1] &&
+      kv->stride[1] < kv->shape[0] * kv->stride[0])
+    return fail(FP8IDX_ERR_INVALID, "kv_cache: the pages of blocks and heads overlap");
+  if (!aligned16(kv->data)) return fail(FP8IDX_ERR_INVALID, "kv_cache must be 16-byte aligned");
+  if (kv->shape[0] * bs >= (1ll << 31))
+    return fail(FP8IDX_ERR_UNSUPPORTED, "kv_cache: %lld blocks of %lld tokens (slots must stay below 2^31)",
+                (long long)kv->shape[0], (long long)bs);
+  *block_size = bs;
+  return FP8IDX_OK;
+}
+
+fp8idx_status paged_store_impl(const fp8idx_tensor* k, const fp8idx_tensor* v, const fp8idx_tensor* slots,
+                               const fp8idx_tensor* kv, void* stream) {
+  g_last_error.clear();
+  const int nd = v ? 3 : 2;
+  if (!k) return fail(FP8IDX_ERR_INVALID, "k: null descriptor");
+  int type = -1;
+  if (k->dtype == FP8IDX_BF16) type = kRowBf16;
+  if (k->dtype == FP8IDX_F16) type = kRowF16;
+  if (k->dtype == FP8IDX_F32) type = kRowF32;
+  if (type < 0) return fail(FP8IDX_ERR_INVALID, "k: wrong dtype %d", k->dtype);
+  const int64_t item = type == kRowF32 ? 4 : 2;
+  TRY(check_tensor(k, "k", k->dtype, nd));
+  const int64_t T = k->shape[0], H = v ? k->shape[1] : 1, D = k->shape[nd - 1];
+  PagedStoreParams p;
+  std::memset(&p, 0, sizeof(p));
+  const fp8idx_tensor* xs[2] = {k, v};
+  for (int i = 0; i < (v ? 2 : 1); ++i) {
+    const fp8idx_tensor* x = xs[i];
+    const char* name = i ? "v" : "k";
+    TRY(check_tensor(x, name, k->dtype, nd));
+    for (int d = 0; d < nd; ++d)
+      if (x->shape[d] != k->shape[d]) return fail(FP8IDX_ERR_INVALID, "v must have the shape of k");
+    if (x->stride[nd - 1] != 1) return fail(FP8IDX_ERR_INVALID, "%s: rows must have unit inner stride", name);
+    p.x[i] = x->data;
+    p.token_stride[i] = T > 1 ? x->stride[0] * item : 0;
+    p.head_stride[i] = v && H > 1 ? x->stride[1] * item : 0;
+    if (!aligned16(x->data) || p.token_stride[i] % 16 != 0 || p.head_stride[i] % 16 != 0)
+      return fail(FP8IDX_ERR_INVALID, "%s: rows must be 16-byte aligned", name);
+  }
+  TRY(check_vector(slots, "slot_mapping", T));
+  if (!row_dim_ok(D)) return fail(FP8IDX_ERR_UNSUPPORTED, "store: head_dim %lld (64 or 128)", (long long)D);
+  int64_t bs = 0;
+  if (v) {
+    TRY(check_kv_cache(kv, D, &bs));
+    if (kv->shape[1] != H) return fail(FP8IDX_ERR_INVALID, "kv_cache has %lld heads, k has %lld", (long long)kv->shape[1], (long long)H);
+    p.block_stride = kv->shape[0] > 1 ? kv->stride[0] : 0;
+    p.cache_head_stride = H > 1 ? kv->stride[1] : 0;
+  } else {
+    TRY(check_tensor(kv, "kv_cache", FP8IDX_U8, 2));
+    if (!contiguous(kv)) return fail(FP8IDX_ERR_INVALID, "kv_cache must be contiguous");
+    if (kv->shape[0] < 1 || kv->shape[1] < 1 || kv->shape[1] % (D + 4) != 0)
+      return fail(FP8IDX_ERR_INVALID, "kv_cache rows must be block_size*(head_dim+4) bytes");
+    bs = kv->shape[1] / (D + 4);
+    if (!block_size_ok(bs))
+      return fail(FP8IDX_ERR_UNSUPPORTED, "store: block_size %lld not in {1, 16, 32, 64, 128}", (long long)bs);
+    if (!aligned16(kv->data)) return fail(FP8IDX_ERR_INVALID, "kv_cache must be 16-byte aligned");
+    if (kv->shape[0] * bs >= (1ll << 31)) return fail(FP8IDX_ERR_UNSUPPORTED, "store: slots must stay below 2^31");
+    p.block_stride = kv->shape[1];
+  }
+  if (T * H * (v ? 2 : 1) * (D / 8) >= (1ll << 38))
+    return fail(FP8IDX_ERR_UNSUPPORTED, "store: %lld tokens of %lld heads in one call", (long long)T, (long long)H);
+  if (T == 0 || H == 0) return ok();
+  p.slots = static_cast<const int32_t*>(slots->data);
+  p.cache = static_cast<uint8_t*>(kv->data);
+  p.num_slots = kv->shape[0] * bs;
+  p.tokens = T;
+  p.heads = (int32_t)H;
+  p.block_size = (int32_t)bs;
+  DeviceInfo dev;
+  TRY(device_info(&dev));
+  cudaError_t e = launch_paged_store(p, type, (int)D, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(FP8IDX_ERR_CUDA, "store launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+// decode: q [batch, next_n, heads, D], cu_seq null; prefill: q [M, heads, D].
+fp8idx_status sparse_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, const fp8idx_tensor* bt,
+                               const fp8idx_tensor* cu, bool prefill, const fp8idx_tensor* idx, float softmax_scale,
+                               const fp8idx_tensor* out, const fp8idx_tensor* lse, const fp8idx_options* opts,
+                               void* stream) {
+  g_last_error.clear();
+  const int nd = prefill ? 3 : 4;
+  TRY(check_tensor(q, "q", FP8IDX_BF16, nd));
+  TRY(check_tensor(out, "out", FP8IDX_BF16, nd));
+  const int64_t H = q->shape[nd - 2], D = q->shape[nd - 1];
+  const int64_t n = prefill ? 1 : q->shape[1], B = q->shape[0], R = B * n;
+  for (int i = 0; i < nd; ++i)
+    if (out->shape[i] != q->shape[i]) return fail(FP8IDX_ERR_INVALID, "out must have the shape of q");
+  if (!row_dim_ok(D)) return fail(FP8IDX_ERR_UNSUPPORTED, "sparse attention: head_dim %lld (64 or 128)", (long long)D);
+  if (q->stride[nd - 1] != 1 || out->stride[nd - 1] != 1)
+    return fail(FP8IDX_ERR_INVALID, "q and out must have unit inner stride");
+  if (H < 1 || n < 1) return fail(FP8IDX_ERR_INVALID, "q has no heads or rows per request");
+  int64_t bs = 0;
+  TRY(check_kv_cache(kv, D, &bs));
+  const int64_t HK = kv->shape[1];
+  if (H % HK != 0) return fail(FP8IDX_ERR_INVALID, "%lld heads are no multiple of %lld kv_heads", (long long)H, (long long)HK);
+  if (H / HK > kAttnMaxGroup)
+    return fail(FP8IDX_ERR_UNSUPPORTED, "sparse attention: %lld heads per key head (at most %d)", (long long)(H / HK), kAttnMaxGroup);
+  TRY(check_tensor(bt, "block_tables", FP8IDX_I32, 2));
+  if (bt->shape[1] > 1 && bt->stride[1] != 1) return fail(FP8IDX_ERR_INVALID, "block_tables rows must be contiguous");
+  if (!prefill && bt->shape[0] != B) return fail(FP8IDX_ERR_INVALID, "block_tables must be [batch, max_blocks]");
+  if (bt->shape[1] < 1 || (prefill && bt->shape[0] < 1)) return fail(FP8IDX_ERR_INVALID, "empty block table");
+  if (bt->shape[1] * bs >= (1ll << 31)) return fail(FP8IDX_ERR_UNSUPPORTED, "positions must stay below 2^31");
+  if (prefill) {
+    if (bt->shape[0] > kMaxBatch)
+      return fail(FP8IDX_ERR_UNSUPPORTED, "sparse attention: %lld requests > %d", (long long)bt->shape[0], kMaxBatch);
+    TRY(check_vector(cu, "cu_seq_lens", bt->shape[0] + 1));
+  }
+  TRY(check_tensor(idx, "indices", FP8IDX_I32, 2));
+  const int64_t k = idx->shape[1];
+  if (k < 1 || k > kAttnMaxK) return fail(FP8IDX_ERR_UNSUPPORTED, "sparse attention: k=%lld not in [1, %d]", (long long)k, kAttnMaxK);
+  if (idx->shape[0] != R || (k > 1 && idx->stride[1] != 1) || (R > 1 && idx->stride[0] < k))
+    return fail(FP8IDX_ERR_INVALID, "indices must be [rows, k] with unit inner stride");
+  if (lse) {
+    TRY(check_tensor(lse, "lse", FP8IDX_F32, 2));
+    if (lse->shape[0] != R || lse->shape[1] != H || !contiguous(lse))
+      return fail(FP8IDX_ERR_INVALID, "lse must be contiguous [rows, heads]");
+  }
+  if (!std::isfinite(softmax_scale)) return fail(FP8IDX_ERR_INVALID, "softmax_scale must be finite");
+  if (R * H >= (1ll << 31)) return fail(FP8IDX_ERR_UNSUPPORTED, "sparse attention: rows*heads must stay below 2^31");
+  const int32_t ctas = opts ? opts->num_ctas : 0;
+  if (ctas != 0 && ctas != 1 && ctas != 2 && ctas != 4 && ctas != 8)
+    return fail(FP8IDX_ERR_UNSUPPORTED, "sparse attention: num_ctas=%d not in {0, 1, 2, 4, 8}", ctas);
+  if (R == 0) return ok();
+  SparseAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  const auto strides = [&](const fp8idx_tensor* t, int64_t* req, int64_t* row, int64_t* head) {
+    *req = B > 1 ? t->stride[0] : 0;
+    *row = !prefill && n > 1 ? t->stride[1] : 0;
+    *head = H > 1 ? t->stride[nd - 2] : 0;
+  };
+  strides(q, &p.q_req_stride, &p.q_row_stride, &p.q_head_stride);
+  strides(out, &p.out_req_stride, &p.out_row_stride, &p.out_head_stride);
+  if (!aligned16(q->data) || ((p.q_req_stride | p.q_row_stride | p.q_head_stride) & 7) != 0)
+    return fail(FP8IDX_ERR_INVALID, "q rows must be 16-byte aligned");
+  p.q = q->data;
+  p.out = out->data;
+  p.lse = lse ? static_cast<float*>(lse->data) : nullptr;
+  p.kv = static_cast<const uint8_t*>(kv->data);
+  p.indices = static_cast<const int32_t*>(idx->data);
+  p.block_tables = static_cast<const int32_t*>(bt->data);
+  p.cu_seq_lens = prefill ? static_cast<const int32_t*>(cu->data) : nullptr;
+  p.idx_stride = R > 1 ? idx->stride[0] : k;
+  p.bt_stride = bt->shape[0] > 1 ? bt->stride[0] : 0;
+  p.block_stride = kv->shape[0] > 1 ? kv->stride[0] : 0;
+  p.kv_head_stride = HK > 1 ? kv->stride[1] : 0;
+  p.num_blocks = kv->shape[0];
+  p.rows = (int32_t)R;
+  p.heads = (int32_t)H;
+  p.kv_heads = (int32_t)HK;
+  p.group = (int32_t)(H / HK);
+  p.next_n = (int32_t)n;
+  p.k = (int32_t)k;
+  p.max_blocks = (int32_t)bt->shape[1];
+  p.block_size = (int32_t)bs;
+  p.n_req = (int32_t)bt->shape[0];
+  p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
+  DeviceInfo dev;
+  TRY(device_info(&dev));
+  cudaError_t e = launch_sparse_attn(p, (int)D, dev.sms, ctas, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(FP8IDX_ERR_CUDA, "sparse attention launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -838,6 +1124,40 @@ fp8idx_status fp8_mqa_topk_ex(const fp8idx_tensor* logits, const fp8idx_tensor* 
   return topk_impl(0, logits, cu_seqlen_ks, cu_seqlen_ke, nullptr, 1, 0, k, indices, opts, stream);
 }
 
+int64_t fp8idx_kv_page_bytes(int32_t block_size, int32_t head_dim) {
+  return block_size_ok(block_size) && row_dim_ok(head_dim) ? kv_page_bytes(block_size, head_dim) : 0;
+}
+
+fp8idx_status fp8idx_paged_step_tables(const fp8idx_tensor* old_lens, const fp8idx_tensor* new_lens,
+                                       const fp8idx_tensor* free_blocks, const fp8idx_tensor* free_count,
+                                       int32_t block_size, const fp8idx_tensor* block_tables,
+                                       const fp8idx_tensor* context_lens, const fp8idx_tensor* cu_new_lens,
+                                       const fp8idx_tensor* slot_mapping, const fp8idx_tensor* counts,
+                                       const fp8idx_tensor* cu_seq_lens, const fp8idx_tensor* cu_seqlen_ks,
+                                       const fp8idx_tensor* cu_seqlen_ke, void* stream) {
+  return step_tables_impl(old_lens, new_lens, free_blocks, free_count, block_size, block_tables, context_lens,
+                          cu_new_lens, slot_mapping, counts, cu_seq_lens, cu_seqlen_ks, cu_seqlen_ke, stream);
+}
+
+fp8idx_status fp8_paged_store(const fp8idx_tensor* k, const fp8idx_tensor* v, const fp8idx_tensor* slot_mapping,
+                              const fp8idx_tensor* kv_cache, void* stream) {
+  return paged_store_impl(k, v, slot_mapping, kv_cache, stream);
+}
+
+fp8idx_status fp8_paged_sparse_attn(const fp8idx_tensor* q, const fp8idx_tensor* kv_cache,
+                                    const fp8idx_tensor* indices, const fp8idx_tensor* block_tables,
+                                    float softmax_scale, const fp8idx_tensor* out, const fp8idx_tensor* lse,
+                                    const fp8idx_options* opts, void* stream) {
+  return sparse_attn_impl(q, kv_cache, block_tables, nullptr, false, indices, softmax_scale, out, lse, opts, stream);
+}
+
+fp8idx_status fp8_mqa_sparse_attn_paged(const fp8idx_tensor* q, const fp8idx_tensor* kv_cache,
+                                        const fp8idx_tensor* block_tables, const fp8idx_tensor* cu_seq_lens,
+                                        const fp8idx_tensor* indices, float softmax_scale, const fp8idx_tensor* out,
+                                        const fp8idx_tensor* lse, const fp8idx_options* opts, void* stream) {
+  return sparse_attn_impl(q, kv_cache, block_tables, cu_seq_lens, true, indices, softmax_scale, out, lse, opts, stream);
+}
+
 int fp8idx_paged_is_supported(int32_t heads, int32_t head_dim, int32_t block_size, int32_t next_n) {
   return paged_supported(heads, head_dim, block_size, next_n) ? 1 : 0;
 }
@@ -918,6 +1238,6 @@ fp8idx_status fp8idx_watchdog_selftest(int32_t limit_us, void* stream) {
   return ok();
 }
 
-int32_t fp8idx_version(void) { return 102; }
+int32_t fp8idx_version(void) { return 103; }
 
 }  // extern "C"

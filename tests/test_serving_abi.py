@@ -1,0 +1,179 @@
+"""Refusals of the operators around the indexer (CPU: host checks with fake
+pointers that are never dereferenced, before any CUDA call), and their plain
+definitions on hand cases."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_fp8_gb300 as fp8idx
+from oracle import serving as ref
+from test_abi import _t
+
+U8, F32, I32, BF16, F16 = 0, 1, 2, 3, 4
+INVALID, UNSUPPORTED = fp8idx.FP8IDX_ERR_INVALID, fp8idx.FP8IDX_ERR_UNSUPPORTED
+R = ctypes.byref
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from sparse_attention_fp8_gb300 import _build
+    _build.build()
+    return fp8idx.library()
+
+
+def refused(lib, st, status, word):
+    assert st == status, (st, lib.fp8idx_last_error())
+    assert word in lib.fp8idx_last_error(), lib.fp8idx_last_error()
+
+
+def test_page_bytes(lib):
+    for bs in (1, 16, 32, 64, 128):
+        for d in (64, 128):
+            assert fp8idx.kv_page_bytes(bs, d) == ref.page_bytes(bs, d)
+    assert fp8idx.kv_page_bytes(8, 128) == 0 and fp8idx.kv_page_bytes(64, 96) == 0
+
+
+def step_args(B=3, T=10, mb=4, **kw):
+    at = iter(range(0x100000, 0x200000, 0x1000))
+    a = dict(old=_t(I32, (B,), next(at)), new=_t(I32, (B,), next(at)), free=_t(I32, (9,), next(at)),
+             count=_t(I32, (1,), next(at)), bs=16, bt=_t(I32, (B, mb), next(at)), ctx=_t(I32, (B,), next(at)),
+             cu=_t(I32, (B + 1,), next(at)), slots=_t(I32, (T,), next(at)), counts=_t(I32, (4,), next(at)),
+             seq=_t(I32, (B + 1,), next(at)), ks=_t(I32, (T,), next(at)), ke=_t(I32, (T,), next(at)))
+    a.update(kw)
+    return [R(v) if isinstance(v, ctypes.Structure) else v for v in a.values()] + [None]
+
+
+def test_step_tables_refusals(lib):
+    f = lib.fp8idx_paged_step_tables
+    refused(lib, f(*step_args(old=None)), INVALID, b"old_lens")
+    refused(lib, f(*step_args(new=_t(I32, (4,)))), INVALID, b"new_lens")
+    refused(lib, f(*step_args(count=_t(I32, (2,)))), INVALID, b"free_count")
+    refused(lib, f(*step_args(counts=_t(I32, (3,)))), INVALID, b"counts")
+    refused(lib, f(*step_args(slots=_t(F32, (10,)))), INVALID, b"slot_mapping")
+    refused(lib, f(*step_args(ks=_t(I32, (9,)))), INVALID, b"cu_seqlen_ks")
+    refused(lib, f(*step_args(bt=_t(I32, (2, 4)))), INVALID, b"block_tables")
+    refused(lib, f(*step_args(bs=8)), UNSUPPORTED, b"block_size")
+    refused(lib, f(*step_args(bs=0)), UNSUPPORTED, b"block_size")
+    refused(lib, f(*step_args(B=4097)), UNSUPPORTED, b"batch")
+    refused(lib, f(*step_args(mb=1 << 27)), UNSUPPORTED, b"2^31")
+    refused(lib, f(*step_args(ctx=_t(I32, (3,), 0x100000))), INVALID, b"overlaps an input")   # old_lens in place
+    refused(lib, f(*step_args(ctx=_t(I32, (3,), 0x107008))), INVALID, b"two outputs")
+    strided = _t(I32, (3,), 0x300000)
+    strided.stride[0] = 2
+    refused(lib, f(*step_args(old=strided)), INVALID, b"old_lens")
+
+
+def test_store_refusals(lib):
+    f = lib.fp8_paged_store
+    k, slots, kv = _t(BF16, (5, 2, 128)), _t(I32, (5,)), _t(U8, (4, 2, 16 * 264))
+    refused(lib, f(None, R(k), R(slots), R(kv), None), INVALID, b"k: null")
+    refused(lib, f(R(_t(I32, (5, 2, 128))), R(k), R(slots), R(kv), None), INVALID, b"dtype")
+    refused(lib, f(R(k), R(_t(F16, (5, 2, 128))), R(slots), R(kv), None), INVALID, b"v: wrong dtype")
+    refused(lib, f(R(k), R(_t(BF16, (5, 1, 128))), R(slots), R(kv), None), INVALID, b"shape of k")
+    refused(lib, f(R(k), R(k), R(_t(I32, (4,))), R(kv), None), INVALID, b"slot_mapping")
+    refused(lib, f(R(k), R(k), R(slots), R(_t(U8, (4, 2, 16 * 264 + 16))), None), INVALID, b"page")
+    refused(lib, f(R(k), R(k), R(slots), R(_t(U8, (4, 2, 8 * 264))), None), UNSUPPORTED, b"block_size")
+    refused(lib, f(R(k), R(k), R(slots), R(_t(U8, (4, 3, 16 * 264))), None), INVALID, b"heads")
+    refused(lib, f(R(k), R(k), R(slots), R(_t(U8, (4, 2, 16 * 264), 0x1008)), None), INVALID, b"aligned")
+    refused(lib, f(R(_t(BF16, (5, 2, 128), 0x1008)), R(k), R(slots), R(kv), None), INVALID, b"aligned")
+    odd = _t(BF16, (5, 2, 128))
+    odd.stride[0] = 260
+    refused(lib, f(R(odd), R(k), R(slots), R(kv), None), INVALID, b"aligned")
+    odd = _t(BF16, (5, 2, 128))
+    odd.stride[2] = 2
+    refused(lib, f(R(odd), R(k), R(slots), R(kv), None), INVALID, b"inner stride")
+    over = _t(U8, (4, 2, 16 * 264))
+    over.stride[0] = over.stride[1] = 16 * 264
+    refused(lib, f(R(k), R(k), R(slots), R(over), None), INVALID, b"overlap")
+    refused(lib, f(R(k), R(k), R(slots), R(_t(U8, (1 << 27, 2, 16 * 264))), None), UNSUPPORTED, b"2^31")
+    k96 = _t(BF16, (5, 2, 96))
+    refused(lib, f(R(k96), R(k96), R(slots), R(_t(U8, (4, 2, 16 * 200))), None), UNSUPPORTED, b"head_dim")
+    # the index cache
+    k2 = _t(F32, (5, 128))
+    refused(lib, f(R(k2), None, R(slots), R(_t(U8, (4, 100))), None), INVALID, b"head_dim+4")
+    refused(lib, f(R(k2), None, R(slots), R(_t(U8, (4, 5 * 132))), None), UNSUPPORTED, b"block_size")
+    refused(lib, f(R(k), None, R(slots), R(_t(U8, (4, 64 * 132))), None), INVALID, b"ndim")
+    refused(lib, f(R(k2), None, R(slots), R(kv), None), INVALID, b"ndim")
+
+
+def attn_args(q=None, kv=None, idx=None, bt=None, scale=1.0, out=None, lse=None, opts=None):
+    q = q or _t(BF16, (2, 3, 8, 128))
+    return [R(q), R(kv or _t(U8, (9, 2, 16 * 264))), R(idx or _t(I32, (6, 50))), R(bt or _t(I32, (2, 5))), scale,
+            R(out or _t(BF16, tuple(q.shape[:q.ndim]))), None if lse is None else R(lse),
+            None if opts is None else R(opts._c()), None]
+
+
+def test_decode_attention_refusals(lib):
+    f = lib.fp8_paged_sparse_attn
+    refused(lib, f(*attn_args(q=_t(F32, (2, 3, 8, 128)))), INVALID, b"q: wrong dtype")
+    refused(lib, f(*attn_args(q=_t(BF16, (6, 8, 128)))), INVALID, b"ndim")
+    refused(lib, f(*attn_args(q=_t(BF16, (2, 3, 8, 96)))), UNSUPPORTED, b"head_dim")
+    # (a page of 4224 bytes is that of 31 tokens of 64 values: 31 * 136 = 4216, padded)
+    refused(lib, f(*attn_args(q=_t(BF16, (2, 3, 8, 64)))), UNSUPPORTED, b"block_size 31")
+    refused(lib, f(*attn_args(kv=_t(U8, (9, 2, 16 * 264 + 32)))), INVALID, b"page")
+    refused(lib, f(*attn_args(out=_t(BF16, (2, 3, 4, 128)))), INVALID, b"shape of q")
+    refused(lib, f(*attn_args(q=_t(BF16, (2, 3, 7, 128)))), INVALID, b"multiple")
+    refused(lib, f(*attn_args(q=_t(BF16, (2, 3, 258, 128)))), UNSUPPORTED, b"heads per key head")
+    refused(lib, f(*attn_args(idx=_t(I32, (5, 50)))), INVALID, b"indices")
+    refused(lib, f(*attn_args(idx=_t(I32, (6, 2049)))), UNSUPPORTED, b"k=2049")
+    refused(lib, f(*attn_args(idx=_t(I32, (6, 0)))), UNSUPPORTED, b"k=0")
+    refused(lib, f(*attn_args(bt=_t(I32, (3, 5)))), INVALID, b"block_tables")
+    refused(lib, f(*attn_args(bt=_t(I32, (2, 0)))), INVALID, b"block table")
+    refused(lib, f(*attn_args(lse=_t(F32, (6, 7)))), INVALID, b"lse")
+    refused(lib, f(*attn_args(scale=float("inf"))), INVALID, b"softmax_scale")
+    refused(lib, f(*attn_args(scale=float("nan"))), INVALID, b"softmax_scale")
+    refused(lib, f(*attn_args(opts=fp8idx.Options(num_ctas=3))), UNSUPPORTED, b"num_ctas")
+    refused(lib, f(*attn_args(q=_t(BF16, (2, 3, 8, 128), 0x1002))), INVALID, b"aligned")
+    odd = _t(BF16, (2, 3, 8, 128))
+    odd.stride[1] = 8 * 128 + 4
+    refused(lib, f(*attn_args(q=odd)), INVALID, b"aligned")
+
+
+def test_prefill_attention_refusals(lib):
+    f = lib.fp8_mqa_sparse_attn_paged
+    q, kv, idx, out = _t(BF16, (6, 8, 128)), _t(U8, (9, 2, 16 * 264)), _t(I32, (6, 50)), _t(BF16, (6, 8, 128))
+    bt, cu = _t(I32, (2, 5)), _t(I32, (3,))
+    refused(lib, f(R(q), R(kv), R(bt), R(_t(I32, (2,))), R(idx), 1.0, R(out), None, None, None), INVALID, b"cu_seq_lens")
+    refused(lib, f(R(q), R(kv), R(bt), None, R(idx), 1.0, R(out), None, None, None), INVALID, b"cu_seq_lens")
+    refused(lib, f(R(q), R(kv), R(_t(I32, (4097, 5))), R(_t(I32, (4098,))), R(idx), 1.0, R(out), None, None, None),
+            UNSUPPORTED, b"requests")
+    refused(lib, f(R(q), R(kv), R(_t(I32, (0, 5))), R(cu), R(idx), 1.0, R(out), None, None, None), INVALID, b"block table")
+
+
+def test_binding_refuses_host_tensors():
+    with pytest.raises(ValueError, match="CUDA"):
+        fp8idx.fp8_paged_store(torch.zeros(2, 128), None, torch.zeros(2, dtype=torch.int32),
+                               torch.zeros(2, 132, dtype=torch.uint8))
+
+
+def test_definition_step_tables_by_hand():
+    tables = np.array([[7, -1, -1], [3, 4, -1]], np.int32)
+    got = ref.step_tables([2, 8], [3, 1], np.array([20, 21, 22, 23]), 4, 4, tables, 6)
+    # request 0: positions 2, 3 in block 7, position 4 in the first block dealt; request 1: position 8
+    assert got["slot_mapping"].tolist() == [30, 31, 92, 88, -1, -1]
+    assert got["block_tables"].tolist() == [[7, 23, -1], [3, 4, 22]]
+    assert got["context_lens"].tolist() == [5, 9] and got["cu_seq_lens"].tolist() == [0, 5, 14]
+    assert got["cu_seqlen_ks"].tolist() == [0, 0, 0, 5, 0, 0] and got["cu_seqlen_ke"].tolist() == [3, 4, 5, 14, 0, 0]
+    assert got["counts"].tolist() == [4, 2, 2, 0] and got["cu_new_lens"].tolist() == [0, 3, 4]
+
+
+def test_definition_of_codes():
+    """The code table against torch's float8 type, and a row by hand."""
+    want = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(np.nan_to_num(ref.e4m3_values(), nan=-1), np.nan_to_num(want, nan=-1))
+    codes, scale = ref.quantise_rows(np.array([[0.0, 448.0, -224.0, 1.0625], [0.0] * 4]))
+    assert scale.tolist() == [1.0, 0.0] and codes.tolist() == [[0, 0x7E, 0xF6, 0x38], [0, 0, 0, 0]]
+
+
+def test_definition_of_attention_by_hand():
+    """Two tokens of equal score: the mean of their values, lse = s + ln 2."""
+    D, bs = 64, 16
+    cache = np.zeros((1, 1, ref.page_bytes(bs, D)), np.uint8)
+    k = np.ones((2, 1, D), np.float32)
+    v = np.stack([np.full((1, D), 2.0), np.full((1, D), 4.0)]).astype(np.float32)
+    ref.store_kv(cache, [3, 9], k, v, bs)
+    out, lse, *_ = ref.sparse_attention(np.full((1, 1, D), 0.5), cache, np.array([[3, 9, -1]]), np.zeros((1, 1), int), bs,
+                                        1.0, next_n=1)
+    assert np.allclose(out, 3.0) and np.allclose(lse, 32 + np.log(2))
