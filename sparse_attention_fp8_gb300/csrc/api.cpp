@@ -10,7 +10,6 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
-#include <numeric>
 #include <string>
 
 #include "fp8idx.h"
@@ -1035,32 +1034,7 @@ fp8idx_status sparse_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, 
   p.block_size = (int32_t)bs;
   p.n_req = (int32_t)bt->shape[0];
   p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
-  // The cache as a matrix whose rows start at every multiple of the largest
-  // common step of its strides; a token's key and value are 128-byte pieces
-  // of it that the gathering copies fetch by row number.
-  const int64_t page = kv->shape[2];
-  int64_t pitch = bs > 1 ? 2 * D : page;
-  if (p.block_stride) pitch = std::gcd(pitch, p.block_stride);
-  if (p.kv_head_stride) pitch = std::gcd(pitch, p.kv_head_stride);
-  if (bs == 1 && p.block_stride) {  // one token per page: any step that holds its 2*D bytes
-    pitch = p.kv_head_stride ? std::gcd(p.block_stride, p.kv_head_stride) : p.block_stride;
-  } else if (bs == 1 && p.kv_head_stride) {
-    pitch = p.kv_head_stride;
-  }
-  if (pitch < (bs == 1 ? 2 * D : 128))
-    return fail(FP8IDX_ERR_UNSUPPORTED, "kv_cache: block and head strides must be multiples of 128 bytes%s",
-                bs == 1 ? " or share a step of at least 2*head_dim" : "");
-  const int64_t span = (p.num_blocks - 1) * p.block_stride + (HK - 1) * p.kv_head_stride + page;
-  const int64_t inner = std::min<int64_t>(pitch, 2 * D);
-  const int64_t mat_rows = (span - inner) / pitch + 1;
-  if (mat_rows >= (1ll << 31)) return fail(FP8IDX_ERR_UNSUPPORTED, "kv_cache: more than 2^31 rows of %lld bytes", (long long)pitch);
-  p.row_block = p.block_stride / pitch;
-  p.row_head = p.kv_head_stride / pitch;
-  p.row_tok = bs > 1 ? (int32_t)(2 * D / pitch) : 0;
-  p.v_dx = (D == 128 && pitch > 128) ? 128 : 0;
-  p.v_dy = (D == 128 && pitch == 128) ? 1 : 0;
   while ((1 << p.block_shift) < p.block_size) ++p.block_shift;
-  p.idx_vec = (aligned16(idx->data) && p.idx_stride % 4 == 0) ? 1 : 0;
   const int gp = attn_pad(p.group);
   p.head_chunks = (p.group + gp - 1) / gp;
   if (R * HK * p.head_chunks * kAttnMaxCtas >= (1ll << 31))
@@ -1084,12 +1058,7 @@ fp8idx_status sparse_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, 
     }
   }
   const int grid = cs == 1 ? std::min(p.units, dev.sms) : p.units * cs;
-  CUtensorMap tm;
-  const uint64_t dims[2] = {(uint64_t)inner, (uint64_t)mat_rows};
-  const uint64_t strides_b[1] = {(uint64_t)pitch};
-  const uint32_t box[2] = {128u, 1u};
-  TRY(encode(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, kv->data, dims, strides_b, box, CU_TENSOR_MAP_SWIZZLE_128B, "kv_cache"));
-  cudaError_t e = launch_sparse_attn(tm, p, (int)D, grid, cs, smem, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_sparse_attn(p, (int)D, grid, cs, smem, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(FP8IDX_ERR_CUDA, "sparse attention launch: %s", cudaGetErrorString(e));
   return ok();
 }

@@ -3,7 +3,6 @@
 #pragma once
 
 #include <cstdint>
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "kernels.h"
@@ -72,12 +71,6 @@ struct SparseAttnParams {
   int32_t next_n;                                           // prefill: 1
   int32_t k, max_blocks, block_size, block_shift, n_req;
   float scale_log2;                                         // softmax_scale * log2(e)
-  // the cache as a matrix of `pitch`-byte rows for the gathering copies:
-  // token t of a page starts in row block*row_block + head*row_head + t*row_tok
-  int64_t row_block, row_head;
-  int32_t row_tok;
-  int32_t v_dx, v_dy;           // head_dim 128: the value row, from the key row (bytes, matrix rows)
-  int32_t idx_vec;              // index rows are 16-byte aligned
   int32_t head_chunks;          // chunks of attn_pad(group) heads that share a key head
   int32_t units;                // rows * kv_heads * head_chunks
   int32_t tiles;                // 128-entry tiles per row
@@ -87,28 +80,37 @@ constexpr int kAttnMaxK = 2048;
 constexpr int kAttnMaxGroup = 128;
 constexpr int kAttnMaxCtas = 8;   // CTAs per unit (portable cluster size)
 constexpr int kAttnTile = 128;    // selected tokens per MMA tile (MMA M of the scores, K of the outputs)
-constexpr int kAttnGroups = 2;    // epilogue warpgroups
 constexpr int kAttnMaxStages = 8;
 // Query heads of a unit, padded to a width that P's rows can be swizzled over.
 __host__ __device__ constexpr int attn_pad(int group) { return group <= 16 ? 16 : group <= 32 ? 32 : 64; }
-// Roles: two epilogue warpgroups, two producer warps, the MMA warp, the query warp.
-constexpr int kAttnThreads = 32 * (4 * kAttnGroups + 4);
+// Roles: two epilogue warpgroups; four producer warps; the warps that issue
+// the scores and each group's outputs; the query warp.
+constexpr int kAttnGroups = 2;
+constexpr int kAttnProducers = 4;
+constexpr int kAttnThreads = 32 * (4 * kAttnGroups + kAttnProducers + 4);
+// Registers a thread after the launch's 128 have been dealt anew:
+// 256 * 168 + 256 * 88 = 512 * 128.
+constexpr int kAttnEpilogueRegs = 168, kAttnOtherRegs = 88;
+// Per group: accumulators of S^T (tensor memory's 512 columns hold them and
+// one of O^T, 2*GP each).  Query buffers: units in work and the next ones.
+__host__ __device__ constexpr int attn_score_buffers(int gp) { return gp <= 32 ? 2 : 1; }
+__host__ __device__ constexpr int attn_query_buffers(int gp) { return gp <= 32 ? 4 : 3; }
 struct AttnSmem {
   uint32_t kv, q, p, scale, mask, flt, bars, misc, total;
 };
 // Floats of the softmax state of one CTA, GP heads (AttnState in sparse_attn.cu).
-__host__ __device__ constexpr int attn_state_floats(int gp) { return 38 * gp + 32; }
+__host__ __device__ constexpr int attn_state_floats(int gp) { return 24 * gp + 32; }
 __host__ __device__ inline AttnSmem attn_smem_layout(int head_dim, int gp, int stages) {
   AttnSmem L;
   uint32_t off = 0;
   L.kv = off;    off += static_cast<uint32_t>(stages) * kAttnTile * 2u * head_dim;  // key tile, value tile
-  L.q = off;     off += 2u * 2u * gp * 128u;             // two buffers of 2*gp rows of 128 bytes
+  L.q = off;     off += attn_query_buffers(gp) * 2u * gp * 128u;  // 2*gp rows of 128 bytes
   L.p = off;     off += kAttnGroups * kAttnTile * 2u * gp;  // a tile of probabilities per group
   L.scale = off; off += static_cast<uint32_t>(stages) * kAttnTile * 8u;
   L.mask = off;  off += static_cast<uint32_t>(stages) * 16u;
   L.flt = off;   off += 4u * attn_state_floats(gp);
   off = (off + 15u) & ~15u;
-  L.bars = off;  off += 8u * (2u * kAttnMaxStages + 16u);
+  L.bars = off;  off += 8u * (2u * kAttnMaxStages + 28u);
   L.misc = off;  off += 32u;
   L.total = off + 1024u;
   return L;
@@ -119,7 +121,7 @@ __host__ inline int attn_stages(int head_dim, int gp, int smem_limit) {
   while (s > 3 && static_cast<int>(attn_smem_layout(head_dim, gp, s).total) > smem_limit) --s;
   return s;
 }
-cudaError_t launch_sparse_attn(const CUtensorMap& tm_kv, const SparseAttnParams& p, int head_dim, int grid, int ctas,
+cudaError_t launch_sparse_attn(const SparseAttnParams& p, int head_dim, int grid, int ctas,
                                int smem_bytes, cudaStream_t stream);
 cudaError_t read_attn_watchdog(unsigned int* value, bool clear);
 

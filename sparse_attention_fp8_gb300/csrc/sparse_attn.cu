@@ -49,7 +49,6 @@
 // Every wait is bounded (common.cuh).  After a wait has run out the group
 // votes, so that its four warps leave together and no barrier is left open.
 #include <cooperative_groups.h>
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -63,18 +62,35 @@ namespace cg = cooperative_groups;
 namespace fp8idx {
 
 static __device__ unsigned int g_attn_watchdog;
+// The row that an entry without a token copies: zeros.
+static __device__ __align__(256) uint8_t g_zero_row[256];
 
 namespace {
 
-constexpr int kProdWarp0 = 4 * kAttnGroups;
-constexpr int kProdWarps = 2;
-constexpr int kMmaWarp = kProdWarp0 + kProdWarps;
-constexpr int kQWarp = kMmaWarp + 1;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kLazy = 2.f;          // log2 of how far a score may pass m before m is set anew
 constexpr float kPScale = 32.f;       // factor of P's e4m3 codes
 constexpr float kMinVScale = 0x1p-120f;
 constexpr float kMinM = -3e38f;       // m stays finite, so that a score of -inf gives probability 0
+
+// One warp-collective bounded wait, in few instructions: this kernel has many
+// roles, and their loops together have to stay in the instruction cache.
+__device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t site) {
+  bool ok = ptx::mbar_test_wait(bar, parity);
+  if (!ok) {
+    const uint64_t since = ptx::globaltimer_ns();
+#pragma unroll 1
+    while (!(ok = ptx::mbar_try_wait(bar, parity))) {
+      if (*abort_flag) break;
+      if (ptx::globaltimer_ns() - since > kWaitTimeoutNs) {
+        *abort_flag = 1u;
+        atomicOr(&g_attn_watchdog, site);
+        break;
+      }
+    }
+  }
+  return __all_sync(kFull, ok);
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -82,45 +98,53 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Floats ordered as signed integers (NaN above all), and back.
-__device__ __forceinline__ int float_key(float x) {
-  const int b = __float_as_int(x);
-  return b >= 0 ? b : b ^ 0x7FFFFFFF;
-}
-__device__ __forceinline__ float key_float(int k) { return __int_as_float(k >= 0 ? k : k ^ 0x7FFFFFFF); }
-
-// Softmax state of a CTA in shared memory.
-template <int GP>
+// Softmax state of a CTA in shared memory; NG epilogue groups.
+template <int GP, int NG, int QB>
 struct AttnState {
-  float nm[2][GP];            // -m of each group (log2 units)
-  float ninf[GP];             // -inf: the row of -m that an entry without a token reads
-  float lred[2][2][4][GP];    // [unit parity][group][warp]: sums of the probabilities
-  float msave[2][2][GP];      // [unit parity][group]: m at the unit's end
-  float wmax[2][4][GP];       // [group][warp]: a tile's maxima
-  float resc[2][GP];          // [group]: factor of a new maximum
-  float fac[GP][2];           // factors of the groups' accumulators
-  float xm[GP], xl[GP];       // cluster: this CTA's maximum and sum per head
-  float csave[2][2];          // [unit parity][group]: the value scale that P is relative to
-  float used[2][2];           // [unit parity][group]: 1 if its accumulator holds anything
-  float cref[2], cfac[2];
-  float wvs[2][4];
-  float qf[2];                // [query buffer]: 2^-e of the query's scaling
+  float nm[NG][GP];            // -m of each group (log2 units), 0 before a unit's first tile
+  float ninf[GP];              // -inf: the row of -m that an entry without a token reads
+  float part[NG][4][GP];       // [group][warp]: a tile's maxima over m; a unit's sums
+  float delta[NG][GP];         // what m grows by
+  float resc[NG][GP];          // 2^-delta
+  float fac[NG][GP];           // a unit's end: factor of the accumulator
+  float xm[NG][GP], xl[NG][GP];  // cluster: the group's maximum and sum per head
+  float cref[NG], cfac[NG];
+  float wvs[NG][4];
+  float qf[QB];                // [query buffer]: 2^-e of the query's scaling
 };
 
-struct Cursor {  // tiles [t0, t1) of units u, u + step, ...
-  int u, t, t0, t1, step;
-  __device__ __forceinline__ bool advance() {  // true: a new unit
-    if (++t < t1) return false;
-    t = t0;
-    u += step;
-    return true;
+// Registers move from the copying and issuing warps to the epilogue's.
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Column j of N (16 or 32) columns, one value per lane and column: the lanes'
+// maximum (or sum), in lane j (and j + 16 for N = 16).  N - 1 (+ 1) shuffles.
+template <int N, bool MAX>
+__device__ __forceinline__ float reduce_columns(float (&v)[N], int lane) {
+#pragma unroll
+  for (int d = N / 2; d > 0; d >>= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int j = 0; j < d; ++j) {
+      const float got = __shfl_xor_sync(kFull, up ? v[j] : v[j + d], d);
+      const float own = up ? v[j + d] : v[j];
+      v[j] = MAX ? fmaxf(own, got) : own + got;
+    }
   }
-};
+  if constexpr (N == 16) {
+    const float got = __shfl_xor_sync(kFull, v[0], 16);
+    v[0] = MAX ? fmaxf(v[0], got) : v[0] + got;
+  }
+  return v[0];
+}
 
-struct Entries {  // a lane's four entries of a tile
-  int32_t idx[4];
-  int row, kvh;
-};
+constexpr uint32_t pow2_at_least(uint32_t n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512; }
 
 __device__ __forceinline__ void unit_of(const SparseAttnParams& p, int u, int* row, int* kvh, int* h0, int gp) {
   const int c = u / p.head_chunks;
@@ -141,28 +165,34 @@ __device__ __forceinline__ void split_pair(__half2 x, uint32_t* h, uint32_t* l) 
 }  // namespace
 
 template <int D, int GP, bool CLUSTER>
-__global__ void __launch_bounds__(kAttnThreads, 1)
-    sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const SparseAttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __grid_constant__ SparseAttnParams p) {
+  constexpr int NG = kAttnGroups;
+  constexpr int kProdWarp0 = 4 * NG, kProdWarps = kAttnProducers;
+  constexpr int kSWarp = kProdWarp0 + kProdWarps, kOWarp0 = kSWarp + 1, kQWarp = kOWarp0 + NG;
+  static_assert(32 * (kQWarp + 1) == kAttnThreads, "roles");
   constexpr int N2 = 2 * GP;                       // columns of S^T and O^T
+  constexpr int SBG = attn_score_buffers(GP);      // accumulators of S^T per group
+  constexpr int QB = attn_query_buffers(GP);
   constexpr uint32_t kStageBytes = kAttnTile * 2u * D;
   constexpr uint32_t kVOff = D == 128 ? kAttnTile * 128u : 0u;  // D = 64: key and value share a 128-byte row
-  constexpr uint32_t kTmemCols = 4u * N2;          // S and O of two groups
-  static_assert(sizeof(AttnState<GP>) <= 4u * attn_state_floats(GP), "state");
+  constexpr uint32_t kTmemCols = pow2_at_least(NG * (SBG + 1) * N2);
+  constexpr uint32_t kTmemO = NG * SBG * N2;       // O^T of group g at kTmemO + g * N2
+  using State = AttnState<GP, NG, QB>;
+  static_assert(sizeof(State) <= 4u * attn_state_floats(GP), "state");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_up_1024(smem_raw);
   const AttnSmem L = attn_smem_layout(D, GP, p.stages);
   const int S = p.stages;
-  AttnState<GP>& stt = *reinterpret_cast<AttnState<GP>*>(smem + L.flt);
+  State& stt = *reinterpret_cast<State*>(smem + L.flt);
   const uint32_t kv0 = ptx::smem_u32(smem + L.kv);
   const uint32_t q0 = ptx::smem_u32(smem + L.q);
-  const uint32_t bars = ptx::smem_u32(smem + L.bars);
-  const uint32_t full0 = bars, empty0 = full0 + 8u * kAttnMaxStages;
-  const uint32_t qf0 = empty0 + 8u * kAttnMaxStages, qe0 = qf0 + 16u;  // query buffers
-  const uint32_t sf0 = qe0 + 16u, se0 = sf0 + 16u;  // [group] scores ready, read
-  const uint32_t pf0 = se0 + 16u, pe0 = pf0 + 16u;  // [group] probabilities ready, used
-  const uint32_t ub = pe0 + 16u, oe = ub + 8u;      // unit ends: both groups done; accumulators read
-  const uint32_t drain_bar = oe + 8u;
+  const uint32_t full0 = ptx::smem_u32(smem + L.bars), empty0 = full0 + 8u * kAttnMaxStages;
+  const uint32_t qf0 = empty0 + 8u * kAttnMaxStages, qe0 = qf0 + 8u * QB;     // query buffers
+  const uint32_t sf0 = qe0 + 8u * QB, se0 = sf0 + 8u * NG * SBG;              // [group][accumulator] scores ready, read
+  const uint32_t pf0 = se0 + 8u * NG * SBG, pe0 = pf0 + 8u * NG;              // [group] probabilities ready, used
+  const uint32_t oe0 = pe0 + 8u * NG;                                         // [group] a unit's outputs read
+  const uint32_t ub = oe0 + 8u * NG, drain0 = ub + 8u;                        // cluster: both groups done; [MMA warp]
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L.misc);
   volatile uint32_t* abort_flag = misc + 1;
 
@@ -170,25 +200,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (threadIdx.x == 0) {
     misc[1] = 0u;
     for (int s = 0; s < S; ++s) {
-      ptx::mbar_init(full0 + 8u * s, 32u + 1u);  // the producer lanes' scale copies, the copies' bytes
-      ptx::mbar_init(empty0 + 8u * s, 1u + 4u);  // the output MMA, the tile's epilogue warps
+      ptx::mbar_init(full0 + 8u * s, 33u * kProdWarps);  // each producer lane's copies, each warp's mask
+      ptx::mbar_init(empty0 + 8u * s, 1u + 4u);          // the output MMA, the tile's epilogue warps
     }
-    for (int g = 0; g < 2; ++g) {
-      ptx::mbar_init(qf0 + 8u * g, 1u);
-      ptx::mbar_init(qe0 + 8u * g, 1u + 4u * kAttnGroups);
-      ptx::mbar_init(sf0 + 8u * g, 1u);
-      ptx::mbar_init(se0 + 8u * g, 4u);
+    for (int i = 0; i < QB; ++i) {
+      ptx::mbar_init(qf0 + 8u * i, 1u);
+      ptx::mbar_init(qe0 + 8u * i, 1u + 4u);             // the last score MMA, the unit's epilogue warps
+    }
+    for (int i = 0; i < NG * SBG; ++i) {
+      ptx::mbar_init(sf0 + 8u * i, 1u);
+      ptx::mbar_init(se0 + 8u * i, 4u);
+    }
+    for (int g = 0; g < NG; ++g) {
       ptx::mbar_init(pf0 + 8u * g, 4u);
       ptx::mbar_init(pe0 + 8u * g, 1u);
+      ptx::mbar_init(oe0 + 8u * g, 4u);
     }
-    ptx::mbar_init(ub, 4u * kAttnGroups);
-    ptx::mbar_init(oe, 4u * kAttnGroups);
-    ptx::mbar_init(drain_bar, 1u);
+    ptx::mbar_init(ub, 4u * NG);
+    for (int i = 0; i < 1 + NG; ++i) ptx::mbar_init(drain0 + 8u * i, 1u);
     ptx::fence_barrier_init();
-    ptx::prefetch_tmap(&tm_kv);
   }
   for (int g = threadIdx.x; g < GP; g += kAttnThreads) stt.ninf[g] = -INFINITY;
-  if (warp == kMmaWarp) {
+  for (int g = threadIdx.x; g < NG * GP; g += kAttnThreads) stt.nm[g / GP][g % GP] = 0.f;
+  if (warp == kSWarp) {
     ptx::tmem_alloc(ptx::smem_u32(misc), kTmemCols);
     ptx::tmem_relinquish();
   }
@@ -197,162 +231,175 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = misc[0];
 
-  // this CTA's units and tiles
+  // This CTA's work: a sequence of tiles that every role walks in the same
+  // order.  A persistent CTA works on NG units at a time, one per group:
+  // round r has the units r*NG .. r*NG + live - 1 of its list, their tiles in
+  // turn.  A cluster's CTA has one unit and deals its tiles to the groups.
   const int C = CLUSTER ? static_cast<int>(cg::this_cluster().num_blocks()) : 1;
   const int crank = CLUSTER ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
   const int per = (p.tiles + C - 1) / C;
   const int t0 = min(crank * per, p.tiles), t1 = min(t0 + per, p.tiles);
   const int u0 = CLUSTER ? static_cast<int>(blockIdx.x) / C : static_cast<int>(blockIdx.x);
-  const int ustep = CLUSTER ? p.units : static_cast<int>(gridDim.x);
-  const int n_units = u0 < p.units ? (p.units - u0 + ustep - 1) / ustep : 0;
-  const int total = n_units * (t1 - t0);
+  const int ustep = static_cast<int>(gridDim.x);
+  const int n_units = CLUSTER ? 1 : (p.units - u0 + ustep - 1) / ustep;
+  const int rounds = CLUSTER ? 1 : (n_units + NG - 1) / NG;
+  const auto live_of = [&](int r) { return CLUSTER ? 1 : min(NG, n_units - r * NG); };
 
-  if (warp >= kProdWarp0 && warp < kProdWarp0 + kProdWarps) {
-    // ============================ producers ============================
-    const int pw = warp - kProdWarp0;
-    const int bs = p.block_size, shift = p.block_shift;
-    const auto load_entries = [&](const Cursor& c, Entries& en) {
-      int h0;
-      unit_of(p, c.u, &en.row, &en.kvh, &h0, GP);
-      const int at = c.t * kAttnTile + 4 * lane;
-      const int32_t* src = p.indices + en.row * p.idx_stride + at;
-      if (p.idx_vec && at + 3 < p.k) {
-        const int4 v = __ldg(reinterpret_cast<const int4*>(src));
-        en.idx[0] = v.x, en.idx[1] = v.y, en.idx[2] = v.z, en.idx[3] = v.w;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) en.idx[i] = at + i < p.k ? __ldg(src + i) : -1;
-      }
-    };
-    // block-table entries (or -1) and places in the page of four entries
-    int req_guess = 0;
-    const auto load_tables = [&](const Entries& en, int32_t (&blk)[4], int (&off)[4]) {
-      const int req_row = en.row / p.next_n;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        int32_t tok = en.idx[i];
-        int req = req_row;
-        bool ok = tok >= 0;
-        if (p.cu_seq_lens != nullptr && ok) {
-          // the request of a column: the last one found, or a search
-          int32_t lo = __ldg(p.cu_seq_lens + req_guess), hi = __ldg(p.cu_seq_lens + req_guess + 1);
-          if (tok < lo || tok >= hi) {
-            int a = 0, b = p.n_req;
-            while (b - a > 1) {
-              const int mid = (a + b) >> 1;
-              if (__ldg(p.cu_seq_lens + mid) <= tok) a = mid; else b = mid;
-            }
-            req_guess = a;
-            lo = __ldg(p.cu_seq_lens + a);
-            hi = __ldg(p.cu_seq_lens + a + 1);
-          }
-          ok = tok >= lo && tok < hi;
-          req = req_guess;
-          tok -= lo;
-        }
-        const int32_t j = tok >> shift;
-        off[i] = tok & (bs - 1);
-        blk[i] = ok && j < p.max_blocks ? __ldg(p.block_tables + req * p.bt_stride + j) : -1;
-      }
-    };
-    Cursor cur{u0, t0, t0, t1, ustep};
-    Ring st{0u, 0u, static_cast<uint32_t>(S)};
-    if (pw < total) {
-      // walk to this warp's first tile, and one of its tiles further for each look-ahead
-      const auto next_own = [&](Cursor& c) {
-        for (int i = 0; i < kProdWarps; ++i) c.advance();
+  if (warp >= 4 * NG) {
+    reg_dec<kAttnOtherRegs>();
+    if (warp < kSWarp) {
+      // =========================== producers ===========================
+      constexpr int kPerLane = kAttnTile / (32 * kProdWarps);  // entries of a lane in a tile
+      constexpr int kRowLanes = 2 * D / 16;                    // lanes that copy a token's 16-byte pieces
+      constexpr int kRowsPerCopy = 32 / kRowLanes;
+      const int pw = warp - kProdWarp0;
+      const int bs = p.block_size, shift = p.block_shift;
+      // Where a tile's entries, block table and pages are.  The divisions
+      // that take a unit apart are done once a unit.
+      struct Place {
+        const int32_t* idx;
+        const int32_t* table;
+        const uint8_t* head;
       };
-      for (int i = 0; i < pw; ++i) {
-        cur.advance();
-        st.next();
-      }
-      Entries en, en1, en2;
-      int32_t blk[4], blk1[4];
-      int off[4], off1[4];
-      Cursor ahead = cur;
-      load_entries(ahead, en);
-      load_tables(en, blk, off);
-      next_own(ahead);
-      if (pw + kProdWarps < total) load_entries(ahead, en1);
-      int issued = 0;
-      bool okay = true;
-      for (int it = pw; it < total && okay; it += kProdWarps) {
-        if (it + kProdWarps < total) load_tables(en1, blk1, off1);
-        next_own(ahead);
-        if (it + 2 * kProdWarps < total) load_entries(ahead, en2);
-        uint32_t own = 0;
-        int32_t row[4];
-        const uint8_t* sc[4];
+      const auto place_of = [&](int i) {
+        int row, kvh, h0;
+        unit_of(p, u0 + i * ustep, &row, &kvh, &h0, GP);
+        return Place{p.indices + row * p.idx_stride,
+                     p.cu_seq_lens != nullptr ? p.block_tables : p.block_tables + row / p.next_n * p.bt_stride,
+                     p.kv + kvh * p.kv_head_stride};
+      };
+      // the look-ahead cursor over the sequence
+      int ar = 0, at = t0, ae = 0;
+      Place units[NG];
+      const auto load_entries = [&](const Place& c, int t, int32_t (&idx)[kPerLane]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool ok = blk[i] >= 0 && blk[i] < p.num_blocks;
-          own |= (ok ? 1u : 0u) << i;
-          row[i] = ok ? static_cast<int32_t>(blk[i] * p.row_block + en.kvh * p.row_head +
-                                             static_cast<int64_t>(off[i]) * p.row_tok)
-                      : -1;
-          sc[i] = p.kv + blk[i] * p.block_stride + en.kvh * p.kv_head_stride + static_cast<int64_t>(bs) * 2 * D + 8 * off[i];
+        for (int r = 0; r < kPerLane; ++r) {
+          const int j = t * kAttnTile + (pw * kPerLane + r) * 32 + lane;
+          idx[r] = j < p.k ? __ldg(c.idx + j) : -1;
         }
-        // tokens 32w .. 32w+31 are the entries of lanes 8w .. 8w+7
-        uint32_t m = own << (4 * (lane & 7));
-        m |= __shfl_xor_sync(kFull, m, 1);
-        m |= __shfl_xor_sync(kFull, m, 2);
-        m |= __shfl_xor_sync(kFull, m, 4);
-        const bool any = __any_sync(kFull, m != 0u);
-        okay = warp_wait_bounded(empty0 + 8u * st.idx, st.phase ^ 1u, abort_flag, &g_attn_watchdog, kSiteStageEmpty);
-        if (!okay) break;
-        if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(smem + L.mask)[4 * st.idx + (lane >> 3)] = m;
-        const uint32_t full = full0 + 8u * st.idx;
-        __syncwarp();
-        if (lane == 0) {
-          if (any)
-            ptx::mbar_arrive_expect_tx(full, kStageBytes);
-          else
-            ptx::mbar_arrive(full);
-        }
-        __syncwarp();
-        if (any) {
-          const uint32_t dst = kv0 + st.idx * kStageBytes + lane * 4u * 128u;
-          ptx::tma_gather4(dst, &tm_kv, full, 0, row[0], row[1], row[2], row[3]);
-          if constexpr (D == 128) {
-            const int dy = p.v_dy;
-            ptx::tma_gather4(dst + kVOff, &tm_kv, full, p.v_dx, row[0] < 0 ? -1 : row[0] + dy,
-                             row[1] < 0 ? -1 : row[1] + dy, row[2] < 0 ? -1 : row[2] + dy,
-                             row[3] < 0 ? -1 : row[3] + dy);
+      };
+      // block-table entries (or -1) of a lane's entries, which become places in the page
+      int req = 0;  // prefill: the request that the last column was found in
+      int32_t req_lo = 0, req_hi = -1;
+      const auto load_tables = [&](const Place& c, int32_t (&idx)[kPerLane], int32_t (&blk)[kPerLane]) {
+#pragma unroll
+        for (int r = 0; r < kPerLane; ++r) {
+          int32_t tok = idx[r];
+          bool ok = tok >= 0;
+          const int32_t* table = c.table;
+          if (p.cu_seq_lens != nullptr) {
+            if (ok && (tok < req_lo || tok >= req_hi)) {
+              int a = 0, b = p.n_req;
+#pragma unroll 1
+              while (b - a > 1) {
+                const int mid = (a + b) >> 1;
+                if (__ldg(p.cu_seq_lens + mid) <= tok) a = mid; else b = mid;
+              }
+              req = a;
+              req_lo = __ldg(p.cu_seq_lens + a);
+              req_hi = __ldg(p.cu_seq_lens + a + 1);
+            }
+            ok = ok && tok >= req_lo && tok < req_hi;
+            tok -= req_lo;
+            table += req * p.bt_stride;
           }
-          const uint32_t sdst = ptx::smem_u32(smem + L.scale) + (st.idx * kAttnTile + 4u * lane) * 8u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (own >> i & 1u) ptx::cp_async_8(sdst + 8u * i, sc[i]);
+          const int32_t j = tok >> shift;
+          idx[r] = tok & (bs - 1);
+          blk[r] = ok && j < p.max_blocks ? __ldg(table + j) : -1;
         }
-        ptx::cp_async_mbar_arrive(full);
-        issued = it + 1;
-        for (int i = 0; i < kProdWarps; ++i) st.next();
-        en = en1;
-        en1 = en2;
+      };
+      // Lane l copies piece l % kRowLanes of every kRowsPerCopy-th token into
+      // its place in the 128-byte swizzle, which depends on the token mod 8.
+      const int piece = lane % kRowLanes, sub = lane / kRowLanes;
+      uint32_t place[8 / kRowsPerCopy];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) blk[i] = blk1[i], off[i] = off1[i];
+      for (int i = 0; i < 8 / kRowsPerCopy; ++i)
+        place[i] = (piece >> 3) * kVOff + sub * 128 + (((piece & 7) ^ ((i * kRowsPerCopy + sub) & 7)) << 4);
+      const int total = n_units * (t1 - t0);
+      if (total > 0) {
+        // entries are loaded two tiles ahead of their copies, table entries one
+        Ring st{0u, 0u, static_cast<uint32_t>(S)};
+        int32_t off[kPerLane] = {}, blk[kPerLane] = {}, off1[kPerLane] = {}, blk1[kPerLane] = {}, idx2[kPerLane] = {};
+        Place cur{}, cur1{}, cur2{};
+#pragma unroll 1
+        for (int it = -2; it < total; ++it) {
+          if (it >= -1 && it + 1 < total) load_tables(cur1, off1, blk1);
+          if (it + 2 < total) {
+            if (at == t0 && ae == 0) {
+#pragma unroll 1
+              for (int e = 0; e < live_of(ar); ++e) {
+                const Place c = place_of(ar * NG + e);
+                if (e == 0) units[0] = c; else units[1] = c;
+              }
+            }
+            cur2 = ae == 0 ? units[0] : units[1];
+            load_entries(cur2, at, idx2);
+            if (++ae >= live_of(ar)) {
+              ae = 0;
+              if (++at >= t1) {
+                at = t0;
+                ++ar;
+              }
+            }
+          }
+          if (it >= 0) {
+            const uint8_t* src[kPerLane];
+            uint32_t m[kPerLane];
+#pragma unroll
+            for (int r = 0; r < kPerLane; ++r) {
+              const bool ok = blk[r] >= 0 && blk[r] < p.num_blocks;
+              m[r] = __ballot_sync(kFull, ok);
+              src[r] = ok ? cur.head + blk[r] * p.block_stride + off[r] * (2 * D) : g_zero_row;
+            }
+            if (!attn_wait(empty0 + 8u * st.idx, st.phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
+            const uint32_t full = full0 + 8u * st.idx;
+#pragma unroll
+            for (int r = 0; r < kPerLane; ++r) {
+              const int tok0 = (pw * kPerLane + r) * 32;
+              const uint32_t dst = kv0 + st.idx * kStageBytes + tok0 * 128u;
+              if (m[r] >> lane & 1u)
+                ptx::cp_async_8(ptx::smem_u32(smem + L.scale) + (st.idx * kAttnTile + tok0 + lane) * 8u,
+                                cur.head + blk[r] * p.block_stride + bs * (2 * D) + 8 * off[r]);
+              if (lane == 0) reinterpret_cast<uint32_t*>(smem + L.mask)[4 * st.idx + pw * kPerLane + r] = m[r];
+              // (addresses first, eight at a time: the exchange's latency is paid once per batch)
+#pragma unroll
+              for (int j0 = 0; j0 < 32; j0 += 8 * kRowsPerCopy) {
+                uint64_t from[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  from[i] = __shfl_sync(kFull, reinterpret_cast<uint64_t>(src[r]), j0 + i * kRowsPerCopy + sub) + piece * 16;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const int j = j0 + i * kRowsPerCopy;
+                  ptx::cp_async_16(dst + place[(j & 7) / kRowsPerCopy] + j * 128u, reinterpret_cast<const void*>(from[i]));
+                }
+              }
+            }
+            ptx::cp_async_mbar_arrive(full);
+            if (lane == 0) ptx::mbar_arrive(full);
+            st.next();
+          }
+          cur = cur1;
+          cur1 = cur2;
+#pragma unroll
+          for (int r = 0; r < kPerLane; ++r) blk[r] = blk1[r], off[r] = off1[r], off1[r] = idx2[r];
+        }
+        ptx::cp_async_wait_all();  // (an abandoned call must not leave copies behind)
       }
-      if (*abort_flag && lane == 0)  // let issued copies land before the CTA exits
-        for (int it = max(0, issued - S); it < issued; ++it)
-          if (it % kProdWarps == pw) wait_drain(full0 + 8u * (it % S), (it / S) & 1, &g_attn_watchdog);
-    }
-  } else if (warp == kQWarp) {
-    // ============================ queries ==============================
-    uint32_t phase = 0;
-    if (total > 0) {
-      for (int i = 0; i < n_units; ++i) {
-        const int buf = i & 1;
+    } else if (warp == kQWarp) {
+      // =========================== queries =============================
+#pragma unroll 1
+      for (int i = 0; i < n_units && t0 < t1; ++i) {
+        const int buf = i % QB;
         int row, kvh, h0;
         unit_of(p, u0 + i * ustep, &row, &kvh, &h0, GP);
         const int nh = min(GP, p.group - h0);
-        if (!warp_wait_bounded(qe0 + 8u * buf, ((phase >> buf) & 1u) ^ 1u, abort_flag, &g_attn_watchdog, kSiteQEmpty))
-          break;
-        phase ^= 1u << buf;
+        if (!attn_wait(qe0 + 8u * buf, ((i / QB) & 1) ^ 1, abort_flag, kSiteQEmpty)) break;
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row / p.next_n * p.q_req_stride +
                                  row % p.next_n * p.q_row_stride + (kvh * p.group + h0) * p.q_head_stride;
         constexpr int kPer = D / 8;  // 16-byte pieces per head
         float amax = 0.f;
-#pragma unroll 4
+#pragma unroll 2
         for (int c = lane; c < nh * kPer; c += 32) {
           const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + c / kPer * p.q_head_stride + c % kPer * 8));
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -369,7 +416,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         e = amax == 0.f ? 0 : min(max(e, -120), 120);
         const float mul = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
         uint8_t* dst = smem + L.q + buf * N2 * 128;
-#pragma unroll 4
+#pragma unroll 1
         for (int c = lane; c < GP * kPer; c += 32) {
           const int g = c / kPer, piece = c % kPer;
           uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
@@ -400,135 +447,135 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(qf0 + 8u * buf);
       }
-    }
-  } else if (warp == kMmaWarp) {
-    // ============================== MMA ================================
-    if (lane == 0 && total > 0) {
-      constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(kAttnTile, N2);
-      constexpr uint32_t kIdescO = ptx::idesc_e4m3_f32(128, N2) | ptx::kIdescMnMajorA | ptx::kIdescMnMajorB;
-      const uint64_t q_desc = ptx::smem_desc_sw128(q0);
-      const uint32_t p0 = ptx::smem_u32(smem + L.p);
-      Cursor cs{u0, t0, t0, t1, ustep}, cp = cs;     // tiles whose scores, outputs come next
-      Ring rs{0u, 0u, static_cast<uint32_t>(S)}, rp = rs;
-      int is = 0, ip = 0, us = 0, up = 0;             // tile and unit counts
-      uint32_t ns = 0, np = 0;                        // bit g: parity of the tiles of group g
-      uint32_t started = 0;                           // bit g: its accumulator holds this unit's sums
-      const auto tile_any = [&](uint32_t stage) {
-        const uint4 m = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * stage);
-        return (m.x | m.y | m.z | m.w) != 0u;
-      };
-      uint64_t since = 0;
-      uint32_t spins = 0;
-      while (ip < total) {
-        bool did = false;
-        if (is < total && ptx::mbar_test_wait(full0 + 8u * rs.idx, rs.phase)) {
-          const uint32_t g = is & 1;
-          const bool any = tile_any(rs.idx);
-          if (!any || (ptx::mbar_test_wait(qf0 + 8u * (us & 1), (us >> 1) & 1) &&
-                       ptx::mbar_test_wait(se0 + 8u * g, ((ns >> g) & 1u) ^ 1u))) {
-            if (any) {
-              ptx::tc_fence_after();
-              const uint64_t a = ptx::smem_desc_sw128(kv0 + rs.idx * kStageBytes);
-              const uint64_t b = q_desc + ((us & 1) * N2 * 128u >> 4);
+    } else {
+      // ============================= MMA ===============================
+      // A warp for the scores and one per group for its outputs, so that no
+      // product waits for another one's operands; lane 0 issues.
+      const bool scores = warp == kSWarp;
+      const int og = warp - kOWarp0;
+      if (lane == 0) {
+        constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(kAttnTile, N2);
+        constexpr uint32_t kIdescO = ptx::idesc_e4m3_f32(128, N2) | ptx::kIdescMnMajorA | ptx::kIdescMnMajorB;
+        const uint64_t a0 = scores ? ptx::smem_desc_sw128(kv0) : ptx::smem_desc_mn(kv0 + kVOff, 128);
+        const uint64_t b0 =
+            scores ? ptx::smem_desc_sw128(q0) : ptx::smem_desc_mn(ptx::smem_u32(smem + L.p) + og * kAttnTile * N2, N2);
+        const auto await = [&](uint32_t bar, uint32_t parity, uint32_t site) {
+          return wait_bounded(bar, parity, abort_flag, &g_attn_watchdog, site);
+        };
+        Ring st{0u, 0u, static_cast<uint32_t>(S)};
+        uint32_t n0 = 0, n1 = 0;      // tiles with entries (scores: per group; outputs: n0)
+        int turn = 0;
+        bool okay = true;
+#pragma unroll 1
+        for (int r = 0; r < rounds && okay; ++r) {
+          const int live = live_of(r);
+          bool first = true;          // outputs: the unit's first tile starts the accumulator anew
+#pragma unroll 1
+          for (int te = (t1 - t0) * live, e = 0; te > 0; --te, e = e + 1 == live ? 0 : e + 1) {
+            const uint32_t stage = st.idx, stage_phase = st.phase;
+            st.next();
+            const int g = CLUSTER ? turn : e;
+            turn = turn + 1 == NG ? 0 : turn + 1;
+            if (!scores && g != og) continue;
+            okay = await(full0 + 8u * stage, stage_phase, kSiteStageFull);
+            if (!okay) break;
+            const uint4 m = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * stage);
+            const bool any = (m.x | m.y | m.z | m.w) != 0u;
+            const uint64_t a = a0 + static_cast<uint64_t>(stage * (kStageBytes >> 4));
+            ptx::fence_proxy_async_smem();  // the tile was written by cp.async
+            if (scores) {
+              const int unit = CLUSTER ? 0 : r * NG + e, buf = unit % QB;
+              if (any) {
+                const uint32_t c = g == 0 ? n0++ : n1++;
+                const uint32_t slot = g * SBG + (SBG == 2 ? c & 1u : 0u), parity = (SBG == 2 ? c >> 1 : c) & 1u;
+                okay = await(qf0 + 8u * buf, (unit / QB) & 1, kSiteQFull) &&
+                       await(se0 + 8u * slot, parity ^ 1u, kSiteAccEmpty);
+                if (!okay) break;
+                ptx::tc_fence_after();
+                const uint64_t b = b0 + static_cast<uint64_t>(buf * (N2 * 128u >> 4));
 #pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk)
-                ptx::mma_f8f6f4(tmem + g * N2, a + 2ull * kk, b + 2ull * kk, kIdescS, kk > 0 ? 1u : 0u);
-              ptx::mma_commit(sf0 + 8u * g);
-              ns ^= 1u << g;
-            }
-            ++is;
-            rs.next();
-            if (cs.advance()) {
-              ptx::mma_commit(qe0 + 8u * (us & 1));
-              ++us;
-            }
-            did = true;
-          }
-        }
-        if (!did && ip < is) {
-          const uint32_t g = ip & 1;
-          const bool any = tile_any(rp.idx);
-          const bool first = !(started >> g & 1u);
-          if (!any || (ptx::mbar_test_wait(pf0 + 8u * g, (np >> g) & 1u) &&
-                       (!first || up == 0 || ptx::mbar_test_wait(oe, (up - 1) & 1)))) {
-            if (any) {
+                for (int kk = 0; kk < D / 32; ++kk)
+                  ptx::mma_f8f6f4(tmem + slot * N2, a + 2ull * kk, b + 2ull * kk, kIdescS, kk > 0 ? 1u : 0u);
+                ptx::mma_commit(sf0 + 8u * slot);
+              }
+              if (te <= live) ptx::mma_commit(qe0 + 8u * buf);  // the unit's last tile
+            } else if (any) {
+              // (the accumulator holds the group's last unit until that has been read)
+              okay = (!first || r == 0 || await(oe0 + 8u * g, (r - 1) & 1, kSiteAccEmpty)) &&
+                     await(pf0 + 8u * g, n0 & 1u, kSiteAccFull);
+              if (!okay) break;
+              ++n0;
               ptx::tc_fence_after();
-              const uint64_t a = ptx::smem_desc_mn(kv0 + rp.idx * kStageBytes + kVOff, 128);
-              const uint64_t b = ptx::smem_desc_mn(p0 + g * kAttnTile * N2, N2);
 #pragma unroll
               for (int kk = 0; kk < kAttnTile / 32; ++kk)
-                ptx::mma_f8f6f4(tmem + (2 + g) * N2, a + kk * (32ull * 128 >> 4), b + kk * (32ull * N2 >> 4), kIdescO,
+                ptx::mma_f8f6f4(tmem + kTmemO + g * N2, a + kk * (32ull * 128 >> 4), b0 + kk * (32ull * N2 >> 4), kIdescO,
                                 (first && kk == 0) ? 0u : 1u);
               ptx::mma_commit(pe0 + 8u * g);
-              ptx::mma_commit(empty0 + 8u * rp.idx);
-              np ^= 1u << g;
-              started |= 1u << g;
+              ptx::mma_commit(empty0 + 8u * stage);
+              first = false;
             } else {
-              ptx::mbar_arrive(empty0 + 8u * rp.idx);
+              ptx::mbar_arrive(empty0 + 8u * stage);
             }
-            ++ip;
-            rp.next();
-            if (cp.advance()) {
-              ++up;
-              started = 0;
-            }
-            did = true;
           }
         }
-        if (did) {
-          spins = 0;
-        } else if ((++spins & 255u) == 0u) {
-          if (*abort_flag) break;
-          const uint64_t now = ptx::globaltimer_ns();
-          if (spins == 256u) {
-            since = now;
-          } else if (now - since > kWaitTimeoutNs) {
-            *abort_flag = 1u;
-            atomicOr(&g_attn_watchdog, static_cast<uint32_t>(kSiteAccEmpty));
-            break;
-          }
+        if (*abort_flag) {
+          const uint32_t bar = drain0 + 8u * (warp - kSWarp);
+          ptx::mma_commit(bar);
+          wait_drain(bar, 0, &g_attn_watchdog);
         }
       }
-      if (*abort_flag) {
-        ptx::mma_commit(drain_bar);
-        wait_drain(drain_bar, 0, &g_attn_watchdog);
-      }
+      __syncwarp();
     }
   } else {
     // ============================ epilogue =============================
+    reg_inc<kAttnEpilogueRegs>();
     const int g = warp >> 2, quad = warp & 3;
     const int tg = threadIdx.x & 127;                 // thread in the group = token = channel
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t s_tm = tmem + g * N2 + lane_off, o_tm = tmem + (2 + g) * N2 + lane_off;
+    const uint32_t o_tm = tmem + kTmemO + g * N2 + lane_off;
     uint8_t* p_row = smem + L.p + g * kAttnTile * N2 + tg * N2;
     // 16-byte chunks of a row of probabilities, swizzled over its N2 bytes
     const uint32_t p_swz = N2 == 128 ? tg & 7 : N2 == 64 ? (tg >> 1) & 3 : (tg >> 2) & 1;
     const int bar_id = 1 + g;
+    // With at most 32 heads the scores stay in registers from the test
+    // against m to the probabilities, and their accumulator goes back at
+    // once; with 64 they are read again, 32 heads at a time.
+    constexpr bool kKeep = GP <= 32;
+    constexpr int CH = kKeep ? GP : 32;
     Ring st{0u, 0u, static_cast<uint32_t>(S)};
-    uint32_t n_tile = 0;                              // this group's tiles so far
-    int it = 0;
+    uint32_t n_tile = 0;                              // this group's tiles with entries
+    int turn = 0;
     bool stop = false;
-    for (int i = 0; i < n_units && !stop; ++i) {
-      const int buf = i & 1, par = i & 1;
+    float tv[CH];                                     // scores over m, log2 units
+#pragma unroll 1
+    for (int r = 0; r < rounds && !stop; ++r) {
+      const int live = live_of(r);
+      if (!CLUSTER && g >= live) break;
+      const int unit = CLUSTER ? 0 : r * NG + g;
       float qscale = 0.f;
       bool ok = true;
-      if (total > 0) {
-        ok = warp_wait_bounded(qf0 + 8u * buf, (i >> 1) & 1, abort_flag, &g_attn_watchdog, kSiteQFull);
-        qscale = stt.qf[buf] * p.scale_log2;
+      if (t0 < t1) {
+        ok = attn_wait(qf0 + 8u * (unit % QB), (unit / QB) & 1, abort_flag, kSiteQFull);
+        qscale = stt.qf[unit % QB] * p.scale_log2;
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(qe0 + 8u * buf);
+        if (lane == 0) ptx::mbar_arrive(qe0 + 8u * (unit % QB));
       }
-      bool has_o = false;
+      uint32_t has_o = 0u;  // whether the group's accumulator holds anything of this unit
       float cref = 0.f;
       float2 l2[GP / 2];
 #pragma unroll
       for (int j = 0; j < GP / 2; ++j) l2[j] = make_float2(0.f, 0.f);
 
-      for (int t = t0; t < t1; ++t, ++it) {
+#pragma unroll 1
+      for (int te = (t1 - t0) * live, e = 0; te > 0; --te) {
         const uint32_t stage = st.idx, stage_phase = st.phase;
         st.next();
-        if ((it & 1) != g) continue;
-        ok = warp_wait_bounded(full0 + 8u * stage, stage_phase, abort_flag, &g_attn_watchdog, kSiteStageFull) && ok;
+        const bool mine = CLUSTER ? turn == g : e == g;
+        if (++turn == NG) turn = 0;
+        if (++e == live) e = 0;
+        if (!mine) continue;
+        asm volatile("" : "+r"(has_o));  // (one copy of the loop: the first tile is not peeled off)
+        ok = attn_wait(full0 + 8u * stage, stage_phase, abort_flag, kSiteStageFull) && ok;
         const uint4 mk = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * stage);
         const bool any = (mk.x | mk.y | mk.z | mk.w) != 0u;
         const uint32_t mw = quad == 0 ? mk.x : quad == 1 ? mk.y : quad == 2 ? mk.z : mk.w;
@@ -539,37 +586,50 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const float c = valid ? sc.x * qscale : 0.f;
         const float vs = valid ? fmaxf(sc.y, 0.f) : 0.f;
         const float4* nm4 = reinterpret_cast<const float4*>(valid ? stt.nm[g] : stt.ninf);
-        const float2 c2 = make_float2(c, c), k16 = make_float2(0.0625f, 0.0625f);
-        bool again = !has_o;  // the group's first tile of a unit sets m
-        if (any) {
-          ok = warp_wait_bounded(sf0 + 8u * g, n_tile & 1u, abort_flag, &g_attn_watchdog, kSiteAccFull) && ok;
-          ptx::tc_fence_after();
-          if (!again) {
-            float top = -INFINITY;
+        const uint32_t slot = g * SBG + (SBG == 2 ? n_tile & 1u : 0u);
+        const uint32_t s_tm = tmem + slot * N2 + lane_off;
+        // scores of heads b .. b+CH-1 over the present m, and their maximum
+        const auto scores = [&](int b) {
+          const float2 c2 = make_float2(c, c), k16 = make_float2(0.0625f, 0.0625f);
+          float top = -INFINITY;
 #pragma unroll
-            for (int b = 0; b < GP; b += 16) {
-              uint32_t hi[16], lo[16];
-              ptx::tmem_ld_32x32b_x16(s_tm + b, hi);
-              ptx::tmem_ld_32x32b_x16(s_tm + GP + b, lo);
-              ptx::tmem_wait_ld_n(hi);
-              ptx::tmem_wait_ld_n(lo);
+          for (int b2 = 0; b2 < CH; b2 += 16) {
+            uint32_t hi[16], lo[16];
+            ptx::tmem_ld_32x32b_x16(s_tm + b + b2, hi);
+            ptx::tmem_ld_32x32b_x16(s_tm + GP + b + b2, lo);
+            ptx::tmem_wait_ld_n(hi);
+            ptx::tmem_wait_ld_n(lo);
 #pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                const float4 nm = nm4[(b + j) / 4];
+            for (int j = 0; j < 16; j += 4) {
+              const float4 nm = nm4[(b + b2 + j) / 4];
 #pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                  const float2 raw = __ffma2_rn(make_float2(__uint_as_float(lo[j + k]), __uint_as_float(lo[j + k + 1])),
-                                                k16,
-                                                make_float2(__uint_as_float(hi[j + k]), __uint_as_float(hi[j + k + 1])));
-                  const float2 t2 = __ffma2_rn(raw, c2, k == 0 ? make_float2(nm.x, nm.y) : make_float2(nm.z, nm.w));
-                  top = fmaxf(top, fmaxf(t2.x, t2.y));
-                }
+              for (int k = 0; k < 4; k += 2) {
+                const float2 raw = __ffma2_rn(make_float2(__uint_as_float(lo[j + k]), __uint_as_float(lo[j + k + 1])), k16,
+                                              make_float2(__uint_as_float(hi[j + k]), __uint_as_float(hi[j + k + 1])));
+                const float2 t2 = __ffma2_rn(raw, c2, k == 0 ? make_float2(nm.x, nm.y) : make_float2(nm.z, nm.w));
+                tv[b2 + j + k] = t2.x;
+                tv[b2 + j + k + 1] = t2.y;
+                top = fmaxf(top, fmaxf(t2.x, t2.y));
               }
             }
-            again = top > kLazy || vs > 2.f * cref;
           }
+          return top;
+        };
+        bool again = false;
+        if (any) {
+          ok = attn_wait(sf0 + 8u * slot, (SBG == 2 ? n_tile >> 1 : n_tile) & 1u, abort_flag, kSiteAccFull) && ok;
+          ptx::tc_fence_after();
+          float top = scores(0);
+          if constexpr (kKeep) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(se0 + 8u * slot);
+          } else {
+#pragma unroll 1
+            for (int b = CH; b < GP; b += CH) top = fmaxf(top, scores(b));
+          }
+          again = !has_o || top > kLazy || vs > 2.f * cref;  // the first tile of a unit sets m
         }
-        if (!any) again = false;
         if (ptx::bar_or(bar_id, 128, again || !ok)) {
           // ---- new maxima (or the end of an abandoned call)
           if (ptx::bar_or(bar_id, 128, !ok)) {
@@ -577,45 +637,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             break;
           }
 #pragma unroll 1
-          for (int b = 0; b < GP; b += 16) {
-            uint32_t hi[16], lo[16];
-            ptx::tmem_ld_32x32b_x16(s_tm + b, hi);
-            ptx::tmem_ld_32x32b_x16(s_tm + GP + b, lo);
-            ptx::tmem_wait_ld_n(hi);
-            ptx::tmem_wait_ld_n(lo);
-            int mine = 0;
+          for (int b = 0; b < GP; b += CH) {
+            if (!kKeep) scores(b);
+            float v[CH];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float s = fmaf(__uint_as_float(lo[j]), 0.0625f, __uint_as_float(hi[j])) * c;
-              const int m = __reduce_max_sync(kFull, float_key(valid ? s : -INFINITY));
-              if (lane == j) mine = m;
-            }
-            if (lane < 16) stt.wmax[g][quad][b + lane] = key_float(mine);
+            for (int j = 0; j < CH; ++j) v[j] = tv[j];
+            const float top = reduce_columns<CH, true>(v, lane);
+            if (lane < CH) stt.part[g][quad][b + lane] = top;
           }
           const float vmax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vs)));
           if (lane == 0) stt.wvs[g][quad] = vmax;
           ptx::bar_sync(bar_id, 128);
           if (tg < GP) {
-            const float old = has_o ? -stt.nm[g][tg] : kMinM;
-            float m = old;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const float x = stt.wmax[g][w][tg];
-              m = (x > m || x != x) ? x : m;
-            }
-            stt.resc[g][tg] = ex2(old - m);
-            stt.nm[g][tg] = -m;
+            float d = fmaxf(fmaxf(stt.part[g][0][tg], stt.part[g][1][tg]), fmaxf(stt.part[g][2][tg], stt.part[g][3][tg]));
+            d = fmaxf(d, has_o ? 0.f : kMinM);
+            stt.delta[g][tg] = d;
+            stt.resc[g][tg] = ex2(-d);
+            stt.nm[g][tg] -= d;
           }
           if (tg == 0) {
-            float m = cref;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) m = fmaxf(m, stt.wvs[g][w]);
-            m = fmaxf(m, kMinVScale);
+            float m = fmaxf(fmaxf(stt.wvs[g][0], stt.wvs[g][1]), fmaxf(stt.wvs[g][2], stt.wvs[g][3]));
+            m = fmaxf(fmaxf(m, cref), kMinVScale);
             stt.cref[g] = m;
-            stt.cfac[g] = cref / m;
+            stt.cfac[g] = __fdividef(cref, m);
           }
           ptx::bar_sync(bar_id, 128);
           cref = stt.cref[g];
+          if constexpr (kKeep) {
+#pragma unroll
+            for (int j = 0; j < GP; j += 4) {
+              const float4 d = *reinterpret_cast<const float4*>(&stt.delta[g][j]);
+              tv[j] -= d.x, tv[j + 1] -= d.y, tv[j + 2] -= d.z, tv[j + 3] -= d.w;
+            }
+          }
           if (has_o) {
 #pragma unroll
             for (int j = 0; j < GP / 2; ++j) {
@@ -623,168 +677,144 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               l2[j] = make_float2(l2[j].x * f.x, l2[j].y * f.y);
             }
             // the group's last output MMA is done before its sums are scaled
-            ok = warp_wait_bounded(pe0 + 8u * g, (n_tile & 1u) ^ 1u, abort_flag, &g_attn_watchdog, kSiteAccEmpty) && ok;
+            ok = attn_wait(pe0 + 8u * g, (n_tile & 1u) ^ 1u, abort_flag, kSiteAccEmpty) && ok;
             ptx::tc_fence_after();
             const float cf = stt.cfac[g];
 #pragma unroll 1
             for (int b = 0; b < N2; b += 16) {
-              uint32_t r[16];
-              ptx::tmem_ld_32x32b_x16(o_tm + b, r);
-              ptx::tmem_wait_ld_n(r);
+              uint32_t v[16];
+              ptx::tmem_ld_32x32b_x16(o_tm + b, v);
+              ptx::tmem_wait_ld_n(v);
+              const float* f = &stt.resc[g][b % GP];
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                r[j] = __float_as_uint(__uint_as_float(r[j]) * (stt.resc[g][(b + j) % GP] * cf));
-              ptx::tmem_st_32x32b_x16(o_tm + b, r);
+              for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * (f[j] * cf));
+              ptx::tmem_st_32x32b_x16(o_tm + b, v);
             }
             ptx::tmem_wait_st();
           }
         }
         if (!any) continue;
         // ---- probabilities; P is free once the group's last output MMA is done
-        ok = warp_wait_bounded(pe0 + 8u * g, (n_tile & 1u) ^ 1u, abort_flag, &g_attn_watchdog, kSiteAccEmpty) && ok;
-        const float w = vs * (kPScale / cref);
+        ok = attn_wait(pe0 + 8u * g, (n_tile & 1u) ^ 1u, abort_flag, kSiteAccEmpty) && ok;
+        const float w = vs * __fdividef(kPScale, cref);
         const float2 w2 = make_float2(w, w);
 #pragma unroll
-        for (int b = 0; b < GP; b += 16) {
-          uint32_t hi[16], lo[16];
-          ptx::tmem_ld_32x32b_x16(s_tm + b, hi);
-          ptx::tmem_ld_32x32b_x16(s_tm + GP + b, lo);
-          ptx::tmem_wait_ld_n(hi);
-          ptx::tmem_wait_ld_n(lo);
-          uint32_t ph[4], pl[4];
+        for (int b = 0; b < GP; b += CH) {
+          if (!kKeep) scores(b);
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 nm = nm4[(b + j) / 4];
-            uint32_t hc[2], lc[2];
+          for (int b2 = 0; b2 < CH; b2 += 16) {
+            uint32_t ph[4], pl[4];
 #pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-              const float2 raw = __ffma2_rn(make_float2(__uint_as_float(lo[j + k]), __uint_as_float(lo[j + k + 1])), k16,
-                                            make_float2(__uint_as_float(hi[j + k]), __uint_as_float(hi[j + k + 1])));
-              const float2 t2 = __ffma2_rn(raw, c2, k == 0 ? make_float2(nm.x, nm.y) : make_float2(nm.z, nm.w));
-              const float2 e2 = make_float2(ex2(t2.x), ex2(t2.y));
-              float2& l = l2[(b + j + k) / 2];
-              l = __fadd2_rn(l, e2);
-              const float2 pw = __fmul2_rn(e2, w2);
-              split_pair(__floats2half2_rn(pw.x, pw.y), &hc[k / 2], &lc[k / 2]);
+            for (int j = 0; j < 16; j += 4) {
+              uint32_t hc[2], lc[2];
+#pragma unroll
+              for (int k = 0; k < 4; k += 2) {
+                const int at = b2 + j + k;
+                const float2 e2 = make_float2(ex2(tv[at]), ex2(tv[at + 1]));
+                float2& l = l2[(b + at) / 2];
+                l = __fadd2_rn(l, e2);
+                const float2 pw = __fmul2_rn(e2, w2);
+                split_pair(__floats2half2_rn(pw.x, pw.y), &hc[k / 2], &lc[k / 2]);
+              }
+              ph[j / 4] = hc[0] | hc[1] << 16;
+              pl[j / 4] = lc[0] | lc[1] << 16;
             }
-            ph[j / 4] = hc[0] | hc[1] << 16;
-            pl[j / 4] = lc[0] | lc[1] << 16;
+            *reinterpret_cast<uint4*>(p_row + ((((b + b2) / 16) ^ p_swz) << 4)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+            *reinterpret_cast<uint4*>(p_row + ((((GP + b + b2) / 16) ^ p_swz) << 4)) =
+                make_uint4(pl[0], pl[1], pl[2], pl[3]);
           }
-          *reinterpret_cast<uint4*>(p_row + (((b / 16) ^ p_swz) << 4)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-          *reinterpret_cast<uint4*>(p_row + ((((GP + b) / 16) ^ p_swz) << 4)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
         }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          ptx::mbar_arrive(se0 + 8u * g);
+          if (!kKeep) ptx::mbar_arrive(se0 + 8u * slot);
           ptx::mbar_arrive(pf0 + 8u * g);
         }
-        has_o = true;
+        has_o = 1u;
         ++n_tile;
       }
       if (stop) break;
 
-      // ---- the unit's end: both groups' sums and maxima meet
-      if (has_o) {
-        warp_wait_bounded(pe0 + 8u * g, (n_tile & 1u) ^ 1u, abort_flag, &g_attn_watchdog, kSiteAccEmpty);
-      }
-#pragma unroll
-      for (int j = 0; j < GP / 2; ++j) {
-        float2 v = l2[j];
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-          v.x += __shfl_xor_sync(kFull, v.x, d);
-          v.y += __shfl_xor_sync(kFull, v.y, d);
-        }
-        if (lane == 0) *reinterpret_cast<float2*>(&stt.lred[par][g][quad][2 * j]) = v;
-      }
-      if (tg < GP) stt.msave[par][g][tg] = has_o ? -stt.nm[g][tg] : kMinM;
-      if (tg == 0) {
-        stt.csave[par][g] = cref;
-        stt.used[par][g] = has_o ? 1.f : 0.f;
-      }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ub);
-      warp_wait_bounded(ub, i & 1, abort_flag, &g_attn_watchdog, kSiteAccFull);
+      // ---- the unit's end: the sums over the group's tokens, and the output
+      if (has_o) attn_wait(pe0 + 8u * g, (n_tile & 1u) ^ 1u, abort_flag, kSiteAccEmpty);
       ptx::tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < GP; b += CH) {
+        float v[CH];
+#pragma unroll
+        for (int j = 0; j < CH; j += 2) v[j] = l2[(b + j) / 2].x, v[j + 1] = l2[(b + j) / 2].y;
+        const float sum = reduce_columns<CH, false>(v, lane);
+        if (lane < CH) stt.part[g][quad][b + lane] = sum;
+      }
+      ptx::bar_sync(bar_id, 128);
       int row, kvh, h0;
-      unit_of(p, u0 + i * ustep, &row, &kvh, &h0, GP);
+      unit_of(p, u0 + unit * ustep, &row, &kvh, &h0, GP);
       const int nh = min(GP, p.group - h0);
-      constexpr int kHalf = GP / 2;  // group g finishes heads [g*kHalf, (g+1)*kHalf)
-      if (tg < kHalf) {
-        const int h = g * kHalf + tg;
-        float ls[2], ms[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          ms[k] = stt.msave[par][k][h];
-          ls[k] = (stt.lred[par][k][0][h] + stt.lred[par][k][1][h]) + (stt.lred[par][k][2][h] + stt.lred[par][k][3][h]);
-        }
-        const float m = (ms[0] > ms[1] || ms[0] != ms[0]) ? ms[0] : ms[1];
-        float f[2], sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          f[k] = stt.used[par][k] != 0.f ? ex2(ms[k] - m) : 0.f;
-          sum += f[k] * ls[k];
-        }
-        const float norm = CLUSTER ? 1.f / kPScale : sum == 0.f ? 0.f : 1.f / (sum * kPScale);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) stt.fac[h][k] = f[k] * stt.csave[par][k] * norm;
+      if (tg < GP) {
+        const float sum = (stt.part[g][0][tg] + stt.part[g][1][tg]) + (stt.part[g][2][tg] + stt.part[g][3][tg]);
+        const float m = has_o ? -stt.nm[g][tg] : kMinM;
+        stt.nm[g][tg] = 0.f;
         if constexpr (CLUSTER) {
-          stt.xm[h] = m;
-          stt.xl[h] = sum;
-        } else if (p.lse != nullptr && h < nh) {
-          p.lse[static_cast<int64_t>(row) * p.heads + kvh * p.group + h0 + h] =
-              sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+          stt.fac[g][tg] = has_o ? cref * (1.f / kPScale) : 0.f;
+          stt.xm[g][tg] = m;
+          stt.xl[g][tg] = sum;
+        } else {
+          stt.fac[g][tg] = sum == 0.f ? 0.f : cref / (sum * kPScale);
+          if (p.lse != nullptr && tg < nh)
+            p.lse[static_cast<int64_t>(row) * p.heads + kvh * p.group + h0 + tg] =
+                sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
         }
       }
-      const bool used0 = stt.used[par][0] != 0.f, used1 = stt.used[par][1] != 0.f;
+      if constexpr (CLUSTER) {  // the outputs go where the tiles were: both groups are done with them
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ub);
+        attn_wait(ub, 0, abort_flag, kSiteAccFull);
+      }
       ptx::bar_sync(bar_id, 128);
       const int ch = D == 128 ? tg : tg - 64;  // D = 64: the value half of the shared rows
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row / p.next_n * p.out_req_stride +
                            row % p.next_n * p.out_row_stride + (kvh * p.group + h0) * p.out_head_stride + ch;
-      float* xo = reinterpret_cast<float*>(smem + L.kv);  // cluster: [GP][128], where the tiles were
+      float* xo = reinterpret_cast<float*>(smem + L.kv) + g * GP * 128 + tg;  // cluster: [group][GP][128]
 #pragma unroll 1
-      for (int b = g * kHalf; b < (g + 1) * kHalf; b += 8) {
+      for (int b = 0; b < GP; b += 8) {
         float v[8];
+        if (has_o) {
+          uint32_t hi[8], lo[8];
+          ptx::tmem_ld_32x32b_x8(o_tm + b, hi);
+          ptx::tmem_ld_32x32b_x8(o_tm + GP + b, lo);
+          ptx::tmem_wait_ld_n(hi);
+          ptx::tmem_wait_ld_n(lo);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+          for (int j = 0; j < 8; ++j)
+            v[j] = fmaf(__uint_as_float(lo[j]), 0.0625f, __uint_as_float(hi[j])) * stt.fac[g][b + j];
+        } else {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (k == 0 ? used0 : used1) {
-            const uint32_t o = tmem + (2 + k) * N2 + lane_off + b;
-            uint32_t hi[8], lo[8];
-            ptx::tmem_ld_32x32b_x8(o, hi);
-            ptx::tmem_ld_32x32b_x8(o + GP, lo);
-            ptx::tmem_wait_ld_n(hi);
-            ptx::tmem_wait_ld_n(lo);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              v[j] = fmaf(fmaf(__uint_as_float(lo[j]), 0.0625f, __uint_as_float(hi[j])), stt.fac[b + j][k], v[j]);
-          }
+          for (int j = 0; j < 8; ++j) v[j] = 0.f;
         }
         if constexpr (CLUSTER) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) xo[(b + j) * 128 + tg] = v[j];
+          for (int j = 0; j < 8; ++j) xo[(b + j) * 128] = v[j];
         } else if (ch >= 0) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (b + j < nh) out[(b + j) * p.out_head_stride] = __float2bfloat16(v[j]);
+          for (int j = 0; j < 8; ++j) {
+            if (b + j < nh) *out = __float2bfloat16(v[j]);
+            out += p.out_head_stride;
+          }
         }
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(oe);
+      if (lane == 0) ptx::mbar_arrive(oe0 + 8u * g);
     }
   }
 
   if constexpr (CLUSTER) {
-    // ---- the CTAs' shares meet: CTA r finishes heads [r*GP/C, (r+1)*GP/C)
+    // ---- the groups of every CTA meet: CTA r finishes heads [r*GP/C, (r+1)*GP/C)
     cg::cluster_group cl = cg::this_cluster();
     __syncwarp();
     cl.sync();
-    if (warp < 4 * kAttnGroups && n_units > 0) {
+    if (warp < 4 * NG) {
       const int tg = threadIdx.x & 127, half = threadIdx.x >> 7;
       const int ch = D == 128 ? tg : tg - 64;
       int row, kvh, h0;
@@ -792,18 +822,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int nh = min(GP, p.group - h0);
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row / p.next_n * p.out_req_stride +
                            row % p.next_n * p.out_row_stride + (kvh * p.group + h0) * p.out_head_stride + ch;
+      const float* xo = reinterpret_cast<const float*>(smem + L.kv) + tg;
       const int h_end = min(nh, (crank + 1) * GP / C);
-      for (int h = crank * GP / C + half; h < h_end; h += 2) {
+#pragma unroll 1
+      for (int h = crank * GP / C + half; h < h_end; h += NG) {
         float m = kMinM;
-        for (int r = 0; r < C; ++r) {
-          const float x = *cl.map_shared_rank(&stt.xm[h], r);
+#pragma unroll 1
+        for (int r = 0; r < C * NG; ++r) {
+          const float x = *cl.map_shared_rank(&stt.xm[r % NG][h], r / NG);
           m = (x > m || x != x) ? x : m;
         }
         float sum = 0.f, v = 0.f;
-        for (int r = 0; r < C; ++r) {
-          const float f = ex2(*cl.map_shared_rank(&stt.xm[h], r) - m);
-          sum = fmaf(f, *cl.map_shared_rank(&stt.xl[h], r), sum);
-          v = fmaf(f, *cl.map_shared_rank(reinterpret_cast<float*>(smem + L.kv) + h * 128 + tg, r), v);
+#pragma unroll 2
+        for (int r = 0; r < C * NG; ++r) {
+          const float f = ex2(*cl.map_shared_rank(&stt.xm[r % NG][h], r / NG) - m);
+          sum = fmaf(f, *cl.map_shared_rank(&stt.xl[r % NG][h], r / NG), sum);
+          v = fmaf(f, *cl.map_shared_rank(const_cast<float*>(xo) + (r % NG * GP + h) * 128, r / NG), v);
         }
         if (ch >= 0) out[h * p.out_head_stride] = __float2bfloat16(sum == 0.f ? 0.f : v / sum);
         if (p.lse != nullptr && tg == 0)
@@ -817,14 +851,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kSWarp) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
 }
 
 namespace {
-using AttnKernel = void (*)(CUtensorMap, SparseAttnParams);
+using AttnKernel = void (*)(SparseAttnParams);
 template <int D, bool CLUSTER>
 AttnKernel attn_instance(int gp) {
   return gp == 16   ? sparse_attn_kernel<D, 16, CLUSTER>
@@ -833,7 +867,7 @@ AttnKernel attn_instance(int gp) {
 }
 }  // namespace
 
-cudaError_t launch_sparse_attn(const CUtensorMap& tm_kv, const SparseAttnParams& p, int head_dim, int grid, int ctas,
+cudaError_t launch_sparse_attn(const SparseAttnParams& p, int head_dim, int grid, int ctas,
                                int smem_bytes, cudaStream_t stream) {
   const int gp = attn_pad(p.group);
   const AttnKernel kern = head_dim == 128 ? (ctas > 1 ? attn_instance<128, true>(gp) : attn_instance<128, false>(gp))
@@ -841,7 +875,7 @@ cudaError_t launch_sparse_attn(const CUtensorMap& tm_kv, const SparseAttnParams&
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem_bytes);
   if (e != cudaSuccess) return e;
   if (ctas == 1) {
-    kern<<<grid, kAttnThreads, smem_bytes, stream>>>(tm_kv, p);
+    kern<<<grid, kAttnThreads, smem_bytes, stream>>>(p);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg = {};
@@ -856,7 +890,7 @@ cudaError_t launch_sparse_attn(const CUtensorMap& tm_kv, const SparseAttnParams&
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tm_kv, p);
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 cudaError_t read_attn_watchdog(unsigned int* value, bool clear) {
