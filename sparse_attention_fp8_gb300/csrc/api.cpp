@@ -1020,10 +1020,21 @@ fp8idx_status sparse_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, 
   p.block_tables = static_cast<const int32_t*>(bt->data);
   p.cu_seq_lens = prefill ? static_cast<const int32_t*>(cu->data) : nullptr;
   p.idx_stride = R > 1 ? idx->stride[0] : k;
-  p.bt_stride = bt->shape[0] > 1 ? bt->stride[0] : 0;
-  p.block_stride = kv->shape[0] > 1 ? kv->stride[0] : 0;
-  p.kv_head_stride = HK > 1 ? kv->stride[1] : 0;
-  p.num_blocks = kv->shape[0];
+  const int64_t bt_stride = bt->shape[0] > 1 ? bt->stride[0] : 0;
+  if (bt_stride < 0 || bt_stride >= (1ll << 31)) return fail(FP8IDX_ERR_UNSUPPORTED, "block_tables: row stride of 2^31 or more");
+  p.bt_stride = (int32_t)bt_stride;
+  const int64_t block_stride = kv->shape[0] > 1 ? kv->stride[0] : 0, head_stride = HK > 1 ? kv->stride[1] : 0;
+  int64_t unit = 16;
+  while (((block_stride | head_stride | 2 * D) & (2 * unit - 1)) == 0) unit *= 2;
+  if ((kv->shape[0] - 1) * block_stride + (HK - 1) * head_stride + kv->shape[2] >= unit << 32)
+    return fail(FP8IDX_ERR_UNSUPPORTED, "kv_cache: spans %lld bytes or more (offsets are 2^32 multiples of %lld)",
+                (long long)(unit << 32), (long long)unit);
+  p.unit = (uint32_t)unit;
+  p.block_units = (uint32_t)(block_stride / unit);
+  p.head_units = (uint32_t)(head_stride / unit);
+  p.tok_units = (uint32_t)(2 * D / unit);
+  p.scale_off = (int32_t)(bs * 2 * D);
+  p.num_blocks = (int32_t)kv->shape[0];
   p.rows = (int32_t)R;
   p.heads = (int32_t)H;
   p.kv_heads = (int32_t)HK;
@@ -1043,21 +1054,23 @@ fp8idx_status sparse_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, 
   p.tiles = (int32_t)((k + kAttnTile - 1) / kAttnTile);
   DeviceInfo dev;
   TRY(device_info(&dev));
+  // Persistent CTAs (two units at a time), or a cluster of CTAs per unit
+  // (which share its tiles): whichever leaves the busiest SM the least to do,
+  // in tiles, a cluster's start, meeting and end counted as about six.
+  int cs = ctas;
+  if (ctas == 0) {
+    const int64_t pair = static_cast<int64_t>(kAttnGroups) * dev.sms;
+    int64_t best = (p.units + pair - 1) / pair * kAttnGroups * p.tiles + 2;
+    for (int c = 1; c <= kAttnMaxCtas && (c == 1 || c / 2 < p.tiles); c *= 2) {
+      const int64_t waves = (static_cast<int64_t>(p.units) * c + dev.sms - 1) / dev.sms;
+      const int64_t cost = waves * ((p.tiles + c - 1) / c + 6);
+      if (cost < best) cs = c, best = cost;
+    }
+  }
+  const int grid = cs == 0 ? std::min(p.units, dev.sms) : p.units * cs;
   p.stages = attn_stages((int)D, gp, dev.smem_optin);
   const int smem = (int)attn_smem_layout((int)D, gp, p.stages).total;
   if (smem > dev.smem_optin) return fail(FP8IDX_ERR_UNSUPPORTED, "sparse attention: shared memory too small");
-  // CTAs per unit: the split whose slowest SM has the fewest tiles to do,
-  // counting a unit's start, hand-over and end as about four tiles.
-  int cs = ctas;
-  if (cs == 0) {
-    int64_t best = 0;
-    for (int c = 1; c <= kAttnMaxCtas && c <= std::max(1, p.tiles); c *= 2) {
-      const int64_t waves = (static_cast<int64_t>(p.units) * c + dev.sms - 1) / dev.sms;
-      const int64_t cost = c == 1 ? waves * p.tiles + 4 : waves * ((p.tiles + c - 1) / c + 4);
-      if (cs == 0 || cost < best) cs = c, best = cost;
-    }
-  }
-  const int grid = cs == 1 ? std::min(p.units, dev.sms) : p.units * cs;
   cudaError_t e = launch_sparse_attn(p, (int)D, grid, cs, smem, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(FP8IDX_ERR_CUDA, "sparse attention launch: %s", cudaGetErrorString(e));
   return ok();

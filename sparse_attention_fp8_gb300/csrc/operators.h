@@ -64,9 +64,12 @@ struct SparseAttnParams {
   int64_t q_req_stride, q_row_stride, q_head_stride;        // elements; row r is (r / next_n, r % next_n)
   int64_t out_req_stride, out_row_stride, out_head_stride;
   int64_t idx_stride;
-  int64_t bt_stride;
-  int64_t block_stride, kv_head_stride;                     // bytes
-  int64_t num_blocks;
+  int32_t bt_stride;
+  int32_t num_blocks;
+  // the cache's strides in units of `unit` bytes, the largest power of two
+  // that divides them all: a token's offset is a 32-bit number of units
+  uint32_t unit, block_units, head_units, tok_units;
+  int32_t scale_off;                                        // bytes from a page to its scales
   int32_t rows, heads, kv_heads, group;                     // group: query heads per key head
   int32_t next_n;                                           // prefill: 1
   int32_t k, max_blocks, block_size, block_shift, n_req;
@@ -83,14 +86,14 @@ constexpr int kAttnTile = 128;    // selected tokens per MMA tile (MMA M of the 
 constexpr int kAttnMaxStages = 8;
 // Query heads of a unit, padded to a width that P's rows can be swizzled over.
 __host__ __device__ constexpr int attn_pad(int group) { return group <= 16 ? 16 : group <= 32 ? 32 : 64; }
-// Roles: two epilogue warpgroups; four producer warps; the warps that issue
-// the scores and each group's outputs; the query warp.
+// Roles: two epilogue warpgroups; two sets of four producer warps; the warps
+// that issue the scores and each group's outputs; the query warp.
 constexpr int kAttnGroups = 2;
-constexpr int kAttnProducers = 4;
-constexpr int kAttnThreads = 32 * (4 * kAttnGroups + kAttnProducers + 4);
-// Registers a thread after the launch's 128 have been dealt anew:
-// 256 * 168 + 256 * 88 = 512 * 128.
-constexpr int kAttnEpilogueRegs = 168, kAttnOtherRegs = 88;
+constexpr int kAttnProducerSets = 2;
+constexpr int kAttnThreads = 32 * (4 * kAttnGroups + 4 * kAttnProducerSets + 2 + kAttnGroups);
+// Registers a thread after the launch's 96 have been dealt anew:
+// 256 * 144 + 384 * 64 = 640 * 96.
+constexpr int kAttnEpilogueRegs = 144, kAttnOtherRegs = 64;
 // Per group: accumulators of S^T (tensor memory's 512 columns hold them and
 // one of O^T, 2*GP each).  Query buffers: units in work and the next ones.
 __host__ __device__ constexpr int attn_score_buffers(int gp) { return gp <= 32 ? 2 : 1; }
@@ -115,12 +118,15 @@ __host__ __device__ inline AttnSmem attn_smem_layout(int head_dim, int gp, int s
   L.total = off + 1024u;
   return L;
 }
-// As many stages as shared memory holds, at most kAttnMaxStages.
+// As many stages as shared memory holds, a multiple of the producer sets.
 __host__ inline int attn_stages(int head_dim, int gp, int smem_limit) {
-  int s = kAttnMaxStages;
-  while (s > 3 && static_cast<int>(attn_smem_layout(head_dim, gp, s).total) > smem_limit) --s;
+  int s = kAttnMaxStages / kAttnProducerSets * kAttnProducerSets;
+  while (s > kAttnProducerSets && static_cast<int>(attn_smem_layout(head_dim, gp, s).total) > smem_limit)
+    s -= kAttnProducerSets;
   return s;
 }
+// ctas 0: persistent CTAs, a unit per epilogue group; 1 .. 8: a cluster of so
+// many CTAs per unit, which share its tiles.
 cudaError_t launch_sparse_attn(const SparseAttnParams& p, int head_dim, int grid, int ctas,
                                int smem_bytes, cudaStream_t stream);
 cudaError_t read_attn_watchdog(unsigned int* value, bool clear);

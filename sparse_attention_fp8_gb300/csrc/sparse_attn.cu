@@ -62,8 +62,6 @@ namespace cg = cooperative_groups;
 namespace fp8idx {
 
 static __device__ unsigned int g_attn_watchdog;
-// The row that an entry without a token copies: zeros.
-static __device__ __align__(256) uint8_t g_zero_row[256];
 
 namespace {
 
@@ -112,6 +110,14 @@ struct AttnState {
   float wvs[NG][4];
   float qf[QB];                // [query buffer]: 2^-e of the query's scaling
 };
+
+// A load that is issued where it stands: the compiler would otherwise sink a
+// load whose value is needed in the loop's next turn past the copies.
+__device__ __forceinline__ int32_t load_now(const int32_t* a) {
+  int32_t v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(a));
+  return v;
+}
 
 // Registers move from the copying and issuing warps to the epilogue's.
 template <int N>
@@ -167,7 +173,7 @@ __device__ __forceinline__ void split_pair(__half2 x, uint32_t* h, uint32_t* l) 
 template <int D, int GP, bool CLUSTER>
 __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __grid_constant__ SparseAttnParams p) {
   constexpr int NG = kAttnGroups;
-  constexpr int kProdWarp0 = 4 * NG, kProdWarps = kAttnProducers;
+  constexpr int kProdWarp0 = 4 * NG, kProdWarps = 4 * kAttnProducerSets;
   constexpr int kSWarp = kProdWarp0 + kProdWarps, kOWarp0 = kSWarp + 1, kQWarp = kOWarp0 + NG;
   static_assert(32 * (kQWarp + 1) == kAttnThreads, "roles");
   constexpr int N2 = 2 * GP;                       // columns of S^T and O^T
@@ -200,8 +206,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
   if (threadIdx.x == 0) {
     misc[1] = 0u;
     for (int s = 0; s < S; ++s) {
-      ptx::mbar_init(full0 + 8u * s, 33u * kProdWarps);  // each producer lane's copies, each warp's mask
-      ptx::mbar_init(empty0 + 8u * s, 1u + 4u);          // the output MMA, the tile's epilogue warps
+      ptx::mbar_init(full0 + 8u * s, 33u * 4u);        // each producer lane's copies, each warp's mask
+      ptx::mbar_init(empty0 + 8u * s, 1u + 1u + 4u);     // both MMA warps, the tile's epilogue warps
     }
     for (int i = 0; i < QB; ++i) {
       ptx::mbar_init(qf0 + 8u * i, 1u);
@@ -249,140 +255,141 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     reg_dec<kAttnOtherRegs>();
     if (warp < kSWarp) {
       // =========================== producers ===========================
-      constexpr int kPerLane = kAttnTile / (32 * kProdWarps);  // entries of a lane in a tile
+      // A cluster's tiles are copied by all warps together (the first tile's
+      // latency counts), a persistent CTA's by one warp each: the entries'
+      // and tables' latencies are then paid by four tiles at once.
+      // Four warps copy a tile, 32 entries each (a lane resolves one), and two
+      // sets of four take turns.  Stages are a multiple of the sets, so that a
+      // stage is always filled by the same one: a set that filled a stage out
+      // of turn could take the free barrier's phase of two uses ago for that
+      // of the last one.
+      constexpr int kSets = kAttnProducerSets;
+      const int set = (warp - kProdWarp0) / 4;
       constexpr int kRowLanes = 2 * D / 16;                    // lanes that copy a token's 16-byte pieces
       constexpr int kRowsPerCopy = 32 / kRowLanes;
-      const int pw = warp - kProdWarp0;
-      const int bs = p.block_size, shift = p.block_shift;
-      // Where a tile's entries, block table and pages are.  The divisions
-      // that take a unit apart are done once a unit.
+      const int tok0 = (warp - kProdWarp0) % 4 * 32;           // this warp's tokens of a tile
+      const int shift = p.block_shift, in_page = p.block_size - 1;
+      // Where a tile's entries, block table (decode) and pages (offset of the
+      // key head) are: the divisions that take a unit apart are done once a
+      // unit.
       struct Place {
         const int32_t* idx;
-        const int32_t* table;
-        const uint8_t* head;
+        int req;
+        uint32_t head;
       };
-      const auto place_of = [&](int i) {
-        int row, kvh, h0;
-        unit_of(p, u0 + i * ustep, &row, &kvh, &h0, GP);
-        return Place{p.indices + row * p.idx_stride,
-                     p.cu_seq_lens != nullptr ? p.block_tables : p.block_tables + row / p.next_n * p.bt_stride,
-                     p.kv + kvh * p.kv_head_stride};
-      };
-      // the look-ahead cursor over the sequence
-      int ar = 0, at = t0, ae = 0;
       Place units[NG];
-      const auto load_entries = [&](const Place& c, int t, int32_t (&idx)[kPerLane]) {
-#pragma unroll
-        for (int r = 0; r < kPerLane; ++r) {
-          const int j = t * kAttnTile + (pw * kPerLane + r) * 32 + lane;
-          idx[r] = j < p.k ? __ldg(c.idx + j) : -1;
-        }
-      };
-      // block-table entries (or -1) of a lane's entries, which become places in the page
-      int req = 0;  // prefill: the request that the last column was found in
-      int32_t req_lo = 0, req_hi = -1;
-      const auto load_tables = [&](const Place& c, int32_t (&idx)[kPerLane], int32_t (&blk)[kPerLane]) {
-#pragma unroll
-        for (int r = 0; r < kPerLane; ++r) {
-          int32_t tok = idx[r];
-          bool ok = tok >= 0;
-          const int32_t* table = c.table;
-          if (p.cu_seq_lens != nullptr) {
-            if (ok && (tok < req_lo || tok >= req_hi)) {
-              int a = 0, b = p.n_req;
-#pragma unroll 1
-              while (b - a > 1) {
-                const int mid = (a + b) >> 1;
-                if (__ldg(p.cu_seq_lens + mid) <= tok) a = mid; else b = mid;
-              }
-              req = a;
-              req_lo = __ldg(p.cu_seq_lens + a);
-              req_hi = __ldg(p.cu_seq_lens + a + 1);
-            }
-            ok = ok && tok >= req_lo && tok < req_hi;
-            tok -= req_lo;
-            table += req * p.bt_stride;
-          }
-          const int32_t j = tok >> shift;
-          idx[r] = tok & (bs - 1);
-          blk[r] = ok && j < p.max_blocks ? __ldg(table + j) : -1;
-        }
-      };
+      int ar = 0, at = t0, ae = 0;  // the look-ahead cursor over the sequence
       // Lane l copies piece l % kRowLanes of every kRowsPerCopy-th token into
       // its place in the 128-byte swizzle, which depends on the token mod 8.
       const int piece = lane % kRowLanes, sub = lane / kRowLanes;
       uint32_t place[8 / kRowsPerCopy];
 #pragma unroll
       for (int i = 0; i < 8 / kRowsPerCopy; ++i)
-        place[i] = (piece >> 3) * kVOff + sub * 128 + (((piece & 7) ^ ((i * kRowsPerCopy + sub) & 7)) << 4);
+        place[i] = kv0 + tok0 * 128 + (piece >> 3) * kVOff + sub * 128 +
+                   (((piece & 7) ^ ((i * kRowsPerCopy + sub) & 7)) << 4);
+      const uint8_t* const my_piece = p.kv + piece * 16;
+      const uint32_t my_scale = ptx::smem_u32(smem + L.scale) + (tok0 + lane) * 8u;
+      uint32_t* const my_mask = reinterpret_cast<uint32_t*>(smem + L.mask) + (tok0 >> 5);
       const int total = n_units * (t1 - t0);
       if (total > 0) {
-        // entries are loaded two tiles ahead of their copies, table entries one
+        // Entries are loaded two of the set's tiles ahead of their copies, table
+        // entries one.  Offsets into the cache are 32-bit numbers of p.unit
+        // bytes.
         Ring st{0u, 0u, static_cast<uint32_t>(S)};
-        int32_t off[kPerLane] = {}, blk[kPerLane] = {}, off1[kPerLane] = {}, blk1[kPerLane] = {}, idx2[kPerLane] = {};
-        Place cur{}, cur1{}, cur2{};
-#pragma unroll 1
-        for (int it = -2; it < total; ++it) {
-          if (it >= -1 && it + 1 < total) load_tables(cur1, off1, blk1);
-          if (it + 2 < total) {
-            if (at == t0 && ae == 0) {
-#pragma unroll 1
-              for (int e = 0; e < live_of(ar); ++e) {
-                const Place c = place_of(ar * NG + e);
-                if (e == 0) units[0] = c; else units[1] = c;
-              }
-            }
-            cur2 = ae == 0 ? units[0] : units[1];
-            load_entries(cur2, at, idx2);
-            if (++ae >= live_of(ar)) {
+        for (int i = 0; i < set; ++i) st.next();
+        int32_t idx1 = -1, blk = -1, off = 0, req1 = 0;
+        uint32_t head = 0, head1 = 0;
+        int opened = -1;
+        int req = 0;  // prefill: the request that the last column was found in
+        int32_t req_lo = 0, req_hi = -1;
+        const auto skip = [&](int n) {
+#pragma unroll
+          for (int i = 0; i < kSets; ++i)
+            if (i < n && ++ae >= live_of(ar)) {
               ae = 0;
               if (++at >= t1) {
                 at = t0;
                 ++ar;
               }
             }
+        };
+        skip(set);
+#pragma unroll 1
+        for (int it = set - 2 * kSets; it < total; it += kSets) {
+          int32_t blk1 = -1, idx2 = -1, req2 = 0, tok = idx1;
+          uint32_t head2 = 0;
+          {  // the next tile's table entries
+            bool ok = tok >= 0;
+            if (p.cu_seq_lens != nullptr) {
+              if (ok && (tok < req_lo || tok >= req_hi)) {
+                int a = 0, b = p.n_req;
+#pragma unroll 1
+                while (b - a > 1) {
+                  const int mid = (a + b) >> 1;
+                  if (__ldg(p.cu_seq_lens + mid) <= tok) a = mid; else b = mid;
+                }
+                req = a;
+                req_lo = __ldg(p.cu_seq_lens + a);
+                req_hi = __ldg(p.cu_seq_lens + a + 1);
+              }
+              ok = ok && tok >= req_lo && tok < req_hi;
+              tok -= req_lo;
+            } else {
+              req = req1;
+            }
+            const int32_t j = tok >> shift;
+            if (ok && j < p.max_blocks) blk1 = load_now(p.block_tables + static_cast<int64_t>(req) * p.bt_stride + j);
+          }
+          if (it + 2 * kSets < total) {  // the entries of the tile after that
+            if (opened != ar) {
+              opened = ar;
+#pragma unroll 1
+              for (int e = 0; e < live_of(ar); ++e) {
+                int row, kvh, h0;
+                unit_of(p, u0 + (ar * NG + e) * ustep, &row, &kvh, &h0, GP);
+                const Place c{p.indices + row * p.idx_stride, row / p.next_n, kvh * p.head_units};
+                if (e == 0) units[0] = c; else units[1] = c;
+              }
+            }
+            const Place c = ae == 0 ? units[0] : units[1];
+            req2 = c.req;
+            head2 = c.head;
+            const int j = at * kAttnTile + tok0 + lane;
+            if (j < p.k) idx2 = load_now(c.idx + j);
+            skip(kSets);
           }
           if (it >= 0) {
-            const uint8_t* src[kPerLane];
-            uint32_t m[kPerLane];
-#pragma unroll
-            for (int r = 0; r < kPerLane; ++r) {
-              const bool ok = blk[r] >= 0 && blk[r] < p.num_blocks;
-              m[r] = __ballot_sync(kFull, ok);
-              src[r] = ok ? cur.head + blk[r] * p.block_stride + off[r] * (2 * D) : g_zero_row;
-            }
+            const bool ok = blk >= 0 && blk < p.num_blocks;
+            const uint32_t m = __ballot_sync(kFull, ok);
+            const uint32_t page = head + static_cast<uint32_t>(blk) * p.block_units;
+            const uint32_t from = page + static_cast<uint32_t>(off) * p.tok_units;
             if (!attn_wait(empty0 + 8u * st.idx, st.phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
-            const uint32_t full = full0 + 8u * st.idx;
+            const uint32_t full = full0 + 8u * st.idx, at_stage = st.idx * kStageBytes;
+            if (ok)
+              ptx::cp_async_8(my_scale + st.idx * (kAttnTile * 8u),
+                              p.kv + static_cast<uint64_t>(page) * p.unit + (p.scale_off + 8 * off));
+            if (lane == 0) my_mask[4 * st.idx] = m;
+            if (m == kFull) {
 #pragma unroll
-            for (int r = 0; r < kPerLane; ++r) {
-              const int tok0 = (pw * kPerLane + r) * 32;
-              const uint32_t dst = kv0 + st.idx * kStageBytes + tok0 * 128u;
-              if (m[r] >> lane & 1u)
-                ptx::cp_async_8(ptx::smem_u32(smem + L.scale) + (st.idx * kAttnTile + tok0 + lane) * 8u,
-                                cur.head + blk[r] * p.block_stride + bs * (2 * D) + 8 * off[r]);
-              if (lane == 0) reinterpret_cast<uint32_t*>(smem + L.mask)[4 * st.idx + pw * kPerLane + r] = m[r];
-              // (addresses first, eight at a time: the exchange's latency is paid once per batch)
-#pragma unroll
-              for (int j0 = 0; j0 < 32; j0 += 8 * kRowsPerCopy) {
-                uint64_t from[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  from[i] = __shfl_sync(kFull, reinterpret_cast<uint64_t>(src[r]), j0 + i * kRowsPerCopy + sub) + piece * 16;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const int j = j0 + i * kRowsPerCopy;
-                  ptx::cp_async_16(dst + place[(j & 7) / kRowsPerCopy] + j * 128u, reinterpret_cast<const void*>(from[i]));
-                }
+              for (int j = 0; j < 32; j += kRowsPerCopy)
+                ptx::cp_async_16(at_stage + place[(j & 7) / kRowsPerCopy] + j * 128u,
+                                 my_piece + static_cast<uint64_t>(__shfl_sync(kFull, from, j + sub)) * p.unit);
+            } else {  // entries without a token copy zeros
+#pragma unroll 1
+              for (int j = 0; j < 32; j += kRowsPerCopy) {
+                const uint32_t f = __shfl_sync(kFull, from, j + sub);
+                const bool valid = m >> (j + sub) & 1u;
+                const uint32_t dst = at_stage + kv0 + (tok0 + j + sub) * 128u + (piece >> 3) * kVOff +
+                                     (((piece ^ (j + sub)) & 7) << 4);
+                ptx::cp_async_16_zfill(dst, valid ? my_piece + static_cast<uint64_t>(f) * p.unit : p.kv, valid ? 16u : 0u);
               }
             }
             ptx::cp_async_mbar_arrive(full);
             if (lane == 0) ptx::mbar_arrive(full);
-            st.next();
+            for (int i = 0; i < kSets; ++i) st.next();
           }
-          cur = cur1;
-          cur1 = cur2;
-#pragma unroll
-          for (int r = 0; r < kPerLane; ++r) blk[r] = blk1[r], off[r] = off1[r], off1[r] = idx2[r];
+          blk = blk1, off = tok & in_page, head = head1;
+          idx1 = idx2, req1 = req2, head1 = head2;
         }
         ptx::cp_async_wait_all();  // (an abandoned call must not leave copies behind)
       }
@@ -498,6 +505,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
                   ptx::mma_f8f6f4(tmem + slot * N2, a + 2ull * kk, b + 2ull * kk, kIdescS, kk > 0 ? 1u : 0u);
                 ptx::mma_commit(sf0 + 8u * slot);
               }
+              // (a tile without entries has no output MMA that follows its scores)
+              ptx::mbar_arrive(empty0 + 8u * stage);
               if (te <= live) ptx::mma_commit(qe0 + 8u * buf);  // the unit's last tile
             } else if (any) {
               // (the accumulator holds the group's last unit until that has been read)
@@ -870,11 +879,11 @@ AttnKernel attn_instance(int gp) {
 cudaError_t launch_sparse_attn(const SparseAttnParams& p, int head_dim, int grid, int ctas,
                                int smem_bytes, cudaStream_t stream) {
   const int gp = attn_pad(p.group);
-  const AttnKernel kern = head_dim == 128 ? (ctas > 1 ? attn_instance<128, true>(gp) : attn_instance<128, false>(gp))
-                                          : (ctas > 1 ? attn_instance<64, true>(gp) : attn_instance<64, false>(gp));
+  const AttnKernel kern = head_dim == 128 ? (ctas > 0 ? attn_instance<128, true>(gp) : attn_instance<128, false>(gp))
+                                          : (ctas > 0 ? attn_instance<64, true>(gp) : attn_instance<64, false>(gp));
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem_bytes);
   if (e != cudaSuccess) return e;
-  if (ctas == 1) {
+  if (ctas == 0) {
     kern<<<grid, kAttnThreads, smem_bytes, stream>>>(p);
     return cudaGetLastError();
   }
