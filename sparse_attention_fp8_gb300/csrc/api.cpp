@@ -1068,8 +1068,7 @@ fp8idx_status sparse_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, 
     }
   }
   const int grid = cs == 0 ? std::min(p.units, dev.sms) : p.units * cs;
-  p.stages = attn_stages((int)D, gp, dev.smem_optin);
-  const int smem = (int)attn_smem_layout((int)D, gp, p.stages).total;
+  const int smem = (int)attn_smem_layout((int)D, gp).total;
   if (smem > dev.smem_optin) return fail(FP8IDX_ERR_UNSUPPORTED, "sparse attention: shared memory too small");
   cudaError_t e = launch_sparse_attn(p, (int)D, grid, cs, smem, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(FP8IDX_ERR_CUDA, "sparse attention launch: %s", cudaGetErrorString(e));

@@ -77,15 +77,14 @@ struct SparseAttnParams {
   int32_t head_chunks;          // chunks of attn_pad(group) heads that share a key head
   int32_t units;                // rows * kv_heads * head_chunks
   int32_t tiles;                // 128-entry tiles per row
-  int32_t stages;
 };
 constexpr int kAttnMaxK = 2048;
 constexpr int kAttnMaxGroup = 128;
 constexpr int kAttnMaxCtas = 8;   // CTAs per unit (portable cluster size)
 constexpr int kAttnTile = 128;    // selected tokens per MMA tile (MMA M of the scores, K of the outputs)
-constexpr int kAttnMaxStages = 8;
-// Query heads of a unit, padded to a width that P's rows can be swizzled over.
-__host__ __device__ constexpr int attn_pad(int group) { return group <= 16 ? 16 : group <= 32 ? 32 : 64; }
+// Query heads of a unit, padded; a larger group is several units, each with
+// its own copy of the tiles (64 heads' sums would not fit in the registers).
+__host__ __device__ constexpr int attn_pad(int group) { return group <= 16 ? 16 : 32; }
 // Roles: two epilogue warpgroups; two sets of four producer warps; the warps
 // that issue the scores and each group's outputs; the query warp.
 constexpr int kAttnGroups = 2;
@@ -94,36 +93,39 @@ constexpr int kAttnThreads = 32 * (4 * kAttnGroups + 4 * kAttnProducerSets + 2 +
 // Registers a thread after the launch's 96 have been dealt anew:
 // 256 * 144 + 384 * 64 = 640 * 96.
 constexpr int kAttnEpilogueRegs = 144, kAttnOtherRegs = 64;
-// Per group: accumulators of S^T (tensor memory's 512 columns hold them and
-// one of O^T, 2*GP each).  Query buffers: units in work and the next ones.
-__host__ __device__ constexpr int attn_score_buffers(int gp) { return gp <= 32 ? 2 : 1; }
-__host__ __device__ constexpr int attn_query_buffers(int gp) { return gp <= 32 ? 4 : 3; }
+// Query buffers: the units in work and the next one.
+constexpr int kAttnQueryBuffers = kAttnGroups + 1;
+// Tiles in flight, even numbers (two producer sets).  head_dim 128: a key
+// half of a stage is free once its scores are computed, a value half only
+// after the softmax and the output MMA, so they are rings of their own;
+// head_dim 64 keeps both in one row of 128 bytes.  As many as fit next to
+// the queries and probabilities.
+constexpr uint32_t kAttnHalfBytes = kAttnTile * 128u;
+__host__ __device__ constexpr int attn_k_stages(int head_dim) { return head_dim == 128 ? 4 : 0; }
+__host__ __device__ constexpr int attn_v_stages(int head_dim, int gp) {
+  return head_dim == 64 || gp == 16 ? 8 : 6;
+}
 struct AttnSmem {
-  uint32_t kv, q, p, scale, mask, flt, bars, misc, total;
+  uint32_t k, v, q, p, scale, mask, flt, bars, misc, total;
 };
 // Floats of the softmax state of one CTA, GP heads (AttnState in sparse_attn.cu).
 __host__ __device__ constexpr int attn_state_floats(int gp) { return 24 * gp + 32; }
-__host__ __device__ inline AttnSmem attn_smem_layout(int head_dim, int gp, int stages) {
-  AttnSmem L;
+__host__ __device__ constexpr AttnSmem attn_smem_layout(int head_dim, int gp) {
+  AttnSmem L{};
+  const uint32_t stages = static_cast<uint32_t>(attn_v_stages(head_dim, gp));
   uint32_t off = 0;
-  L.kv = off;    off += static_cast<uint32_t>(stages) * kAttnTile * 2u * head_dim;  // key tile, value tile
-  L.q = off;     off += attn_query_buffers(gp) * 2u * gp * 128u;  // 2*gp rows of 128 bytes
+  L.k = off;     off += attn_k_stages(head_dim) * kAttnHalfBytes;
+  L.v = off;     off += stages * kAttnHalfBytes;
+  L.q = off;     off += kAttnQueryBuffers * 2u * gp * 128u;  // 2*gp rows of 128 bytes
   L.p = off;     off += kAttnGroups * kAttnTile * 2u * gp;  // a tile of probabilities per group
-  L.scale = off; off += static_cast<uint32_t>(stages) * kAttnTile * 8u;
-  L.mask = off;  off += static_cast<uint32_t>(stages) * 16u;
+  L.scale = off; off += stages * kAttnTile * 8u;
+  L.mask = off;  off += stages * 16u;
   L.flt = off;   off += 4u * attn_state_floats(gp);
   off = (off + 15u) & ~15u;
-  L.bars = off;  off += 8u * (2u * kAttnMaxStages + 28u);
+  L.bars = off;  off += 8u * 64u;
   L.misc = off;  off += 32u;
   L.total = off + 1024u;
   return L;
-}
-// As many stages as shared memory holds, a multiple of the producer sets.
-__host__ inline int attn_stages(int head_dim, int gp, int smem_limit) {
-  int s = kAttnMaxStages / kAttnProducerSets * kAttnProducerSets;
-  while (s > kAttnProducerSets && static_cast<int>(attn_smem_layout(head_dim, gp, s).total) > smem_limit)
-    s -= kAttnProducerSets;
-  return s;
 }
 // ctas 0: persistent CTAs, a unit per epilogue group; 1 .. 8: a cluster of so
 // many CTAs per unit, which share its tiles.

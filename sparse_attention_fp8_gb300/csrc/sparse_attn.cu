@@ -3,12 +3,12 @@
 //
 //   s[h, j] = softmax_scale * <q[h], K[i_j]>,  out[h] = sum_j softmax(s)[h, j] V[i_j]
 //
-// A unit of work is (row, key head, up to 64 of its query heads); its entries
+// A unit of work is (row, key head, up to 32 of its query heads); its entries
 // are taken in tiles of 128 tokens.  Both products of a tile run on the fp8
 // tensor cores straight from the cache's bytes:
 //   S^T [128 tokens x 2 GP] = K tile (A, K-major) * [Qh; Ql]^T
 //   O^T [128 channels x 2 GP] += V tile^T (A, MN-major) * [Ph | Pl] (B, MN-major)
-// GP is the head count padded to 16, 32 or 64.  The 16-bit operands are split
+// GP is the head count padded to 16 or 32.  The 16-bit operands are split
 // into two e4m3 values: x = h + l / 16 with h = e4m3(x), l = e4m3(16 (x - h)).
 // That keeps 8 significant bits -- a bf16 query exactly, a probability to
 // 2^-8 -- down to 2^-21 of the largest query element (queries are scaled by a
@@ -66,8 +66,13 @@ static __device__ unsigned int g_attn_watchdog;
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr float kLazy = 2.f;          // log2 of how far a score may pass m before m is set anew
-constexpr float kPScale = 32.f;       // factor of P's e4m3 codes
+// P's codes reach from 448 (the largest e4m3 value) down to steps of 2^-13
+// (the smallest one of the second part).  A probability over m may grow to
+// kMaxP and a value scale to kMaxW times the one in hand before both are
+// taken anew, at m = the largest score + kMargin: with normally distributed
+// scores a unit of 2048 entries then does that once, at its first tile.
+constexpr float kMaxP = 4.f, kMaxW = 1.25f, kPScale = 89.6f;  // 4 * 1.25 * 89.6 = 448
+constexpr float kMargin = 1.4854268f;  // log2(89.6 / 32): a step is 2^-18 of the largest probability
 constexpr float kMinVScale = 0x1p-120f;
 constexpr float kMinM = -3e38f;       // m stays finite, so that a score of -inf gives probability 0
 
@@ -90,6 +95,14 @@ __device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(kFull, ok);
 }
 
+// Two at once: one round of tests in the usual case that both are complete.
+__device__ __forceinline__ bool attn_wait2(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
+                                           volatile uint32_t* abort_flag, uint32_t site0, uint32_t site1) {
+  const bool a = ptx::mbar_test_wait(bar0, parity0), b = ptx::mbar_test_wait(bar1, parity1);
+  if (__all_sync(kFull, a && b)) return true;
+  return attn_wait(bar0, parity0, abort_flag, site0) && attn_wait(bar1, parity1, abort_flag, site1);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -102,8 +115,7 @@ struct AttnState {
   float nm[NG][GP];            // -m of each group (log2 units), 0 before a unit's first tile
   float ninf[GP];              // -inf: the row of -m that an entry without a token reads
   float part[NG][4][GP];       // [group][warp]: a tile's maxima over m; a unit's sums
-  float delta[NG][GP];         // what m grows by
-  float resc[NG][GP];          // 2^-delta
+  float resc[NG][GP];          // a new maximum: 2^-(what m grows by)
   float fac[NG][GP];           // a unit's end: factor of the accumulator
   float xm[NG][GP], xl[NG][GP];  // cluster: the group's maximum and sum per head
   float cref[NG], cfac[NG];
@@ -177,10 +189,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
   constexpr int kSWarp = kProdWarp0 + kProdWarps, kOWarp0 = kSWarp + 1, kQWarp = kOWarp0 + NG;
   static_assert(32 * (kQWarp + 1) == kAttnThreads, "roles");
   constexpr int N2 = 2 * GP;                       // columns of S^T and O^T
-  constexpr int SBG = attn_score_buffers(GP);      // accumulators of S^T per group
-  constexpr int QB = attn_query_buffers(GP);
-  constexpr uint32_t kStageBytes = kAttnTile * 2u * D;
-  constexpr uint32_t kVOff = D == 128 ? kAttnTile * 128u : 0u;  // D = 64: key and value share a 128-byte row
+  constexpr int SBG = 2;                           // accumulators of S^T per group
+  constexpr int QB = kAttnQueryBuffers;
+  constexpr int KS = attn_k_stages(D), S = attn_v_stages(D, GP);  // D = 64: keys and values share the rows of S
   constexpr uint32_t kTmemCols = pow2_at_least(NG * (SBG + 1) * N2);
   constexpr uint32_t kTmemO = NG * SBG * N2;       // O^T of group g at kTmemO + g * N2
   using State = AttnState<GP, NG, QB>;
@@ -188,13 +199,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_up_1024(smem_raw);
-  const AttnSmem L = attn_smem_layout(D, GP, p.stages);
-  const int S = p.stages;
+  constexpr AttnSmem L = attn_smem_layout(D, GP);
+  static_assert(L.total <= kMaxSmem, "shared memory");
   State& stt = *reinterpret_cast<State*>(smem + L.flt);
-  const uint32_t kv0 = ptx::smem_u32(smem + L.kv);
+  const uint32_t k0 = ptx::smem_u32(smem + L.k), v0 = ptx::smem_u32(smem + L.v);
   const uint32_t q0 = ptx::smem_u32(smem + L.q);
-  const uint32_t full0 = ptx::smem_u32(smem + L.bars), empty0 = full0 + 8u * kAttnMaxStages;
-  const uint32_t qf0 = empty0 + 8u * kAttnMaxStages, qe0 = qf0 + 8u * QB;     // query buffers
+  const uint32_t full0 = ptx::smem_u32(smem + L.bars), empty0 = full0 + 8u * S;
+  const uint32_t ke0 = empty0 + 8u * S;                                       // keys' scores computed
+  const uint32_t qf0 = ke0 + 8u * KS, qe0 = qf0 + 8u * QB;                    // query buffers
   const uint32_t sf0 = qe0 + 8u * QB, se0 = sf0 + 8u * NG * SBG;              // [group][accumulator] scores ready, read
   const uint32_t pf0 = se0 + 8u * NG * SBG, pe0 = pf0 + 8u * NG;              // [group] probabilities ready, used
   const uint32_t oe0 = pe0 + 8u * NG;                                         // [group] a unit's outputs read
@@ -209,6 +221,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       ptx::mbar_init(full0 + 8u * s, 33u * 4u);        // each producer lane's copies, each warp's mask
       ptx::mbar_init(empty0 + 8u * s, 1u + 1u + 4u);     // both MMA warps, the tile's epilogue warps
     }
+    for (int s = 0; s < KS; ++s) ptx::mbar_init(ke0 + 8u * s, 1u);
     for (int i = 0; i < QB; ++i) {
       ptx::mbar_init(qf0 + 8u * i, 1u);
       ptx::mbar_init(qe0 + 8u * i, 1u + 4u);             // the last score MMA, the unit's epilogue warps
@@ -285,8 +298,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       uint32_t place[8 / kRowsPerCopy];
 #pragma unroll
       for (int i = 0; i < 8 / kRowsPerCopy; ++i)
-        place[i] = kv0 + tok0 * 128 + (piece >> 3) * kVOff + sub * 128 +
-                   (((piece & 7) ^ ((i * kRowsPerCopy + sub) & 7)) << 4);
+        place[i] = (tok0 + sub) * 128 + (((piece & 7) ^ ((i * kRowsPerCopy + sub) & 7)) << 4);
       const uint8_t* const my_piece = p.kv + piece * 16;
       const uint32_t my_scale = ptx::smem_u32(smem + L.scale) + (tok0 + lane) * 8u;
       uint32_t* const my_mask = reinterpret_cast<uint32_t*>(smem + L.mask) + (tok0 >> 5);
@@ -295,8 +307,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         // Entries are loaded two of the set's tiles ahead of their copies, table
         // entries one.  Offsets into the cache are 32-bit numbers of p.unit
         // bytes.
-        Ring st{0u, 0u, static_cast<uint32_t>(S)};
-        for (int i = 0; i < set; ++i) st.next();
+        Ring st{0u, 0u, static_cast<uint32_t>(S)}, kst{0u, 0u, static_cast<uint32_t>(KS)};
+        for (int i = 0; i < set; ++i) {
+          st.next();
+          kst.next();
+        }
         int32_t idx1 = -1, blk = -1, off = 0, req1 = 0;
         uint32_t head = 0, head1 = 0;
         int opened = -1;
@@ -364,7 +379,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
             const uint32_t page = head + static_cast<uint32_t>(blk) * p.block_units;
             const uint32_t from = page + static_cast<uint32_t>(off) * p.tok_units;
             if (!attn_wait(empty0 + 8u * st.idx, st.phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
-            const uint32_t full = full0 + 8u * st.idx, at_stage = st.idx * kStageBytes;
+            if (KS > 0 && !attn_wait(ke0 + 8u * kst.idx, kst.phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
+            const uint32_t full = full0 + 8u * st.idx;
+            const uint32_t at_stage = KS > 0 && piece < 8 ? k0 + kst.idx * kAttnHalfBytes : v0 + st.idx * kAttnHalfBytes;
             if (ok)
               ptx::cp_async_8(my_scale + st.idx * (kAttnTile * 8u),
                               p.kv + static_cast<uint64_t>(page) * p.unit + (p.scale_off + 8 * off));
@@ -379,14 +396,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
               for (int j = 0; j < 32; j += kRowsPerCopy) {
                 const uint32_t f = __shfl_sync(kFull, from, j + sub);
                 const bool valid = m >> (j + sub) & 1u;
-                const uint32_t dst = at_stage + kv0 + (tok0 + j + sub) * 128u + (piece >> 3) * kVOff +
-                                     (((piece ^ (j + sub)) & 7) << 4);
+                const uint32_t dst = at_stage + (tok0 + j + sub) * 128u + (((piece ^ (j + sub)) & 7) << 4);
                 ptx::cp_async_16_zfill(dst, valid ? my_piece + static_cast<uint64_t>(f) * p.unit : p.kv, valid ? 16u : 0u);
               }
             }
             ptx::cp_async_mbar_arrive(full);
             if (lane == 0) ptx::mbar_arrive(full);
-            for (int i = 0; i < kSets; ++i) st.next();
+            for (int i = 0; i < kSets; ++i) {
+              st.next();
+              kst.next();
+            }
           }
           blk = blk1, off = tok & in_page, head = head1;
           idx1 = idx2, req1 = req2, head1 = head2;
@@ -405,49 +424,50 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row / p.next_n * p.q_req_stride +
                                  row % p.next_n * p.q_row_stride + (kvh * p.group + h0) * p.q_head_stride;
         constexpr int kPer = D / 8;  // 16-byte pieces per head
-        float amax = 0.f;
-#pragma unroll 2
+        // The largest element's exponent, from the elements' bits: bf16 values
+        // without their sign are ordered as integers; infinities and NaN (from
+        // 0x7F80) do not count.
+        uint32_t top = 0, odd = 0;
+#pragma unroll 8
         for (int c = lane; c < nh * kPer; c += 32) {
           const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + c / kPer * p.q_head_stride + c % kPer * 8));
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float a = fabsf(__uint_as_float(w[k] << 16)), b = fabsf(__uint_as_float(w[k] & 0xFFFF0000u));
-            if (a < INFINITY) amax = fmaxf(amax, a);
-            if (b < INFINITY) amax = fmaxf(amax, b);
+            const uint32_t m = w[k] & 0x7FFF7FFFu;
+            const uint32_t special = __vcmpgeu2(m, 0x7F807F80u);
+            odd |= special;
+            top = __vmaxu2(top, m & ~special);
           }
         }
-        amax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(amax)));
+        top = __reduce_max_sync(kFull, max(top >> 16, top & 0xFFFFu));
+        odd = __any_sync(kFull, odd != 0u);
         // 2^e puts the largest finite element into [128, 256)
-        int e = 134 - static_cast<int>(__float_as_uint(amax) >> 23);
-        e = amax == 0.f ? 0 : min(max(e, -120), 120);
+        int e = 134 - static_cast<int>(top >> 7);
+        e = top == 0u ? 0 : min(max(e, -120), 120);
         const float mul = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
         uint8_t* dst = smem + L.q + buf * N2 * 128;
-#pragma unroll 1
+#pragma unroll 4
         for (int c = lane; c < GP * kPer; c += 32) {
           const int g = c / kPer, piece = c % kPer;
-          uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-          if (g < nh) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + g * p.q_head_stride + piece * 8));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (g < nh) v = __ldg(reinterpret_cast<const uint4*>(q + g * p.q_head_stride + piece * 8));
+          uint32_t w[4] = {v.x, v.y, v.z, v.w}, h[4], l[4];
+          if (odd) {  // an infinity becomes NaN: as a code it would be the largest value
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float a = __uint_as_float(w[k] << 16) * mul, b = __uint_as_float(w[k] & 0xFFFF0000u) * mul;
-              if (isinf(a)) a = NAN;  // (an infinity must not become the largest code)
-              if (isinf(b)) b = NAN;
-              const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-              const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-              const __nv_fp8x2_storage_t l = __nv_cvt_float2_to_fp8x2(
-                  make_float2(16.f * (a - back.x), 16.f * (b - back.y)), __NV_SATFINITE, __NV_E4M3);
-              hi[k >> 1] |= static_cast<uint32_t>(h) << (16 * (k & 1));
-              lo[k >> 1] |= static_cast<uint32_t>(l) << (16 * (k & 1));
-            }
+            for (int k = 0; k < 4; ++k) w[k] |= __vcmpeq2(w[k] & 0x7FFF7FFFu, 0x7F807F80u) & 0x7FFF7FFFu;
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            split_pair(__floats2half2_rn(__uint_as_float(w[k] << 16) * mul, __uint_as_float(w[k] & 0xFFFF0000u) * mul),
+                       &h[k], &l[k]);
           // rows of 128 bytes in the 128-byte swizzle (16-byte chunks)
           const int chunk = piece >> 1, half = (piece & 1) * 8;
           const int r1 = g, r2 = GP + g;
-          *reinterpret_cast<uint2*>(dst + r1 * 128 + ((chunk ^ (r1 & 7)) << 4) + half) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(dst + r2 * 128 + ((chunk ^ (r2 & 7)) << 4) + half) = make_uint2(lo[0], lo[1]);
+          *reinterpret_cast<uint2*>(dst + r1 * 128 + ((chunk ^ (r1 & 7)) << 4) + half) =
+              make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+          *reinterpret_cast<uint2*>(dst + r2 * 128 + ((chunk ^ (r2 & 7)) << 4) + half) =
+              make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
         }
         if (lane == 0) stt.qf[buf] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         ptx::fence_proxy_async_smem();
@@ -463,14 +483,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       if (lane == 0) {
         constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(kAttnTile, N2);
         constexpr uint32_t kIdescO = ptx::idesc_e4m3_f32(128, N2) | ptx::kIdescMnMajorA | ptx::kIdescMnMajorB;
-        const uint64_t a0 = scores ? ptx::smem_desc_sw128(kv0) : ptx::smem_desc_mn(kv0 + kVOff, 128);
+        const uint64_t a0 = scores ? ptx::smem_desc_sw128(KS > 0 ? k0 : v0) : ptx::smem_desc_mn(v0, 128);
         const uint64_t b0 =
             scores ? ptx::smem_desc_sw128(q0) : ptx::smem_desc_mn(ptx::smem_u32(smem + L.p) + og * kAttnTile * N2, N2);
         const auto await = [&](uint32_t bar, uint32_t parity, uint32_t site) {
           return wait_bounded(bar, parity, abort_flag, &g_attn_watchdog, site);
         };
-        Ring st{0u, 0u, static_cast<uint32_t>(S)};
-        uint32_t n0 = 0, n1 = 0;      // tiles with entries (scores: per group; outputs: n0)
+        Ring st{0u, 0u, static_cast<uint32_t>(S)}, kst{0u, 0u, static_cast<uint32_t>(KS > 0 ? KS : S)};
+        uint32_t n0 = 0, n1 = 0;      // tiles (scores: per group; outputs: n0 with entries)
         int turn = 0;
         bool okay = true;
 #pragma unroll 1
@@ -479,8 +499,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
           bool first = true;          // outputs: the unit's first tile starts the accumulator anew
 #pragma unroll 1
           for (int te = (t1 - t0) * live, e = 0; te > 0; --te, e = e + 1 == live ? 0 : e + 1) {
-            const uint32_t stage = st.idx, stage_phase = st.phase;
+            const uint32_t stage = st.idx, stage_phase = st.phase, k_stage = kst.idx;
             st.next();
+            kst.next();
             const int g = CLUSTER ? turn : e;
             turn = turn + 1 == NG ? 0 : turn + 1;
             if (!scores && g != og) continue;
@@ -488,25 +509,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
             if (!okay) break;
             const uint4 m = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * stage);
             const bool any = (m.x | m.y | m.z | m.w) != 0u;
-            const uint64_t a = a0 + static_cast<uint64_t>(stage * (kStageBytes >> 4));
+            const uint64_t a = a0 + static_cast<uint64_t>((scores ? k_stage : stage) * (kAttnHalfBytes >> 4));
             ptx::fence_proxy_async_smem();  // the tile was written by cp.async
             if (scores) {
               const int unit = CLUSTER ? 0 : r * NG + e, buf = unit % QB;
+              const uint32_t c = g == 0 ? n0++ : n1++;
+              const uint32_t slot = g * SBG + (c & 1u), parity = (c >> 1) & 1u;
+              okay = await(qf0 + 8u * buf, (unit / QB) & 1, kSiteQFull) &&
+                     await(se0 + 8u * slot, parity ^ 1u, kSiteAccEmpty);
+              if (!okay) break;
               if (any) {
-                const uint32_t c = g == 0 ? n0++ : n1++;
-                const uint32_t slot = g * SBG + (SBG == 2 ? c & 1u : 0u), parity = (SBG == 2 ? c >> 1 : c) & 1u;
-                okay = await(qf0 + 8u * buf, (unit / QB) & 1, kSiteQFull) &&
-                       await(se0 + 8u * slot, parity ^ 1u, kSiteAccEmpty);
-                if (!okay) break;
                 ptx::tc_fence_after();
                 const uint64_t b = b0 + static_cast<uint64_t>(buf * (N2 * 128u >> 4));
 #pragma unroll
                 for (int kk = 0; kk < D / 32; ++kk)
                   ptx::mma_f8f6f4(tmem + slot * N2, a + 2ull * kk, b + 2ull * kk, kIdescS, kk > 0 ? 1u : 0u);
-                ptx::mma_commit(sf0 + 8u * slot);
               }
+              ptx::mma_commit(sf0 + 8u * slot);
               // (a tile without entries has no output MMA that follows its scores)
               ptx::mbar_arrive(empty0 + 8u * stage);
+              if (KS > 0) ptx::mma_commit(ke0 + 8u * k_stage);
               if (te <= live) ptx::mma_commit(qe0 + 8u * buf);  // the unit's last tile
             } else if (any) {
               // (the accumulator holds the group's last unit until that has been read)
@@ -544,18 +566,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     const uint32_t o_tm = tmem + kTmemO + g * N2 + lane_off;
     uint8_t* p_row = smem + L.p + g * kAttnTile * N2 + tg * N2;
     // 16-byte chunks of a row of probabilities, swizzled over its N2 bytes
-    const uint32_t p_swz = N2 == 128 ? tg & 7 : N2 == 64 ? (tg >> 1) & 3 : (tg >> 2) & 1;
+    const uint32_t p_swz = N2 == 64 ? (tg >> 1) & 3 : (tg >> 2) & 1;
     const int bar_id = 1 + g;
-    // With at most 32 heads the scores stay in registers from the test
-    // against m to the probabilities, and their accumulator goes back at
-    // once; with 64 they are read again, 32 heads at a time.
-    constexpr bool kKeep = GP <= 32;
-    constexpr int CH = kKeep ? GP : 32;
     Ring st{0u, 0u, static_cast<uint32_t>(S)};
-    uint32_t n_tile = 0;                              // this group's tiles with entries
+    uint32_t n_own = 0, n_tile = 0;                   // this group's tiles, those with entries
     int turn = 0;
     bool stop = false;
-    float tv[CH];                                     // scores over m, log2 units
 #pragma unroll 1
     for (int r = 0; r < rounds && !stop; ++r) {
       const int live = live_of(r);
@@ -584,7 +600,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         if (++e == live) e = 0;
         if (!mine) continue;
         asm volatile("" : "+r"(has_o));  // (one copy of the loop: the first tile is not peeled off)
-        ok = attn_wait(full0 + 8u * stage, stage_phase, abort_flag, kSiteStageFull) && ok;
+        const uint32_t slot = g * SBG + (n_own & 1u), slot_parity = (n_own >> 1) & 1u;
+        ++n_own;
+        ok = attn_wait2(full0 + 8u * stage, stage_phase, sf0 + 8u * slot, slot_parity, abort_flag, kSiteStageFull,
+                        kSiteAccFull) && ok;
         const uint4 mk = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * stage);
         const bool any = (mk.x | mk.y | mk.z | mk.w) != 0u;
         const uint32_t mw = quad == 0 ? mk.x : quad == 1 ? mk.y : quad == 2 ? mk.z : mk.w;
@@ -595,72 +614,91 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         const float c = valid ? sc.x * qscale : 0.f;
         const float vs = valid ? fmaxf(sc.y, 0.f) : 0.f;
         const float4* nm4 = reinterpret_cast<const float4*>(valid ? stt.nm[g] : stt.ninf);
-        const uint32_t slot = g * SBG + (SBG == 2 ? n_tile & 1u : 0u);
         const uint32_t s_tm = tmem + slot * N2 + lane_off;
-        // scores of heads b .. b+CH-1 over the present m, and their maximum
-        const auto scores = [&](int b) {
+        ptx::tc_fence_after();
+        // scores of heads b .. b+15 over the present m, in log2 units
+        const auto scores = [&](int b, float (&t)[16]) {
           const float2 c2 = make_float2(c, c), k16 = make_float2(0.0625f, 0.0625f);
-          float top = -INFINITY;
+          uint32_t hi[16], lo[16];
+          ptx::tmem_ld_32x32b_x16(s_tm + b, hi);
+          ptx::tmem_ld_32x32b_x16(s_tm + GP + b, lo);
+          ptx::tmem_wait_ld_n(hi);
+          ptx::tmem_wait_ld_n(lo);
 #pragma unroll
-          for (int b2 = 0; b2 < CH; b2 += 16) {
-            uint32_t hi[16], lo[16];
-            ptx::tmem_ld_32x32b_x16(s_tm + b + b2, hi);
-            ptx::tmem_ld_32x32b_x16(s_tm + GP + b + b2, lo);
-            ptx::tmem_wait_ld_n(hi);
-            ptx::tmem_wait_ld_n(lo);
+          for (int j = 0; j < 16; j += 4) {
+            const float4 nm = nm4[(b + j) / 4];
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 nm = nm4[(b + b2 + j) / 4];
-#pragma unroll
-              for (int k = 0; k < 4; k += 2) {
-                const float2 raw = __ffma2_rn(make_float2(__uint_as_float(lo[j + k]), __uint_as_float(lo[j + k + 1])), k16,
-                                              make_float2(__uint_as_float(hi[j + k]), __uint_as_float(hi[j + k + 1])));
-                const float2 t2 = __ffma2_rn(raw, c2, k == 0 ? make_float2(nm.x, nm.y) : make_float2(nm.z, nm.w));
-                tv[b2 + j + k] = t2.x;
-                tv[b2 + j + k + 1] = t2.y;
-                top = fmaxf(top, fmaxf(t2.x, t2.y));
-              }
+            for (int k = 0; k < 4; k += 2) {
+              const float2 raw = __ffma2_rn(make_float2(__uint_as_float(lo[j + k]), __uint_as_float(lo[j + k + 1])), k16,
+                                            make_float2(__uint_as_float(hi[j + k]), __uint_as_float(hi[j + k + 1])));
+              const float2 t2 = __ffma2_rn(raw, c2, k == 0 ? make_float2(nm.x, nm.y) : make_float2(nm.z, nm.w));
+              t[j + k] = t2.x;
+              t[j + k + 1] = t2.y;
             }
           }
-          return top;
         };
-        bool again = false;
-        if (any) {
-          ok = attn_wait(sf0 + 8u * slot, (SBG == 2 ? n_tile >> 1 : n_tile) & 1u, abort_flag, kSiteAccFull) && ok;
-          ptx::tc_fence_after();
-          float top = scores(0);
-          if constexpr (kKeep) {
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(se0 + 8u * slot);
-          } else {
+        // The probabilities are computed and stored against the m in hand; if
+        // one of them shows that m is too small (or m is not set yet), the
+        // group takes the maxima and does them over.
+        ok = attn_wait(pe0 + 8u * g, (n_tile & 1u) ^ 1u, abort_flag, kSiteAccEmpty) && ok;  // P is free
 #pragma unroll 1
-            for (int b = CH; b < GP; b += CH) top = fmaxf(top, scores(b));
+        for (bool fresh = false;; fresh = true) {
+          bool again = any && !fresh && (!has_o || vs > kMaxW * cref);
+          if (any && (has_o || fresh)) {
+            const float w = vs * __fdividef(kPScale, cref);
+            const __half2 w2 = __floats2half2_rn(w, w);
+            __half2 top = __floats2half2_rn(0.f, 0.f);
+#pragma unroll
+            for (int b = 0; b < GP; b += 16) {
+              float t[16];
+              scores(b, t);
+              uint32_t ph[4], pl[4];
+#pragma unroll
+              for (int j = 0; j < 16; j += 4) {
+                uint32_t hc[2], lc[2];
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                  const float2 e = make_float2(ex2(t[j + k]), ex2(t[j + k + 1]));
+                  float2& l = l2[(b + j + k) / 2];
+                  l = __fadd2_rn(l, e);
+                  const __half2 h2 = __floats2half2_rn(e.x, e.y);  // (11 bits; above 65504 infinite, which is caught)
+                  top = __hmax2(top, h2);
+                  split_pair(__hmul2(h2, w2), &hc[k / 2], &lc[k / 2]);
+                }
+                ph[j / 4] = hc[0] | hc[1] << 16;
+                pl[j / 4] = lc[0] | lc[1] << 16;
+              }
+              *reinterpret_cast<uint4*>(p_row + (((b / 16) ^ p_swz) << 4)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+              *reinterpret_cast<uint4*>(p_row + ((((GP + b) / 16) ^ p_swz) << 4)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+            }
+            again = again || (!fresh && !__hble2(top, __floats2half2_rn(kMaxP, kMaxP)));
           }
-          again = !has_o || top > kLazy || vs > 2.f * cref;  // the first tile of a unit sets m
-        }
-        if (ptx::bar_or(bar_id, 128, again || !ok)) {
-          // ---- new maxima (or the end of an abandoned call)
-          if (ptx::bar_or(bar_id, 128, !ok)) {
+          if (!ptx::bar_or(bar_id, 128, again || !ok)) break;
+          if (ptx::bar_or(bar_id, 128, !ok)) {  // an abandoned call: all four warps leave
             stop = true;
             break;
           }
-#pragma unroll 1
-          for (int b = 0; b < GP; b += CH) {
-            if (!kKeep) scores(b);
-            float v[CH];
+          // ---- new maxima
+          {
+            float v[GP];
 #pragma unroll
-            for (int j = 0; j < CH; ++j) v[j] = tv[j];
-            const float top = reduce_columns<CH, true>(v, lane);
-            if (lane < CH) stt.part[g][quad][b + lane] = top;
+            for (int b = 0; b < GP; b += 16) scores(b, *reinterpret_cast<float(*)[16]>(&v[b]));
+            if (has_o) {  // take the tile's sums back (what a huge one leaves is nothing beside it)
+#pragma unroll
+              for (int j = 0; j < GP / 2; ++j) {
+                const float ex = ex2(v[2 * j]), ey = ex2(v[2 * j + 1]);
+                l2[j] = make_float2(ex < 0x1p100f ? l2[j].x - ex : 0.f, ey < 0x1p100f ? l2[j].y - ey : 0.f);
+              }
+            }
+            const float t = reduce_columns<GP, true>(v, lane);
+            if (lane < GP) stt.part[g][quad][lane] = t;
           }
           const float vmax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vs)));
           if (lane == 0) stt.wvs[g][quad] = vmax;
           ptx::bar_sync(bar_id, 128);
           if (tg < GP) {
             float d = fmaxf(fmaxf(stt.part[g][0][tg], stt.part[g][1][tg]), fmaxf(stt.part[g][2][tg], stt.part[g][3][tg]));
-            d = fmaxf(d, has_o ? 0.f : kMinM);
-            stt.delta[g][tg] = d;
+            d = fmaxf(d, has_o ? -kMargin : kMinM) + kMargin;
             stt.resc[g][tg] = ex2(-d);
             stt.nm[g][tg] -= d;
           }
@@ -672,22 +710,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
           }
           ptx::bar_sync(bar_id, 128);
           cref = stt.cref[g];
-          if constexpr (kKeep) {
-#pragma unroll
-            for (int j = 0; j < GP; j += 4) {
-              const float4 d = *reinterpret_cast<const float4*>(&stt.delta[g][j]);
-              tv[j] -= d.x, tv[j + 1] -= d.y, tv[j + 2] -= d.z, tv[j + 3] -= d.w;
-            }
-          }
-          if (has_o) {
+          if (has_o) {  // (P was free: the group's last output MMA is done)
 #pragma unroll
             for (int j = 0; j < GP / 2; ++j) {
               const float2 f = *reinterpret_cast<const float2*>(&stt.resc[g][2 * j]);
               l2[j] = make_float2(l2[j].x * f.x, l2[j].y * f.y);
             }
-            // the group's last output MMA is done before its sums are scaled
-            ok = attn_wait(pe0 + 8u * g, (n_tile & 1u) ^ 1u, abort_flag, kSiteAccEmpty) && ok;
-            ptx::tc_fence_after();
             const float cf = stt.cfac[g];
 #pragma unroll 1
             for (int b = 0; b < N2; b += 16) {
@@ -702,42 +730,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
             ptx::tmem_wait_st();
           }
         }
-        if (!any) continue;
-        // ---- probabilities; P is free once the group's last output MMA is done
-        ok = attn_wait(pe0 + 8u * g, (n_tile & 1u) ^ 1u, abort_flag, kSiteAccEmpty) && ok;
-        const float w = vs * __fdividef(kPScale, cref);
-        const float2 w2 = make_float2(w, w);
-#pragma unroll
-        for (int b = 0; b < GP; b += CH) {
-          if (!kKeep) scores(b);
-#pragma unroll
-          for (int b2 = 0; b2 < CH; b2 += 16) {
-            uint32_t ph[4], pl[4];
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              uint32_t hc[2], lc[2];
-#pragma unroll
-              for (int k = 0; k < 4; k += 2) {
-                const int at = b2 + j + k;
-                const float2 e2 = make_float2(ex2(tv[at]), ex2(tv[at + 1]));
-                float2& l = l2[(b + at) / 2];
-                l = __fadd2_rn(l, e2);
-                const float2 pw = __fmul2_rn(e2, w2);
-                split_pair(__floats2half2_rn(pw.x, pw.y), &hc[k / 2], &lc[k / 2]);
-              }
-              ph[j / 4] = hc[0] | hc[1] << 16;
-              pl[j / 4] = lc[0] | lc[1] << 16;
-            }
-            *reinterpret_cast<uint4*>(p_row + ((((b + b2) / 16) ^ p_swz) << 4)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-            *reinterpret_cast<uint4*>(p_row + ((((GP + b + b2) / 16) ^ p_swz) << 4)) =
-                make_uint4(pl[0], pl[1], pl[2], pl[3]);
-          }
+        if (stop) break;
+        ptx::tc_fence_before();
+        if (!any) {
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(se0 + 8u * slot);
+          continue;
         }
         ptx::fence_proxy_async_smem();
-        ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (!kKeep) ptx::mbar_arrive(se0 + 8u * slot);
+          ptx::mbar_arrive(se0 + 8u * slot);
           ptx::mbar_arrive(pf0 + 8u * g);
         }
         has_o = 1u;
@@ -748,13 +751,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       // ---- the unit's end: the sums over the group's tokens, and the output
       if (has_o) attn_wait(pe0 + 8u * g, (n_tile & 1u) ^ 1u, abort_flag, kSiteAccEmpty);
       ptx::tc_fence_after();
+      {
+        float v[GP];
 #pragma unroll
-      for (int b = 0; b < GP; b += CH) {
-        float v[CH];
-#pragma unroll
-        for (int j = 0; j < CH; j += 2) v[j] = l2[(b + j) / 2].x, v[j + 1] = l2[(b + j) / 2].y;
-        const float sum = reduce_columns<CH, false>(v, lane);
-        if (lane < CH) stt.part[g][quad][b + lane] = sum;
+        for (int j = 0; j < GP; j += 2) v[j] = l2[j / 2].x, v[j + 1] = l2[j / 2].y;
+        const float sum = reduce_columns<GP, false>(v, lane);
+        if (lane < GP) stt.part[g][quad][lane] = sum;
       }
       ptx::bar_sync(bar_id, 128);
       int row, kvh, h0;
@@ -784,7 +786,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       const int ch = D == 128 ? tg : tg - 64;  // D = 64: the value half of the shared rows
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row / p.next_n * p.out_req_stride +
                            row % p.next_n * p.out_row_stride + (kvh * p.group + h0) * p.out_head_stride + ch;
-      float* xo = reinterpret_cast<float*>(smem + L.kv) + g * GP * 128 + tg;  // cluster: [group][GP][128]
+      float* xo = reinterpret_cast<float*>(smem + L.k) + g * GP * 128 + tg;  // cluster: [group][GP][128]
 #pragma unroll 1
       for (int b = 0; b < GP; b += 8) {
         float v[8];
@@ -831,7 +833,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       const int nh = min(GP, p.group - h0);
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row / p.next_n * p.out_req_stride +
                            row % p.next_n * p.out_row_stride + (kvh * p.group + h0) * p.out_head_stride + ch;
-      const float* xo = reinterpret_cast<const float*>(smem + L.kv) + tg;
+      const float* xo = reinterpret_cast<const float*>(smem + L.k) + tg;
       const int h_end = min(nh, (crank + 1) * GP / C);
 #pragma unroll 1
       for (int h = crank * GP / C + half; h < h_end; h += NG) {
@@ -870,9 +872,7 @@ namespace {
 using AttnKernel = void (*)(SparseAttnParams);
 template <int D, bool CLUSTER>
 AttnKernel attn_instance(int gp) {
-  return gp == 16   ? sparse_attn_kernel<D, 16, CLUSTER>
-         : gp == 32 ? sparse_attn_kernel<D, 32, CLUSTER>
-                    : sparse_attn_kernel<D, 64, CLUSTER>;
+  return gp == 16 ? sparse_attn_kernel<D, 16, CLUSTER> : sparse_attn_kernel<D, 32, CLUSTER>;
 }
 }  // namespace
 
