@@ -936,7 +936,7 @@ fp8idx_status paged_store_impl(const fp8idx_tensor* k, const fp8idx_tensor* v, c
     if (kv->shape[0] * bs >= (1ll << 31)) return fail(FP8IDX_ERR_UNSUPPORTED, "store: slots must stay below 2^31");
     p.block_stride = kv->shape[1];
   }
-  if (T * H * (v ? 2 : 1) * (D / 8) >= (1ll << 38))
+  if (T * H * (v ? 2 : 1) >= (1ll << 31) - 4096)
     return fail(FP8IDX_ERR_UNSUPPORTED, "store: %lld tokens of %lld heads in one call", (long long)T, (long long)H);
   if (T == 0 || H == 0) return ok();
   p.slots = static_cast<const int32_t*>(slots->data);
@@ -944,10 +944,20 @@ fp8idx_status paged_store_impl(const fp8idx_tensor* k, const fp8idx_tensor* v, c
   p.num_slots = kv->shape[0] * bs;
   p.tokens = T;
   p.heads = (int32_t)H;
-  p.block_size = (int32_t)bs;
+  while ((1 << p.block_shift) < bs) ++p.block_shift;
+  // rows are numbered below 2^31: with s = ceil(log2 d), row / d is
+  // row * ceil(2^(31+s) / d) >> (31 + s)
+  const uint64_t d = (uint64_t)H * (v ? 2 : 1);
+  p.div_shift = -1;
+  if (d > 1) {
+    int s = 1;
+    while ((1ull << s) < d) ++s;
+    p.div_mul = (uint32_t)(((1ull << (31 + s)) + d - 1) / d);
+    p.div_shift = s - 1;
+  }
   DeviceInfo dev;
   TRY(device_info(&dev));
-  cudaError_t e = launch_paged_store(p, type, (int)D, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_paged_store(p, type, (int)D, dev.sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(FP8IDX_ERR_CUDA, "store launch: %s", cudaGetErrorString(e));
   return ok();
 }

@@ -48,9 +48,11 @@ struct PagedStoreParams {
   int64_t num_slots;           // num_blocks * block_size
   int64_t tokens;
   int32_t heads;
-  int32_t block_size;
+  int32_t block_shift;         // log2(block_size)
+  uint32_t div_mul;            // row / (heads * parts) as a product: (row * div_mul >> 32) >> div_shift
+  int32_t div_shift;           // -1: the divisor is 1
 };
-cudaError_t launch_paged_store(const PagedStoreParams& p, int row_type, int head_dim, cudaStream_t stream);
+cudaError_t launch_paged_store(const PagedStoreParams& p, int row_type, int head_dim, int sms, cudaStream_t stream);
 
 // ------------------------------------------------------- sparse attention
 struct SparseAttnParams {
