@@ -180,6 +180,50 @@ __device__ __forceinline__ void split_pair(__half2 x, uint32_t* h, uint32_t* l) 
   *l = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
 }
 
+// The query's split: every element times 2^e, which puts the unit's largest
+// finite one into [128, 256), as two e4m3 values.
+struct QueryScale {
+  uint32_t top;  // the largest element's bits without its sign (bf16 values are then ordered as integers)
+  bool odd;      // infinities or NaN among them (from 0x7F80; they do not count)
+  __device__ __forceinline__ void add(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m2 = 0, s2 = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t m = w[k] & 0x7FFF7FFFu, special = __vcmpgeu2(m, 0x7F807F80u);
+      s2 |= special;
+      m2 = __vmaxu2(m2, m & ~special);
+    }
+    top = max(top, max(m2 >> 16, m2 & 0xFFFFu));
+    odd |= s2 != 0u;
+  }
+  __device__ __forceinline__ int exponent() const {
+    const int e = 134 - static_cast<int>(top >> 7);
+    return top == 0u ? 0 : min(max(e, -120), 120);
+  }
+};
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// Eight elements of head g (16-byte piece `piece` of its row) into the two
+// parts' rows: 128 bytes each, 128-byte swizzle.
+template <int GP>
+__device__ __forceinline__ void store_query(uint8_t* dst, int g, int piece, const uint4& v, float mul, bool odd) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w}, h[4], l[4];
+  if (odd) {  // an infinity becomes NaN: as a code it would be the largest value
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] |= __vcmpeq2(w[k] & 0x7FFF7FFFu, 0x7F807F80u) & 0x7FFF7FFFu;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    split_pair(__floats2half2_rn(__uint_as_float(w[k] << 16) * mul, __uint_as_float(w[k] & 0xFFFF0000u) * mul), &h[k],
+               &l[k]);
+  const int chunk = piece >> 1, half = (piece & 1) * 8, r1 = g, r2 = GP + g;
+  *reinterpret_cast<uint2*>(dst + r1 * 128 + ((chunk ^ (r1 & 7)) << 4) + half) =
+      make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  *reinterpret_cast<uint2*>(dst + r2 * 128 + ((chunk ^ (r2 & 7)) << 4) + half) =
+      make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+
 }  // namespace
 
 template <int D, int GP, bool CLUSTER>
@@ -223,7 +267,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     }
     for (int s = 0; s < KS; ++s) ptx::mbar_init(ke0 + 8u * s, 1u);
     for (int i = 0; i < QB; ++i) {
-      ptx::mbar_init(qf0 + 8u * i, 1u);
+      ptx::mbar_init(qf0 + 8u * i, CLUSTER ? 4u * NG : 1u);
       ptx::mbar_init(qe0 + 8u * i, 1u + 4u);             // the last score MMA, the unit's epilogue warps
     }
     for (int i = 0; i < NG * SBG; ++i) {
@@ -415,7 +459,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     } else if (warp == kQWarp) {
       // =========================== queries =============================
 #pragma unroll 1
-      for (int i = 0; i < n_units && t0 < t1; ++i) {
+      for (int i = 0; !CLUSTER && i < n_units; ++i) {  // (a cluster's epilogue warps do it)
         const int buf = i % QB;
         int row, kvh, h0;
         unit_of(p, u0 + i * ustep, &row, &kvh, &h0, GP);
@@ -424,52 +468,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row / p.next_n * p.q_req_stride +
                                  row % p.next_n * p.q_row_stride + (kvh * p.group + h0) * p.q_head_stride;
         constexpr int kPer = D / 8;  // 16-byte pieces per head
-        // The largest element's exponent, from the elements' bits: bf16 values
-        // without their sign are ordered as integers; infinities and NaN (from
-        // 0x7F80) do not count.
-        uint32_t top = 0, odd = 0;
+        QueryScale qs{0u, false};
 #pragma unroll 8
-        for (int c = lane; c < nh * kPer; c += 32) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + c / kPer * p.q_head_stride + c % kPer * 8));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t m = w[k] & 0x7FFF7FFFu;
-            const uint32_t special = __vcmpgeu2(m, 0x7F807F80u);
-            odd |= special;
-            top = __vmaxu2(top, m & ~special);
-          }
-        }
-        top = __reduce_max_sync(kFull, max(top >> 16, top & 0xFFFFu));
-        odd = __any_sync(kFull, odd != 0u);
-        // 2^e puts the largest finite element into [128, 256)
-        int e = 134 - static_cast<int>(top >> 7);
-        e = top == 0u ? 0 : min(max(e, -120), 120);
-        const float mul = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        uint8_t* dst = smem + L.q + buf * N2 * 128;
+        for (int c = lane; c < nh * kPer; c += 32)
+          qs.add(__ldg(reinterpret_cast<const uint4*>(q + c / kPer * p.q_head_stride + c % kPer * 8)));
+        qs.top = __reduce_max_sync(kFull, qs.top);
+        qs.odd = __any_sync(kFull, qs.odd);
+        const int e = qs.exponent();
 #pragma unroll 4
         for (int c = lane; c < GP * kPer; c += 32) {
           const int g = c / kPer, piece = c % kPer;
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
           if (g < nh) v = __ldg(reinterpret_cast<const uint4*>(q + g * p.q_head_stride + piece * 8));
-          uint32_t w[4] = {v.x, v.y, v.z, v.w}, h[4], l[4];
-          if (odd) {  // an infinity becomes NaN: as a code it would be the largest value
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] |= __vcmpeq2(w[k] & 0x7FFF7FFFu, 0x7F807F80u) & 0x7FFF7FFFu;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            split_pair(__floats2half2_rn(__uint_as_float(w[k] << 16) * mul, __uint_as_float(w[k] & 0xFFFF0000u) * mul),
-                       &h[k], &l[k]);
-          // rows of 128 bytes in the 128-byte swizzle (16-byte chunks)
-          const int chunk = piece >> 1, half = (piece & 1) * 8;
-          const int r1 = g, r2 = GP + g;
-          *reinterpret_cast<uint2*>(dst + r1 * 128 + ((chunk ^ (r1 & 7)) << 4) + half) =
-              make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-          *reinterpret_cast<uint2*>(dst + r2 * 128 + ((chunk ^ (r2 & 7)) << 4) + half) =
-              make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+          store_query<GP>(smem + L.q + buf * N2 * 128, g, piece, v, power_of_two(e), qs.odd);
         }
-        if (lane == 0) stt.qf[buf] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        if (lane == 0) stt.qf[buf] = power_of_two(-e);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(qf0 + 8u * buf);
@@ -572,6 +585,45 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     uint32_t n_own = 0, n_tile = 0;                   // this group's tiles, those with entries
     int turn = 0;
     bool stop = false;
+    if (CLUSTER && t0 < t1) {
+      // The unit's query: nothing else is to be done yet, and 256 threads have
+      // it ready by the time the first tile is.
+      int row, kvh, h0;
+      unit_of(p, u0, &row, &kvh, &h0, GP);
+      const int nh = min(GP, p.group - h0);
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row / p.next_n * p.q_req_stride +
+                               row % p.next_n * p.q_row_stride + (kvh * p.group + h0) * p.q_head_stride;
+      constexpr int kPer = D / 8, kPieces = (GP * kPer + 255) / 256;
+      uint4 v[kPieces];
+      QueryScale qs{0u, false};
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int c = static_cast<int>(threadIdx.x) + 256 * i;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (c < nh * kPer) v[i] = __ldg(reinterpret_cast<const uint4*>(q + c / kPer * p.q_head_stride + c % kPer * 8));
+        qs.add(v[i]);
+      }
+      const uint32_t both = __reduce_max_sync(kFull, qs.top) | (__any_sync(kFull, qs.odd) ? 0x10000u : 0u);
+      if (lane == 0) stt.part[0][0][warp] = __uint_as_float(both);
+      ptx::bar_sync(1 + NG, 4 * NG * 32);
+      qs.top = 0u;
+#pragma unroll
+      for (int w = 0; w < 4 * NG; ++w) {
+        const uint32_t x = __float_as_uint(stt.part[0][0][w]);
+        qs.top = max(qs.top, x & 0xFFFFu);
+        qs.odd |= x >> 16 != 0u;
+      }
+      const int e = qs.exponent();
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int c = static_cast<int>(threadIdx.x) + 256 * i;
+        if (c < GP * kPer) store_query<GP>(smem + L.q, c / kPer, c % kPer, v[i], power_of_two(e), qs.odd);
+      }
+      if (threadIdx.x == 0) stt.qf[0] = power_of_two(-e);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(qf0);
+    }
 #pragma unroll 1
     for (int r = 0; r < rounds && !stop; ++r) {
       const int live = live_of(r);
@@ -767,7 +819,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         const float m = has_o ? -stt.nm[g][tg] : kMinM;
         stt.nm[g][tg] = 0.f;
         if constexpr (CLUSTER) {
-          stt.fac[g][tg] = has_o ? cref * (1.f / kPScale) : 0.f;
+          stt.fac[g][tg] = has_o ? __fdividef(cref, kPScale) : 0.f;
           stt.xm[g][tg] = m;
           stt.xl[g][tg] = sum;
         } else {
@@ -825,35 +877,44 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     cg::cluster_group cl = cg::this_cluster();
     __syncwarp();
     cl.sync();
-    if (warp < 4 * NG) {
-      const int tg = threadIdx.x & 127, half = threadIdx.x >> 7;
-      const int ch = D == 128 ? tg : tg - 64;
+    const int R = C * NG, heads = GP / C, first = crank * heads;  // partial results, heads of this CTA
+    if (warp < 4 * NG) {  // (the others have few registers left)
       int row, kvh, h0;
       unit_of(p, u0, &row, &kvh, &h0, GP);
       const int nh = min(GP, p.group - h0);
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row / p.next_n * p.out_req_stride +
-                           row % p.next_n * p.out_row_stride + (kvh * p.group + h0) * p.out_head_stride + ch;
-      const float* xo = reinterpret_cast<const float*>(smem + L.k) + tg;
-      const int h_end = min(nh, (crank + 1) * GP / C);
-#pragma unroll 1
-      for (int h = crank * GP / C + half; h < h_end; h += NG) {
-        float m = kMinM;
-#pragma unroll 1
-        for (int r = 0; r < C * NG; ++r) {
-          const float x = *cl.map_shared_rank(&stt.xm[r % NG][h], r / NG);
-          m = (x > m || x != x) ? x : m;
+      // thread (head, r), r fastest: the factor of partial result r
+      if (threadIdx.x < GP * NG) {
+        const int r = static_cast<int>(threadIdx.x) % R, h = first + static_cast<int>(threadIdx.x) / R;
+        const float m_r = *cl.map_shared_rank(&stt.xm[r % NG][h], r / NG);
+        const float l_r = *cl.map_shared_rank(&stt.xl[r % NG][h], r / NG);
+        const uint32_t lanes = GP * NG < 32 ? (1u << (GP * NG % 32)) - 1u : kFull;
+        float m = m_r;
+        bool nan = m_r != m_r;
+        for (int d = R / 2; d > 0; d >>= 1) {
+          m = fmaxf(m, __shfl_xor_sync(lanes, m, d));
+          nan |= __shfl_xor_sync(lanes, nan, d);
         }
-        float sum = 0.f, v = 0.f;
-#pragma unroll 2
-        for (int r = 0; r < C * NG; ++r) {
-          const float f = ex2(*cl.map_shared_rank(&stt.xm[r % NG][h], r / NG) - m);
-          sum = fmaf(f, *cl.map_shared_rank(&stt.xl[r % NG][h], r / NG), sum);
-          v = fmaf(f, *cl.map_shared_rank(const_cast<float*>(xo) + (r % NG * GP + h) * 128, r / NG), v);
-        }
-        if (ch >= 0) out[h * p.out_head_stride] = __float2bfloat16(sum == 0.f ? 0.f : v / sum);
-        if (p.lse != nullptr && tg == 0)
+        const float f = nan ? NAN : ex2(m_r - m);
+        float sum = f * l_r;
+        for (int d = R / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(lanes, sum, d);
+        (&stt.fac[0][0])[threadIdx.x] = sum == 0.f ? 0.f : __fdividef(f, sum);
+        if (p.lse != nullptr && r == 0 && h < nh)
           p.lse[static_cast<int64_t>(row) * p.heads + kvh * p.group + h0 + h] =
               sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+      }
+      ptx::bar_sync(1 + NG, 4 * NG * 32);
+      const int tg = threadIdx.x & 127, ch = D == 128 ? tg : tg - 64;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row / p.next_n * p.out_req_stride +
+                           row % p.next_n * p.out_row_stride + (kvh * p.group + h0) * p.out_head_stride + ch;
+      float* const xo = reinterpret_cast<float*>(smem + L.k) + tg;
+#pragma unroll 4
+      for (int i = static_cast<int>(threadIdx.x) >> 7; i < heads; i += NG) {
+        const int h = first + i;
+        float v = 0.f;
+#pragma unroll 2
+        for (int r = 0; r < R; ++r)
+          v = fmaf((&stt.fac[0][0])[i * R + r], *cl.map_shared_rank(xo + (r % NG * GP + h) * 128, r / NG), v);
+        if (h < nh && ch >= 0) out[h * p.out_head_stride] = __float2bfloat16(v);
       }
     }
     __syncwarp();
