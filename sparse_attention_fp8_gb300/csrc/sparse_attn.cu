@@ -253,8 +253,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
   const uint32_t qf0 = ke0 + 8u * KS, qe0 = qf0 + 8u * QB;                    // query buffers
   const uint32_t sf0 = qe0 + 8u * QB, se0 = sf0 + 8u * NG * SBG;              // [group][accumulator] scores ready, read
   const uint32_t pf0 = se0 + 8u * NG * SBG, pe0 = pf0 + 8u * NG;              // [group] probabilities ready, used
-  const uint32_t oe0 = pe0 + 8u * NG;                                         // [group] a unit's outputs read
-  const uint32_t ub = oe0 + 8u * NG, drain0 = ub + 8u;                        // cluster: both groups done; [MMA warp]
+  const uint32_t ub = pe0 + 8u * NG, drain0 = ub + 8u;                        // cluster: both groups done; [MMA warp]
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L.misc);
   volatile uint32_t* abort_flag = misc + 1;
 
@@ -277,7 +276,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     for (int g = 0; g < NG; ++g) {
       ptx::mbar_init(pf0 + 8u * g, 4u);
       ptx::mbar_init(pe0 + 8u * g, 1u);
-      ptx::mbar_init(oe0 + 8u * g, 4u);
     }
     ptx::mbar_init(ub, 4u * NG);
     for (int i = 0; i < 1 + NG; ++i) ptx::mbar_init(drain0 + 8u * i, 1u);
@@ -490,83 +488,110 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     } else {
       // ============================= MMA ===============================
       // A warp for the scores and one per group for its outputs, so that no
-      // product waits for another one's operands; lane 0 issues.
+      // product waits for another one's operands.  The whole warp walks the
+      // tiles (its values stay uniform), one lane issues.
       const bool scores = warp == kSWarp;
       const int og = warp - kOWarp0;
-      if (lane == 0) {
-        constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(kAttnTile, N2);
-        constexpr uint32_t kIdescO = ptx::idesc_e4m3_f32(128, N2) | ptx::kIdescMnMajorA | ptx::kIdescMnMajorB;
-        const uint64_t a0 = scores ? ptx::smem_desc_sw128(KS > 0 ? k0 : v0) : ptx::smem_desc_mn(v0, 128);
-        const uint64_t b0 =
-            scores ? ptx::smem_desc_sw128(q0) : ptx::smem_desc_mn(ptx::smem_u32(smem + L.p) + og * kAttnTile * N2, N2);
-        const auto await = [&](uint32_t bar, uint32_t parity, uint32_t site) {
-          return wait_bounded(bar, parity, abort_flag, &g_attn_watchdog, site);
-        };
+      constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(kAttnTile, N2);
+      constexpr uint32_t kIdescO = ptx::idesc_e4m3_f32(128, N2) | ptx::kIdescMnMajorA | ptx::kIdescMnMajorB;
+      if (scores) {
+        const uint64_t a0 = ptx::smem_desc_sw128(KS > 0 ? k0 : v0), b0 = ptx::smem_desc_sw128(q0);
         Ring st{0u, 0u, static_cast<uint32_t>(S)}, kst{0u, 0u, static_cast<uint32_t>(KS > 0 ? KS : S)};
-        uint32_t n0 = 0, n1 = 0;      // tiles (scores: per group; outputs: n0 with entries)
+        uint32_t n0 = 0, n1 = 0;      // tiles per group
         int turn = 0;
         bool okay = true;
 #pragma unroll 1
         for (int r = 0; r < rounds && okay; ++r) {
           const int live = live_of(r);
-          bool first = true;          // outputs: the unit's first tile starts the accumulator anew
 #pragma unroll 1
-          for (int te = (t1 - t0) * live, e = 0; te > 0; --te, e = e + 1 == live ? 0 : e + 1) {
-            const uint32_t stage = st.idx, stage_phase = st.phase, k_stage = kst.idx;
-            st.next();
-            kst.next();
+          for (int te = (t1 - t0) * live, left = te, e = 0; te > 0; --te, e = e + 1 == live ? 0 : e + 1) {
             const int g = CLUSTER ? turn : e;
             turn = turn + 1 == NG ? 0 : turn + 1;
-            if (!scores && g != og) continue;
-            okay = await(full0 + 8u * stage, stage_phase, kSiteStageFull);
+            const int buf = CLUSTER ? 0 : (r * NG + e) % QB;
+            if (left - te < live && !CLUSTER || te == left)  // a unit's first tile
+              okay = attn_wait(qf0 + 8u * buf, CLUSTER ? 0 : ((r * NG + e) / QB) & 1, abort_flag, kSiteQFull);
+            const uint32_t c = g == 0 ? n0++ : n1++;
+            const uint32_t slot = g * SBG + (c & 1u), parity = (c >> 1) & 1u;
+            okay = okay && attn_wait2(full0 + 8u * st.idx, st.phase, se0 + 8u * slot, parity ^ 1u, abort_flag,
+                                      kSiteStageFull, kSiteAccEmpty);
             if (!okay) break;
-            const uint4 m = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * stage);
+            const uint4 m = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * st.idx);
             const bool any = (m.x | m.y | m.z | m.w) != 0u;
-            const uint64_t a = a0 + static_cast<uint64_t>((scores ? k_stage : stage) * (kAttnHalfBytes >> 4));
             ptx::fence_proxy_async_smem();  // the tile was written by cp.async
-            if (scores) {
-              const int unit = CLUSTER ? 0 : r * NG + e, buf = unit % QB;
-              const uint32_t c = g == 0 ? n0++ : n1++;
-              const uint32_t slot = g * SBG + (c & 1u), parity = (c >> 1) & 1u;
-              okay = await(qf0 + 8u * buf, (unit / QB) & 1, kSiteQFull) &&
-                     await(se0 + 8u * slot, parity ^ 1u, kSiteAccEmpty);
-              if (!okay) break;
+            ptx::tc_fence_after();
+            const uint32_t a_stage = KS > 0 ? kst.idx : st.idx;
+            const uint64_t a = a0 + static_cast<uint64_t>(a_stage * (kAttnHalfBytes >> 4));
+            const uint64_t b = b0 + static_cast<uint64_t>(buf * (N2 * 128u >> 4));
+            if (ptx::elect_one()) {
               if (any) {
-                ptx::tc_fence_after();
-                const uint64_t b = b0 + static_cast<uint64_t>(buf * (N2 * 128u >> 4));
 #pragma unroll
                 for (int kk = 0; kk < D / 32; ++kk)
                   ptx::mma_f8f6f4(tmem + slot * N2, a + 2ull * kk, b + 2ull * kk, kIdescS, kk > 0 ? 1u : 0u);
               }
               ptx::mma_commit(sf0 + 8u * slot);
+              if (KS > 0) ptx::mma_commit(ke0 + 8u * kst.idx);
               // (a tile without entries has no output MMA that follows its scores)
-              ptx::mbar_arrive(empty0 + 8u * stage);
-              if (KS > 0) ptx::mma_commit(ke0 + 8u * k_stage);
+              ptx::mbar_arrive(empty0 + 8u * st.idx);
               if (te <= live) ptx::mma_commit(qe0 + 8u * buf);  // the unit's last tile
-            } else if (any) {
-              // (the accumulator holds the group's last unit until that has been read)
-              okay = (!first || r == 0 || await(oe0 + 8u * g, (r - 1) & 1, kSiteAccEmpty)) &&
-                     await(pf0 + 8u * g, n0 & 1u, kSiteAccFull);
-              if (!okay) break;
-              ++n0;
-              ptx::tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < kAttnTile / 32; ++kk)
-                ptx::mma_f8f6f4(tmem + kTmemO + g * N2, a + kk * (32ull * 128 >> 4), b0 + kk * (32ull * N2 >> 4), kIdescO,
-                                (first && kk == 0) ? 0u : 1u);
-              ptx::mma_commit(pe0 + 8u * g);
-              ptx::mma_commit(empty0 + 8u * stage);
-              first = false;
-            } else {
-              ptx::mbar_arrive(empty0 + 8u * stage);
             }
+            __syncwarp();
+            st.next();
+            kst.next();
           }
         }
-        if (*abort_flag) {
-          const uint32_t bar = drain0 + 8u * (warp - kSWarp);
-          ptx::mma_commit(bar);
-          wait_drain(bar, 0, &g_attn_watchdog);
+      } else {
+        const uint64_t a0 = ptx::smem_desc_mn(v0, 128);
+        const uint64_t b0 = ptx::smem_desc_mn(ptx::smem_u32(smem + L.p) + og * kAttnTile * N2, N2);
+        Ring st{0u, 0u, static_cast<uint32_t>(S)};
+        uint32_t n = 0;               // the group's tiles with entries
+        int turn = 0;
+        bool okay = true;
+#pragma unroll 1
+        for (int r = 0; r < rounds && okay; ++r) {
+          const int live = live_of(r);
+          bool first = true;          // the unit's first tile starts the accumulator anew
+#pragma unroll 1
+          for (int te = (t1 - t0) * live, e = 0; te > 0; --te, e = e + 1 == live ? 0 : e + 1) {
+            const uint32_t stage = st.idx, stage_phase = st.phase;
+            st.next();
+            const int g = CLUSTER ? turn : e;
+            turn = turn + 1 == NG ? 0 : turn + 1;
+            if (g != og) continue;
+            okay = attn_wait(full0 + 8u * stage, stage_phase, abort_flag, kSiteStageFull);
+            if (!okay) break;
+            const uint4 m = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * stage);
+            const bool any = (m.x | m.y | m.z | m.w) != 0u;
+            ptx::fence_proxy_async_smem();  // the tile was written by cp.async
+            const uint64_t a = a0 + static_cast<uint64_t>(stage * (kAttnHalfBytes >> 4));
+            if (any) {
+              // (the group makes its next unit's first probabilities after it has read the last unit's outputs)
+              okay = attn_wait(pf0 + 8u * og, n & 1u, abort_flag, kSiteAccFull);
+              if (!okay) break;
+              ++n;
+              ptx::tc_fence_after();
+            }
+            if (ptx::elect_one()) {
+              if (any) {
+#pragma unroll
+                for (int kk = 0; kk < kAttnTile / 32; ++kk)
+                  ptx::mma_f8f6f4(tmem + kTmemO + og * N2, a + kk * (32ull * 128 >> 4), b0 + kk * (32ull * N2 >> 4), kIdescO,
+                                  (first && kk == 0) ? 0u : 1u);
+                ptx::mma_commit(pe0 + 8u * og);
+                ptx::mma_commit(empty0 + 8u * stage);
+              } else {
+                ptx::mbar_arrive(empty0 + 8u * stage);
+              }
+            }
+            __syncwarp();
+            if (any) first = false;
+          }
         }
+      }
+      __syncwarp();
+      if (*abort_flag && lane == 0) {
+        const uint32_t bar = drain0 + 8u * (warp - kSWarp);
+        ptx::mma_commit(bar);
+        wait_drain(bar, 0, &g_attn_watchdog);
       }
       __syncwarp();
     }
@@ -866,17 +891,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
           }
         }
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(oe0 + 8u * g);
+      ptx::tc_fence_before();  // (ordered before the barrier of the next unit's first probabilities)
     }
   }
 
   if constexpr (CLUSTER) {
     // ---- the groups of every CTA meet: CTA r finishes heads [r*GP/C, (r+1)*GP/C)
     cg::cluster_group cl = cg::this_cluster();
-    __syncwarp();
-    cl.sync();
+    const auto meet = [&] {
+      __syncwarp();
+      if (C > 1) cl.sync(); else __syncthreads();
+    };
+    meet();
     const int R = C * NG, heads = GP / C, first = crank * heads;  // partial results, heads of this CTA
     if (warp < 4 * NG) {  // (the others have few registers left)
       int row, kvh, h0;
@@ -903,22 +929,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
               sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
       }
       ptx::bar_sync(1 + NG, 4 * NG * 32);
-      const int tg = threadIdx.x & 127, ch = D == 128 ? tg : tg - 64;
+      // a warp per head, four channels a lane
+      const int ch = 4 * lane - (D == 128 ? 0 : 64);
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row / p.next_n * p.out_req_stride +
                            row % p.next_n * p.out_row_stride + (kvh * p.group + h0) * p.out_head_stride + ch;
-      float* const xo = reinterpret_cast<float*>(smem + L.k) + tg;
-#pragma unroll 4
-      for (int i = static_cast<int>(threadIdx.x) >> 7; i < heads; i += NG) {
+      const uint32_t xo = ptx::smem_u32(smem + L.k) + 16u * lane;
+#pragma unroll 1
+      for (int i = warp; i < heads; i += 4 * NG) {
         const int h = first + i;
-        float v = 0.f;
-#pragma unroll 2
-        for (int r = 0; r < R; ++r)
-          v = fmaf((&stt.fac[0][0])[i * R + r], *cl.map_shared_rank(xo + (r % NG * GP + h) * 128, r / NG), v);
-        if (h < nh && ch >= 0) out[h * p.out_head_stride] = __float2bfloat16(v);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int r = 0; r < R; ++r) {
+          const float f = (&stt.fac[0][0])[i * R + r];
+          const float4 x = ptx::ld_cluster_f4(ptx::map_rank(xo + (r % NG * GP + h) * 512u, r / NG));
+          v = make_float4(fmaf(f, x.x, v.x), fmaf(f, x.y, v.y), fmaf(f, x.z, v.z), fmaf(f, x.w, v.w));
+        }
+        if (h < nh && ch >= 0) {
+          __nv_bfloat16* o = out + h * p.out_head_stride;
+          o[0] = __float2bfloat16(v.x), o[1] = __float2bfloat16(v.y);
+          o[2] = __float2bfloat16(v.z), o[3] = __float2bfloat16(v.w);
+        }
       }
     }
-    __syncwarp();
-    cl.sync();  // no CTA leaves while another reads its shared memory
+    meet();  // no CTA leaves while another reads its shared memory
   }
 
   ptx::tc_fence_before();
