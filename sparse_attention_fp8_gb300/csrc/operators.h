@@ -87,17 +87,17 @@ constexpr int kAttnTile = 128;    // selected tokens per MMA tile (MMA M of the 
 // Query heads of a unit, padded; a larger group is several units, each with
 // its own copy of the tiles (64 heads' sums would not fit in the registers).
 __host__ __device__ constexpr int attn_pad(int group) { return group <= 16 ? 16 : 32; }
-// Roles: two epilogue warpgroups; two sets of four producer warps; the warps
-// that issue the scores and each group's outputs; the query warp.
+// Roles: two epilogue warpgroups, each with four producer warps and a warp that
+// issues its products; the query warp (and an idle one: register
+// shares go by groups of four warps).
 constexpr int kAttnGroups = 2;
-constexpr int kAttnProducerSets = 2;
-constexpr int kAttnThreads = 32 * (4 * kAttnGroups + 4 * kAttnProducerSets + 2 + kAttnGroups);
+constexpr int kAttnThreads = 32 * (4 * kAttnGroups + 4 * kAttnGroups + kAttnGroups + 2);
 // Registers a thread after the launch's 96 have been dealt anew:
 // 256 * 144 + 384 * 64 = 640 * 96.
 constexpr int kAttnEpilogueRegs = 144, kAttnOtherRegs = 64;
 // Query buffers: the units in work and the next one.
 constexpr int kAttnQueryBuffers = kAttnGroups + 1;
-// Tiles in flight, even numbers (two producer sets).  head_dim 128: a key
+// Tiles in flight, half of them a group's.  head_dim 128: a key
 // half of a stage is free once its scores are computed, a value half only
 // after the softmax and the output MMA, so they are rings of their own;
 // head_dim 64 keeps both in one row of 128 bytes.  As many as fit next to

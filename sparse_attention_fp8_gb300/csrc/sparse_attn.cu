@@ -229,13 +229,15 @@ __device__ __forceinline__ void store_query(uint8_t* dst, int g, int piece, cons
 template <int D, int GP, bool CLUSTER>
 __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __grid_constant__ SparseAttnParams p) {
   constexpr int NG = kAttnGroups;
-  constexpr int kProdWarp0 = 4 * NG, kProdWarps = 4 * kAttnProducerSets;
-  constexpr int kSWarp = kProdWarp0 + kProdWarps, kOWarp0 = kSWarp + 1, kQWarp = kOWarp0 + NG;
-  static_assert(32 * (kQWarp + 1) == kAttnThreads, "roles");
+  constexpr int kProdWarp0 = 4 * NG, kProdWarps = 4 * NG;
+  constexpr int kMmaWarp0 = kProdWarp0 + kProdWarps, kQWarp = kMmaWarp0 + NG;
+  static_assert(32 * (kQWarp + 1) <= kAttnThreads, "roles");
   constexpr int N2 = 2 * GP;                       // columns of S^T and O^T
   constexpr int SBG = 2;                           // accumulators of S^T per group
   constexpr int QB = kAttnQueryBuffers;
   constexpr int KS = attn_k_stages(D), S = attn_v_stages(D, GP);  // D = 64: keys and values share the rows of S
+  constexpr int KSG = KS > 0 ? KS / NG : 1, SG = S / NG;         // a group's share
+  static_assert(KS % NG == 0 && S % NG == 0, "stages");
   constexpr uint32_t kTmemCols = pow2_at_least(NG * (SBG + 1) * N2);
   constexpr uint32_t kTmemO = NG * SBG * N2;       // O^T of group g at kTmemO + g * N2
   using State = AttnState<GP, NG, QB>;
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     misc[1] = 0u;
     for (int s = 0; s < S; ++s) {
       ptx::mbar_init(full0 + 8u * s, 33u * 4u);        // each producer lane's copies, each warp's mask
-      ptx::mbar_init(empty0 + 8u * s, 1u + 1u + 4u);     // both MMA warps, the tile's epilogue warps
+      ptx::mbar_init(empty0 + 8u * s, 1u + 4u);          // the output MMA, the tile's epilogue warps
     }
     for (int s = 0; s < KS; ++s) ptx::mbar_init(ke0 + 8u * s, 1u);
     for (int i = 0; i < QB; ++i) {
@@ -278,12 +280,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       ptx::mbar_init(pe0 + 8u * g, 1u);
     }
     ptx::mbar_init(ub, 4u * NG);
-    for (int i = 0; i < 1 + NG; ++i) ptx::mbar_init(drain0 + 8u * i, 1u);
+    for (int i = 0; i < NG; ++i) ptx::mbar_init(drain0 + 8u * i, 1u);
     ptx::fence_barrier_init();
   }
   for (int g = threadIdx.x; g < GP; g += kAttnThreads) stt.ninf[g] = -INFINITY;
   for (int g = threadIdx.x; g < NG * GP; g += kAttnThreads) stt.nm[g / GP][g % GP] = 0.f;
-  if (warp == kSWarp) {
+  if (warp == kMmaWarp0) {
     ptx::tmem_alloc(ptx::smem_u32(misc), kTmemCols);
     ptx::tmem_relinquish();
   }
@@ -292,10 +294,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
   ptx::tc_fence_after();
   const uint32_t tmem = misc[0];
 
-  // This CTA's work: a sequence of tiles that every role walks in the same
-  // order.  A persistent CTA works on NG units at a time, one per group:
-  // round r has the units r*NG .. r*NG + live - 1 of its list, their tiles in
-  // turn.  A cluster's CTA has one unit and deals its tiles to the groups.
+  // This CTA's work.  Each epilogue group has a producer set, an issuing warp
+  // and rings of stages of its own: NG pipelines side by side that share
+  // nothing but the query warp.  In a persistent CTA group g takes the units
+  // g, g + NG, ... of the CTA's list; in a cluster's CTA, which has one unit,
+  // every NG-th of its tiles.
   const int C = CLUSTER ? static_cast<int>(cg::this_cluster().num_blocks()) : 1;
   const int crank = CLUSTER ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
   const int per = (p.tiles + C - 1) / C;
@@ -303,37 +306,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
   const int u0 = CLUSTER ? static_cast<int>(blockIdx.x) / C : static_cast<int>(blockIdx.x);
   const int ustep = static_cast<int>(gridDim.x);
   const int n_units = CLUSTER ? 1 : (p.units - u0 + ustep - 1) / ustep;
-  const int rounds = CLUSTER ? 1 : (n_units + NG - 1) / NG;
-  const auto live_of = [&](int r) { return CLUSTER ? 1 : min(NG, n_units - r * NG); };
+  const auto own_units = [&](int g) { return CLUSTER ? 1 : (n_units - g + NG - 1) / NG; };
+  const auto unit_tiles = [&](int g) { return CLUSTER ? (t1 - t0 - g + NG - 1) / NG : t1 - t0; };
 
   if (warp >= 4 * NG) {
     reg_dec<kAttnOtherRegs>();
-    if (warp < kSWarp) {
+    if (warp < kMmaWarp0) {
       // =========================== producers ===========================
-      // A cluster's tiles are copied by all warps together (the first tile's
-      // latency counts), a persistent CTA's by one warp each: the entries'
-      // and tables' latencies are then paid by four tiles at once.
-      // Four warps copy a tile, 32 entries each (a lane resolves one), and two
-      // sets of four take turns.  Stages are a multiple of the sets, so that a
-      // stage is always filled by the same one: a set that filled a stage out
-      // of turn could take the free barrier's phase of two uses ago for that
-      // of the last one.
-      constexpr int kSets = kAttnProducerSets;
-      const int set = (warp - kProdWarp0) / 4;
+      // The four warps of a group's set copy its tiles, 32 entries each (a lane
+      // resolves one).
+      const int g = (warp - kProdWarp0) / 4;
       constexpr int kRowLanes = 2 * D / 16;                    // lanes that copy a token's 16-byte pieces
       constexpr int kRowsPerCopy = 32 / kRowLanes;
       const int tok0 = (warp - kProdWarp0) % 4 * 32;           // this warp's tokens of a tile
       const int shift = p.block_shift, in_page = p.block_size - 1;
-      // Where a tile's entries, block table (decode) and pages (offset of the
-      // key head) are: the divisions that take a unit apart are done once a
-      // unit.
-      struct Place {
-        const int32_t* idx;
-        int req;
-        uint32_t head;
-      };
-      Place units[NG];
-      int ar = 0, at = t0, ae = 0;  // the look-ahead cursor over the sequence
       // Lane l copies piece l % kRowLanes of every kRowsPerCopy-th token into
       // its place in the 128-byte swizzle, which depends on the token mod 8.
       const int piece = lane % kRowLanes, sub = lane / kRowLanes;
@@ -344,37 +330,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       const uint8_t* const my_piece = p.kv + piece * 16;
       const uint32_t my_scale = ptx::smem_u32(smem + L.scale) + (tok0 + lane) * 8u;
       uint32_t* const my_mask = reinterpret_cast<uint32_t*>(smem + L.mask) + (tok0 >> 5);
-      const int total = n_units * (t1 - t0);
+      const int per_unit = unit_tiles(g), total = own_units(g) * per_unit;
       if (total > 0) {
-        // Entries are loaded two of the set's tiles ahead of their copies, table
-        // entries one.  Offsets into the cache are 32-bit numbers of p.unit
-        // bytes.
-        Ring st{0u, 0u, static_cast<uint32_t>(S)}, kst{0u, 0u, static_cast<uint32_t>(KS)};
-        for (int i = 0; i < set; ++i) {
-          st.next();
-          kst.next();
-        }
-        int32_t idx1 = -1, blk = -1, off = 0, req1 = 0;
-        uint32_t head = 0, head1 = 0;
-        int opened = -1;
+        // Entries are loaded two tiles ahead of their copies, table entries one.
+        // Offsets into the cache are 32-bit numbers of p.unit bytes.
+        Ring st{0u, 0u, static_cast<uint32_t>(SG)}, kst{0u, 0u, static_cast<uint32_t>(KSG)};
+        int32_t idx1 = -1, blk = -1, off = 0, req1 = 0, req2 = 0;
+        uint32_t head = 0, head1 = 0, head2 = 0;
+        // the look-ahead: the next tile's place, tiles left in its unit, the next unit
+        const int32_t* at = nullptr;
+        int room = 0, left = 0, unit = g;
         int req = 0;  // prefill: the request that the last column was found in
         int32_t req_lo = 0, req_hi = -1;
-        const auto skip = [&](int n) {
-#pragma unroll
-          for (int i = 0; i < kSets; ++i)
-            if (i < n && ++ae >= live_of(ar)) {
-              ae = 0;
-              if (++at >= t1) {
-                at = t0;
-                ++ar;
-              }
-            }
-        };
-        skip(set);
 #pragma unroll 1
-        for (int it = set - 2 * kSets; it < total; it += kSets) {
-          int32_t blk1 = -1, idx2 = -1, req2 = 0, tok = idx1;
-          uint32_t head2 = 0;
+        for (int it = -2; it < total; ++it) {
+          int32_t blk1 = -1, idx2 = -1, tok = idx1;
           {  // the next tile's table entries
             bool ok = tok >= 0;
             if (p.cu_seq_lens != nullptr) {
@@ -397,37 +367,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
             const int32_t j = tok >> shift;
             if (ok && j < p.max_blocks) blk1 = load_now(p.block_tables + static_cast<int64_t>(req) * p.bt_stride + j);
           }
-          if (it + 2 * kSets < total) {  // the entries of the tile after that
-            if (opened != ar) {
-              opened = ar;
-#pragma unroll 1
-              for (int e = 0; e < live_of(ar); ++e) {
-                int row, kvh, h0;
-                unit_of(p, u0 + (ar * NG + e) * ustep, &row, &kvh, &h0, GP);
-                const Place c{p.indices + row * p.idx_stride, row / p.next_n, kvh * p.head_units};
-                if (e == 0) units[0] = c; else units[1] = c;
-              }
+          if (it + 2 < total) {  // the entries of the tile after that
+            if (left == 0) {     // a new unit: taken apart once
+              int row, kvh, h0;
+              unit_of(p, u0 + (CLUSTER ? 0 : unit) * ustep, &row, &kvh, &h0, GP);
+              const int first = (t0 + (CLUSTER ? g : 0)) * kAttnTile + tok0 + lane;
+              at = p.indices + row * p.idx_stride + first;
+              room = p.k - first;
+              req2 = row / p.next_n;
+              head2 = kvh * p.head_units;
+              left = per_unit;
+              unit += NG;
             }
-            const Place c = ae == 0 ? units[0] : units[1];
-            req2 = c.req;
-            head2 = c.head;
-            const int j = at * kAttnTile + tok0 + lane;
-            if (j < p.k) idx2 = load_now(c.idx + j);
-            skip(kSets);
+            if (room > 0) idx2 = load_now(at);
+            at += (CLUSTER ? NG : 1) * kAttnTile;
+            room -= (CLUSTER ? NG : 1) * kAttnTile;
+            --left;
           }
           if (it >= 0) {
             const bool ok = blk >= 0 && blk < p.num_blocks;
             const uint32_t m = __ballot_sync(kFull, ok);
             const uint32_t page = head + static_cast<uint32_t>(blk) * p.block_units;
             const uint32_t from = page + static_cast<uint32_t>(off) * p.tok_units;
-            if (!attn_wait(empty0 + 8u * st.idx, st.phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
-            if (KS > 0 && !attn_wait(ke0 + 8u * kst.idx, kst.phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
-            const uint32_t full = full0 + 8u * st.idx;
-            const uint32_t at_stage = KS > 0 && piece < 8 ? k0 + kst.idx * kAttnHalfBytes : v0 + st.idx * kAttnHalfBytes;
+            const uint32_t stage = g * SG + st.idx, k_stage = g * KSG + kst.idx;
+            if (!attn_wait(empty0 + 8u * stage, st.phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
+            if (KS > 0 && !attn_wait(ke0 + 8u * k_stage, kst.phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
+            const uint32_t full = full0 + 8u * stage;
+            const uint32_t at_stage = KS > 0 && piece < 8 ? k0 + k_stage * kAttnHalfBytes : v0 + stage * kAttnHalfBytes;
             if (ok)
-              ptx::cp_async_8(my_scale + st.idx * (kAttnTile * 8u),
+              ptx::cp_async_8(my_scale + stage * (kAttnTile * 8u),
                               p.kv + static_cast<uint64_t>(page) * p.unit + (p.scale_off + 8 * off));
-            if (lane == 0) my_mask[4 * st.idx] = m;
+            if (lane == 0) my_mask[4 * stage] = m;
             if (m == kFull) {
 #pragma unroll
               for (int j = 0; j < 32; j += kRowsPerCopy)
@@ -444,10 +414,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
             }
             ptx::cp_async_mbar_arrive(full);
             if (lane == 0) ptx::mbar_arrive(full);
-            for (int i = 0; i < kSets; ++i) {
-              st.next();
-              kst.next();
-            }
+            st.next();
+            kst.next();
           }
           blk = blk1, off = tok & in_page, head = head1;
           idx1 = idx2, req1 = req2, head1 = head2;
@@ -485,111 +453,115 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(qf0 + 8u * buf);
       }
-    } else {
+    } else if (warp < kQWarp) {
       // ============================= MMA ===============================
-      // A warp for the scores and one per group for its outputs, so that no
-      // product waits for another one's operands.  The whole warp walks the
+      // A warp per group issues its products: the scores of a later tile
+      // whenever that tile is there and an accumulator free, else the output
+      // of the oldest tile whose probabilities are.  The whole warp walks the
       // tiles (its values stay uniform), one lane issues.
-      const bool scores = warp == kSWarp;
-      const int og = warp - kOWarp0;
+      const int g = warp - kMmaWarp0;
       constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(kAttnTile, N2);
       constexpr uint32_t kIdescO = ptx::idesc_e4m3_f32(128, N2) | ptx::kIdescMnMajorA | ptx::kIdescMnMajorB;
-      if (scores) {
-        const uint64_t a0 = ptx::smem_desc_sw128(KS > 0 ? k0 : v0), b0 = ptx::smem_desc_sw128(q0);
-        Ring st{0u, 0u, static_cast<uint32_t>(S)}, kst{0u, 0u, static_cast<uint32_t>(KS > 0 ? KS : S)};
-        uint32_t n0 = 0, n1 = 0;      // tiles per group
-        int turn = 0;
-        bool okay = true;
+      const uint64_t sa0 = ptx::smem_desc_sw128(KS > 0 ? k0 : v0), sb0 = ptx::smem_desc_sw128(q0);
+      const uint64_t oa0 = ptx::smem_desc_mn(v0, 128);
+      const uint64_t ob = ptx::smem_desc_mn(ptx::smem_u32(smem + L.p) + g * kAttnTile * N2, N2);
+      Ring ss{0u, 0u, static_cast<uint32_t>(SG)}, ks{0u, 0u, static_cast<uint32_t>(KSG)}, so = ss;
+      const int per_unit = unit_tiles(g), own = own_units(g) * per_unit;
+      int is = 0, io = 0, left_s = per_unit, left_o = per_unit;  // tiles scored, put out; left in the unit
+      int unit_s = CLUSTER ? 0 : g;
+      uint32_t n_out = 0;             // outputs issued
+      bool first = true;              // the unit's first output starts the accumulator anew
+      uint64_t since = 0;
+      uint32_t spins = 0;
+      const auto tile_any = [&](uint32_t stage) {
+        const uint4 m = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * stage);
+        return (m.x | m.y | m.z | m.w) != 0u;
+      };
 #pragma unroll 1
-        for (int r = 0; r < rounds && okay; ++r) {
-          const int live = live_of(r);
-#pragma unroll 1
-          for (int te = (t1 - t0) * live, left = te, e = 0; te > 0; --te, e = e + 1 == live ? 0 : e + 1) {
-            const int g = CLUSTER ? turn : e;
-            turn = turn + 1 == NG ? 0 : turn + 1;
-            const int buf = CLUSTER ? 0 : (r * NG + e) % QB;
-            if (left - te < live && !CLUSTER || te == left)  // a unit's first tile
-              okay = attn_wait(qf0 + 8u * buf, CLUSTER ? 0 : ((r * NG + e) / QB) & 1, abort_flag, kSiteQFull);
-            const uint32_t c = g == 0 ? n0++ : n1++;
-            const uint32_t slot = g * SBG + (c & 1u), parity = (c >> 1) & 1u;
-            okay = okay && attn_wait2(full0 + 8u * st.idx, st.phase, se0 + 8u * slot, parity ^ 1u, abort_flag,
-                                      kSiteStageFull, kSiteAccEmpty);
-            if (!okay) break;
-            const uint4 m = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * st.idx);
-            const bool any = (m.x | m.y | m.z | m.w) != 0u;
-            ptx::fence_proxy_async_smem();  // the tile was written by cp.async
-            ptx::tc_fence_after();
-            const uint32_t a_stage = KS > 0 ? kst.idx : st.idx;
-            const uint64_t a = a0 + static_cast<uint64_t>(a_stage * (kAttnHalfBytes >> 4));
-            const uint64_t b = b0 + static_cast<uint64_t>(buf * (N2 * 128u >> 4));
-            if (ptx::elect_one()) {
-              if (any) {
-#pragma unroll
-                for (int kk = 0; kk < D / 32; ++kk)
-                  ptx::mma_f8f6f4(tmem + slot * N2, a + 2ull * kk, b + 2ull * kk, kIdescS, kk > 0 ? 1u : 0u);
-              }
-              ptx::mma_commit(sf0 + 8u * slot);
-              if (KS > 0) ptx::mma_commit(ke0 + 8u * kst.idx);
-              // (a tile without entries has no output MMA that follows its scores)
-              ptx::mbar_arrive(empty0 + 8u * st.idx);
-              if (te <= live) ptx::mma_commit(qe0 + 8u * buf);  // the unit's last tile
-            }
-            __syncwarp();
-            st.next();
-            kst.next();
-          }
-        }
-      } else {
-        const uint64_t a0 = ptx::smem_desc_mn(v0, 128);
-        const uint64_t b0 = ptx::smem_desc_mn(ptx::smem_u32(smem + L.p) + og * kAttnTile * N2, N2);
-        Ring st{0u, 0u, static_cast<uint32_t>(S)};
-        uint32_t n = 0;               // the group's tiles with entries
-        int turn = 0;
-        bool okay = true;
-#pragma unroll 1
-        for (int r = 0; r < rounds && okay; ++r) {
-          const int live = live_of(r);
-          bool first = true;          // the unit's first tile starts the accumulator anew
-#pragma unroll 1
-          for (int te = (t1 - t0) * live, e = 0; te > 0; --te, e = e + 1 == live ? 0 : e + 1) {
-            const uint32_t stage = st.idx, stage_phase = st.phase;
-            st.next();
-            const int g = CLUSTER ? turn : e;
-            turn = turn + 1 == NG ? 0 : turn + 1;
-            if (g != og) continue;
-            okay = attn_wait(full0 + 8u * stage, stage_phase, abort_flag, kSiteStageFull);
-            if (!okay) break;
-            const uint4 m = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * stage);
-            const bool any = (m.x | m.y | m.z | m.w) != 0u;
-            ptx::fence_proxy_async_smem();  // the tile was written by cp.async
-            const uint64_t a = a0 + static_cast<uint64_t>(stage * (kAttnHalfBytes >> 4));
+      while (io < own) {
+        const uint32_t slot = g * SBG + (is & 1), parity = (is >> 1) & 1;
+        bool go = is < own && ptx::mbar_test_wait(full0 + 8u * (g * SG + ss.idx), ss.phase) &&
+                  ptx::mbar_test_wait(se0 + 8u * slot, parity ^ 1u);
+        if (__all_sync(kFull, go)) {
+          const int buf = unit_s % QB;
+          if (left_s == per_unit && !attn_wait(qf0 + 8u * buf, (unit_s / QB) & 1, abort_flag, kSiteQFull)) break;
+          const uint32_t stage = g * SG + ss.idx, k_stage = g * KSG + ks.idx;
+          const bool any = tile_any(stage);
+          ptx::fence_proxy_async_smem();  // the tile was written by cp.async
+          ptx::tc_fence_after();
+          const uint64_t a = sa0 + static_cast<uint64_t>((KS > 0 ? k_stage : stage) * (kAttnHalfBytes >> 4));
+          const uint64_t b = sb0 + static_cast<uint64_t>(buf * (N2 * 128u >> 4));
+          if (ptx::elect_one()) {
             if (any) {
-              // (the group makes its next unit's first probabilities after it has read the last unit's outputs)
-              okay = attn_wait(pf0 + 8u * og, n & 1u, abort_flag, kSiteAccFull);
-              if (!okay) break;
-              ++n;
-              ptx::tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                ptx::mma_f8f6f4(tmem + slot * N2, a + 2ull * kk, b + 2ull * kk, kIdescS, kk > 0 ? 1u : 0u);
             }
+            ptx::mma_commit(sf0 + 8u * slot);
+            if (KS > 0) ptx::mma_commit(ke0 + 8u * k_stage);
+            if (left_s == 1) ptx::mma_commit(qe0 + 8u * buf);  // the unit's last tile
+          }
+          __syncwarp();
+          ++is;
+          ss.next();
+          ks.next();
+          if (--left_s == 0) {
+            left_s = per_unit;
+            unit_s += NG;
+          }
+          spins = 0;
+          continue;
+        }
+        if (io < is) {
+          const uint32_t stage = g * SG + so.idx;
+          const bool any = tile_any(stage);
+          go = !any || ptx::mbar_test_wait(pf0 + 8u * g, n_out & 1u);
+          if (__all_sync(kFull, go)) {
+            // (the group makes its next unit's first probabilities after it has read the last unit's outputs)
+            ptx::tc_fence_after();
+            const uint64_t a = oa0 + static_cast<uint64_t>(stage * (kAttnHalfBytes >> 4));
             if (ptx::elect_one()) {
               if (any) {
 #pragma unroll
                 for (int kk = 0; kk < kAttnTile / 32; ++kk)
-                  ptx::mma_f8f6f4(tmem + kTmemO + og * N2, a + kk * (32ull * 128 >> 4), b0 + kk * (32ull * N2 >> 4), kIdescO,
+                  ptx::mma_f8f6f4(tmem + kTmemO + g * N2, a + kk * (32ull * 128 >> 4), ob + kk * (32ull * N2 >> 4), kIdescO,
                                   (first && kk == 0) ? 0u : 1u);
-                ptx::mma_commit(pe0 + 8u * og);
+                ptx::mma_commit(pe0 + 8u * g);
                 ptx::mma_commit(empty0 + 8u * stage);
               } else {
                 ptx::mbar_arrive(empty0 + 8u * stage);
               }
             }
             __syncwarp();
-            if (any) first = false;
+            if (any) {
+              first = false;
+              ++n_out;
+            }
+            ++io;
+            so.next();
+            if (--left_o == 0) {
+              left_o = per_unit;
+              first = true;
+            }
+            spins = 0;
+            continue;
           }
+        }
+        if ((++spins & 63u) == 0u) {
+          bool give_up = *abort_flag != 0u;
+          const uint64_t now = ptx::globaltimer_ns();
+          if (spins == 64u) since = now;
+          if (now - since > kWaitTimeoutNs) {
+            give_up = true;
+            *abort_flag = 1u;
+            if (lane == 0) atomicOr(&g_attn_watchdog, static_cast<uint32_t>(kSiteAccEmpty));
+          }
+          if (__any_sync(kFull, give_up)) break;
         }
       }
       __syncwarp();
       if (*abort_flag && lane == 0) {
-        const uint32_t bar = drain0 + 8u * (warp - kSWarp);
+        const uint32_t bar = drain0 + 8u * g;
         ptx::mma_commit(bar);
         wait_drain(bar, 0, &g_attn_watchdog);
       }
@@ -606,9 +578,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     // 16-byte chunks of a row of probabilities, swizzled over its N2 bytes
     const uint32_t p_swz = N2 == 64 ? (tg >> 1) & 3 : (tg >> 2) & 1;
     const int bar_id = 1 + g;
-    Ring st{0u, 0u, static_cast<uint32_t>(S)};
+    Ring st{0u, 0u, static_cast<uint32_t>(SG)};
     uint32_t n_own = 0, n_tile = 0;                   // this group's tiles, those with entries
-    int turn = 0;
     bool stop = false;
     if (CLUSTER && t0 < t1) {
       // The unit's query: nothing else is to be done yet, and 256 threads have
@@ -650,9 +621,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       if (lane == 0) ptx::mbar_arrive(qf0);
     }
 #pragma unroll 1
-    for (int r = 0; r < rounds && !stop; ++r) {
-      const int live = live_of(r);
-      if (!CLUSTER && g >= live) break;
+    for (int r = 0; r < own_units(g) && !stop; ++r) {
       const int unit = CLUSTER ? 0 : r * NG + g;
       float qscale = 0.f;
       bool ok = true;
@@ -669,13 +638,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       for (int j = 0; j < GP / 2; ++j) l2[j] = make_float2(0.f, 0.f);
 
 #pragma unroll 1
-      for (int te = (t1 - t0) * live, e = 0; te > 0; --te) {
-        const uint32_t stage = st.idx, stage_phase = st.phase;
+      for (int left = unit_tiles(g); left > 0; --left) {
+        const uint32_t stage = g * SG + st.idx, stage_phase = st.phase;
         st.next();
-        const bool mine = CLUSTER ? turn == g : e == g;
-        if (++turn == NG) turn = 0;
-        if (++e == live) e = 0;
-        if (!mine) continue;
         asm volatile("" : "+r"(has_o));  // (one copy of the loop: the first tile is not peeled off)
         const uint32_t slot = g * SBG + (n_own & 1u), slot_parity = (n_own >> 1) & 1u;
         ++n_own;
@@ -956,7 +921,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == kSWarp) {
+  if (warp == kMmaWarp0) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }

@@ -243,6 +243,31 @@ def test_more_rows_than_sms(fp8idx):
     prefill(fp8idx, bf16(rng.standard_normal((M, 6, 64))), cache, idx, tables, cu, 16, 0.125)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H", [3, 20])
+@pytest.mark.parametrize("rows_per_sm,k", [(2, 700), (3, 513), (5, 130), (7, 300)])
+def test_several_units_a_cta(fp8idx, D, H, rows_per_sm, k):
+    """Odd and even numbers of rows on an SM, one more on some of them, with
+    tiles and rows that select nothing among them."""
+    rng = np.random.default_rng(rows_per_sm + k + D)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    M, bs, length = rows_per_sm * sms + 37, 32, 900
+    cache = filled_cache(rng, 40, 1, bs, D)
+    blocks = -(-length // bs)
+    tables = rng.permutation(40)[:blocks].astype(np.int32).reshape(1, blocks)
+    idx = np.sort(rng.integers(0, length, (M, k)), axis=1).astype(np.int32)
+    for r in range(M):
+        what = rng.integers(0, 6)
+        if what == 0:
+            idx[r] = -1
+        elif what == 1:
+            idx[r, int(rng.integers(0, k)):] = -1
+        elif what == 2:
+            t = int(rng.integers(0, -(-k // 128)))
+            idx[r, 128 * t: 128 * (t + 1)] = -1
+    prefill(fp8idx, bf16(rng.standard_normal((M, H, D))), cache, idx, tables, np.array([0, length], np.int32), bs, D**-0.5)
+
+
 def test_strides(fp8idx):
     """q and out as slices of wider tensors, indices with a longer row
     stride, the cache one layer of a larger one, a sliced block table."""
