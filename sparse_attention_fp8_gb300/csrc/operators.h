@@ -95,6 +95,9 @@ constexpr int kAttnThreads = 32 * (4 * kAttnGroups + 4 * kAttnGroups + kAttnGrou
 // Registers a thread after the launch's 96 have been dealt anew:
 // 256 * 144 + 384 * 64 = 640 * 96.
 constexpr int kAttnEpilogueRegs = 144, kAttnOtherRegs = 64;
+// Probability buffers of a group: one is multiplied with the values while the
+// next is written.
+constexpr int kAttnProbBuffers = 2;
 // Query buffers: the units in work and the next one.
 constexpr int kAttnQueryBuffers = kAttnGroups + 1;
 // Tiles in flight, half of them a group's.  head_dim 128: a key
@@ -105,7 +108,7 @@ constexpr int kAttnQueryBuffers = kAttnGroups + 1;
 constexpr uint32_t kAttnHalfBytes = kAttnTile * 128u;
 __host__ __device__ constexpr int attn_k_stages(int head_dim) { return head_dim == 128 ? 4 : 0; }
 __host__ __device__ constexpr int attn_v_stages(int head_dim, int gp) {
-  return head_dim == 64 || gp == 16 ? 8 : 6;
+  return head_dim == 64 ? 8 : 6;
 }
 struct AttnSmem {
   uint32_t k, v, q, p, scale, mask, flt, bars, misc, total;
@@ -119,7 +122,7 @@ __host__ __device__ constexpr AttnSmem attn_smem_layout(int head_dim, int gp) {
   L.k = off;     off += attn_k_stages(head_dim) * kAttnHalfBytes;
   L.v = off;     off += stages * kAttnHalfBytes;
   L.q = off;     off += kAttnQueryBuffers * 2u * gp * 128u;  // 2*gp rows of 128 bytes
-  L.p = off;     off += kAttnGroups * kAttnTile * 2u * gp;  // a tile of probabilities per group
+  L.p = off;     off += kAttnGroups * kAttnProbBuffers * kAttnTile * 2u * gp;  // tiles of probabilities
   L.scale = off; off += stages * kAttnTile * 8u;
   L.mask = off;  off += stages * 16u;
   L.flt = off;   off += 4u * attn_state_floats(gp);

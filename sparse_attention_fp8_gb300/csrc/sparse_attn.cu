@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
   static_assert(32 * (kQWarp + 1) <= kAttnThreads, "roles");
   constexpr int N2 = 2 * GP;                       // columns of S^T and O^T
   constexpr int SBG = 2;                           // accumulators of S^T per group
-  constexpr int QB = kAttnQueryBuffers;
+  constexpr int QB = kAttnQueryBuffers, PB = kAttnProbBuffers;
+  static_assert(PB == 2, "the parities below");
   constexpr int KS = attn_k_stages(D), S = attn_v_stages(D, GP);  // D = 64: keys and values share the rows of S
   constexpr int KSG = KS > 0 ? KS / NG : 1, SG = S / NG;         // a group's share
   static_assert(KS % NG == 0 && S % NG == 0, "stages");
@@ -254,8 +255,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
   const uint32_t ke0 = empty0 + 8u * S;                                       // keys' scores computed
   const uint32_t qf0 = ke0 + 8u * KS, qe0 = qf0 + 8u * QB;                    // query buffers
   const uint32_t sf0 = qe0 + 8u * QB, se0 = sf0 + 8u * NG * SBG;              // [group][accumulator] scores ready, read
-  const uint32_t pf0 = se0 + 8u * NG * SBG, pe0 = pf0 + 8u * NG;              // [group] probabilities ready, used
-  const uint32_t ub = pe0 + 8u * NG, drain0 = ub + 8u;                        // cluster: both groups done; [MMA warp]
+  const uint32_t pf0 = se0 + 8u * NG * SBG, pe0 = pf0 + 8u * NG * PB;    // [group][buffer] probabilities ready, used
+  const uint32_t ub = pe0 + 8u * NG * PB, drain0 = ub + 8u;                        // cluster: both groups done; [MMA warp]
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L.misc);
   volatile uint32_t* abort_flag = misc + 1;
 
@@ -275,9 +276,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       ptx::mbar_init(sf0 + 8u * i, 1u);
       ptx::mbar_init(se0 + 8u * i, 4u);
     }
-    for (int g = 0; g < NG; ++g) {
-      ptx::mbar_init(pf0 + 8u * g, 4u);
-      ptx::mbar_init(pe0 + 8u * g, 1u);
+    for (int i = 0; i < NG * PB; ++i) {
+      ptx::mbar_init(pf0 + 8u * i, 4u);
+      ptx::mbar_init(pe0 + 8u * i, 1u);
     }
     ptx::mbar_init(ub, 4u * NG);
     for (int i = 0; i < NG; ++i) ptx::mbar_init(drain0 + 8u * i, 1u);
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       constexpr uint32_t kIdescO = ptx::idesc_e4m3_f32(128, N2) | ptx::kIdescMnMajorA | ptx::kIdescMnMajorB;
       const uint64_t sa0 = ptx::smem_desc_sw128(KS > 0 ? k0 : v0), sb0 = ptx::smem_desc_sw128(q0);
       const uint64_t oa0 = ptx::smem_desc_mn(v0, 128);
-      const uint64_t ob = ptx::smem_desc_mn(ptx::smem_u32(smem + L.p) + g * kAttnTile * N2, N2);
+      const uint64_t ob = ptx::smem_desc_mn(ptx::smem_u32(smem + L.p) + g * PB * kAttnTile * N2, N2);
       Ring ss{0u, 0u, static_cast<uint32_t>(SG)}, ks{0u, 0u, static_cast<uint32_t>(KSG)}, so = ss;
       const int per_unit = unit_tiles(g), own = own_units(g) * per_unit;
       int is = 0, io = 0, left_s = per_unit, left_o = per_unit;  // tiles scored, put out; left in the unit
@@ -515,18 +516,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         if (io < is) {
           const uint32_t stage = g * SG + so.idx;
           const bool any = tile_any(stage);
-          go = !any || ptx::mbar_test_wait(pf0 + 8u * g, n_out & 1u);
+          const uint32_t pbuf = n_out & 1u;
+          go = !any || ptx::mbar_test_wait(pf0 + 8u * (g * PB + pbuf), (n_out >> 1) & 1u);
           if (__all_sync(kFull, go)) {
             // (the group makes its next unit's first probabilities after it has read the last unit's outputs)
             ptx::tc_fence_after();
             const uint64_t a = oa0 + static_cast<uint64_t>(stage * (kAttnHalfBytes >> 4));
+            const uint64_t b = ob + static_cast<uint64_t>(pbuf * (kAttnTile * N2 >> 4));
             if (ptx::elect_one()) {
               if (any) {
 #pragma unroll
                 for (int kk = 0; kk < kAttnTile / 32; ++kk)
-                  ptx::mma_f8f6f4(tmem + kTmemO + g * N2, a + kk * (32ull * 128 >> 4), ob + kk * (32ull * N2 >> 4), kIdescO,
+                  ptx::mma_f8f6f4(tmem + kTmemO + g * N2, a + kk * (32ull * 128 >> 4), b + kk * (32ull * N2 >> 4), kIdescO,
                                   (first && kk == 0) ? 0u : 1u);
-                ptx::mma_commit(pe0 + 8u * g);
+                ptx::mma_commit(pe0 + 8u * (g * PB + pbuf));
                 ptx::mma_commit(empty0 + 8u * stage);
               } else {
                 ptx::mbar_arrive(empty0 + 8u * stage);
@@ -574,13 +577,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     const int tg = threadIdx.x & 127;                 // thread in the group = token = channel
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t o_tm = tmem + kTmemO + g * N2 + lane_off;
-    uint8_t* p_row = smem + L.p + g * kAttnTile * N2 + tg * N2;
+    uint8_t* const p_rows = smem + L.p + g * PB * kAttnTile * N2 + tg * N2;
     // 16-byte chunks of a row of probabilities, swizzled over its N2 bytes
     const uint32_t p_swz = N2 == 64 ? (tg >> 1) & 3 : (tg >> 2) & 1;
     const int bar_id = 1 + g;
     Ring st{0u, 0u, static_cast<uint32_t>(SG)};
     uint32_t n_own = 0, n_tile = 0;                   // this group's tiles, those with entries
     bool stop = false;
+    // the output MMA of the last tile with entries (they complete in order)
+    const auto last_out = [&] { return pe0 + 8u * (g * PB + ((n_tile - 1u) & 1u)); };
+    const auto last_parity = [&] { return ((n_tile - 1u) >> 1) & 1u; };
     if (CLUSTER && t0 < t1) {
       // The unit's query: nothing else is to be done yet, and 256 threads have
       // it ready by the time the first tile is.
@@ -682,7 +688,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         // The probabilities are computed and stored against the m in hand; if
         // one of them shows that m is too small (or m is not set yet), the
         // group takes the maxima and does them over.
-        ok = attn_wait(pe0 + 8u * g, (n_tile & 1u) ^ 1u, abort_flag, kSiteAccEmpty) && ok;  // P is free
+        const uint32_t pbuf = n_tile & 1u;
+        uint8_t* const p_row = p_rows + pbuf * kAttnTile * N2;
+        ok = attn_wait(pe0 + 8u * (g * PB + pbuf), ((n_tile >> 1) & 1u) ^ 1u, abort_flag, kSiteAccEmpty) && ok;  // P is free
 #pragma unroll 1
         for (bool fresh = false;; fresh = true) {
           bool again = any && !fresh && (!has_o || vs > kMaxW * cref);
@@ -713,6 +721,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
               *reinterpret_cast<uint4*>(p_row + (((b / 16) ^ p_swz) << 4)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
               *reinterpret_cast<uint4*>(p_row + ((((GP + b) / 16) ^ p_swz) << 4)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
             }
+            ptx::fence_proxy_async_smem();  // (before the vote, which hides some of its wait)
             again = again || (!fresh && !__hble2(top, __floats2half2_rn(kMaxP, kMaxP)));
           }
           if (!ptx::bar_or(bar_id, 128, again || !ok)) break;
@@ -752,7 +761,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
           }
           ptx::bar_sync(bar_id, 128);
           cref = stt.cref[g];
-          if (has_o) {  // (P was free: the group's last output MMA is done)
+          if (has_o) {
+            attn_wait(last_out(), last_parity(), abort_flag, kSiteAccEmpty);
+            ptx::tc_fence_after();
 #pragma unroll
             for (int j = 0; j < GP / 2; ++j) {
               const float2 f = *reinterpret_cast<const float2*>(&stt.resc[g][2 * j]);
@@ -779,11 +790,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
           if (lane == 0) ptx::mbar_arrive(se0 + 8u * slot);
           continue;
         }
-        ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           ptx::mbar_arrive(se0 + 8u * slot);
-          ptx::mbar_arrive(pf0 + 8u * g);
+          ptx::mbar_arrive(pf0 + 8u * (g * PB + pbuf));
         }
         has_o = 1u;
         ++n_tile;
@@ -791,7 +801,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       if (stop) break;
 
       // ---- the unit's end: the sums over the group's tokens, and the output
-      if (has_o) attn_wait(pe0 + 8u * g, (n_tile & 1u) ^ 1u, abort_flag, kSiteAccEmpty);
+      if (has_o) attn_wait(last_out(), last_parity(), abort_flag, kSiteAccEmpty);
       ptx::tc_fence_after();
       {
         float v[GP];
