@@ -103,6 +103,16 @@ __device__ __forceinline__ bool attn_wait2(uint32_t bar0, uint32_t parity0, uint
   return attn_wait(bar0, parity0, abort_flag, site0) && attn_wait(bar1, parity1, abort_flag, site1);
 }
 
+__device__ __forceinline__ bool attn_wait3(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, uint32_t bar2,
+                                           uint32_t parity2, volatile uint32_t* abort_flag, uint32_t site0, uint32_t site1,
+                                           uint32_t site2) {
+  const bool a = ptx::mbar_test_wait(bar0, parity0), b = ptx::mbar_test_wait(bar1, parity1);
+  const bool c = ptx::mbar_test_wait(bar2, parity2);
+  if (__all_sync(kFull, a && b && c)) return true;
+  return attn_wait(bar0, parity0, abort_flag, site0) && attn_wait(bar1, parity1, abort_flag, site1) &&
+         attn_wait(bar2, parity2, abort_flag, site2);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -235,10 +245,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
   constexpr int N2 = 2 * GP;                       // columns of S^T and O^T
   constexpr int SBG = 2;                           // accumulators of S^T per group
   constexpr int QB = kAttnQueryBuffers, PB = kAttnProbBuffers;
-  static_assert(PB == 2, "the parities below");
   constexpr int KS = attn_k_stages(D), S = attn_v_stages(D, GP);  // D = 64: keys and values share the rows of S
   constexpr int KSG = KS > 0 ? KS / NG : 1, SG = S / NG;         // a group's share
-  static_assert(KS % NG == 0 && S % NG == 0, "stages");
+  static_assert(KS % NG == 0 && S % NG == 0 && SG >= SBG, "stages");
+  static_assert(SBG == 2 && PB == 2 && (KS == 0 || KSG == SBG), "rings that go in step");
   constexpr uint32_t kTmemCols = pow2_at_least(NG * (SBG + 1) * N2);
   constexpr uint32_t kTmemO = NG * SBG * N2;       // O^T of group g at kTmemO + g * N2
   using State = AttnState<GP, NG, QB>;
@@ -252,11 +262,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
   const uint32_t k0 = ptx::smem_u32(smem + L.k), v0 = ptx::smem_u32(smem + L.v);
   const uint32_t q0 = ptx::smem_u32(smem + L.q);
   const uint32_t full0 = ptx::smem_u32(smem + L.bars), empty0 = full0 + 8u * S;
-  const uint32_t ke0 = empty0 + 8u * S;                                       // keys' scores computed
-  const uint32_t qf0 = ke0 + 8u * KS, qe0 = qf0 + 8u * QB;                    // query buffers
-  const uint32_t sf0 = qe0 + 8u * QB, se0 = sf0 + 8u * NG * SBG;              // [group][accumulator] scores ready, read
-  const uint32_t pf0 = se0 + 8u * NG * SBG, pe0 = pf0 + 8u * NG * PB;    // [group][buffer] probabilities ready, used
-  const uint32_t ub = pe0 + 8u * NG * PB, drain0 = ub + 8u;                        // cluster: both groups done; [MMA warp]
+  const uint32_t qf0 = empty0 + 8u * S, qe0 = qf0 + 8u * QB;                  // query buffers
+  const uint32_t sf0 = qe0 + 8u * QB;                                         // [group][buffer] scores ready
+  const uint32_t pf0 = sf0 + 8u * NG * SBG, pe0 = pf0 + 8u * NG * PB;         // [group][buffer] probabilities ready, used
+  const uint32_t ub = pe0 + 8u * NG * PB, drain0 = ub + 8u;                   // cluster: both groups done; [MMA warp]
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L.misc);
   volatile uint32_t* abort_flag = misc + 1;
 
@@ -265,17 +274,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     misc[1] = 0u;
     for (int s = 0; s < S; ++s) {
       ptx::mbar_init(full0 + 8u * s, 33u * 4u);        // each producer lane's copies, each warp's mask
-      ptx::mbar_init(empty0 + 8u * s, 1u + 4u);          // the output MMA, the tile's epilogue warps
+      ptx::mbar_init(empty0 + 8u * s, 1u);               // the output MMA
     }
-    for (int s = 0; s < KS; ++s) ptx::mbar_init(ke0 + 8u * s, 1u);
     for (int i = 0; i < QB; ++i) {
       ptx::mbar_init(qf0 + 8u * i, CLUSTER ? 4u * NG : 1u);
       ptx::mbar_init(qe0 + 8u * i, 1u + 4u);             // the last score MMA, the unit's epilogue warps
     }
-    for (int i = 0; i < NG * SBG; ++i) {
-      ptx::mbar_init(sf0 + 8u * i, 1u);
-      ptx::mbar_init(se0 + 8u * i, 4u);
-    }
+    for (int i = 0; i < NG * SBG; ++i) ptx::mbar_init(sf0 + 8u * i, 1u);
     for (int i = 0; i < NG * PB; ++i) {
       ptx::mbar_init(pf0 + 8u * i, 4u);
       ptx::mbar_init(pe0 + 8u * i, 1u);
@@ -391,8 +396,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
             const uint32_t page = head + static_cast<uint32_t>(blk) * p.block_units;
             const uint32_t from = page + static_cast<uint32_t>(off) * p.tok_units;
             const uint32_t stage = g * SG + st.idx, k_stage = g * KSG + kst.idx;
-            if (!attn_wait(empty0 + 8u * stage, st.phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
-            if (KS > 0 && !attn_wait(ke0 + 8u * k_stage, kst.phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
+            // (a key stage is free once the scores of the tile in it are: their buffers take turns like the stages)
+            if (KS > 0 ? !attn_wait2(empty0 + 8u * stage, st.phase ^ 1u, sf0 + 8u * k_stage, kst.phase ^ 1u, abort_flag,
+                                     kSiteStageEmpty, kSiteAccFull)
+                       : !attn_wait(empty0 + 8u * stage, st.phase ^ 1u, abort_flag, kSiteStageEmpty))
+              break;
             const uint32_t full = full0 + 8u * stage;
             const uint32_t at_stage = KS > 0 && piece < 8 ? k0 + k_stage * kAttnHalfBytes : v0 + stage * kAttnHalfBytes;
             if (ok)
@@ -400,10 +408,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
                               p.kv + static_cast<uint64_t>(page) * p.unit + (p.scale_off + 8 * off));
             if (lane == 0) my_mask[4 * stage] = m;
             if (m == kFull) {
+              uint32_t f[32 / kRowsPerCopy];  // (all shuffles first: none waits for a copy to be issued)
+#pragma unroll
+              for (int j = 0; j < 32 / kRowsPerCopy; ++j) f[j] = __shfl_sync(kFull, from, j * kRowsPerCopy + sub);
 #pragma unroll
               for (int j = 0; j < 32; j += kRowsPerCopy)
                 ptx::cp_async_16(at_stage + place[(j & 7) / kRowsPerCopy] + j * 128u,
-                                 my_piece + static_cast<uint64_t>(__shfl_sync(kFull, from, j + sub)) * p.unit);
+                                 my_piece + static_cast<uint64_t>(f[j / kRowsPerCopy]) * p.unit);
             } else {  // entries without a token copy zeros
 #pragma unroll 1
               for (int j = 0; j < 32; j += kRowsPerCopy) {
@@ -456,9 +467,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       }
     } else if (warp < kQWarp) {
       // ============================= MMA ===============================
-      // A warp per group issues its products: the scores of a later tile
-      // whenever that tile is there and an accumulator free, else the output
-      // of the oldest tile whose probabilities are.  The whole warp walks the
+      // A warp per group issues its products: the output of the oldest tile
+      // whose probabilities are there, else the scores of a tile (two ahead
+      // at most: their accumulators take turns).  The whole warp walks the
       // tiles (its values stay uniform), one lane issues.
       const int g = warp - kMmaWarp0;
       constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(kAttnTile, N2);
@@ -466,80 +477,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       const uint64_t sa0 = ptx::smem_desc_sw128(KS > 0 ? k0 : v0), sb0 = ptx::smem_desc_sw128(q0);
       const uint64_t oa0 = ptx::smem_desc_mn(v0, 128);
       const uint64_t ob = ptx::smem_desc_mn(ptx::smem_u32(smem + L.p) + g * PB * kAttnTile * N2, N2);
-      Ring ss{0u, 0u, static_cast<uint32_t>(SG)}, ks{0u, 0u, static_cast<uint32_t>(KSG)}, so = ss;
+      Ring ss{0u, 0u, static_cast<uint32_t>(SG)}, so = ss;
       const int per_unit = unit_tiles(g), own = own_units(g) * per_unit;
       int is = 0, io = 0, left_s = per_unit, left_o = per_unit;  // tiles scored, put out; left in the unit
       int unit_s = CLUSTER ? 0 : g;
-      uint32_t n_out = 0;             // outputs issued
+      uint32_t live = 0;              // [is & 1]: whether a scored tile has entries
       bool first = true;              // the unit's first output starts the accumulator anew
       uint64_t since = 0;
       uint32_t spins = 0;
-      const auto tile_any = [&](uint32_t stage) {
-        const uint4 m = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * stage);
-        return (m.x | m.y | m.z | m.w) != 0u;
-      };
 #pragma unroll 1
       while (io < own) {
-        const uint32_t slot = g * SBG + (is & 1), parity = (is >> 1) & 1;
-        bool go = is < own && ptx::mbar_test_wait(full0 + 8u * (g * SG + ss.idx), ss.phase) &&
-                  ptx::mbar_test_wait(se0 + 8u * slot, parity ^ 1u);
-        if (__all_sync(kFull, go)) {
-          const int buf = unit_s % QB;
-          if (left_s == per_unit && !attn_wait(qf0 + 8u * buf, (unit_s / QB) & 1, abort_flag, kSiteQFull)) break;
-          const uint32_t stage = g * SG + ss.idx, k_stage = g * KSG + ks.idx;
-          const bool any = tile_any(stage);
-          ptx::fence_proxy_async_smem();  // the tile was written by cp.async
-          ptx::tc_fence_after();
-          const uint64_t a = sa0 + static_cast<uint64_t>((KS > 0 ? k_stage : stage) * (kAttnHalfBytes >> 4));
-          const uint64_t b = sb0 + static_cast<uint64_t>(buf * (N2 * 128u >> 4));
-          if (ptx::elect_one()) {
-            if (any) {
-#pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk)
-                ptx::mma_f8f6f4(tmem + slot * N2, a + 2ull * kk, b + 2ull * kk, kIdescS, kk > 0 ? 1u : 0u);
-            }
-            ptx::mma_commit(sf0 + 8u * slot);
-            if (KS > 0) ptx::mma_commit(ke0 + 8u * k_stage);
-            if (left_s == 1) ptx::mma_commit(qe0 + 8u * buf);  // the unit's last tile
-          }
-          __syncwarp();
-          ++is;
-          ss.next();
-          ks.next();
-          if (--left_s == 0) {
-            left_s = per_unit;
-            unit_s += NG;
-          }
-          spins = 0;
-          continue;
-        }
         if (io < is) {
-          const uint32_t stage = g * SG + so.idx;
-          const bool any = tile_any(stage);
-          const uint32_t pbuf = n_out & 1u;
-          go = !any || ptx::mbar_test_wait(pf0 + 8u * (g * PB + pbuf), (n_out >> 1) & 1u);
-          if (__all_sync(kFull, go)) {
+          const uint32_t buf = io & 1, bar = 8u * (g * PB + buf);
+          if (__all_sync(kFull, ptx::mbar_test_wait(pf0 + bar, (io >> 1) & 1))) {
             // (the group makes its next unit's first probabilities after it has read the last unit's outputs)
             ptx::tc_fence_after();
+            const bool any = live >> buf & 1u;
+            const uint32_t stage = g * SG + so.idx;
             const uint64_t a = oa0 + static_cast<uint64_t>(stage * (kAttnHalfBytes >> 4));
-            const uint64_t b = ob + static_cast<uint64_t>(pbuf * (kAttnTile * N2 >> 4));
+            const uint64_t b = ob + static_cast<uint64_t>(buf * (kAttnTile * N2 >> 4));
             if (ptx::elect_one()) {
               if (any) {
 #pragma unroll
                 for (int kk = 0; kk < kAttnTile / 32; ++kk)
                   ptx::mma_f8f6f4(tmem + kTmemO + g * N2, a + kk * (32ull * 128 >> 4), b + kk * (32ull * N2 >> 4), kIdescO,
                                   (first && kk == 0) ? 0u : 1u);
-                ptx::mma_commit(pe0 + 8u * (g * PB + pbuf));
-                ptx::mma_commit(empty0 + 8u * stage);
-              } else {
-                ptx::mbar_arrive(empty0 + 8u * stage);
               }
+              ptx::mma_commit(pe0 + bar);
+              ptx::mma_commit(empty0 + 8u * stage);
             }
             __syncwarp();
-            if (any) {
-              first = false;
-              ++n_out;
-            }
+            first = first && !any;
             ++io;
             so.next();
             if (--left_o == 0) {
@@ -549,6 +517,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
             spins = 0;
             continue;
           }
+        }
+        if (is < own && is < io + SBG && __all_sync(kFull, ptx::mbar_test_wait(full0 + 8u * (g * SG + ss.idx), ss.phase))) {
+          const int buf = unit_s % QB;
+          if (left_s == per_unit && !attn_wait(qf0 + 8u * buf, (unit_s / QB) & 1, abort_flag, kSiteQFull)) break;
+          const uint32_t stage = g * SG + ss.idx, slot = g * SBG + (is & 1);
+          const uint4 m = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * stage);
+          const bool any = (m.x | m.y | m.z | m.w) != 0u;
+          live = (live & ~(1u << (is & 1))) | static_cast<uint32_t>(any) << (is & 1);
+          ptx::fence_proxy_async_smem();  // the tile was written by cp.async
+          ptx::tc_fence_after();
+          const uint64_t a = sa0 + static_cast<uint64_t>((KS > 0 ? slot : stage) * (kAttnHalfBytes >> 4));
+          const uint64_t b = sb0 + static_cast<uint64_t>(buf * (N2 * 128u >> 4));
+          if (ptx::elect_one()) {
+            if (any) {
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                ptx::mma_f8f6f4(tmem + slot * N2, a + 2ull * kk, b + 2ull * kk, kIdescS, kk > 0 ? 1u : 0u);
+            }
+            ptx::mma_commit(sf0 + 8u * slot);
+            if (left_s == 1) ptx::mma_commit(qe0 + 8u * buf);  // the unit's last tile
+          }
+          __syncwarp();
+          ++is;
+          ss.next();
+          if (--left_s == 0) {
+            left_s = per_unit;
+            unit_s += NG;
+          }
+          spins = 0;
+          continue;
         }
         if ((++spins & 63u) == 0u) {
           bool give_up = *abort_flag != 0u;
@@ -582,11 +580,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     const uint32_t p_swz = N2 == 64 ? (tg >> 1) & 3 : (tg >> 2) & 1;
     const int bar_id = 1 + g;
     Ring st{0u, 0u, static_cast<uint32_t>(SG)};
-    uint32_t n_own = 0, n_tile = 0;                   // this group's tiles, those with entries
+    uint32_t n = 0;                                   // this group's tiles so far
     bool stop = false;
-    // the output MMA of the last tile with entries (they complete in order)
-    const auto last_out = [&] { return pe0 + 8u * (g * PB + ((n_tile - 1u) & 1u)); };
-    const auto last_parity = [&] { return ((n_tile - 1u) >> 1) & 1u; };
+    // the output MMA of the last tile before this one (they complete in order)
+    const auto wait_outputs = [&] {
+      attn_wait(pe0 + 8u * (g * PB + ((n - 1u) & 1u)), ((n - 1u) >> 1) & 1u, abort_flag, kSiteAccEmpty);
+      ptx::tc_fence_after();
+    };
     if (CLUSTER && t0 < t1) {
       // The unit's query: nothing else is to be done yet, and 256 threads have
       // it ready by the time the first tile is.
@@ -648,17 +648,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         const uint32_t stage = g * SG + st.idx, stage_phase = st.phase;
         st.next();
         asm volatile("" : "+r"(has_o));  // (one copy of the loop: the first tile is not peeled off)
-        const uint32_t slot = g * SBG + (n_own & 1u), slot_parity = (n_own >> 1) & 1u;
-        ++n_own;
-        ok = attn_wait2(full0 + 8u * stage, stage_phase, sf0 + 8u * slot, slot_parity, abort_flag, kSiteStageFull,
-                        kSiteAccFull) && ok;
+        // (accumulators of scores and buffers of probabilities take turns alike)
+        const uint32_t buf = n & 1u, parity = (n >> 1) & 1u;
+        const uint32_t slot = g * SBG + buf, pbar = 8u * (g * PB + buf);
+        uint8_t* const p_row = p_rows + buf * kAttnTile * N2;
+        ok = attn_wait3(full0 + 8u * stage, stage_phase, sf0 + 8u * slot, parity, pe0 + pbar, parity ^ 1u, abort_flag,
+                        kSiteStageFull, kSiteAccFull, kSiteAccEmpty) && ok;
         const uint4 mk = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * stage);
         const bool any = (mk.x | mk.y | mk.z | mk.w) != 0u;
         const uint32_t mw = quad == 0 ? mk.x : quad == 1 ? mk.y : quad == 2 ? mk.z : mk.w;
         const bool valid = mw >> lane & 1u;
         const float2 sc = reinterpret_cast<const float2*>(smem + L.scale)[stage * kAttnTile + tg];
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(empty0 + 8u * stage);
         const float c = valid ? sc.x * qscale : 0.f;
         const float vs = valid ? fmaxf(sc.y, 0.f) : 0.f;
         const float4* nm4 = reinterpret_cast<const float4*>(valid ? stt.nm[g] : stt.ninf);
@@ -688,9 +688,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         // The probabilities are computed and stored against the m in hand; if
         // one of them shows that m is too small (or m is not set yet), the
         // group takes the maxima and does them over.
-        const uint32_t pbuf = n_tile & 1u;
-        uint8_t* const p_row = p_rows + pbuf * kAttnTile * N2;
-        ok = attn_wait(pe0 + 8u * (g * PB + pbuf), ((n_tile >> 1) & 1u) ^ 1u, abort_flag, kSiteAccEmpty) && ok;  // P is free
 #pragma unroll 1
         for (bool fresh = false;; fresh = true) {
           bool again = any && !fresh && (!has_o || vs > kMaxW * cref);
@@ -762,8 +759,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
           ptx::bar_sync(bar_id, 128);
           cref = stt.cref[g];
           if (has_o) {
-            attn_wait(last_out(), last_parity(), abort_flag, kSiteAccEmpty);
-            ptx::tc_fence_after();
+            wait_outputs();
 #pragma unroll
             for (int j = 0; j < GP / 2; ++j) {
               const float2 f = *reinterpret_cast<const float2*>(&stt.resc[g][2 * j]);
@@ -785,24 +781,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         }
         if (stop) break;
         ptx::tc_fence_before();
-        if (!any) {
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(se0 + 8u * slot);
-          continue;
-        }
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(se0 + 8u * slot);
-          ptx::mbar_arrive(pf0 + 8u * (g * PB + pbuf));
-        }
-        has_o = 1u;
-        ++n_tile;
+        if (lane == 0) ptx::mbar_arrive(pf0 + pbar);  // (of a tile without entries: that it has been looked at)
+        has_o |= any;
+        ++n;
       }
       if (stop) break;
 
       // ---- the unit's end: the sums over the group's tokens, and the output
-      if (has_o) attn_wait(last_out(), last_parity(), abort_flag, kSiteAccEmpty);
-      ptx::tc_fence_after();
       {
         float v[GP];
 #pragma unroll
@@ -810,10 +796,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         const float sum = reduce_columns<GP, false>(v, lane);
         if (lane < GP) stt.part[g][quad][lane] = sum;
       }
-      ptx::bar_sync(bar_id, 128);
       int row, kvh, h0;
       unit_of(p, u0 + unit * ustep, &row, &kvh, &h0, GP);
       const int nh = min(GP, p.group - h0);
+      const int ch = D == 128 ? tg : tg - 64;  // D = 64: the value half of the shared rows
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row / p.next_n * p.out_req_stride +
+                           row % p.next_n * p.out_row_stride + (kvh * p.group + h0) * p.out_head_stride + ch;
+      ptx::bar_sync(bar_id, 128);
       if (tg < GP) {
         const float sum = (stt.part[g][0][tg] + stt.part[g][1][tg]) + (stt.part[g][2][tg] + stt.part[g][3][tg]);
         const float m = has_o ? -stt.nm[g][tg] : kMinM;
@@ -829,38 +818,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
                 sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
         }
       }
+      if (has_o) wait_outputs();
       if constexpr (CLUSTER) {  // the outputs go where the tiles were: both groups are done with them
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ub);
         attn_wait(ub, 0, abort_flag, kSiteAccFull);
       }
       ptx::bar_sync(bar_id, 128);
-      const int ch = D == 128 ? tg : tg - 64;  // D = 64: the value half of the shared rows
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row / p.next_n * p.out_req_stride +
-                           row % p.next_n * p.out_row_stride + (kvh * p.group + h0) * p.out_head_stride + ch;
       float* xo = reinterpret_cast<float*>(smem + L.k) + g * GP * 128 + tg;  // cluster: [group][GP][128]
 #pragma unroll 1
-      for (int b = 0; b < GP; b += 8) {
-        float v[8];
+      for (int b = 0; b < GP; b += 16) {
+        float v[16];
         if (has_o) {
-          uint32_t hi[8], lo[8];
-          ptx::tmem_ld_32x32b_x8(o_tm + b, hi);
-          ptx::tmem_ld_32x32b_x8(o_tm + GP + b, lo);
+          uint32_t hi[16], lo[16];
+          ptx::tmem_ld_32x32b_x16(o_tm + b, hi);
+          ptx::tmem_ld_32x32b_x16(o_tm + GP + b, lo);
           ptx::tmem_wait_ld_n(hi);
           ptx::tmem_wait_ld_n(lo);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+          for (int j = 0; j < 16; ++j)
             v[j] = fmaf(__uint_as_float(lo[j]), 0.0625f, __uint_as_float(hi[j])) * stt.fac[g][b + j];
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = 0.f;
+          for (int j = 0; j < 16; ++j) v[j] = 0.f;
         }
         if constexpr (CLUSTER) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) xo[(b + j) * 128] = v[j];
+          for (int j = 0; j < 16; ++j) xo[(b + j) * 128] = v[j];
         } else if (ch >= 0) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 16; ++j) {
             if (b + j < nh) *out = __float2bfloat16(v[j]);
             out += p.out_head_stride;
           }
