@@ -114,7 +114,7 @@ struct AttnSmem {
   uint32_t k, v, q, p, scale, mask, flt, bars, misc, total;
 };
 // Floats of the softmax state of one CTA, GP heads (AttnState in sparse_attn.cu).
-__host__ __device__ constexpr int attn_state_floats(int gp) { return 24 * gp + 32; }
+__host__ __device__ constexpr int attn_state_floats(int gp) { return 24 * gp + 48; }
 __host__ __device__ constexpr AttnSmem attn_smem_layout(int head_dim, int gp) {
   AttnSmem L{};
   const uint32_t stages = static_cast<uint32_t>(attn_v_stages(head_dim, gp));

@@ -119,9 +119,22 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Where a unit's results go: elements from `out` and `lse` on, heads it has.
+struct UnitPlace {
+  int64_t out;
+  int32_t lse, heads;
+};
+__device__ __forceinline__ UnitPlace place_of(const SparseAttnParams& p, int row, int head, int heads) {
+  const int req = row / p.next_n;
+  return {req * p.out_req_stride + (row - req * p.next_n) * p.out_row_stride + head * p.out_head_stride,
+          row * p.heads + head, heads};
+}
+
 // Softmax state of a CTA in shared memory; NG epilogue groups.
 template <int GP, int NG, int QB>
 struct AttnState {
+  UnitPlace qplace[QB];        // [query buffer]
+  UnitPlace place[NG];         // [group]
   float nm[NG][GP];            // -m of each group (log2 units), 0 before a unit's first tile
   float ninf[GP];              // -inf: the row of -m that an entry without a token reads
   float part[NG][4][GP];       // [group][warp]: a tile's maxima over m; a unit's sums
@@ -460,7 +473,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
           if (g < nh) v = __ldg(reinterpret_cast<const uint4*>(q + g * p.q_head_stride + piece * 8));
           store_query<GP>(smem + L.q + buf * N2 * 128, g, piece, v, power_of_two(e), qs.odd);
         }
-        if (lane == 0) stt.qf[buf] = power_of_two(-e);
+        if (lane == 0) {
+          stt.qf[buf] = power_of_two(-e);
+          stt.qplace[buf] = place_of(p, row, kvh * p.group + h0, nh);
+        }
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(qf0 + 8u * buf);
@@ -621,10 +637,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         const int c = static_cast<int>(threadIdx.x) + 256 * i;
         if (c < GP * kPer) store_query<GP>(smem + L.q, c / kPer, c % kPer, v[i], power_of_two(e), qs.odd);
       }
-      if (threadIdx.x == 0) stt.qf[0] = power_of_two(-e);
+      if (threadIdx.x == 0) {
+        stt.qf[0] = power_of_two(-e);
+        stt.qplace[0] = place_of(p, row, kvh * p.group + h0, nh);
+      }
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(qf0);
+    }
+    if (CLUSTER && t0 >= t1 && threadIdx.x == 0) {  // (a CTA without tiles finishes heads as well)
+      int row, kvh, h0;
+      unit_of(p, u0, &row, &kvh, &h0, GP);
+      stt.qplace[0] = place_of(p, row, kvh * p.group + h0, min(GP, p.group - h0));
     }
 #pragma unroll 1
     for (int r = 0; r < own_units(g) && !stop; ++r) {
@@ -634,6 +658,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       if (t0 < t1) {
         ok = attn_wait(qf0 + 8u * (unit % QB), (unit / QB) & 1, abort_flag, kSiteQFull);
         qscale = stt.qf[unit % QB] * p.scale_log2;
+        if (!CLUSTER && tg == 0) stt.place[g] = stt.qplace[unit % QB];  // (read between the unit's last two barriers)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(qe0 + 8u * (unit % QB));
       }
@@ -654,6 +679,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         uint8_t* const p_row = p_rows + buf * kAttnTile * N2;
         ok = attn_wait3(full0 + 8u * stage, stage_phase, sf0 + 8u * slot, parity, pe0 + pbar, parity ^ 1u, abort_flag,
                         kSiteStageFull, kSiteAccFull, kSiteAccEmpty) && ok;
+        ptx::tc_fence_after();
+        const uint32_t s_tm = tmem + slot * N2 + lane_off;
+        // The scores of the first 16 heads (of no meaning in a tile without
+        // entries); 32 heads need the registers (early: 342 us, late: 333 us).
+        uint32_t hi[16], lo[16];
+        if constexpr (GP == 16) {
+          ptx::tmem_ld_32x32b_x16(s_tm, hi);
+          ptx::tmem_ld_32x32b_x16(s_tm + GP, lo);
+        }
         const uint4 mk = *reinterpret_cast<const uint4*>(smem + L.mask + 16 * stage);
         const bool any = (mk.x | mk.y | mk.z | mk.w) != 0u;
         const uint32_t mw = quad == 0 ? mk.x : quad == 1 ? mk.y : quad == 2 ? mk.z : mk.w;
@@ -662,16 +696,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         const float c = valid ? sc.x * qscale : 0.f;
         const float vs = valid ? fmaxf(sc.y, 0.f) : 0.f;
         const float4* nm4 = reinterpret_cast<const float4*>(valid ? stt.nm[g] : stt.ninf);
-        const uint32_t s_tm = tmem + slot * N2 + lane_off;
-        ptx::tc_fence_after();
         // scores of heads b .. b+15 over the present m, in log2 units
-        const auto scores = [&](int b, float (&t)[16]) {
+        const auto scores = [&](int b, const uint32_t (&hi)[16], const uint32_t (&lo)[16], float (&t)[16]) {
           const float2 c2 = make_float2(c, c), k16 = make_float2(0.0625f, 0.0625f);
-          uint32_t hi[16], lo[16];
-          ptx::tmem_ld_32x32b_x16(s_tm + b, hi);
-          ptx::tmem_ld_32x32b_x16(s_tm + GP + b, lo);
-          ptx::tmem_wait_ld_n(hi);
-          ptx::tmem_wait_ld_n(lo);
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const float4 nm = nm4[(b + j) / 4];
@@ -685,20 +712,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
             }
           }
         };
+        if constexpr (GP == 16) {
+          ptx::tmem_wait_ld_n(hi);
+          ptx::tmem_wait_ld_n(lo);
+        }
         // The probabilities are computed and stored against the m in hand; if
         // one of them shows that m is too small (or m is not set yet), the
         // group takes the maxima and does them over.
 #pragma unroll 1
         for (bool fresh = false;; fresh = true) {
-          bool again = any && !fresh && (!has_o || vs > kMaxW * cref);
+          bool again = false;
           if (any && (has_o || fresh)) {
             const float w = vs * __fdividef(kPScale, cref);
             const __half2 w2 = __floats2half2_rn(w, w);
             __half2 top = __floats2half2_rn(0.f, 0.f);
+            float t[16];
+            if constexpr (GP > 16) {
+              ptx::tmem_ld_32x32b_x16(s_tm, hi);
+              ptx::tmem_ld_32x32b_x16(s_tm + GP, lo);
+              ptx::tmem_wait_ld_n(hi);
+              ptx::tmem_wait_ld_n(lo);
+            }
+            scores(0, hi, lo, t);
 #pragma unroll
             for (int b = 0; b < GP; b += 16) {
-              float t[16];
-              scores(b, t);
               uint32_t ph[4], pl[4];
 #pragma unroll
               for (int j = 0; j < 16; j += 4) {
@@ -717,20 +754,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
               }
               *reinterpret_cast<uint4*>(p_row + (((b / 16) ^ p_swz) << 4)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
               *reinterpret_cast<uint4*>(p_row + ((((GP + b) / 16) ^ p_swz) << 4)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+              if (b + 16 < GP) {
+                uint32_t hi1[16], lo1[16];
+                ptx::tmem_ld_32x32b_x16(s_tm + b + 16, hi1);
+                ptx::tmem_ld_32x32b_x16(s_tm + GP + b + 16, lo1);
+                ptx::tmem_wait_ld_n(hi1);
+                ptx::tmem_wait_ld_n(lo1);
+                scores(b + 16, hi1, lo1, t);
+              }
             }
             ptx::fence_proxy_async_smem();  // (before the vote, which hides some of its wait)
-            again = again || (!fresh && !__hble2(top, __floats2half2_rn(kMaxP, kMaxP)));
+            again = !fresh && (vs > kMaxW * cref || !__hble2(top, __floats2half2_rn(kMaxP, kMaxP)));
           }
-          if (!ptx::bar_or(bar_id, 128, again || !ok)) break;
-          if (ptx::bar_or(bar_id, 128, !ok)) {  // an abandoned call: all four warps leave
-            stop = true;
-            break;
-          }
+          // (a unit's first tile with entries needs no vote)
+          if ((!any || has_o || fresh) && !ptx::bar_or(bar_id, 128, again || !ok)) break;
           // ---- new maxima
           {
             float v[GP];
 #pragma unroll
-            for (int b = 0; b < GP; b += 16) scores(b, *reinterpret_cast<float(*)[16]>(&v[b]));
+            for (int b = 0; b < GP; b += 16) {
+              uint32_t h[16], l[16];
+              ptx::tmem_ld_32x32b_x16(s_tm + b, h);
+              ptx::tmem_ld_32x32b_x16(s_tm + GP + b, l);
+              ptx::tmem_wait_ld_n(h);
+              ptx::tmem_wait_ld_n(l);
+              scores(b, h, l, *reinterpret_cast<float(*)[16]>(&v[b]));
+            }
             if (has_o) {  // take the tile's sums back (what a huge one leaves is nothing beside it)
 #pragma unroll
               for (int j = 0; j < GP / 2; ++j) {
@@ -743,7 +792,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
           }
           const float vmax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vs)));
           if (lane == 0) stt.wvs[g][quad] = vmax;
-          ptx::bar_sync(bar_id, 128);
+          if (ptx::bar_or(bar_id, 128, !ok)) {  // an abandoned call: all four warps leave
+            stop = true;
+            break;
+          }
           if (tg < GP) {
             float d = fmaxf(fmaxf(stt.part[g][0][tg], stt.part[g][1][tg]), fmaxf(stt.part[g][2][tg], stt.part[g][3][tg]));
             d = fmaxf(d, has_o ? -kMargin : kMinM) + kMargin;
@@ -796,13 +848,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         const float sum = reduce_columns<GP, false>(v, lane);
         if (lane < GP) stt.part[g][quad][lane] = sum;
       }
-      int row, kvh, h0;
-      unit_of(p, u0 + unit * ustep, &row, &kvh, &h0, GP);
-      const int nh = min(GP, p.group - h0);
-      const int ch = D == 128 ? tg : tg - 64;  // D = 64: the value half of the shared rows
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row / p.next_n * p.out_req_stride +
-                           row % p.next_n * p.out_row_stride + (kvh * p.group + h0) * p.out_head_stride + ch;
       ptx::bar_sync(bar_id, 128);
+      const UnitPlace pl = stt.place[g];  // (a cluster's outputs go out further down)
+      const int nh = pl.heads;
       if (tg < GP) {
         const float sum = (stt.part[g][0][tg] + stt.part[g][1][tg]) + (stt.part[g][2][tg] + stt.part[g][3][tg]);
         const float m = has_o ? -stt.nm[g][tg] : kMinM;
@@ -814,7 +862,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         } else {
           stt.fac[g][tg] = sum == 0.f ? 0.f : cref / (sum * kPScale);
           if (p.lse != nullptr && tg < nh)
-            p.lse[static_cast<int64_t>(row) * p.heads + kvh * p.group + h0 + tg] =
+            p.lse[pl.lse + tg] =
                 sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
         }
       }
@@ -825,6 +873,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         attn_wait(ub, 0, abort_flag, kSiteAccFull);
       }
       ptx::bar_sync(bar_id, 128);
+      const int ch = D == 128 ? tg : tg - 64;  // D = 64: the value half of the shared rows
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + pl.out + ch;
       float* xo = reinterpret_cast<float*>(smem + L.k) + g * GP * 128 + tg;  // cluster: [group][GP][128]
 #pragma unroll 1
       for (int b = 0; b < GP; b += 16) {
@@ -867,9 +917,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     meet();
     const int R = C * NG, heads = GP / C, first = crank * heads;  // partial results, heads of this CTA
     if (warp < 4 * NG) {  // (the others have few registers left)
-      int row, kvh, h0;
-      unit_of(p, u0, &row, &kvh, &h0, GP);
-      const int nh = min(GP, p.group - h0);
+      const UnitPlace pl = stt.qplace[0];
+      const int nh = pl.heads;
       // thread (head, r), r fastest: the factor of partial result r
       if (threadIdx.x < GP * NG) {
         const int r = static_cast<int>(threadIdx.x) % R, h = first + static_cast<int>(threadIdx.x) / R;
@@ -887,14 +936,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         for (int d = R / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(lanes, sum, d);
         (&stt.fac[0][0])[threadIdx.x] = sum == 0.f ? 0.f : __fdividef(f, sum);
         if (p.lse != nullptr && r == 0 && h < nh)
-          p.lse[static_cast<int64_t>(row) * p.heads + kvh * p.group + h0 + h] =
+          p.lse[pl.lse + h] =
               sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
       }
       ptx::bar_sync(1 + NG, 4 * NG * 32);
       // a warp per head, four channels a lane
       const int ch = 4 * lane - (D == 128 ? 0 : 64);
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row / p.next_n * p.out_req_stride +
-                           row % p.next_n * p.out_row_stride + (kvh * p.group + h0) * p.out_head_stride + ch;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + pl.out + ch;
       const uint32_t xo = ptx::smem_u32(smem + L.k) + 16u * lane;
 #pragma unroll 1
       for (int i = warp; i < heads; i += 4 * NG) {
