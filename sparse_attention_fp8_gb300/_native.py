@@ -92,6 +92,8 @@ def library_path() -> str:
 def library():
     """The loaded libfp8idx; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -178,15 +180,20 @@ def _host_mapped(t) -> int:
     return dev.value
 
 
-def _pack(t, ptr: int) -> bytes:
-    """Packs tensor t's dtype, shape and strides with data address ptr into
-    fp8idx_tensor bytes."""
+def _dtype_code(dtype):
+    """The library's code of a torch dtype, None if it has none."""
     global _dtype_codes
     if _dtype_codes is None:
         import torch
         _dtype_codes = {torch.uint8: _U8, torch.float8_e4m3fn: _U8, torch.float32: _F32, torch.int32: _I32,
                         torch.bfloat16: _BF16, torch.float16: _F16}
-    dt = _dtype_codes.get(t.dtype)
+    return _dtype_codes.get(dtype)
+
+
+def _pack(t, ptr: int) -> bytes:
+    """Packs tensor t's dtype, shape and strides with data address ptr into
+    fp8idx_tensor bytes."""
+    dt = _dtype_code(t.dtype)
     if dt is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
     shape = t.shape
@@ -326,20 +333,40 @@ def fp8_paged_mqa_topk(q_fp8, kv_cache, weights, context_lens, block_tables, max
     return indices
 
 
-def _on_current_device(*tensors):
-    """The library launches on the current device: every tensor has to be
-    there (a kernel cannot be sent after the data of another device)."""
+def _descs(*tensors):
+    """The packed descriptors of a call (None stays None).  The library
+    launches on the current device: every tensor has to be there (a kernel
+    cannot be sent after the data of another device).  One pass over the
+    tensors with the row-shaped cases spelt out: a step's tables have twelve
+    descriptors, which costs 6 us this way and 13 us tensor by tensor."""
     import torch
+    _dtype_code(torch.uint8)
+    codes, pack = _dtype_codes, _TENSOR_PACK.pack
     dev = None
+    out = []
     for t in tensors:
         if t is None:
+            out.append(None)
             continue
-        if not t.is_cuda:
-            raise ValueError("inputs must be CUDA tensors")
-        if dev is None:
+        at = t.get_device()
+        if at != dev:
+            if at < 0:
+                raise ValueError("inputs must be CUDA tensors")
             dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+            if at != dev:
+                raise ValueError(f"a tensor is on cuda:{at}, the current device is cuda:{dev}")
+        dt = codes.get(t.dtype)
+        shape, stride = t.shape, t.stride()
+        n = len(shape)
+        if dt is None or n > 4:
+            _pack(t, 0)  # (says what is wrong)
+        if n == 1:
+            out.append(pack(t.data_ptr(), dt, 1, shape[0], 0, 0, 0, stride[0], 0, 0, 0))
+        elif n == 2:
+            out.append(pack(t.data_ptr(), dt, 2, shape[0], shape[1], 0, 0, stride[0], stride[1], 0, 0))
+        else:
+            out.append(pack(t.data_ptr(), dt, n, *shape, *_PAD[n:], *stride, *_PAD[n:]))
+    return out
 
 
 def kv_page_bytes(block_size, head_dim) -> int:
@@ -354,10 +381,8 @@ def paged_step_tables(old_lens, new_lens, free_blocks, free_count, block_size, b
     context lengths, slots and prefill windows from the requests' lengths.
     Returns slot_mapping; counts holds [new tokens, blocks dealt, free blocks
     left, blocks missing]."""
-    ts = (old_lens, new_lens, free_blocks, free_count, block_tables, context_lens, cu_new_lens, slot_mapping, counts,
-          cu_seq_lens, cu_seqlen_ks, cu_seqlen_ke)
-    _on_current_device(*ts)
-    d = [None if t is None else _pack(t, t.data_ptr()) for t in ts]
+    d = _descs(old_lens, new_lens, free_blocks, free_count, block_tables, context_lens, cu_new_lens, slot_mapping, counts,
+               cu_seq_lens, cu_seqlen_ks, cu_seqlen_ke)
     _check(library().fp8idx_paged_step_tables(*d[:4], int(block_size), *d[4:], _stream(stream, old_lens)))
     return slot_mapping
 
@@ -367,9 +392,7 @@ def fp8_paged_store(k, v, slot_mapping, kv_cache, stream=None):
     writes them at their slots (a negative slot is skipped): k [tokens, D]
     into an index cache (v None), or k and v [tokens, kv_heads, D] into a
     key/value cache."""
-    ts = (k, v, slot_mapping, kv_cache)
-    _on_current_device(*ts)
-    d = [None if t is None else _pack(t, t.data_ptr()) for t in ts]
+    d = _descs(k, v, slot_mapping, kv_cache)
     _check(library().fp8_paged_store(*d, _stream(stream, k)))
     return kv_cache
 
@@ -379,9 +402,7 @@ def fp8_paged_sparse_attn(q, kv_cache, indices, block_tables, softmax_scale, out
     """Decode attention of q [batch, next_n, heads, D] over the positions
     indices [batch*next_n, k] of each request (-1: no position) into ``out``,
     and the log-sum-exp of the scores into ``lse``."""
-    ts = (q, kv_cache, indices, block_tables, out, lse)
-    _on_current_device(*ts)
-    d = [None if t is None else _pack(t, t.data_ptr()) for t in ts]
+    d = _descs(q, kv_cache, indices, block_tables, out, lse)
     oc = options._c() if options is not None else None
     _check(library().fp8_paged_sparse_attn(*d[:4], float(softmax_scale), *d[4:],
                                            ctypes.byref(oc) if oc is not None else None, _stream(stream, q)))
@@ -393,9 +414,7 @@ def fp8_mqa_sparse_attn_paged(q, kv_cache, block_tables, cu_seq_lens, indices, s
     """Prefill attention of q [M, heads, D] over the columns indices [M, k]
     of the packed requests (column i with cu_seq_lens[r] <= i <
     cu_seq_lens[r+1] is a token of request r; -1: no column)."""
-    ts = (q, kv_cache, block_tables, cu_seq_lens, indices, out, lse)
-    _on_current_device(*ts)
-    d = [None if t is None else _pack(t, t.data_ptr()) for t in ts]
+    d = _descs(q, kv_cache, block_tables, cu_seq_lens, indices, out, lse)
     oc = options._c() if options is not None else None
     _check(library().fp8_mqa_sparse_attn_paged(*d[:5], float(softmax_scale), *d[5:],
                                                ctypes.byref(oc) if oc is not None else None, _stream(stream, q)))
