@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         // group takes the maxima and does them over.
 #pragma unroll 1
         for (bool fresh = false;; fresh = true) {
-          bool again = false;
+          bool again = any && !has_o && !fresh;
           if (any && (has_o || fresh)) {
             const float w = vs * __fdividef(kPScale, cref);
             const __half2 w2 = __floats2half2_rn(w, w);
@@ -766,8 +766,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
             ptx::fence_proxy_async_smem();  // (before the vote, which hides some of its wait)
             again = !fresh && (vs > kMaxW * cref || !__hble2(top, __floats2half2_rn(kMaxP, kMaxP)));
           }
-          // (a unit's first tile with entries needs no vote)
-          if ((!any || has_o || fresh) && !ptx::bar_or(bar_id, 128, again || !ok)) break;
+          // (every warp votes in every pass: an abandoned call may have left them with different masks)
+          if (!ptx::bar_or(bar_id, 128, again || !ok)) break;
           // ---- new maxima
           {
             float v[GP];
