@@ -153,6 +153,6 @@ def sparse_attention(q, cache, indices, block_tables, block_size, scale, next_n=
                 lse[r, h] = top + np.log(z)
                 out[r, h] = w @ val
                 mag[r, h] = w @ np.abs(val)
-                floor[r, h] = w.max() * sc[:, 1].max() * np.abs(codes[:, D:]).sum(0)
+                floor[r, h] = w.max() * np.abs(sc[:, 1]).max() * np.abs(codes[:, D:]).sum(0)
                 sabs[r, h] = (np.abs(scale) * (np.abs(key) @ np.abs(q[r, h]))).max()
     return out, lse, mag, floor, sabs

@@ -10,42 +10,49 @@
 //   O^T [128 channels x 2 GP] += V tile^T (A, MN-major) * [Ph | Pl] (B, MN-major)
 // GP is the head count padded to 16 or 32.  The 16-bit operands are split
 // into two e4m3 values: x = h + l / 16 with h = e4m3(x), l = e4m3(16 (x - h)).
-// That keeps 8 significant bits -- a bf16 query exactly, a probability to
-// 2^-8 -- down to 2^-21 of the largest query element (queries are scaled by a
-// power of two so that it lies in [128, 256)).  The two halves have their own
-// accumulator columns and meet in f32.  Dequantising the tile to 16 bits
-// instead would take a conversion per cache byte and twice the shared memory.
+// That keeps 8 significant bits: a bf16 query exactly (down to 2^-21 of the
+// unit's largest element; queries are scaled by a power of two that puts it
+// into [128, 256)), a probability to 2^-8 of itself, or to half a step of
+// 2^-18 of the largest one.  The two halves have their own accumulator columns
+// and meet in f32.  Dequantising the tile to 16 bits instead would take a
+// conversion per cache byte and twice the shared memory.
 //
-// The gather bounds this kernel: a unit reads 2*D + 8 bytes per entry, once
-// per row and key head, mostly from L2, while the two products need little
-// (with 32 heads a tile's eight MMAs take about a third of its copy).  So a
-// unit's tile is M = 128 tokens by all heads of the key head, every byte is
-// fetched once, and a ring of tiles keeps the copies of several tiles in
-// flight.
+// A CTA (20 warps) is two pipelines side by side, which share nothing but the
+// query warp.  Each has
+//  * four producer warps: a lane resolves one entry of the tile to its cache
+//    row (indices are loaded two tiles ahead, block-table entries one), then
+//    the warp copies its 32 rows, 16 bytes a lane, into the 128-byte swizzle
+//    that the tensor cores read, and the scales.  Entries that select nothing
+//    copy zeros; a tile without any entry costs no product.  (cp.async: a
+//    gathering TMA copy of four rows takes 67 clocks to issue, 4300 a tile of
+//    head_dim 128, where this takes 900.)
+//  * an issuing warp: the output product of the oldest tile whose
+//    probabilities are there, else the scores of a tile, at most two ahead:
+//    accumulators of scores, buffers of probabilities and key stages take
+//    turns in step, so one barrier each way serves all three.
+//  * an epilogue warpgroup (thread = token): scores times the token's scale,
+//    probability 2^(t - m), its sum per head in the thread, and P (times the
+//    token's value scale) into shared memory as the next product's operand.
+//    m is the maximum of the tile in which it was last set, plus a margin: a
+//    later tile keeps it unless a probability exceeds 4, or a value scale 1.25
+//    times the largest one in hand, which takes one vote of the group a tile
+//    instead of a maximum per head across its 128 threads.  A tile that does
+//    not keep it takes the exact maxima, rescales the sums and the accumulator
+//    and is done over.
+// Many units: persistent CTAs, each pipeline with units of its own.  Few: a
+// cluster of 1, 2, 4 or 8 CTAs per unit, whose pipelines share its tiles; their
+// results meet in f32 through distributed shared memory.  Which one, by the
+// tiles of the busiest SM, is decided on the host (api.cpp).
 //
-// Roles of a CTA (12 warps; persistent over units, or one unit per cluster):
-//  * Producer warps (two, alternate tiles): each lane resolves four entries
-//    to cache rows (block-table entries loaded one tile ahead, indices two)
-//    and fetches their key and value rows with gathering TMA copies of four
-//    rows, their scales with 8-byte cp.async.  Entries that select nothing
-//    read row -1, which the copy fills with zeros; a tile without any entry
-//    is published empty and costs no copy and no MMA.
-//  * Query warp: splits the next unit's query into Qh and Ql.
-//  * MMA warp: issues S of a later tile whenever its data is there, else the
-//    output MMA of the oldest tile whose probabilities are.
-//  * Epilogue warpgroups (two, alternate tiles; thread = token): scores times
-//    the token's scale, probability 2^(t - m), its sum per head in the
-//    thread, and P (scaled by the token's value scale) into shared memory as
-//    the next MMA's operand.  Each group keeps its own maximum m, sums and
-//    output accumulator, so the groups meet once per unit.
-//    m is the maximum of the tile in which it was last set: a later tile that
-//    stays below m + 2 (in log2) keeps it, so a tile needs one vote of the
-//    group instead of a maximum per head across its 128 threads; a tile that
-//    does not takes the exact maxima and rescales the sums and the
-//    accumulator.  P then is at most 8 (4 for the score, 2 for the value
-//    scale, kept the same way), 256 after the factor 32.
-//  * Few units: a cluster of 2, 4 or 8 CTAs per unit, each with a share of
-//    the tiles; their outputs meet in f32 through distributed shared memory.
+// What bounds it: 16 query heads and more per key head, the softmax's latency
+// (a tile of 32 heads takes a warpgroup 2600 clocks, 1150 of them arithmetic,
+// the rest waits, votes and fences between roles; two pipelines fill 60% of the
+// issue slots; the products need a tenth of it).  4096 prompt rows of 32 heads
+// and 2048 entries: 332 us, 414 TFLOP/s.  8 heads a key head over pages of one
+// token: the scattered rows (1.3 GB through L2 in 241 us; 182 us if the pages
+// lie in order, 137 us with pages of 64 tokens).  One decode row: latency,
+// 9.2 us, of which two dependent loads before the first copy take 1.4, the
+// meeting of the cluster 2.
 // Every wait is bounded (common.cuh).  After a wait has run out the group
 // votes, so that its four warps leave together and no barrier is left open.
 #include <cooperative_groups.h>
@@ -67,7 +74,7 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 // P's codes reach from 448 (the largest e4m3 value) down to steps of 2^-13
-// (the smallest one of the second part).  A probability over m may grow to
+// (the smallest one of the second part: 2^-9 / 16).  A probability over m may grow to
 // kMaxP and a value scale to kMaxW times the one in hand before both are
 // taken anew, at m = the largest score + kMargin: with normally distributed
 // scores a unit of 2048 entries then does that once, at its first tile.
@@ -694,7 +701,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         const bool valid = mw >> lane & 1u;
         const float2 sc = reinterpret_cast<const float2*>(smem + L.scale)[stage * kAttnTile + tg];
         const float c = valid ? sc.x * qscale : 0.f;
-        const float vs = valid ? fmaxf(sc.y, 0.f) : 0.f;
+        const float vs = valid ? sc.y : 0.f;
         const float4* nm4 = reinterpret_cast<const float4*>(valid ? stt.nm[g] : stt.ninf);
         // scores of heads b .. b+15 over the present m, in log2 units
         const auto scores = [&](int b, const uint32_t (&hi)[16], const uint32_t (&lo)[16], float (&t)[16]) {
@@ -764,7 +771,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
               }
             }
             ptx::fence_proxy_async_smem();  // (before the vote, which hides some of its wait)
-            again = !fresh && (vs > kMaxW * cref || !__hble2(top, __floats2half2_rn(kMaxP, kMaxP)));
+            again = !fresh && (fabsf(vs) > kMaxW * cref || !__hble2(top, __floats2half2_rn(kMaxP, kMaxP)));
           }
           // (every warp votes in every pass: an abandoned call may have left them with different masks)
           if (!ptx::bar_or(bar_id, 128, again || !ok)) break;
@@ -790,7 +797,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
             const float t = reduce_columns<GP, true>(v, lane);
             if (lane < GP) stt.part[g][quad][lane] = t;
           }
-          const float vmax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vs)));
+          const float vmax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fabsf(vs))));
           if (lane == 0) stt.wvs[g][quad] = vmax;
           if (ptx::bar_or(bar_id, 128, !ok)) {  // an abandoned call: all four warps leave
             stop = true;

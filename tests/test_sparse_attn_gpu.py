@@ -171,6 +171,48 @@ def test_value_scales_far_apart(fp8idx):
         decode(fp8idx, q, cache, idx, tables, 64, 0.01, ctas=ctas)
 
 
+def test_scales_of_either_sign(fp8idx):
+    """A cache that another writer filled: key and value scales below 0."""
+    rng = np.random.default_rng(27)
+    D, bs = 128, 16
+    q, cache, tables = setup(rng, 2, 1, 6, 1, D, bs, 700)
+    sc = cache[..., bs * 2 * D:].copy().view(np.float32)
+    sc *= rng.choice([-1, 1], sc.shape).astype(np.float32)
+    cache[..., bs * 2 * D:] = sc.view(np.uint8)
+    idx = pick(rng, 2, 640, 700)
+    for ctas in (0, 1, 2):
+        decode(fp8idx, q, cache, idx, tables, bs, 0.09, ctas=ctas)
+
+
+def test_selected_nan_reaches_its_row_alone(fp8idx):
+    """A NaN key, value or scale makes the rows that select it NaN, and no
+    other row."""
+    rng = np.random.default_rng(28)
+    D, bs = 128, 16
+    q, cache, tables = setup(rng, 1, 6, 4, 1, D, bs, 400)
+    idx = np.stack([np.arange(5, 305), np.arange(100, 400)] * 3).astype(np.int32)
+    bad = cache.copy()
+    for at, lo, value in ((0, 0, 0x7F), (1, D, 0x7F), (2, None, 0xFF), (3, None, 0xFF)):  # tokens 0 .. 3
+        b = tables[0, 0]
+        if lo is not None:
+            bad[b, 0, at * 2 * D + lo] = value
+        else:
+            o = bs * 2 * D + 8 * at + (4 if at == 3 else 0)
+            bad[b, 0, o: o + 4] = value
+    out, _ = decode(fp8idx, q, bad, idx, tables, bs, 0.09)
+    for at in range(4):
+        one = idx.copy()
+        one[2, 0] = at
+        dq = torch.from_numpy(bf16(q)).to(torch.bfloat16).cuda()
+        got = torch.empty_like(dq)
+        fp8idx.fp8_paged_sparse_attn(dq, torch.from_numpy(bad).cuda(), torch.from_numpy(one).cuda(),
+                                     torch.from_numpy(tables).cuda(), 0.09, got)
+        others = [0, 1, 3, 4, 5]
+        assert torch.equal(got[:, others], out[:, others]), at
+        hit = got[0, 2].isnan()
+        assert (hit[:, 0].all() and hit.sum() == 4) if at == 1 else hit.all(), at
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.1, 1e-30, 3.0])
 def test_softmax_scales(fp8idx, scale):
     rng = np.random.default_rng(18)
@@ -189,6 +231,23 @@ def test_query_sizes(fp8idx):
     cache2 = cache.copy()
     idx = pick(rng, 4, 200, 256)
     decode(fp8idx, q, cache2, idx, tables, 16, 1e-3)
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_query_without_a_value_spoils_its_head_alone(fp8idx, value):
+    rng = np.random.default_rng(29)
+    q, cache, tables = setup(rng, 2, 1, 6, 1, 128, 16, 256)
+    q[1, 0, 2] = 0
+    idx = pick(rng, 2, 200, 256)
+    want, _ = decode(fp8idx, q, cache, idx, tables, 16, 0.09)
+    dq = torch.from_numpy(bf16(q)).to(torch.bfloat16).cuda()
+    dq[1, 0, 2, 77] = value
+    got = torch.empty_like(dq)
+    fp8idx.fp8_paged_sparse_attn(dq, torch.from_numpy(cache).cuda(), torch.from_numpy(idx).cuda(),
+                                 torch.from_numpy(tables).cuda(), 0.09, got)
+    assert got[1, 0, 2].isnan().all()
+    got[1, 0, 2] = want[1, 0, 2]
+    assert torch.equal(got, want)
 
 
 def prefill(fp8idx, q, cache, idx, tables, cu, bs, scale, what=""):
