@@ -484,19 +484,29 @@ fp8idx_status fp8_paged_store(const fp8idx_tensor* k, const fp8idx_tensor* v,
  *  q             [batch, next_n, heads, head_dim] (decode) or [M, heads,
  *                head_dim] (prefill) BF16, unit inner stride, other strides
  *                multiples of 8, 16-byte aligned; head_dim 64 or 128.
- *  kv_cache      as for fp8_paged_store with v.
- *  block_tables  [batch or requests, max_blocks] I32, rows contiguous.
+ *  kv_cache      as for fp8_paged_store with v; with u the largest power of
+ *                two that divides its strides and 2*head_dim, it spans less
+ *                than 2^32 * u bytes (u >= 16: at least 64 GiB).
+ *  block_tables  [batch or requests, max_blocks] I32, rows contiguous, row
+ *                stride below 2^31; max_blocks*block_size < 2^31.
  *  cu_seq_lens   [requests + 1] I32, contiguous, requests <= 4096.
- *  indices       [rows, k] I32, unit inner stride, k 1 .. 2048.
- *  out           shape and type of q, unit inner stride.
+ *  indices       [rows, k] I32, unit inner stride, any row stride >= 0 (0:
+ *                every row selects the same), k 1 .. 2048.
+ *  out           shape and type of q, unit inner stride, rows that do not
+ *                overlap one another or an input.
  *  lse           [rows, heads] F32, contiguous, or NULL.
  *  heads a multiple of kv_heads, heads/kv_heads <= 128.
- *  opts          NULL or num_ctas: the CTAs per row and key head (0 =
- *                heuristic; 1, 2, 4 or 8), other fields ignored.
+ *  opts          NULL or num_ctas: the CTAs per row, key head and 32 query
+ *                heads (0 = heuristic; 1, 2, 4 or 8), other fields ignored.
+ *                The rounding of sums depends on it, and so, by the
+ *                heuristic, on the number of rows of the call.
  * Scores, softmax statistics and sums are f32; the kernel splits each query
- * and each probability into two e4m3 values for the tensor cores (8
- * significant bits, those of bf16: queries lose nothing).  No workspace; one
- * kernel on `stream`.
+ * and each probability into two e4m3 values for the tensor cores: 8
+ * significant bits, those of bf16, down to 2^-21 of the largest element of a
+ * row's (up to) 32 heads for a query, 2^-18 steps of the largest probability
+ * for a probability.  A NaN or an infinity in q makes its head's outputs NaN;
+ * a NaN in a key, value or scale reaches the rows that select it, no others.
+ * No workspace; one kernel on `stream`, the same bits on every run.
  */
 fp8idx_status fp8_paged_sparse_attn(const fp8idx_tensor* q,
                                     const fp8idx_tensor* kv_cache,

@@ -307,8 +307,7 @@ fp8idx_status paged_setup(const fp8idx_tensor* q, const fp8idx_tensor* kv, const
   if (!contiguous(w)) return fail(FP8IDX_ERR_INVALID, "weights must be contiguous");
   if (cl->shape[0] != B || (B > 1 && cl->stride[0] != 1)) return fail(FP8IDX_ERR_INVALID, "context_lens must be [batch] contiguous");
   if (w->shape[0] != B * next_n || w->shape[1] != H) return fail(FP8IDX_ERR_INVALID, "weights must be [batch*next_n, heads]");
-  if (bt->shape[0] != B || (B > 0 && bt->shape[1] > 1 && bt->stride[1] != 1) ||
-      (B > 1 && bt->stride[0] < bt->shape[1]))
+  if (bt->shape[0] != B || (bt->shape[1] > 1 && bt->stride[1] != 1) || (B > 1 && bt->stride[0] < bt->shape[1]))
     return fail(FP8IDX_ERR_INVALID, "block_tables must be [batch, max_blocks] with unit inner stride");
   if (D <= 0 || kv->shape[1] % (D + 4) != 0) return fail(FP8IDX_ERR_INVALID, "kv_cache row is not block_size*(head_dim+4) bytes");
   const int64_t blk = kv->shape[1] / (D + 4);
@@ -978,6 +977,10 @@ fp8idx_status sparse_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, 
   if (!row_dim_ok(D)) return fail(FP8IDX_ERR_UNSUPPORTED, "sparse attention: head_dim %lld (64 or 128)", (long long)D);
   if (q->stride[nd - 1] != 1 || out->stride[nd - 1] != 1)
     return fail(FP8IDX_ERR_INVALID, "q and out must have unit inner stride");
+  for (int i = 0; i < nd - 1; ++i) {
+    if (q->shape[i] > 1 && q->stride[i] < 0) return fail(FP8IDX_ERR_INVALID, "q: negative stride");
+    if (out->shape[i] > 1 && out->stride[i] < D) return fail(FP8IDX_ERR_INVALID, "out: rows overlap");
+  }
   if (H < 1 || n < 1) return fail(FP8IDX_ERR_INVALID, "q has no heads or rows per request");
   int64_t bs = 0;
   TRY(check_kv_cache(kv, D, &bs));
@@ -998,14 +1001,14 @@ fp8idx_status sparse_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, 
   TRY(check_tensor(idx, "indices", FP8IDX_I32, 2));
   const int64_t k = idx->shape[1];
   if (k < 1 || k > kAttnMaxK) return fail(FP8IDX_ERR_UNSUPPORTED, "sparse attention: k=%lld not in [1, %d]", (long long)k, kAttnMaxK);
-  if (idx->shape[0] != R || (k > 1 && idx->stride[1] != 1) || (R > 1 && idx->stride[0] < k))
+  if (idx->shape[0] != R || (k > 1 && idx->stride[1] != 1) || (R > 1 && idx->stride[0] < 0))
     return fail(FP8IDX_ERR_INVALID, "indices must be [rows, k] with unit inner stride");
   if (lse) {
     TRY(check_tensor(lse, "lse", FP8IDX_F32, 2));
     if (lse->shape[0] != R || lse->shape[1] != H || !contiguous(lse))
       return fail(FP8IDX_ERR_INVALID, "lse must be contiguous [rows, heads]");
   }
-  if (!std::isfinite(softmax_scale)) return fail(FP8IDX_ERR_INVALID, "softmax_scale must be finite");
+  if (!std::isfinite(softmax_scale * 1.4426950408889634f)) return fail(FP8IDX_ERR_INVALID, "softmax_scale must be finite (times log2 e, too)");
   if (R * H >= (1ll << 31)) return fail(FP8IDX_ERR_UNSUPPORTED, "sparse attention: rows*heads must stay below 2^31");
   const int32_t ctas = opts ? opts->num_ctas : 0;
   if (ctas != 0 && ctas != 1 && ctas != 2 && ctas != 4 && ctas != 8)

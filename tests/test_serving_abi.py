@@ -129,6 +129,14 @@ def test_decode_attention_refusals(lib):
     odd = _t(BF16, (2, 3, 8, 128))
     odd.stride[1] = 8 * 128 + 4
     refused(lib, f(*attn_args(q=odd)), INVALID, b"aligned")
+    refused(lib, f(*attn_args(scale=3e38)), INVALID, b"softmax_scale")
+    for dim in range(3):
+        same = _t(BF16, (2, 3, 8, 128))
+        same.stride[dim] = 0
+        refused(lib, f(*attn_args(out=same)), INVALID, b"overlap")
+    back = _t(I32, (6, 50))
+    back.stride[0] = -50
+    refused(lib, f(*attn_args(idx=back)), INVALID, b"indices")
 
 
 def test_prefill_attention_refusals(lib):

@@ -352,6 +352,22 @@ def test_strides(fp8idx):
     assert (wide_o[:, 0] == 5).all() and (wide_o[..., 0] == 5).all() and (wide_o[..., D + 1:] == 5).all()
 
 
+def test_one_selection_for_all_rows(fp8idx):
+    """indices and q as broadcast tensors (row stride 0)."""
+    rng = np.random.default_rng(30)
+    q, cache, tables = setup(rng, 1, 4, 8, 2, 64, 16, 300)
+    idx = pick(rng, 1, 250, 300)
+    one = torch.from_numpy(bf16(q[:, :1])).to(torch.bfloat16).cuda()
+    out = torch.empty((1, 4, 8, 64), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((4, 8), device="cuda")
+    fp8idx.fp8_paged_sparse_attn(one.expand(1, 4, 8, 64), torch.from_numpy(cache).cuda(),
+                                 torch.from_numpy(idx).cuda().expand(4, 250), torch.from_numpy(tables).cuda(), 0.125, out,
+                                 lse=lse)
+    want = ref.sparse_attention(np.repeat(bf16(q[0, :1]), 4, 0).astype(np.float64), cache, np.repeat(idx, 4, 0), tables, 16,
+                                0.125, next_n=4)
+    assert_attention(out[0].float().cpu().numpy(), lse.cpu().numpy(), want)
+
+
 def test_captured_and_on_two_streams(fp8idx):
     """A captured call replayed on new inputs, and two calls at once on two
     streams (no shared scratch)."""
