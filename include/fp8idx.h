@@ -502,9 +502,9 @@ fp8idx_status fp8_paged_store(const fp8idx_tensor* k, const fp8idx_tensor* v,
  *                heuristic, on the number of rows of the call.
  * Scores, softmax statistics and sums are f32; the kernel splits each query
  * and each probability into two e4m3 values for the tensor cores: 8
- * significant bits, those of bf16, down to 2^-21 of the largest element of a
- * row's (up to) 32 heads for a query, 2^-18 steps of the largest probability
- * for a probability.  A NaN or an infinity in q makes its head's outputs NaN;
+ * significant bits, those of bf16.  A query's elements below 2^-10 of its
+ * head's largest one may be off by 2^-18 of that, a probability below 2^-11 of
+ * its row's largest one by 2^-19 of that.  A NaN or an infinity in q makes its head's outputs NaN;
  * a NaN in a key, value or scale reaches the rows that select it, no others.
  * No workspace; one kernel on `stream`, the same bits on every run.
  */

@@ -88,8 +88,8 @@ constexpr int kAttnTile = 128;    // selected tokens per MMA tile (MMA M of the 
 // its own copy of the tiles (64 heads' sums would not fit in the registers).
 __host__ __device__ constexpr int attn_pad(int group) { return group <= 16 ? 16 : 32; }
 // Roles: two epilogue warpgroups, each with four producer warps and a warp that
-// issues its products; the query warp (and an idle one: register
-// shares go by groups of four warps).
+// issues its products; two query warps (register shares go by groups of four
+// warps).
 constexpr int kAttnGroups = 2;
 constexpr int kAttnThreads = 32 * (4 * kAttnGroups + 4 * kAttnGroups + kAttnGroups + 2);
 // Registers a thread after the launch's 96 have been dealt anew:
@@ -98,7 +98,8 @@ constexpr int kAttnEpilogueRegs = 144, kAttnOtherRegs = 64;
 // Probability buffers of a group: one is multiplied with the values while the
 // next is written.
 constexpr int kAttnProbBuffers = 2;
-// Query buffers: the units in work and the next one.
+// Query buffers: the units in work and the next one (filled in the units'
+// order, whichever pipeline they are for).
 constexpr int kAttnQueryBuffers = kAttnGroups + 1;
 // Tiles in flight, half of them a group's.  head_dim 128: a key
 // half of a stage is free once its scores are computed, a value half only
@@ -114,7 +115,7 @@ struct AttnSmem {
   uint32_t k, v, q, p, scale, mask, flt, bars, misc, total;
 };
 // Floats of the softmax state of one CTA, GP heads (AttnState in sparse_attn.cu).
-__host__ __device__ constexpr int attn_state_floats(int gp) { return 24 * gp + 48; }
+__host__ __device__ constexpr int attn_state_floats(int gp) { return 25 * gp + 40; }
 __host__ __device__ constexpr AttnSmem attn_smem_layout(int head_dim, int gp) {
   AttnSmem L{};
   const uint32_t stages = static_cast<uint32_t>(attn_v_stages(head_dim, gp));
@@ -127,7 +128,7 @@ __host__ __device__ constexpr AttnSmem attn_smem_layout(int head_dim, int gp) {
   L.mask = off;  off += stages * 16u;
   L.flt = off;   off += 4u * attn_state_floats(gp);
   off = (off + 15u) & ~15u;
-  L.bars = off;  off += 8u * 64u;
+  L.bars = off;  off += 8u * 48u;
   L.misc = off;  off += 32u;
   L.total = off + 1024u;
   return L;

@@ -10,15 +10,15 @@
 //   O^T [128 channels x 2 GP] += V tile^T (A, MN-major) * [Ph | Pl] (B, MN-major)
 // GP is the head count padded to 16 or 32.  The 16-bit operands are split
 // into two e4m3 values: x = h + l / 16 with h = e4m3(x), l = e4m3(16 (x - h)).
-// That keeps 8 significant bits: a bf16 query exactly (down to 2^-21 of the
-// unit's largest element; queries are scaled by a power of two that puts it
-// into [128, 256)), a probability to 2^-8 of itself, or to half a step of
+// That keeps 8 significant bits: a bf16 query exactly (down to 2^-10 of its
+// head's largest element; powers of two bring a unit, and where they are far
+// apart its heads, into the range), a probability to 2^-8 of itself, or to half a step of
 // 2^-18 of the largest one.  The two halves have their own accumulator columns
 // and meet in f32.  Dequantising the tile to 16 bits instead would take a
 // conversion per cache byte and twice the shared memory.
 //
-// A CTA (20 warps) is two pipelines side by side, which share nothing but the
-// query warp.  Each has
+// A CTA (20 warps) is two pipelines side by side, which share nothing but two
+// warps that split the next unit's query.  Each has
 //  * four producer warps: a lane resolves one entry of the tile to its cache
 //    row (indices are loaded two tiles ahead, block-table entries one), then
 //    the warp copies its 32 rows, 16 bytes a lane, into the 128-byte swizzle
@@ -151,6 +151,10 @@ struct AttnState {
   float cref[NG], cfac[NG];
   float wvs[NG][4];
   float qf[QB];                // [query buffer]: 2^-e of the query's scaling
+  uint32_t spread[QB];         // whether its heads have factors
+  int8_t qhead[QB][GP], head[NG][4][GP];  // log2 of the heads' factors: [query buffer], [group][warp]
+  uint32_t top[GP];            // cluster: largest element per head
+  uint2 qpart[2][2];           // [queries take turns][query warp]: its heads' largest and lowest `top`
 };
 
 // A load that is issued where it stands: the compiler would otherwise sink a
@@ -210,12 +214,16 @@ __device__ __forceinline__ void split_pair(__half2 x, uint32_t* h, uint32_t* l) 
   *l = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
 }
 
-// The query's split: every element times 2^e, which puts the unit's largest
-// finite one into [128, 256), as two e4m3 values.
-struct QueryScale {
+// The query's split: every element of a unit times the 2^e that puts the
+// unit's largest finite one into [128, 256), as two e4m3 values.  If the
+// largest element of one of its heads is less than 1/16 of that, every head
+// gets an e of its own, and its scores the factor 2^(unit's e - its e).  So a
+// head's elements are exact down to 2^-10 of its largest one, and off by at
+// most 2^-18 of that below (half a step of 2^-13).
+struct QueryPiece {
   uint32_t top;  // the largest element's bits without its sign (bf16 values are then ordered as integers)
   bool odd;      // infinities or NaN among them (from 0x7F80; they do not count)
-  __device__ __forceinline__ void add(const uint4& v) {
+  __device__ __forceinline__ explicit QueryPiece(const uint4& v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t m2 = 0, s2 = 0;
 #pragma unroll
@@ -224,14 +232,23 @@ struct QueryScale {
       s2 |= special;
       m2 = __vmaxu2(m2, m & ~special);
     }
-    top = max(top, max(m2 >> 16, m2 & 0xFFFFu));
-    odd |= s2 != 0u;
-  }
-  __device__ __forceinline__ int exponent() const {
-    const int e = 134 - static_cast<int>(top >> 7);
-    return top == 0u ? 0 : min(max(e, -120), 120);
+    top = max(m2 >> 16, m2 & 0xFFFFu);
+    odd = s2 != 0u;
   }
 };
+__device__ __forceinline__ int query_exponent(uint32_t top) {
+  const int e = 134 - static_cast<int>(top >> 7);
+  return top == 0u ? 0 : min(max(e, -120), 120);
+}
+// The exponent of a head with largest element `top` (0: none) in a unit whose
+// heads' are between `low` (of those that have one, else 0xFFFF) and `high`.
+__device__ __forceinline__ int head_exponent(uint32_t top, uint32_t low, uint32_t high, bool* apart) {
+  const int unit_e = query_exponent(high);
+  *apart = low != 0xFFFFu && query_exponent(low) > unit_e + 4;
+  return *apart && top != 0u ? query_exponent(top) : unit_e;
+}
+__device__ __forceinline__ uint32_t low_of(uint32_t top) { return top == 0u ? 0xFFFFu : top; }
+
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // Eight elements of head g (16-byte piece `piece` of its row) into the two
@@ -260,8 +277,8 @@ template <int D, int GP, bool CLUSTER>
 __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __grid_constant__ SparseAttnParams p) {
   constexpr int NG = kAttnGroups;
   constexpr int kProdWarp0 = 4 * NG, kProdWarps = 4 * NG;
-  constexpr int kMmaWarp0 = kProdWarp0 + kProdWarps, kQWarp = kMmaWarp0 + NG;
-  static_assert(32 * (kQWarp + 1) <= kAttnThreads, "roles");
+  constexpr int kMmaWarp0 = kProdWarp0 + kProdWarps, kQWarp = kMmaWarp0 + NG, kQWarps = 2;
+  static_assert(32 * (kQWarp + kQWarps) == kAttnThreads, "roles");
   constexpr int N2 = 2 * GP;                       // columns of S^T and O^T
   constexpr int SBG = 2;                           // accumulators of S^T per group
   constexpr int QB = kAttnQueryBuffers, PB = kAttnProbBuffers;
@@ -297,7 +314,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       ptx::mbar_init(empty0 + 8u * s, 1u);               // the output MMA
     }
     for (int i = 0; i < QB; ++i) {
-      ptx::mbar_init(qf0 + 8u * i, CLUSTER ? 4u * NG : 1u);
+      ptx::mbar_init(qf0 + 8u * i, CLUSTER ? 4u * NG : kQWarps);
       ptx::mbar_init(qe0 + 8u * i, 1u + 4u);             // the last score MMA, the unit's epilogue warps
     }
     for (int i = 0; i < NG * SBG; ++i) ptx::mbar_init(sf0 + 8u * i, 1u);
@@ -309,7 +326,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     for (int i = 0; i < NG; ++i) ptx::mbar_init(drain0 + 8u * i, 1u);
     ptx::fence_barrier_init();
   }
-  for (int g = threadIdx.x; g < GP; g += kAttnThreads) stt.ninf[g] = -INFINITY;
+  for (int g = threadIdx.x; g < GP; g += kAttnThreads) stt.ninf[g] = -INFINITY, stt.top[g] = 0u;
   for (int g = threadIdx.x; g < NG * GP; g += kAttnThreads) stt.nm[g / GP][g % GP] = 0.f;
   if (warp == kMmaWarp0) {
     ptx::tmem_alloc(ptx::smem_u32(misc), kTmemCols);
@@ -322,7 +339,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
 
   // This CTA's work.  Each epilogue group has a producer set, an issuing warp
   // and rings of stages of its own: NG pipelines side by side that share
-  // nothing but the query warp.  In a persistent CTA group g takes the units
+  // nothing but the query warps.  In a persistent CTA group g takes the units
   // g, g + NG, ... of the CTA's list; in a cluster's CTA, which has one unit,
   // every NG-th of its tiles.
   const int C = CLUSTER ? static_cast<int>(cg::this_cluster().num_blocks()) : 1;
@@ -454,41 +471,73 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         }
         ptx::cp_async_wait_all();  // (an abandoned call must not leave copies behind)
       }
-    } else if (warp == kQWarp) {
+    } else if (warp >= kQWarp) {
       // =========================== queries =============================
+      // Two warps, half of the unit's heads each: kHeads rows a round, kPer
+      // lanes a row, and after a reduction of all rounds together lane l has
+      // the largest element of head head_of.
+      constexpr int kPer = D / 8, kHeads = 32 / kPer, kRounds = GP / kQWarps / kHeads;
+      const int w = warp - kQWarp, head_of = lane % kPer % kRounds * kHeads + lane / kPer;
 #pragma unroll 1
       for (int i = 0; !CLUSTER && i < n_units; ++i) {  // (a cluster's epilogue warps do it)
         const int buf = i % QB;
         int row, kvh, h0;
         unit_of(p, u0 + i * ustep, &row, &kvh, &h0, GP);
-        const int nh = min(GP, p.group - h0);
-        if (!attn_wait(qe0 + 8u * buf, ((i / QB) & 1) ^ 1, abort_flag, kSiteQEmpty)) break;
+        const int nh = min(GP, p.group - h0), first = w * (GP / kQWarps);
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row / p.next_n * p.q_req_stride +
                                  row % p.next_n * p.q_row_stride + (kvh * p.group + h0) * p.q_head_stride;
-        constexpr int kPer = D / 8;  // 16-byte pieces per head
-        QueryScale qs{0u, false};
-#pragma unroll 8
-        for (int c = lane; c < nh * kPer; c += 32)
-          qs.add(__ldg(reinterpret_cast<const uint4*>(q + c / kPer * p.q_head_stride + c % kPer * 8)));
-        qs.top = __reduce_max_sync(kFull, qs.top);
-        qs.odd = __any_sync(kFull, qs.odd);
-        const int e = qs.exponent();
-#pragma unroll 4
-        for (int c = lane; c < GP * kPer; c += 32) {
-          const int g = c / kPer, piece = c % kPer;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (g < nh) v = __ldg(reinterpret_cast<const uint4*>(q + g * p.q_head_stride + piece * 8));
-          store_query<GP>(smem + L.q + buf * N2 * 128, g, piece, v, power_of_two(e), qs.odd);
+        uint4 v[kRounds];
+        uint32_t t[kRounds];
+        bool odd = false;
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+          const int h = first + r * kHeads + lane / kPer;
+          v[r] = make_uint4(0u, 0u, 0u, 0u);
+          if (h < nh) v[r] = __ldg(reinterpret_cast<const uint4*>(q + h * p.q_head_stride + lane % kPer * 8));
         }
-        if (lane == 0) {
-          stt.qf[buf] = power_of_two(-e);
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+          const QueryPiece piece(v[r]);
+          t[r] = piece.top;
+          odd |= piece.odd;
+        }
+#pragma unroll
+        for (int d = kRounds / 2; d > 0; d >>= 1) {
+          const bool up = lane & d;
+#pragma unroll
+          for (int j = 0; j < d; ++j) {
+            const uint32_t got = __shfl_xor_sync(kFull, up ? t[j] : t[j + d], d);
+            t[j] = max(up ? t[j + d] : t[j], got);
+          }
+        }
+#pragma unroll
+        for (int d = kRounds; d < kPer; d *= 2) t[0] = max(t[0], __shfl_xor_sync(kFull, t[0], d));
+        const uint32_t high = __reduce_max_sync(kFull, t[0]), low = __reduce_min_sync(kFull, low_of(t[0]));
+        odd = __any_sync(kFull, odd);
+        if (lane == 0) stt.qpart[i & 1][w] = make_uint2(high | (odd ? 0x10000u : 0u), low);
+        const bool ok = attn_wait(qe0 + 8u * buf, ((i / QB) & 1) ^ 1, abort_flag, kSiteQEmpty);
+        if (ptx::bar_or(2 + NG, 32 * kQWarps, !ok)) break;
+        const uint2 x = stt.qpart[i & 1][0], y = stt.qpart[i & 1][1];
+        odd = ((x.x | y.x) & 0x10000u) != 0u;
+        const uint32_t top = max(x.x & 0xFFFFu, y.x & 0xFFFFu);
+        bool apart;
+        const int e = head_exponent(t[0], min(x.y, y.y), top, &apart), unit_e = query_exponent(top);
+        stt.qhead[buf][first + head_of] = static_cast<int8_t>(max(unit_e - e, -126));
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+          const float mul = power_of_two(__shfl_sync(kFull, e, lane / kPer * kPer + r));  // (lane of the row's head)
+          store_query<GP>(smem + L.q + buf * N2 * 128, first + r * kHeads + lane / kPer, lane % kPer, v[r], mul, odd);
+        }
+        if (w == 0 && lane == 0) {
+          stt.qf[buf] = power_of_two(-unit_e);
+          stt.spread[buf] = apart;
           stt.qplace[buf] = place_of(p, row, kvh * p.group + h0, nh);
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(qf0 + 8u * buf);
       }
-    } else if (warp < kQWarp) {
+    } else {
       // ============================= MMA ===============================
       // A warp per group issues its products: the output of the oldest tile
       // whose probabilities are there, else the scores of a tile (two ahead
@@ -620,32 +669,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
                                row % p.next_n * p.q_row_stride + (kvh * p.group + h0) * p.q_head_stride;
       constexpr int kPer = D / 8, kPieces = (GP * kPer + 255) / 256;
       uint4 v[kPieces];
-      QueryScale qs{0u, false};
+      bool odd = false;
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int c = static_cast<int>(threadIdx.x) + 256 * i;
         v[i] = make_uint4(0u, 0u, 0u, 0u);
         if (c < nh * kPer) v[i] = __ldg(reinterpret_cast<const uint4*>(q + c / kPer * p.q_head_stride + c % kPer * 8));
-        qs.add(v[i]);
+        const QueryPiece piece(v[i]);
+        if (c < GP * kPer) atomicMax(&stt.top[c / kPer], piece.top);
+        odd |= piece.odd;
       }
-      const uint32_t both = __reduce_max_sync(kFull, qs.top) | (__any_sync(kFull, qs.odd) ? 0x10000u : 0u);
-      if (lane == 0) stt.part[0][0][warp] = __uint_as_float(both);
-      ptx::bar_sync(1 + NG, 4 * NG * 32);
-      qs.top = 0u;
-#pragma unroll
-      for (int w = 0; w < 4 * NG; ++w) {
-        const uint32_t x = __float_as_uint(stt.part[0][0][w]);
-        qs.top = max(qs.top, x & 0xFFFFu);
-        qs.odd |= x >> 16 != 0u;
-      }
-      const int e = qs.exponent();
+      odd = ptx::bar_or(1 + NG, 4 * NG * 32, odd);
+      const uint32_t top = lane < GP ? stt.top[lane % GP] : 0u, high = __reduce_max_sync(kFull, top);
+      bool apart;
+      const int e = head_exponent(top, __reduce_min_sync(kFull, low_of(top)), high, &apart), unit_e = query_exponent(high);
+      if (threadIdx.x < GP) stt.qhead[0][threadIdx.x] = static_cast<int8_t>(max(unit_e - e, -126));
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        const int c = static_cast<int>(threadIdx.x) + 256 * i;
-        if (c < GP * kPer) store_query<GP>(smem + L.q, c / kPer, c % kPer, v[i], power_of_two(e), qs.odd);
+        const int c = static_cast<int>(threadIdx.x) + 256 * i, head = min(c / kPer, GP - 1);
+        const float mul = power_of_two(__shfl_sync(kFull, e, head));
+        if (c < GP * kPer) store_query<GP>(smem + L.q, head, c % kPer, v[i], mul, odd);
       }
       if (threadIdx.x == 0) {
-        stt.qf[0] = power_of_two(-e);
+        stt.qf[0] = power_of_two(-unit_e);
+        stt.spread[0] = apart;
         stt.qplace[0] = place_of(p, row, kvh * p.group + h0, nh);
       }
       ptx::fence_proxy_async_smem();
@@ -661,10 +708,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
     for (int r = 0; r < own_units(g) && !stop; ++r) {
       const int unit = CLUSTER ? 0 : r * NG + g;
       float qscale = 0.f;
-      bool ok = true;
+      bool ok = true, spread = false;
       if (t0 < t1) {
         ok = attn_wait(qf0 + 8u * (unit % QB), (unit / QB) & 1, abort_flag, kSiteQFull);
         qscale = stt.qf[unit % QB] * p.scale_log2;
+        spread = stt.spread[unit % QB] != 0u;
+        if (lane < GP) stt.head[g][quad][lane] = stt.qhead[unit % QB][lane];
         if (!CLUSTER && tg == 0) stt.place[g] = stt.qplace[unit % QB];  // (read between the unit's last two barriers)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(qe0 + 8u * (unit % QB));
@@ -688,6 +737,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
                         kSiteStageFull, kSiteAccFull, kSiteAccEmpty) && ok;
         ptx::tc_fence_after();
         const uint32_t s_tm = tmem + slot * N2 + lane_off;
+        if (spread) {  // heads far apart: their factors go into the accumulator, out of the way of the usual case
+#pragma unroll 1
+          for (int b = 0; b < N2; b += 16) {
+            uint32_t v[16];
+            ptx::tmem_ld_32x32b_x16(s_tm + b, v);
+            ptx::tmem_wait_ld_n(v);
+            const int8_t* f = &stt.head[g][quad][b % GP];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * power_of_two(f[j]));
+            ptx::tmem_st_32x32b_x16(s_tm + b, v);
+          }
+          ptx::tmem_wait_st();
+        }
         // The scores of the first 16 heads (of no meaning in a tile without
         // entries); 32 heads need the registers (early: 342 us, late: 333 us).
         uint32_t hi[16], lo[16];

@@ -233,6 +233,17 @@ def test_query_sizes(fp8idx):
     decode(fp8idx, q, cache2, idx, tables, 16, 1e-3)
 
 
+@pytest.mark.parametrize("n", [2, 320])
+def test_heads_of_far_apart_sizes(fp8idx, n):
+    """The heads' query rows differ by up to 2^20: each keeps its own bits
+    (a cluster per row, and persistent CTAs)."""
+    rng = np.random.default_rng(33)
+    q, cache, tables = setup(rng, 1, n, 20, 1, 64, 16, 200)
+    q[:, ::2] *= np.exp2(rng.integers(-16, 5, (1, (n + 1) // 2, 20, 1)))
+    q[:, :, 7] = 0
+    decode(fp8idx, q, cache, pick(rng, n, 150, 200), tables, 16, 0.125)
+
+
 @pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
 def test_query_without_a_value_spoils_its_head_alone(fp8idx, value):
     rng = np.random.default_rng(29)
