@@ -15,7 +15,9 @@
 // instructions: 32 us for 16384 tokens of 8 heads.)
 // DRAM bound (2 or 4 bytes read and one written a value), so with many rows a
 // lane loads its pieces of two rows before it works on them; with few the rows
-// are spread over more warps.
+// are spread over more warps.  16384 tokens of 8 heads, keys and values: 23.8 us,
+// 4.3 TB/s of the 102 MB that have to move (63% of a copy's rate); 4096 index
+// keys 1.9 us, 96 of them 1.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -6,11 +6,13 @@ The attention's error bound, per output, from what the kernel rounds:
     it is off by at most 2^-8 of itself, and by at most 2^-19 of the largest
     probability (times the largest value scale) where it is so small that
     the e4m3 range ends;
-  * a score of D <= 128 products summed in f32 (the query's two e4m3 parts
-    are exact) is off by at most 2^-16 of the sum of its |products| (2*128
-    f32 roundings of 2^-24 each, and two more for the scales), which changes
-    a probability by the same relative amount; 2^-20 covers the exponential
-    and the f32 sums;
+  * a score of D <= 128 products summed in f32 is off by at most 2^-16 of the
+    sum of its |products| (128 f32 additions of 2^-24 each for either part, a
+    few more to join and scale them; the query's two e4m3 parts are exact,
+    but for elements below 2^-10 of their head's largest one, which are off by
+    at most 2^-18 of that and of which a row of 64 or 128 normal values has
+    one at most), which changes a probability by the same relative amount;
+    2^-20 covers the exponential and the f32 sums;
 so |error| <= 2^-8 |out| + (2^-8 + 2^-20 + 2 * 2^-16 S) sum w|v|
               + 2^-19 * floor, all but the first times (1 + 2^-7) for the
 second order, with S the largest sum of |products| of a score.
