@@ -15,8 +15,8 @@
 // instructions: 32 us for 16384 tokens of 8 heads.)
 // DRAM bound (2 or 4 bytes read and one written a value), so with many rows a
 // lane loads its pieces of two rows before it works on them; with few the rows
-// are spread over more warps.  16384 tokens of 8 heads, keys and values: 23.8 us,
-// 4.3 TB/s of the 102 MB that have to move (63% of a copy's rate); 4096 index
+// are spread over more warps.  16384 tokens of 8 heads, keys and values: 22.0 us,
+// 4.6 TB/s of the 102 MB that have to move (68% of a copy's rate); 4096 index
 // keys 1.9 us, 96 of them 1.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -28,7 +28,7 @@
 namespace fp8idx {
 namespace {
 
-constexpr int kStoreThreads = 256;
+constexpr int kStoreThreads = 128;  // (256: 23.8 us where this takes 22.0; the registers then hold fewer warps)
 
 // Eight values as they lie in memory: one or two 16-byte pieces.
 template <int TYPE>
@@ -172,9 +172,9 @@ StoreKernel store_instance(int row_type, int head_dim, int parts) {
 
 cudaError_t launch_paged_store(const PagedStoreParams& p, int row_type, int head_dim, int sms, cudaStream_t stream) {
   const int parts = p.x[1] ? 2 : 1;
-  // two rows a lane once that still makes four CTAs for every SM
+  // two rows a lane once that still makes eight CTAs for every SM
   const int64_t rows = p.tokens * p.heads * parts, per_cta = kStoreThreads / (head_dim / 16);
-  const int per_lane = rows >= per_cta * 2 * 4 * sms ? 2 : 1;
+  const int per_lane = rows >= per_cta * 2 * 8 * sms ? 2 : 1;
   const StoreKernel kern = per_lane == 2 ? store_instance<2>(row_type, head_dim, parts)
                                          : store_instance<1>(row_type, head_dim, parts);
   kern<<<static_cast<unsigned>((rows + per_cta * per_lane - 1) / (per_cta * per_lane)), kStoreThreads, 0, stream>>>(p);
