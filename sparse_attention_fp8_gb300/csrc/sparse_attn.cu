@@ -404,12 +404,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
                 req_hi = __ldg(p.cu_seq_lens + a + 1);
               }
               ok = ok && tok >= req_lo && tok < req_hi;
-              tok -= req_lo;
+              tok = static_cast<int32_t>(static_cast<uint32_t>(tok) - static_cast<uint32_t>(req_lo));
             } else {
               req = req1;
             }
-            const int32_t j = tok >> shift;
-            if (ok && j < p.max_blocks) blk1 = load_now(p.block_tables + static_cast<int64_t>(req) * p.bt_stride + j);
+            // (unsigned: lengths that are no prefix sums must not lead out of the table)
+            const uint32_t j = static_cast<uint32_t>(tok >> shift);
+            if (ok && j < static_cast<uint32_t>(p.max_blocks))
+              blk1 = load_now(p.block_tables + static_cast<int64_t>(req) * p.bt_stride + j);
           }
           if (it + 2 < total) {  // the entries of the tile after that
             if (left == 0) {     // a new unit: taken apart once

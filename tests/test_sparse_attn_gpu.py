@@ -297,6 +297,27 @@ def test_prefill(fp8idx, D, bs):
     prefill(fp8idx, q, cache, idx, tables, cu, bs, D**-0.5)
 
 
+@pytest.mark.parametrize("cu", [[-(2**31), 400], [-5, 100], [300, 200], [2**31 - 1, -(2**31)], [0, 2**31 - 1]])
+def test_prefill_lengths_that_are_no_prefix_sums(fp8idx, cu):
+    """Columns whose place would lie outside the request's table select
+    nothing (the call reads nothing outside of it)."""
+    rng = np.random.default_rng(34)
+    cache = filled_cache(rng, 12, 1, 16, 64)
+    tables = rng.permutation(12).astype(np.int32).reshape(1, 12)
+    cu = np.array(cu, np.int64)
+    idx = np.sort(rng.integers(0, 400, (3, 150)), axis=1).astype(np.int32)
+    q = bf16(rng.standard_normal((3, 4, 64)))
+    out = torch.empty((3, 4, 64), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((3, 4), device="cuda")
+    fp8idx.fp8_mqa_sparse_attn_paged(torch.from_numpy(q).to(torch.bfloat16).cuda(), torch.from_numpy(cache).cuda(),
+                                     torch.from_numpy(tables).cuda(), torch.from_numpy(cu.astype(np.int32)).cuda(),
+                                     torch.from_numpy(idx).cuda(), 0.125, out, lse=lse)
+    tok = np.where((idx >= cu[0]) & (idx < cu[1]), idx - cu[0], -1)
+    tok = np.where(tok < 12 * 16, tok, -1).astype(np.int32)
+    want = ref.sparse_attention(q.astype(np.float64), cache, tok, np.repeat(tables, 3, 0), 16, 0.125, next_n=1)
+    assert_attention(out.float().cpu().numpy(), lse.cpu().numpy(), want)
+
+
 def test_more_rows_than_sms(fp8idx):
     """More units of work than the GPU runs at once, with uneven selections."""
     rng = np.random.default_rng(22)
