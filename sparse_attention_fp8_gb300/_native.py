@@ -37,6 +37,7 @@ class _Tensor(ctypes.Structure):
 # pointers, which costs a third of filling ctypes structures field by field.
 _TENSOR_PACK = struct.Struct("=qii4q4q")
 assert _TENSOR_PACK.size == ctypes.sizeof(_Tensor)
+_PACK_1D, _PACK_2D = struct.Struct("=qiiq24xq24x"), struct.Struct("=qiiqq16xqq16x")
 _PAD = (0, 0, 0, 0)
 _dtype_codes = None
 
@@ -337,11 +338,11 @@ def _descs(*tensors):
     """The packed descriptors of a call (None stays None).  The library
     launches on the current device: every tensor has to be there (a kernel
     cannot be sent after the data of another device).  One pass over the
-    tensors with the row-shaped cases spelt out: a step's tables have twelve
-    descriptors, which costs 6 us this way and 13 us tensor by tensor."""
+    tensors with vectors and matrices spelt out: a step's tables have twelve
+    descriptors, which costs 5 us this way and 13 us tensor by tensor."""
     import torch
     _dtype_code(torch.uint8)
-    codes, pack = _dtype_codes, _TENSOR_PACK.pack
+    codes, pack_1d, pack_2d = _dtype_codes, _PACK_1D.pack, _PACK_2D.pack
     dev = None
     out = []
     for t in tensors:
@@ -356,16 +357,15 @@ def _descs(*tensors):
             if at != dev:
                 raise ValueError(f"a tensor is on cuda:{at}, the current device is cuda:{dev}")
         dt = codes.get(t.dtype)
-        shape, stride = t.shape, t.stride()
-        n = len(shape)
-        if dt is None or n > 4:
-            _pack(t, 0)  # (says what is wrong)
-        if n == 1:
-            out.append(pack(t.data_ptr(), dt, 1, shape[0], 0, 0, 0, stride[0], 0, 0, 0))
-        elif n == 2:
-            out.append(pack(t.data_ptr(), dt, 2, shape[0], shape[1], 0, 0, stride[0], stride[1], 0, 0))
+        n = t.dim()
+        if n == 1 and dt is not None:
+            out.append(pack_1d(t.data_ptr(), dt, 1, t.numel(), t.stride()[0]))
+        elif n == 2 and dt is not None:
+            rows, cols = t.shape
+            step, inner = t.stride()
+            out.append(pack_2d(t.data_ptr(), dt, 2, rows, cols, step, inner))
         else:
-            out.append(pack(t.data_ptr(), dt, n, *shape, *_PAD[n:], *stride, *_PAD[n:]))
+            out.append(_pack(t, t.data_ptr()))
     return out
 
 

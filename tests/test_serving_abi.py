@@ -156,6 +156,35 @@ def test_binding_refuses_host_tensors():
                                torch.zeros(2, 132, dtype=torch.uint8))
 
 
+class OnDevice:
+    """A host tensor that says it lies on a device."""
+
+    def __init__(self, t, at):
+        self.t, self.at = t, at
+
+    def get_device(self):
+        return self.at
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_binding_descriptors_and_devices(monkeypatch):
+    from sparse_attention_fp8_gb300 import _native
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for t in (torch.zeros(5, dtype=torch.int32), torch.zeros(10)[::2], torch.zeros((3, 4), dtype=torch.uint8).t(),
+              torch.zeros((2, 3, 4, 5)), torch.zeros((0, 7)), torch.zeros(()), torch.zeros((2, 3, 4))):
+        assert _native._descs(OnDevice(t, 1), None) == [_native._pack(t, t.data_ptr()), None], t.shape
+    with pytest.raises(TypeError):
+        _native._descs(OnDevice(torch.zeros(3, dtype=torch.int64), 1))
+    with pytest.raises(ValueError):
+        _native._descs(OnDevice(torch.zeros((1, 1, 1, 1, 1)), 1))
+    one, other = OnDevice(torch.zeros(3), 1), OnDevice(torch.zeros(3), 0)
+    for ts in ((other,), (one, other), (one, torch.zeros(3))):
+        with pytest.raises(ValueError):
+            _native._descs(*ts)
+
+
 def test_definition_step_tables_by_hand():
     tables = np.array([[7, -1, -1], [3, 4, -1]], np.int32)
     got = ref.step_tables([2, 8], [3, 1], np.array([20, 21, 22, 23]), 4, 4, tables, 6)
