@@ -104,6 +104,33 @@ def test_extreme_values(fp8idx):
     assert np.array_equal(dev.cpu().numpy(), cache)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_subnormal_nan_and_infinite_values(fp8idx, dtype):
+    """A row of subnormal numbers, one with a NaN (which keeps its place and
+    changes no other value), one with an infinity (whose scale is infinite)."""
+    D = 64
+    rng = np.random.default_rng(5)
+    x = torch.from_numpy(np.stack([rng.standard_normal(D) * f for f in (1e-39, 1.0, 1.0, 1.0)]).astype(np.float32)).to(dtype)
+    y = x.clone()
+    y[1, 5], y[2, 9], y[3, 11] = float("nan"), float("inf"), -float("inf")
+    slots = np.arange(4, dtype=np.int32)
+    want = np.zeros((4, 68), np.uint8)
+    rest = x.float().numpy().copy()
+    rest[1, 5] = 0
+    ref.store_index(want, slots, rest, 1)
+    dev = torch.zeros((4, 68), dtype=torch.uint8, device="cuda")
+    fp8idx.fp8_paged_store(y.cuda(), None, torch.from_numpy(slots).cuda(), dev)
+    got = dev.cpu().numpy()
+    assert np.array_equal(got[0], want[0])
+    assert got[1, 5] & 0x7F == 0x7F
+    got[1, 5] = want[1, 5]
+    assert np.array_equal(got[1], want[1])
+    for r, at in ((2, 9), (3, 11)):
+        assert np.isposinf(got[r, 64:].view(np.float32)).all()
+        assert got[r, at] & 0x7F == 0x7F
+        assert (np.delete(got[r, :64], at) & 0x7F == 0).all()
+
+
 def test_no_tokens_and_capture(fp8idx):
     cache = torch.zeros((4, 64 * 132), dtype=torch.uint8, device="cuda")
     none = torch.empty((0,), dtype=torch.int32, device="cuda")
