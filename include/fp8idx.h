@@ -501,12 +501,18 @@ fp8idx_status fp8_paged_store(const fp8idx_tensor* k, const fp8idx_tensor* v,
  *                heads (0 = heuristic; 1, 2, 4 or 8), other fields ignored.
  *                The rounding of sums depends on it, and so, by the
  *                heuristic, on the number of rows of the call.
- * Scores, softmax statistics and sums are f32; the kernel splits each query
- * and each probability into two e4m3 values for the tensor cores: 8
- * significant bits, those of bf16.  A query's elements below 2^-10 of its
- * head's largest one may be off by 2^-18 of that, a probability below 2^-11 of
- * its row's largest one by 2^-19 of that.  A NaN or an infinity in q makes its head's outputs NaN;
- * a NaN in a key, value or scale reaches the rows that select it, no others.
+ * Scores, softmax statistics and sums are f32; the kernel splits each query,
+ * and each product of a probability and its value's scale, into two e4m3 values
+ * for the tensor cores: 8 significant bits, those of bf16 (the products are
+ * rounded to f16 first, the sums that divide them are not).  A query's elements
+ * below 2^-10 of its head's largest one may be off by 2^-18 of that, a product
+ * below 2^-11 of its row and head's largest one by 2^-19 of that.  The value
+ * scales that a row selects may lie up to 2^80 apart: with a wider range, or
+ * where every product is less than 2^-80 of the row's largest probability times
+ * its largest value scale, the smaller ones have fewer bits.
+ * A NaN or an infinity in q makes its head's outputs NaN; a NaN in a key, value
+ * or scale, and an infinite value scale, reaches the rows that select it, no
+ * others.
  * No workspace; one kernel on `stream`, the same bits on every run.
  */
 fp8idx_status fp8_paged_sparse_attn(const fp8idx_tensor* q,

@@ -121,11 +121,12 @@ def selected(idx, row, block_tables, block_size, num_blocks, next_n=None, cu_seq
     return out
 
 
-def sparse_attention(q, cache, indices, block_tables, block_size, scale, next_n=None, cu_seq_lens=None):
+def sparse_attention(q, cache, indices, block_tables, block_size, scale, next_n=None, cu_seq_lens=None, by_product=False):
     """q [R, H, D] f64, cache [num_blocks, kv_heads, page] u8.  Returns out
     [R, H, D], lse [R, H] and three figures that an error bound needs: the
     sum of weight * |value| per output [R, H, D], the largest weight times
-    the largest value scale times the sum of |value code| [R, H, D], and the
+    the largest value scale (by_product: the largest product of an entry's
+    weight and value scale) times the sum of |value code| [R, H, D], and the
     largest sum of |scale * q * k| of a score [R, H]."""
     R, H, D = q.shape
     HK = cache.shape[1]
@@ -153,6 +154,7 @@ def sparse_attention(q, cache, indices, block_tables, block_size, scale, next_n=
                 lse[r, h] = top + np.log(z)
                 out[r, h] = w @ val
                 mag[r, h] = w @ np.abs(val)
-                floor[r, h] = w.max() * np.abs(sc[:, 1]).max() * np.abs(codes[:, D:]).sum(0)
+                most = (w * np.abs(sc[:, 1])).max() if by_product else w.max() * np.abs(sc[:, 1]).max()
+                floor[r, h] = most * np.abs(codes[:, D:]).sum(0)
                 sabs[r, h] = (np.abs(scale) * (np.abs(key) @ np.abs(q[r, h]))).max()
     return out, lse, mag, floor, sabs

@@ -12,10 +12,11 @@
 // into two e4m3 values: x = h + l / 16 with h = e4m3(x), l = e4m3(16 (x - h)).
 // That keeps 8 significant bits: a bf16 query exactly (down to 2^-10 of its
 // head's largest element; powers of two bring a unit, and where they are far
-// apart its heads, into the range), a probability to 2^-8 of itself, or to half a step of
-// 2^-18 of the largest one.  The two halves have their own accumulator columns
-// and meet in f32.  Dequantising the tile to 16 bits instead would take a
-// conversion per cache byte and twice the shared memory.
+// apart its heads, into the range), the product of a probability and its
+// value's scale to 2^-8 of itself, or to half a step of 2^-18 of the row's
+// largest one.  The two halves have their own accumulator columns and meet in
+// f32.  Dequantising the tile to 16 bits instead would take a conversion per
+// cache byte and twice the shared memory.
 //
 // A CTA (20 warps) is two pipelines side by side, which share nothing but two
 // warps that split the next unit's query.  Each has
@@ -33,12 +34,11 @@
 //  * an epilogue warpgroup (thread = token): scores times the token's scale,
 //    probability 2^(t - m), its sum per head in the thread, and P (times the
 //    token's value scale) into shared memory as the next product's operand.
-//    m is the maximum of the tile in which it was last set, plus a margin: a
-//    later tile keeps it unless a probability exceeds 4, or a value scale 1.25
-//    times the largest one in hand, which takes one vote of the group a tile
-//    instead of a maximum per head across its 128 threads.  A tile that does
-//    not keep it takes the exact maxima, rescales the sums and the accumulator
-//    and is done over.
+//    m goes by the largest P of the tile in which it was last set: a later
+//    tile keeps it unless a P is 14 times as large, which takes one vote of the
+//    group a tile instead of a maximum per head across its 128 threads.  A tile
+//    that does not keep it takes the exact maxima, rescales the sums and the
+//    accumulator and is done over.
 // Many units: persistent CTAs, each pipeline with units of its own.  Few: a
 // cluster of 1, 2, 4 or 8 CTAs per unit, whose pipelines share its tiles; their
 // results meet in f32 through distributed shared memory.  Which one, by the
@@ -48,8 +48,8 @@
 // tile of 32 heads takes a warpgroup 2600 clocks, 1150 of them arithmetic, the
 // rest waits, the vote and fences between roles; half of the issue slots are
 // filled, the tensor cores are busy 14% of the time).  4096 prompt rows of 32
-// heads and 2048 entries: 337 us, 408 TFLOP/s; a verify step of 96 such rows
-// 22 us; 128 heads on one key head 22 us (500 to 600 GB/s through the gather).
+// heads and 2048 entries: 328 us, 419 TFLOP/s; a verify step of 96 such rows
+// 22 us; 128 heads on one key head 21 us (500 to 600 GB/s through the gather).
 // 8 heads a key head over pages of one token: the scattered rows, 1.3 GB through
 // L2 in 242 us (182 us if the pages lie in order, 137 us with pages of 64
 // tokens).  One decode row: latency, 9.2 us, of which two dependent loads before
@@ -74,13 +74,20 @@ static __device__ unsigned int g_attn_watchdog;
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-// P's codes reach from 448 (the largest e4m3 value) down to steps of 2^-13
-// (the smallest one of the second part: 2^-9 / 16).  A probability over m may grow to
-// kMaxP and a value scale to kMaxW times the one in hand before both are
-// taken anew, at m = the largest score + kMargin: with normally distributed
-// scores a unit of 2048 entries then does that once, at its first tile.
-constexpr float kMaxP = 4.f, kMaxW = 1.25f, kPScale = 89.6f;  // 4 * 1.25 * 89.6 = 448
-constexpr float kMargin = 1.4854268f;  // log2(89.6 / 32): a step is 2^-18 of the largest probability
+// What is multiplied with a value's code is P = 2^(t - m) * kTopCode * vs / cref
+// (t the score in log2 units, vs the value's scale).  P's codes reach from 448
+// (the largest e4m3 value) down to steps of 2^-13 (the smallest one of the
+// second part: 2^-9 / 16), so m goes by the products, not by the scores alone:
+// it is the largest t + log2(vs / cref) of the tile in which it was last set,
+// which then has the code 32 and the others steps of 2^-18 of it.  It is set
+// anew when a P exceeds 448; with normally distributed scores a unit of 2048
+// entries does that once, at its first tile.
+// cref is the first tile's largest value scale.  Sums are of 2^(t - m), so
+// log2(vs / cref) is taken as no less than -80 (values that small, or zero,
+// with nearly all of the weight: their 2^(t - m) is up to 2^80, a thread's sums
+// up to 2^100), and a scale more than 2^80 times cref becomes the new one.
+constexpr float kTopCode = 32.f, kMaxCode = 448.f;
+constexpr float kValueSpan = 0x1p80f, kLogSpan = 80.f, kMaxSum = 0x1p100f;
 constexpr float kMinVScale = 0x1p-120f;
 constexpr float kMinM = -3e38f;       // m stays finite, so that a score of -inf gives probability 0
 
@@ -149,8 +156,7 @@ struct AttnState {
   float resc[NG][GP];          // a new maximum: 2^-(what m grows by)
   float fac[NG][GP];           // a unit's end: factor of the accumulator
   float xm[NG][GP], xl[NG][GP];  // cluster: the group's maximum and sum per head
-  float cref[NG], cfac[NG];
-  float wvs[NG][4];
+  float wvs[NG][4];            // a tile's largest value scales
   float qf[QB];                // [query buffer]: 2^-e of the query's scaling
   uint32_t spread[QB];         // whether its heads have factors
   int8_t qhead[QB][GP], head[NG][4][GP];  // log2 of the heads' factors: [query buffer], [group][warp]
@@ -722,7 +728,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         if (lane == 0) ptx::mbar_arrive(qe0 + 8u * (unit % QB));
       }
       uint32_t has_o = 0u;  // whether the group's accumulator holds anything of this unit
-      float cref = 0.f;
+      float cref = 0.f, wref = 0.f;  // the value scales' reference, kTopCode over it
       float2 l2[GP / 2];
 #pragma unroll
       for (int j = 0; j < GP / 2; ++j) l2[j] = make_float2(0.f, 0.f);
@@ -795,8 +801,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         for (bool fresh = false;; fresh = true) {
           bool again = any && !has_o && !fresh;
           if (any && (has_o || fresh)) {
-            const float w = vs * __fdividef(kPScale, cref);
-            const __half2 w2 = __floats2half2_rn(w, w);
+            const float w = vs * wref;
+            const float2 w2 = make_float2(w, w);
             __half2 top = __floats2half2_rn(0.f, 0.f);
             float t[16];
             if constexpr (GP > 16) {
@@ -817,9 +823,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
                   const float2 e = make_float2(ex2(t[j + k]), ex2(t[j + k + 1]));
                   float2& l = l2[(b + j + k) / 2];
                   l = __fadd2_rn(l, e);
-                  const __half2 h2 = __floats2half2_rn(e.x, e.y);  // (11 bits; above 65504 infinite, which is caught)
-                  top = __hmax2(top, h2);
-                  split_pair(__hmul2(h2, w2), &hc[k / 2], &lc[k / 2]);
+                  const float2 pf = __fmul2_rn(e, w2);
+                  const __half2 p2 = __floats2half2_rn(pf.x, pf.y);  // (11 bits; above 65504 infinite, which is caught)
+                  top = __hmax2(top, __habs2(p2));
+                  split_pair(p2, &hc[k / 2], &lc[k / 2]);
                 }
                 ph[j / 4] = hc[0] | hc[1] << 16;
                 pl[j / 4] = lc[0] | lc[1] << 16;
@@ -836,12 +843,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
               }
             }
             ptx::fence_proxy_async_smem();  // (before the vote, which hides some of its wait)
-            again = !fresh && (fabsf(vs) > kMaxW * cref || !__hble2(top, __floats2half2_rn(kMaxP, kMaxP)));
+            again = fabsf(w) > kTopCode * kValueSpan || !__hble2(top, __floats2half2_rn(kMaxCode, kMaxCode));
+            if (valid && !(fabsf(w) * kValueSpan >= kTopCode)) {  // a scale so small (or NaN) that P does not bound the sums
+              float sum = 0.f;
+#pragma unroll
+              for (int j = 0; j < GP / 2; ++j) sum = fmaxf(sum, fmaxf(l2[j].x, l2[j].y));
+              again |= sum > kMaxSum;
+            }
+            again = again && !fresh;
           }
           // (every warp votes in every pass: an abandoned call may have left them with different masks)
           if (!ptx::bar_or(bar_id, 128, again || !ok)) break;
           // ---- new maxima
+          const float vmax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fabsf(vs))));
+          if (lane == 0) stt.wvs[g][quad] = vmax;
+          if (ptx::bar_or(bar_id, 128, !ok)) {  // an abandoned call: all four warps leave
+            stop = true;
+            break;
+          }
+          const float last_cref = cref;
           {
+            const float m = fmaxf(fmaxf(stt.wvs[g][0], stt.wvs[g][1]), fmaxf(stt.wvs[g][2], stt.wvs[g][3]));
+            if (!has_o || m > kValueSpan * cref) cref = fmaxf(m, kMinVScale);
+            wref = kTopCode / cref;
+          }
+          {
+            const float lv = fminf(fmaxf(__log2f(fabsf(vs)) - __log2f(cref), -kLogSpan), kLogSpan);
             float v[GP];
 #pragma unroll
             for (int b = 0; b < GP; b += 16) {
@@ -856,32 +883,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
 #pragma unroll
               for (int j = 0; j < GP / 2; ++j) {
                 const float ex = ex2(v[2 * j]), ey = ex2(v[2 * j + 1]);
-                l2[j] = make_float2(ex < 0x1p100f ? l2[j].x - ex : 0.f, ey < 0x1p100f ? l2[j].y - ey : 0.f);
+                l2[j] = make_float2(ex < 0x1p125f ? l2[j].x - ex : 0.f, ey < 0x1p125f ? l2[j].y - ey : 0.f);
               }
             }
+#pragma unroll
+            for (int j = 0; j < GP; ++j) v[j] += lv;
             const float t = reduce_columns<GP, true>(v, lane);
             if (lane < GP) stt.part[g][quad][lane] = t;
           }
-          const float vmax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fabsf(vs))));
-          if (lane == 0) stt.wvs[g][quad] = vmax;
-          if (ptx::bar_or(bar_id, 128, !ok)) {  // an abandoned call: all four warps leave
-            stop = true;
-            break;
-          }
+          ptx::bar_sync(bar_id, 128);
           if (tg < GP) {
-            float d = fmaxf(fmaxf(stt.part[g][0][tg], stt.part[g][1][tg]), fmaxf(stt.part[g][2][tg], stt.part[g][3][tg]));
-            d = fmaxf(d, has_o ? -kMargin : kMinM) + kMargin;
+            const float d = fmaxf(fmaxf(fmaxf(stt.part[g][0][tg], stt.part[g][1][tg]),
+                                        fmaxf(stt.part[g][2][tg], stt.part[g][3][tg])),
+                                  has_o ? 0.f : kMinM);
             stt.resc[g][tg] = ex2(-d);
             stt.nm[g][tg] -= d;
           }
-          if (tg == 0) {
-            float m = fmaxf(fmaxf(stt.wvs[g][0], stt.wvs[g][1]), fmaxf(stt.wvs[g][2], stt.wvs[g][3]));
-            m = fmaxf(fmaxf(m, cref), kMinVScale);
-            stt.cref[g] = m;
-            stt.cfac[g] = __fdividef(cref, m);
-          }
           ptx::bar_sync(bar_id, 128);
-          cref = stt.cref[g];
           if (has_o) {
             wait_outputs();
 #pragma unroll
@@ -889,7 +907,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
               const float2 f = *reinterpret_cast<const float2*>(&stt.resc[g][2 * j]);
               l2[j] = make_float2(l2[j].x * f.x, l2[j].y * f.y);
             }
-            const float cf = stt.cfac[g];
+            const float cf = last_cref / cref;
 #pragma unroll 1
             for (int b = 0; b < N2; b += 16) {
               uint32_t v[16];
@@ -927,15 +945,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         const float sum = (stt.part[g][0][tg] + stt.part[g][1][tg]) + (stt.part[g][2][tg] + stt.part[g][3][tg]);
         const float m = has_o ? -stt.nm[g][tg] : kMinM;
         stt.nm[g][tg] = 0.f;
+        stt.fac[g][tg] = sum == 0.f ? 0.f : cref / (sum * kTopCode);
         if constexpr (CLUSTER) {
-          stt.fac[g][tg] = has_o ? __fdividef(cref, kPScale) : 0.f;
           stt.xm[g][tg] = m;
           stt.xl[g][tg] = sum;
-        } else {
-          stt.fac[g][tg] = sum == 0.f ? 0.f : cref / (sum * kPScale);
-          if (p.lse != nullptr && tg < nh)
-            p.lse[pl.lse + tg] =
-                sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+        } else if (p.lse != nullptr && tg < nh) {
+          p.lse[pl.lse + tg] =
+              sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
         }
       }
       if (has_o) wait_outputs();
@@ -1003,8 +1019,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
           m = fmaxf(m, __shfl_xor_sync(lanes, m, d));
           nan |= __shfl_xor_sync(lanes, nan, d);
         }
-        const float f = nan ? NAN : ex2(m_r - m);
-        float sum = f * l_r;
+        const float f = nan ? NAN : ex2(m_r - m) * l_r;
+        float sum = f;
         for (int d = R / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(lanes, sum, d);
         (&stt.fac[0][0])[threadIdx.x] = sum == 0.f ? 0.f : __fdividef(f, sum);
         if (p.lse != nullptr && r == 0 && h < nh)
