@@ -442,10 +442,12 @@ fp8idx_status fp8idx_paged_step_tables(
  * Each row x of head_dim values becomes scale = max|x| / 448 (f32) and codes
  * e4m3(clamp(x / scale, -448, 448)), rounded to nearest even; a row of zeros
  * has scale 0 and codes 0.  A NaN does not count in the maximum and keeps a NaN
- * code; an infinity makes the scale infinite.  Token t goes to slot s = slot_mapping[t]: token
- * s % block_size of block s / block_size.  A slot that is negative or past
- * the cache is skipped.  The slots of one call must differ (otherwise which
- * token's bytes remain is unspecified).
+ * code (in a row without other values than zeros, too); an infinity makes the
+ * scale infinite, and its own code NaN.
+ * Token t goes to slot s = slot_mapping[t]: token s % block_size of block
+ * s / block_size.  A slot that is negative or past the cache is skipped.  The
+ * slots of one call must differ (otherwise which token's bytes remain is
+ * unspecified).
  *
  *  k             [tokens, head_dim] (index cache) or [tokens, kv_heads,
  *                head_dim] (key/value cache), BF16, F16 or F32, unit inner

@@ -47,12 +47,13 @@ def step_tables(old_lens, new_lens, free_blocks, free_count, block_size, block_t
 
 def quantise_rows(x):
     """x [..., D] f32 -> (e4m3 codes u8 [..., D], scales f32 [...]): scale =
-    max|x| / 448 and x / scale in f32, codes rounded to nearest even."""
+    max|x| / 448 (NaN do not count) and x / scale in f32, codes rounded to
+    nearest even, NaN codes for NaN."""
     x = np.asarray(x, np.float32)
-    amax = np.abs(x).max(-1)
+    amax = np.fmax.reduce(np.abs(x), axis=-1, initial=0)
     scale = (amax / np.float32(448)).astype(np.float32)
     with np.errstate(invalid="ignore", divide="ignore"):
-        y = np.where(amax[..., None] == 0, np.float32(0), x / scale[..., None]).astype(np.float32)
+        y = np.where((amax[..., None] == 0) & ~np.isnan(x), np.float32(0), x / scale[..., None]).astype(np.float32)
     y = np.clip(y, -448, 448)
     return torch.from_numpy(np.ascontiguousarray(y)).to(torch.float8_e4m3fn).view(torch.uint8).numpy(), scale
 

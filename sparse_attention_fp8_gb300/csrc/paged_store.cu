@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kStoreThreads) paged_store_kernel(const PagedS
       }
       if (divide) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = amax == 0.f ? 0.f : __fdiv_rn(x[j], scale);
+        for (int j = 0; j < 8; ++j)  // (amax is 0 for a row of zeros and NaN, too: the NaN stay)
+          y[j] = amax != 0.f ? __fdiv_rn(x[j], scale) : x[j] == 0.f ? 0.f : x[j];
       }
       uint32_t codes[2];
 #pragma unroll

@@ -152,3 +152,37 @@ def test_no_tokens_and_capture(fp8idx):
     got = cache.cpu().numpy()
     assert np.array_equal(got[1, 36 * 128: 56 * 128], want[1, 36 * 128: 56 * 128])
     assert np.array_equal(got[1, 64 * 128 + 144: 64 * 128 + 224], want[1, 64 * 128 + 144: 64 * 128 + 224])
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_without_a_number_above_zero_keep_their_nan(fp8idx, kind, D):
+    """A row of NaN, and NaN among zeros: the maximum is 0, the scale 0, and
+    each NaN keeps a NaN code (keys and values, index keys)."""
+    H, bs = 2, 16
+    x = torch.zeros((4, H, D))
+    x[0] = float("nan")
+    x[1, :, 5] = float("nan")
+    x[2, 0, D - 1] = -float("nan")
+    x[3, 1, ::3] = float("nan")
+    y = x.flip(0)
+    want = np.zeros((2, H, ref.page_bytes(bs, D)), np.uint8)
+    slots = np.array([3, 17, 0, 31], np.int32)
+    cache = torch.full(want.shape, 0x55, dtype=torch.uint8, device="cuda")
+    fp8idx.fp8_paged_store(x.to(TYPES[kind]).cuda(), y.to(TYPES[kind]).cuda(), torch.from_numpy(slots).cuda(), cache)
+    got = cache.cpu().numpy()
+    index = torch.full((2, bs * (D + 4)), 0x55, dtype=torch.uint8, device="cuda")
+    fp8idx.fp8_paged_store(x[:, 0].to(TYPES[kind]).cuda(), None, torch.from_numpy(slots).cuda(), index)
+    got_index = index.cpu().numpy()
+    for t, s in enumerate(slots.tolist()):
+        b, o = divmod(s, bs)
+        for part, rows in enumerate((x, y)):
+            for h in range(H):
+                a = (2 * o + part) * D
+                codes, nan = got[b, h, a: a + D], rows[t, h].isnan().numpy()
+                assert (codes[nan] & 0x7F == 0x7F).all() and (codes[~nan] == 0).all(), (t, part, h)
+                a = bs * 2 * D + 4 * (2 * o + part)
+                assert got[b, h, a: a + 4].view(np.float32)[0] == 0
+        codes, nan = got_index[b, o * D: (o + 1) * D], x[t, 0].isnan().numpy()
+        assert (codes[nan] & 0x7F == 0x7F).all() and (codes[~nan] == 0).all(), t
+        assert got_index[b, bs * D + 4 * o: bs * D + 4 * o + 4].view(np.float32)[0] == 0
