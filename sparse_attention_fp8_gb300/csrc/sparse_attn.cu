@@ -223,9 +223,9 @@ __device__ __forceinline__ void split_pair(__half2 x, uint32_t* h, uint32_t* l) 
 
 // The query's split: every element of a unit times the 2^e that puts the
 // unit's largest finite one into [128, 256), as two e4m3 values.  If the
-// largest element of one of its heads is less than 1/16 of that, every head
-// gets an e of its own, and its scores the factor 2^(unit's e - its e).  So a
-// head's elements are exact down to 2^-10 of its largest one, and off by at
+// largest element of one of its heads lies below 16 then, every head gets an e
+// of its own, and its scores the factor 2^(unit's e - its e).  So a head's
+// elements are exact from 2^-6 on, 2^-10 of its largest one, and off by at
 // most 2^-18 of that below (half a step of 2^-13).
 struct QueryPiece {
   uint32_t top;  // the largest element's bits without its sign (bf16 values are then ordered as integers)
@@ -251,7 +251,7 @@ __device__ __forceinline__ int query_exponent(uint32_t top) {
 // heads' are between `low` (of those that have one, else 0xFFFF) and `high`.
 __device__ __forceinline__ int head_exponent(uint32_t top, uint32_t low, uint32_t high, bool* apart) {
   const int unit_e = query_exponent(high);
-  *apart = low != 0xFFFFu && query_exponent(low) > unit_e + 4;
+  *apart = low != 0xFFFFu && query_exponent(low) > unit_e + 3;
   return *apart && top != 0u ? query_exponent(top) : unit_e;
 }
 __device__ __forceinline__ uint32_t low_of(uint32_t top) { return top == 0u ? 0xFFFFu : top; }

@@ -229,3 +229,25 @@ def test_value_scales_that_are_no_numbers(fp8idx, value, ctas):
     assert np.isnan(got[0]).all()
     assert (np.abs(z[0] - want[1][0]) <= 2.0**-16 * (1 + want[4][0])).all()
     assert_attention(got[1:], z[1:], tuple(w[1:] for w in want))
+
+
+@pytest.mark.parametrize("n", [1, 320])
+@pytest.mark.parametrize("D", [64, 128])
+def test_heads_eight_times_smaller_keep_their_bits(fp8idx, D, n):
+    """A head whose largest element lies in [8, 16) where the unit's lies in
+    [128, 256): its elements down to 2^-10 of its largest one are exact."""
+    rng = np.random.default_rng(43)
+    H = 20
+    q, cache, tables = setup(rng, 1, n, H, 1, D, 16, 64, extra=0)
+    q[:] = 0
+    q[:, :, 0, 0] = 200.0
+    q[:, :, 1:, 0] = 8.0
+    # (eight significant bits, the last of them set)
+    q[:, :, 1:, 1] = 2.0**-7 * (1 + rng.integers(0, 64, (1, n, H - 1)) / 64 + 1 / 128)
+    cache[:, 0, : 16 * 2 * D].reshape(-1, 16, 2, D)[:, :, 0] = 0
+    codes = rng.integers(0x70, 0x7F, (4, 16))
+    cache[:, 0, : 16 * 2 * D].reshape(-1, 16, 2, D)[:, :, 0, 1] = codes
+    sc, put = scales_of(cache, 16, D)
+    sc[..., 0] = 1.0
+    put()
+    attend(fp8idx, q, cache, pick(rng, n, 60, 64), tables, 16, 1.0)
