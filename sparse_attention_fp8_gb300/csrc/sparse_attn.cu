@@ -226,7 +226,11 @@ __device__ __forceinline__ void split_pair(__half2 x, uint32_t* h, uint32_t* l) 
 // largest element of one of its heads lies below 16 then, every head gets an e
 // of its own, and its scores the factor 2^(unit's e - its e).  So a head's
 // elements are exact from 2^-6 on, 2^-10 of its largest one, and off by at
-// most 2^-18 of that below (half a step of 2^-13).
+// most 2^-18 of that below (half a step of 2^-13).  Factors go down to 2^-126:
+// where heads are further apart than that, the unit's e is so much larger, and
+// its scores in the accumulator (at most 2^24 before) so much larger with it.
+// It takes 96 at most: heads more than 2^222 below the largest, whose elements
+// are below 2^-94, then have scores off by less than 2^-78 times the scales.
 struct QueryPiece {
   uint32_t top;  // the largest element's bits without its sign (bf16 values are then ordered as integers)
   bool odd;      // infinities or NaN among them (from 0x7F80; they do not count)
@@ -248,11 +252,13 @@ __device__ __forceinline__ int query_exponent(uint32_t top) {
   return top == 0u ? 0 : min(max(e, -120), 120);
 }
 // The exponent of a head with largest element `top` (0: none) in a unit whose
-// heads' are between `low` (of those that have one, else 0xFFFF) and `high`.
-__device__ __forceinline__ int head_exponent(uint32_t top, uint32_t low, uint32_t high, bool* apart) {
-  const int unit_e = query_exponent(high);
-  *apart = low != 0xFFFFu && query_exponent(low) > unit_e + 3;
-  return *apart && top != 0u ? query_exponent(top) : unit_e;
+// heads' are between `low` (of those that have one, else 0xFFFF) and `high`;
+// unit_e: the unit's.
+__device__ __forceinline__ int head_exponent(uint32_t top, uint32_t low, uint32_t high, bool* apart, int* unit_e) {
+  const int e = query_exponent(high), gap = low != 0xFFFFu ? query_exponent(low) - e : 0;
+  *apart = gap > 3;
+  *unit_e = e + min(max(gap - 126, 0), 96);
+  return *apart && top != 0u ? query_exponent(top) : *unit_e;
 }
 __device__ __forceinline__ uint32_t low_of(uint32_t top) { return top == 0u ? 0xFFFFu : top; }
 
@@ -530,7 +536,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
         odd = ((x.x | y.x) & 0x10000u) != 0u;
         const uint32_t top = max(x.x & 0xFFFFu, y.x & 0xFFFFu);
         bool apart;
-        const int e = head_exponent(t[0], min(x.y, y.y), top, &apart), unit_e = query_exponent(top);
+        int unit_e;
+        const int e = head_exponent(t[0], min(x.y, y.y), top, &apart, &unit_e);
         stt.qhead[buf][first + head_of] = static_cast<int8_t>(max(unit_e - e, -126));
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
@@ -691,7 +698,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       odd = ptx::bar_or(1 + NG, 4 * NG * 32, odd);
       const uint32_t top = lane < GP ? stt.top[lane % GP] : 0u, high = __reduce_max_sync(kFull, top);
       bool apart;
-      const int e = head_exponent(top, __reduce_min_sync(kFull, low_of(top)), high, &apart), unit_e = query_exponent(high);
+      int unit_e;
+      const int e = head_exponent(top, __reduce_min_sync(kFull, low_of(top)), high, &apart, &unit_e);
       if (threadIdx.x < GP) stt.qhead[0][threadIdx.x] = static_cast<int8_t>(max(unit_e - e, -126));
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {

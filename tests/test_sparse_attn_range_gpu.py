@@ -251,3 +251,20 @@ def test_heads_eight_times_smaller_keep_their_bits(fp8idx, D, n):
     sc[..., 0] = 1.0
     put()
     attend(fp8idx, q, cache, pick(rng, n, 60, 64), tables, 16, 1.0)
+
+
+@pytest.mark.parametrize("n", [1, 320])
+@pytest.mark.parametrize("top", [-80, -40, -10, 0, 40, 100])
+def test_heads_as_far_apart_as_bf16_goes(fp8idx, top, n):
+    """Heads of 2^127 next to ones of 2^top: keys that are zero where the
+    large heads are not leave those a score of 0."""
+    rng = np.random.default_rng(44)
+    D, H = 64, 20
+    q, cache, tables = setup(rng, 1, n, H, 1, D, 16, 64, extra=0)
+    q[:, :, 0::2, 32:] = 0
+    q[:, :, 0::2, :32] = 2.0**127 * rng.uniform(1, 1.9, (1, n, H // 2, 32))
+    q[:, :, 1::2, :32] = 0
+    q[:, :, 1::2, 32:] *= 2.0**top
+    q[:, :, 3] = 0
+    cache[:, 0, : 16 * 2 * D].reshape(-1, 16, 2, D)[:, :, 0, :32] = 0
+    attend(fp8idx, q, cache, pick(rng, n, 60, 64), tables, 16, 0.3 * 2.0**-top)
