@@ -769,22 +769,74 @@ fp8idx_status check_vector(const fp8idx_tensor* t, const char* name, int64_t n) 
   return FP8IDX_OK;
 }
 
-// Whether the bytes of two tensors (with non-negative strides) can overlap,
-// as ranges of addresses.
-bool ranges_overlap(const fp8idx_tensor* a, const fp8idx_tensor* b) {
-  const auto range = [](const fp8idx_tensor* t, uintptr_t* lo, uintptr_t* hi) {
-    const int64_t size = t->dtype == FP8IDX_U8 ? 1 : (t->dtype == FP8IDX_BF16 || t->dtype == FP8IDX_F16) ? 2 : 4;
-    int64_t last = 0;
-    for (int i = 0; i < t->ndim; ++i) {
-      if (t->shape[i] == 0) return false;
-      last += (t->shape[i] - 1) * t->stride[i];
+// The bytes of a tensor with non-negative strides: runs of `run` bytes, spaced
+// by the strides of the dimensions that are not part of a run (largest first;
+// a stride of 0 repeats the same bytes).
+struct Extent {
+  uintptr_t at = 0;
+  int64_t run = 0, size = 0;  // bytes of a run (0: empty), from the first byte to the last
+  int dims = 0;
+  int64_t count[4], stride[4];
+
+  explicit Extent(const fp8idx_tensor* t) {
+    at = reinterpret_cast<uintptr_t>(t->data);
+    const int64_t item = t->dtype == FP8IDX_U8 ? 1 : (t->dtype == FP8IDX_BF16 || t->dtype == FP8IDX_F16) ? 2 : 4;
+    run = item;
+    for (int i = t->ndim - 1; i >= 0; --i) {
+      if (t->shape[i] == 0) {
+        run = size = 0;
+        return;
+      }
+      if (t->shape[i] == 1 || t->stride[i] == 0) continue;
+      const int64_t step = t->stride[i] * item;
+      if (dims == 0 && step == run) {
+        run *= t->shape[i];
+        continue;
+      }
+      int j = dims++;
+      for (; j > 0 && stride[j - 1] < step; --j) stride[j] = stride[j - 1], count[j] = count[j - 1];
+      stride[j] = step;
+      count[j] = t->shape[i];
     }
-    *lo = reinterpret_cast<uintptr_t>(t->data);
-    *hi = *lo + static_cast<uintptr_t>((last + 1) * size);
-    return true;
-  };
-  uintptr_t al, ah, bl, bh;
-  return range(a, &al, &ah) && range(b, &bl, &bh) && al < bh && bl < ah;
+    size = run;
+    for (int i = 0; i < dims; ++i) size += (count[i] - 1) * stride[i];
+  }
+  // One step of the outermost dimension, moved by `by` bytes.
+  Extent inner(int64_t by) const {
+    Extent e = *this;
+    e.at += static_cast<uintptr_t>(by);
+    e.size -= (count[0] - 1) * stride[0];
+    --e.dims;
+    for (int i = 0; i < e.dims; ++i) e.count[i] = count[i + 1], e.stride[i] = stride[i + 1];
+    return e;
+  }
+};
+
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0 ? 1 : 0); }
+
+// Whether two tensors share bytes.  Slices of one tensor that lie between one
+// another do not.  Both are taken apart step by step, at most `budget` steps,
+// after which they count as overlapping.
+bool share_bytes(const Extent& a, const Extent& b, int* budget) {
+  if (a.run == 0 || b.run == 0 || a.at >= b.at + static_cast<uintptr_t>(b.size) ||
+      b.at >= a.at + static_cast<uintptr_t>(a.size))
+    return false;
+  if (a.dims == 0 && b.dims == 0) return true;
+  if (a.dims == 0 || (b.dims > 0 && b.stride[0] > a.stride[0])) return share_bytes(b, a, budget);
+  // the steps k of a's outermost dimension (with equal strides: the difference
+  // of both's steps) that come near b
+  const bool both = b.dims > 0 && b.stride[0] == a.stride[0];
+  const Extent x = a.inner(0), y = both ? b.inner(0) : b;
+  const int64_t s = a.stride[0], d = static_cast<int64_t>(y.at - x.at);
+  const int64_t lo = std::max(floor_div(d - x.size, s) + 1, both ? 1 - b.count[0] : int64_t{0});
+  const int64_t hi = std::min(floor_div(d + y.size - 1, s), a.count[0] - 1);
+  for (int64_t k = lo; k <= hi; ++k)
+    if (--*budget < 0 || share_bytes(a.inner(k * s), y, budget)) return true;
+  return false;
+}
+bool tensors_overlap(const fp8idx_tensor* a, const fp8idx_tensor* b) {
+  int budget = 1024;
+  return share_bytes(Extent(a), Extent(b), &budget);
 }
 
 fp8idx_status step_tables_impl(const fp8idx_tensor* old_lens, const fp8idx_tensor* new_lens,
@@ -823,10 +875,10 @@ fp8idx_status step_tables_impl(const fp8idx_tensor* old_lens, const fp8idx_tenso
   for (int i = 0; i < 8; ++i) {
     if (!outs[i]) continue;
     for (const fp8idx_tensor* in : ins)
-      if (ranges_overlap(in, outs[i]))
+      if (tensors_overlap(in, outs[i]))
         return fail(FP8IDX_ERR_INVALID, "step tables: an output overlaps an input");
     for (int j = 0; j < i; ++j)
-      if (outs[j] && ranges_overlap(outs[j], outs[i]))
+      if (outs[j] && tensors_overlap(outs[j], outs[i]))
         return fail(FP8IDX_ERR_INVALID, "step tables: two outputs overlap");
   }
   StepTablesParams p;

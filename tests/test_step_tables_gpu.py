@@ -150,3 +150,23 @@ def test_strided_tables(fp8idx):
     want = ref.step_tables(old, new, free, len(free), 16, tables, rows)
     assert np.array_equal(view.cpu().numpy(), want["block_tables"])
     assert (wide[:, :9] == 4242).all() and (wide[:, 21:] == 4242).all()
+
+
+def test_outputs_between_the_rows_of_a_table(fp8idx):
+    """The block table as columns of a wider tensor whose other columns hold
+    a step's vectors: nothing overlaps."""
+    rng = np.random.default_rng(10)
+    old, new, free, tables = batch(rng, 5, 16, 12, 30)
+    wide = torch.full((5, 60), 4242, dtype=torch.int32, device="cuda")
+    view, ctx, cu, count, counts = wide[:, 9:21], wide[0, 30:35], wide[1, 30:36], wide[2, 30:31], wide[3, 30:34]
+    view.copy_(torch.from_numpy(tables))
+    count.fill_(len(free))
+    d = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).cuda()  # noqa: E731
+    rows = int(new.sum())
+    slots = torch.empty(rows, dtype=torch.int32, device="cuda")
+    fp8idx.paged_step_tables(d(old), d(new), d(free), count, 16, view, ctx, cu, slots, counts)
+    want = ref.step_tables(old, new, free, len(free), 16, tables, rows)
+    for t, name in ((view, "block_tables"), (ctx, "context_lens"), (cu, "cu_new_lens"), (counts, "counts"),
+                    (slots, "slot_mapping")):
+        assert np.array_equal(t.cpu().numpy(), want[name]), name
+    assert (wide[:, :9] == 4242).all() and (wide[:, 21:30] == 4242).all() and (wide[:, 36:] == 4242).all()
