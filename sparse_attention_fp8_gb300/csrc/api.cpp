@@ -810,6 +810,16 @@ struct Extent {
     for (int i = 0; i < e.dims; ++i) e.count[i] = count[i + 1], e.stride[i] = stride[i + 1];
     return e;
   }
+  // Whether two elements share bytes.  (Exact for views of a tensor, whose
+  // dimensions lie within one another.)
+  bool overlaps_itself() const {
+    int64_t within = run;
+    for (int i = dims - 1; i >= 0; --i) {
+      if (stride[i] < within) return true;
+      within += (count[i] - 1) * stride[i];
+    }
+    return false;
+  }
 };
 
 int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0 ? 1 : 0); }
@@ -1033,6 +1043,7 @@ fp8idx_status sparse_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, 
     if (q->shape[i] > 1 && q->stride[i] < 0) return fail(FP8IDX_ERR_INVALID, "q: negative stride");
     if (out->shape[i] > 1 && out->stride[i] < D) return fail(FP8IDX_ERR_INVALID, "out: rows overlap");
   }
+  if (Extent(out).overlaps_itself()) return fail(FP8IDX_ERR_INVALID, "out: rows overlap");
   if (H < 1 || n < 1) return fail(FP8IDX_ERR_INVALID, "q has no heads or rows per request");
   int64_t bs = 0;
   TRY(check_kv_cache(kv, D, &bs));

@@ -214,3 +214,17 @@ def test_definition_of_attention_by_hand():
     out, lse, *_ = ref.sparse_attention(np.full((1, 1, D), 0.5), cache, np.array([[3, 9, -1]]), np.zeros((1, 1), int), bs,
                                         1.0, next_n=1)
     assert np.allclose(out, 3.0) and np.allclose(lse, 32 + np.log(2))
+
+
+def strided(t, *stride):
+    for i, s in enumerate(stride):
+        t.stride[i] = s
+    return t
+
+
+@pytest.mark.parametrize("stride", [(128, 128, 128, 1), (8192, 128, 128, 1), (128, 256, 640, 1), (1024, 1024, 128, 1),
+                                    (1024, 1920, 128, 1), (3 * 8 * 128 - 8, 8 * 128, 128, 1), (3 * 8 * 128, 8 * 128, 120, 1)])
+def test_outputs_whose_rows_overlap(lib, stride):
+    """Strides that are each no less than a row, but not next to one another."""
+    out = strided(_t(BF16, (2, 3, 8, 128), 0x900000), *stride)
+    refused(lib, lib.fp8_paged_sparse_attn(*attn_args(out=out)), INVALID, b"out: rows overlap")

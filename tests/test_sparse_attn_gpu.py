@@ -453,3 +453,22 @@ def test_no_rows(fp8idx):
     q = torch.empty((0, 1, 4, 64), dtype=torch.bfloat16, device="cuda")
     fp8idx.fp8_paged_sparse_attn(q, cache, torch.empty((0, 8), dtype=torch.int32, device="cuda"),
                                  torch.empty((0, 2), dtype=torch.int32, device="cuda"), 1.0, torch.empty_like(q))
+
+
+def test_outputs_between_inputs_and_in_other_orders(fp8idx):
+    """q and out as column ranges of one tensor (their rows lie between one
+    another), and an out whose heads lie outermost."""
+    rng = np.random.default_rng(31)
+    B, n, H, HK, D, bs = 2, 3, 8, 2, 64, 16
+    q, cache, tables = setup(rng, B, n, H, HK, D, bs, 300)
+    idx = pick(rng, B * n, 250, 300)
+    dc, di, dt = (torch.from_numpy(a).cuda() for a in (cache, idx, tables))
+    both = torch.full((B, n, H, 3 * D), 5.0, dtype=torch.bfloat16, device="cuda")
+    both[..., D: 2 * D] = torch.from_numpy(q).to(torch.bfloat16)
+    turned = torch.full((H, B, n, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    want = ref.sparse_attention(bf16(q).reshape(B * n, H, D).astype(np.float64), cache, idx, tables, bs, 0.1, next_n=n)
+    for out in (both[..., 2 * D:], turned.permute(1, 2, 0, 3)):
+        lse = torch.full((B * n, H), float("nan"), device="cuda")
+        fp8idx.fp8_paged_sparse_attn(both[..., D: 2 * D], dc, di, dt, 0.1, out, lse=lse)
+        assert_attention(out.float().cpu().numpy().reshape(B * n, H, D), lse.cpu().numpy(), want)
+    assert (both[..., :D] == 5).all()
