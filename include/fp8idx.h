@@ -459,7 +459,8 @@ fp8idx_status fp8idx_paged_step_tables(
  *                kv_heads, page] U8 as described above (any block and head
  *                strides that are multiples of 16 bytes; pages contiguous);
  *                16-byte aligned; block_size 1, 16, 32, 64 or 128;
- *                num_blocks*block_size < 2^31.
+ *                num_blocks*block_size < 2^31; shares no bytes with k, v or
+ *                slot_mapping.
  * One kernel on `stream`.
  */
 fp8idx_status fp8_paged_store(const fp8idx_tensor* k, const fp8idx_tensor* v,
@@ -497,7 +498,8 @@ fp8idx_status fp8_paged_store(const fp8idx_tensor* k, const fp8idx_tensor* v,
  *                every row selects the same), k 1 .. 2048.
  *  out           shape and type of q, unit inner stride, rows that do not
  *                overlap one another or an input.
- *  lse           [rows, heads] F32, contiguous, or NULL.
+ *  lse           [rows, heads] F32, contiguous, or NULL; shares no bytes with
+ *                the other arguments.
  *  heads a multiple of kv_heads, heads/kv_heads <= 128.
  *  opts          NULL or num_ctas: the CTAs per row, key head and 32 query
  *                heads (0 = heuristic; 1, 2, 4 or 8), other fields ignored.

@@ -1000,6 +1000,8 @@ fp8idx_status paged_store_impl(const fp8idx_tensor* k, const fp8idx_tensor* v, c
   if (T * H * (v ? 2 : 1) >= (1ll << 31) - 4096)
     return fail(FP8IDX_ERR_UNSUPPORTED, "store: %lld tokens of %lld heads in one call", (long long)T, (long long)H);
   if (T == 0 || H == 0) return ok();
+  if (tensors_overlap(kv, k) || (v && tensors_overlap(kv, v)) || tensors_overlap(kv, slots))
+    return fail(FP8IDX_ERR_INVALID, "store: the cache overlaps an input");
   p.slots = static_cast<const int32_t*>(slots->data);
   p.cache = static_cast<uint8_t*>(kv->data);
   p.num_slots = kv->shape[0] * bs;
@@ -1128,6 +1130,11 @@ fp8idx_status sparse_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, 
     return fail(FP8IDX_ERR_UNSUPPORTED, "sparse attention: too many rows");
   p.units = (int32_t)(R * HK * p.head_chunks);
   p.tiles = (int32_t)((k + kAttnTile - 1) / kAttnTile);
+  const fp8idx_tensor* ins[] = {q, kv, idx, bt, prefill ? cu : bt};
+  for (const fp8idx_tensor* in : ins)
+    if (tensors_overlap(out, in) || (lse && tensors_overlap(lse, in)))
+      return fail(FP8IDX_ERR_INVALID, "sparse attention: an output overlaps an input");
+  if (lse && tensors_overlap(out, lse)) return fail(FP8IDX_ERR_INVALID, "sparse attention: out and lse overlap");
   DeviceInfo dev;
   TRY(device_info(&dev));
   // Persistent CTAs (two units at a time), or a cluster of CTAs per unit

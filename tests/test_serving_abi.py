@@ -228,3 +228,34 @@ def test_outputs_whose_rows_overlap(lib, stride):
     """Strides that are each no less than a row, but not next to one another."""
     out = strided(_t(BF16, (2, 3, 8, 128), 0x900000), *stride)
     refused(lib, lib.fp8_paged_sparse_attn(*attn_args(out=out)), INVALID, b"out: rows overlap")
+
+
+def test_outputs_that_overlap_inputs(lib):
+    f, g = lib.fp8_paged_sparse_attn, lib.fp8_mqa_sparse_attn_paged
+    far = dict(q=_t(BF16, (2, 3, 8, 128), 0x10000), kv=_t(U8, (9, 2, 16 * 264), 0x100000), idx=_t(I32, (6, 50), 0x20000),
+               bt=_t(I32, (2, 5), 0x30000), out=_t(BF16, (2, 3, 8, 128), 0x40000), lse=_t(F32, (6, 8), 0x50000))
+
+    def moved(name, at):
+        t = {"out": _t(BF16, (2, 3, 8, 128), at), "lse": _t(F32, (6, 8), at)}[name]
+        refused(lib, f(*attn_args(**{**far, name: t})), INVALID, b"overlap")
+    for at in (0x10000, 0x10000 + 12286, 0x10000 - 12286, 0x100010, 0x20004, 0x30008, 0x50000):
+        moved("out", at)
+    for at in (0x10000, 0x100000 + 9 * 2 * 16 * 264 - 4, 0x20000, 0x30000 - 4, 0x40000):
+        moved("lse", at)
+    # a head of every row of out lies on one of q's
+    q = strided(_t(BF16, (2, 3, 8, 128), 0x10000), 3 * 8 * 1024, 8 * 1024, 1024)
+    out = strided(_t(BF16, (2, 3, 8, 128), 0x10000 + 2 * (1024 - 120)), 3 * 8 * 1024, 8 * 1024, 1024)
+    refused(lib, f(*attn_args(**{**far, "q": q, "out": out, "kv": _t(U8, (9, 2, 16 * 264), 0x1000000)})), INVALID, b"overlap")
+    cu = _t(I32, (3,), 0x60000)
+    refused(lib, g(R(_t(BF16, (6, 8, 128), 0x10000)), R(far["kv"]), R(far["bt"]), R(cu), R(far["idx"]), 1.0,
+                   R(_t(BF16, (6, 8, 128), 0x60000 + 8)), None, None, None), INVALID, b"overlap")
+
+
+def test_caches_that_overlap_rows(lib):
+    f = lib.fp8_paged_store
+    k, v, slots = _t(BF16, (5, 2, 128), 0x10000), _t(BF16, (5, 2, 128), 0x20000), _t(I32, (5,), 0x30000)
+    size = 4 * 2 * 16 * 264
+    for at in (0x10000, 0x20000 - size + 16, 0x30000):
+        refused(lib, f(R(k), R(v), R(slots), R(_t(U8, (4, 2, 16 * 264), at)), None), INVALID, b"overlap")
+    refused(lib, f(R(_t(F32, (5, 128), 0x10000)), None, R(slots), R(_t(U8, (4, 64 * 132), 0x10000 + 256)), None), INVALID,
+            b"overlap")
