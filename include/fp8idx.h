@@ -20,11 +20,11 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *    stream).  Work is enqueued asynchronously; no call synchronises the
  *    host, so the compute calls can be captured in a CUDA graph.
- *  - Shapes, dtypes, strides and alignment are checked on the host before
- *    anything is launched.  A non-OK status launches nothing (except
- *    FP8IDX_ERR_CUDA, returned when the launch itself failed); the message
- *    for the last non-OK status on the calling thread is available from
- *    fp8idx_last_error().
+ *  - Shapes, dtypes, strides and alignment (at least that of an element) are
+ *    checked on the host before anything is launched.  A non-OK status
+ *    launches nothing (except FP8IDX_ERR_CUDA, returned when the launch itself
+ *    failed); the message for the last non-OK status on the calling thread is
+ *    available from fp8idx_last_error().
  *  - Values are not checked (they live on the device).  Preconditions:
  *    kv_scale >= 0 (the hoist of the scale out of the ReLU relies on it);
  *    no NaN in owned Q/K/scales/weights; block ids in range.  Indices read

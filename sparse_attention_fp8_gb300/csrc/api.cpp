@@ -148,6 +148,7 @@ fp8idx_status encode(CUtensorMap* m, CUtensorMapDataType dt, int rank, const voi
 }
 
 // ------------------------------------------------------------ validation
+int element_bytes(int dtype) { return dtype == FP8IDX_U8 ? 1 : (dtype == FP8IDX_BF16 || dtype == FP8IDX_F16) ? 2 : 4; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 fp8idx_status check_tensor(const fp8idx_tensor* t, const char* name, int dtype, int ndim) {
@@ -160,6 +161,8 @@ fp8idx_status check_tensor(const fp8idx_tensor* t, const char* name, int dtype, 
     numel *= t->shape[i];
   }
   if (numel > 0 && !t->data) return fail(FP8IDX_ERR_INVALID, "%s: null data pointer", name);
+  if (numel > 0 && reinterpret_cast<uintptr_t>(t->data) % element_bytes(dtype) != 0)
+    return fail(FP8IDX_ERR_INVALID, "%s: data is not aligned to its elements", name);
   return FP8IDX_OK;
 }
 
@@ -780,7 +783,7 @@ struct Extent {
 
   explicit Extent(const fp8idx_tensor* t) {
     at = reinterpret_cast<uintptr_t>(t->data);
-    const int64_t item = t->dtype == FP8IDX_U8 ? 1 : (t->dtype == FP8IDX_BF16 || t->dtype == FP8IDX_F16) ? 2 : 4;
+    const int64_t item = element_bytes(t->dtype);
     run = item;
     for (int i = t->ndim - 1; i >= 0; --i) {
       if (t->shape[i] == 0) {

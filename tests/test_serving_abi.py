@@ -259,3 +259,27 @@ def test_caches_that_overlap_rows(lib):
         refused(lib, f(R(k), R(v), R(slots), R(_t(U8, (4, 2, 16 * 264), at)), None), INVALID, b"overlap")
     refused(lib, f(R(_t(F32, (5, 128), 0x10000)), None, R(slots), R(_t(U8, (4, 64 * 132), 0x10000 + 256)), None), INVALID,
             b"overlap")
+
+
+def test_data_between_elements(lib):
+    """A pointer that is no multiple of its element's size cannot be read or
+    written by a kernel."""
+    f = lib.fp8_paged_sparse_attn
+    far = dict(q=_t(BF16, (2, 3, 8, 128), 0x10000), kv=_t(U8, (9, 2, 16 * 264), 0x100000), idx=_t(I32, (6, 50), 0x20000),
+               bt=_t(I32, (2, 5), 0x30000), out=_t(BF16, (2, 3, 8, 128), 0x40000), lse=_t(F32, (6, 8), 0x50000))
+    for name, by in (("out", 1), ("idx", 2), ("bt", 1), ("lse", 2)):
+        t = _native_copy(far[name])
+        t.data += by
+        refused(lib, f(*attn_args(**{**far, name: t})), INVALID, b"aligned")
+    refused(lib, lib.fp8idx_paged_step_tables(*step_args(counts=_t(I32, (4,), 0x300002))), INVALID, b"aligned")
+    k, kv = _t(BF16, (5, 2, 128), 0x10000), _t(U8, (4, 2, 16 * 264), 0x100000)
+    refused(lib, lib.fp8_paged_store(R(k), R(k), R(_t(I32, (5,), 0x20001)), R(kv), None), INVALID, b"aligned")
+    # the calls that were there before
+    refused(lib, lib.fp8_paged_topk(R(_t(F32, (6, 100), 0x10002)), R(_t(I32, (2,), 0x20000)), 3, 100, 10,
+                                    R(_t(I32, (6, 10), 0x30000)), None), INVALID, b"aligned")
+
+
+def _native_copy(t):
+    c = type(t)()
+    ctypes.memmove(R(c), R(t), ctypes.sizeof(t))
+    return c
