@@ -39,7 +39,7 @@ _TENSOR_PACK = struct.Struct("=qii4q4q")
 assert _TENSOR_PACK.size == ctypes.sizeof(_Tensor)
 _PACK_1D, _PACK_2D = struct.Struct("=qiiq24xq24x"), struct.Struct("=qiiqq16xqq16x")
 _PAD = (0, 0, 0, 0)
-_dtype_codes = None
+_dtype_codes = _row_codes = None
 
 
 class _Options(ctypes.Structure):
@@ -181,20 +181,21 @@ def _host_mapped(t) -> int:
     return dev.value
 
 
-def _dtype_code(dtype):
-    """The library's code of a torch dtype, None if it has none."""
-    global _dtype_codes
-    if _dtype_codes is None:
+def _codes(rows: bool = False):
+    """The library's codes of torch dtypes: those of the logits and top-k
+    calls, or (rows) also the 16-bit types of the operators around them."""
+    global _dtype_codes, _row_codes
+    if _row_codes is None:
         import torch
-        _dtype_codes = {torch.uint8: _U8, torch.float8_e4m3fn: _U8, torch.float32: _F32, torch.int32: _I32,
-                        torch.bfloat16: _BF16, torch.float16: _F16}
-    return _dtype_codes.get(dtype)
+        _dtype_codes = {torch.uint8: _U8, torch.float8_e4m3fn: _U8, torch.float32: _F32, torch.int32: _I32}
+        _row_codes = {**_dtype_codes, torch.bfloat16: _BF16, torch.float16: _F16}
+    return _row_codes if rows else _dtype_codes
 
 
-def _pack(t, ptr: int) -> bytes:
+def _pack(t, ptr: int, rows: bool = False) -> bytes:
     """Packs tensor t's dtype, shape and strides with data address ptr into
     fp8idx_tensor bytes."""
-    dt = _dtype_code(t.dtype)
+    dt = _codes(rows).get(t.dtype)
     if dt is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
     shape = t.shape
@@ -341,8 +342,7 @@ def _descs(*tensors):
     tensors with vectors and matrices spelt out: a step's tables have twelve
     descriptors, which costs 5 us this way and 13 us tensor by tensor."""
     import torch
-    _dtype_code(torch.uint8)
-    codes, pack_1d, pack_2d = _dtype_codes, _PACK_1D.pack, _PACK_2D.pack
+    codes, pack_1d, pack_2d = _codes(rows=True), _PACK_1D.pack, _PACK_2D.pack
     dev = None
     out = []
     for t in tensors:
@@ -365,7 +365,7 @@ def _descs(*tensors):
             step, inner = t.stride()
             out.append(pack_2d(t.data_ptr(), dt, 2, rows, cols, step, inner))
         else:
-            out.append(_pack(t, t.data_ptr()))
+            out.append(_pack(t, t.data_ptr(), rows=True))
     return out
 
 

@@ -283,3 +283,19 @@ def _native_copy(t):
     c = type(t)()
     ctypes.memmove(R(c), R(t), ctypes.sizeof(t))
     return c
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_binding_of_the_logits_calls_refuses_16_bit_types(monkeypatch, dtype):
+    """The types that the operators around them take: a TypeError of the
+    binding, before the library is called, as for any other type."""
+    from sparse_attention_fp8_gb300 import _native
+    t = torch.zeros((2, 3, 4), dtype=dtype)
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        _native._pack(t, t.data_ptr())
+    monkeypatch.setattr(_native, "_desc", lambda x, out=False: _native._pack(x, x.data_ptr()))
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        fp8idx.fp8_paged_topk(t[0], i, 1, 4, 2, i, stream=0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert len(_native._descs(OnDevice(t, 1))) == 1
