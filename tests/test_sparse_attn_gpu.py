@@ -472,3 +472,68 @@ def test_outputs_between_inputs_and_in_other_orders(fp8idx):
         fp8idx.fp8_paged_sparse_attn(both[..., D: 2 * D], dc, di, dt, 0.1, out, lse=lse)
         assert_attention(out.float().cpu().numpy().reshape(B * n, H, D), lse.cpu().numpy(), want)
     assert (both[..., :D] == 5).all()
+
+
+def test_lse_with_strided_arguments(fp8idx):
+    """As test_strides, with the log-sum-exp compared."""
+    rng = np.random.default_rng(35)
+    B, n, H, HK, D, bs = 2, 3, 8, 2, 128, 32
+    q, cache, tables = setup(rng, B, n, H, HK, D, bs, 300)
+    idx = pick(rng, B * n, 250, 300)
+    wide_q = torch.randn((B, n, H + 4, 2 * D), device="cuda").to(torch.bfloat16)
+    wide_q[:, :, 2: 2 + H, D:] = torch.from_numpy(q).to(torch.bfloat16).cuda()
+    wide_o = torch.full((B, n + 1, H, D + 3), 5.0, dtype=torch.bfloat16, device="cuda")
+    out = wide_o[:, 1:, :, 1: 1 + D]
+    want = ref.sparse_attention(q.reshape(B * n, H, D).astype(np.float64), cache, idx, tables, bs, 0.1, next_n=n)
+    for ctas in (0, 1, 2):
+        more = torch.full((B * n + 2, H), 7.0, device="cuda")
+        lse = more[1:-1]
+        fp8idx.fp8_paged_sparse_attn(wide_q[:, :, 2: 2 + H, D:], torch.from_numpy(cache).cuda(), torch.from_numpy(idx).cuda(),
+                                     torch.from_numpy(tables).cuda(), 0.1, out, lse=lse,
+                                     options=fp8idx.Options(num_ctas=ctas))
+        assert_attention(out.float().cpu().numpy().reshape(B * n, H, D), lse.cpu().numpy(), want)
+        assert (more[0] == 7).all() and (more[-1] == 7).all()
+
+
+def test_lse_of_a_replayed_call(fp8idx):
+    rng = np.random.default_rng(36)
+    q, cache, tables = setup(rng, 2, 2, 16, 1, 128, 64, 1200)
+    idx = pick(rng, 4, 1024, 1200)
+    dq, dc, dt = torch.from_numpy(q).to(torch.bfloat16).cuda(), torch.from_numpy(cache).cuda(), torch.from_numpy(tables).cuda()
+    di = torch.from_numpy(idx).cuda()
+    out, lse = torch.empty_like(dq), torch.empty((4, 16), device="cuda")
+    fp8idx.fp8_paged_sparse_attn(dq, dc, di, dt, 0.1, out, lse=lse)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fp8idx.fp8_paged_sparse_attn(dq, dc, di, dt, 0.1, out, lse=lse)
+    for length in (700, 3, 1200):
+        q2, idx2 = bf16(rng.standard_normal(q.shape)), pick(rng, 4, 1024, length)
+        dq.copy_(torch.from_numpy(q2)), di.copy_(torch.from_numpy(idx2))
+        out.fill_(float("nan")), lse.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        want = ref.sparse_attention(q2.reshape(4, 16, 128).astype(np.float64), cache, idx2, tables, 64, 0.1, next_n=2)
+        assert_attention(out.float().cpu().numpy().reshape(4, 16, 128), lse.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("D,H,rows", [(128, 8, 1), (64, 20, 320)])
+def test_lse_and_prompt_rows_past_32_bits_of_offset(fp8idx, D, H, rows):
+    rng = np.random.default_rng(37)
+    bs = 64
+    page = ref.page_bytes(bs, D)
+    blocks = (5 << 30) // page
+    dev = torch.zeros((blocks, 1, page), dtype=torch.uint8, device="cuda")
+    small = filled_cache(rng, 6, 1, bs, D)
+    ids = np.array([0, blocks - 1, blocks // 2, (1 << 32) // page + 1, (1 << 31) // page + 1, 7])
+    dev[torch.from_numpy(ids).cuda()] = torch.from_numpy(small).cuda()
+    q = bf16(rng.standard_normal((rows, H, D)))
+    idx = pick(rng, rows, 300, 6 * bs)
+    out = torch.empty((rows, H, D), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((rows, H), device="cuda")
+    fp8idx.fp8_mqa_sparse_attn_paged(torch.from_numpy(q).to(torch.bfloat16).cuda(), dev,
+                                     torch.from_numpy(ids.astype(np.int32)[None]).cuda(),
+                                     torch.tensor([0, 6 * bs], dtype=torch.int32, device="cuda"), torch.from_numpy(idx).cuda(),
+                                     0.1, out, lse=lse)
+    want = ref.sparse_attention(q.astype(np.float64), small, idx, np.arange(6, dtype=np.int32)[None], bs, 0.1,
+                                cu_seq_lens=np.array([0, 6 * bs]))
+    assert_attention(out.float().cpu().numpy(), lse.cpu().numpy(), want)
