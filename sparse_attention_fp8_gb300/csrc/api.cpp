@@ -1116,7 +1116,6 @@ fp8idx_status sparse_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, 
   p.tok_units = (uint32_t)(2 * D / unit);
   p.scale_off = (int32_t)(bs * 2 * D);
   p.num_blocks = (int32_t)kv->shape[0];
-  p.rows = (int32_t)R;
   p.heads = (int32_t)H;
   p.kv_heads = (int32_t)HK;
   p.group = (int32_t)(H / HK);

@@ -72,7 +72,7 @@ struct SparseAttnParams {
   // that divides them all: a token's offset is a 32-bit number of units
   uint32_t unit, block_units, head_units, tok_units;
   int32_t scale_off;                                        // bytes from a page to its scales
-  int32_t rows, heads, kv_heads, group;                     // group: query heads per key head
+  int32_t heads, kv_heads, group;                           // group: query heads per key head
   int32_t next_n;                                           // prefill: 1
   int32_t k, max_blocks, block_size, block_shift, n_req;
   float scale_log2;                                         // softmax_scale * log2(e)
@@ -80,6 +80,8 @@ struct SparseAttnParams {
   int32_t units;                // rows * kv_heads * head_chunks
   int32_t tiles;                // 128-entry tiles per row
 };
+// (tested ranges: the top-k's largest k, and the largest group in use; no
+// buffer depends on either)
 constexpr int kAttnMaxK = 2048;
 constexpr int kAttnMaxGroup = 128;
 constexpr int kAttnMaxCtas = 8;   // CTAs per unit (portable cluster size)
@@ -108,9 +110,7 @@ constexpr int kAttnQueryBuffers = kAttnGroups + 1;
 // the queries and probabilities.
 constexpr uint32_t kAttnHalfBytes = kAttnTile * 128u;
 __host__ __device__ constexpr int attn_k_stages(int head_dim) { return head_dim == 128 ? 4 : 0; }
-__host__ __device__ constexpr int attn_v_stages(int head_dim, int gp) {
-  return head_dim == 64 ? 8 : 6;
-}
+__host__ __device__ constexpr int attn_v_stages(int head_dim) { return head_dim == 64 ? 8 : 6; }
 struct AttnSmem {
   uint32_t k, v, q, p, scale, mask, flt, bars, misc, total;
 };
@@ -118,7 +118,7 @@ struct AttnSmem {
 __host__ __device__ constexpr int attn_state_floats(int gp) { return 25 * gp + 40; }
 __host__ __device__ constexpr AttnSmem attn_smem_layout(int head_dim, int gp) {
   AttnSmem L{};
-  const uint32_t stages = static_cast<uint32_t>(attn_v_stages(head_dim, gp));
+  const uint32_t stages = static_cast<uint32_t>(attn_v_stages(head_dim));
   uint32_t off = 0;
   L.k = off;     off += attn_k_stages(head_dim) * kAttnHalfBytes;
   L.v = off;     off += stages * kAttnHalfBytes;

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
   constexpr int N2 = 2 * GP;                       // columns of S^T and O^T
   constexpr int SBG = 2;                           // accumulators of S^T per group
   constexpr int QB = kAttnQueryBuffers, PB = kAttnProbBuffers;
-  constexpr int KS = attn_k_stages(D), S = attn_v_stages(D, GP);  // D = 64: keys and values share the rows of S
+  constexpr int KS = attn_k_stages(D), S = attn_v_stages(D);  // D = 64: keys and values share the rows of S
   constexpr int KSG = KS > 0 ? KS / NG : 1, SG = S / NG;         // a group's share
   static_assert(KS % NG == 0 && S % NG == 0 && SG >= SBG, "stages");
   static_assert(SBG == 2 && PB == 2 && (KS == 0 || KSG == SBG), "rings that go in step");
