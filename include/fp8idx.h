@@ -510,10 +510,11 @@ fp8idx_status fp8_paged_store(const fp8idx_tensor* k, const fp8idx_tensor* v,
  * for the tensor cores: 8 significant bits, those of bf16 (the products are
  * rounded to f16 first, the sums that divide them are not).  A query's elements
  * below 2^-10 of its head's largest one may be off by 2^-18 of that, a product
- * below 2^-11 of its row and head's largest one by 2^-19 of that.  The value
- * scales that a row selects may lie up to 2^80 apart: with a wider range, or
- * where every product is less than 2^-80 of the row's largest probability times
- * its largest value scale, the smaller ones have fewer bits.
+ * below 2^-11 of its row and head's largest one by 2^-19 of that.  This holds
+ * while the value scales that a row selects (but for zeros) lie within 2^64 of
+ * one another and its largest product is no less than 2^-110 of its largest
+ * probability times its largest value scale; past that products have fewer
+ * bits.
  * A NaN or an infinity in q makes its head's outputs NaN; a NaN in a key, value
  * or scale, and an infinite value scale, reaches the rows that select it, no
  * others.

@@ -82,12 +82,14 @@ constexpr uint32_t kFull = 0xffffffffu;
 // which then has the code 32 and the others steps of 2^-18 of it.  It is set
 // anew when a P exceeds 448; with normally distributed scores a unit of 2048
 // entries does that once, at its first tile.
-// cref is the first tile's largest value scale.  Sums are of 2^(t - m), so
-// log2(vs / cref) is taken as no less than -80 (values that small, or zero,
-// with nearly all of the weight: their 2^(t - m) is up to 2^80, a thread's sums
-// up to 2^100), and a scale more than 2^80 times cref becomes the new one.
+// cref is the first tile's largest value scale over 2^16; one more than 2^80
+// times cref becomes the new one.  Sums are of 2^(t - m), so log2(vs / cref) is
+// taken as no less than -96: entries with values that small (or zero) and
+// nearly all of the weight then have a 2^(t - m) of up to 2^96, and a thread's
+// 16 of them a sum up to 2^104.
 constexpr float kTopCode = 32.f, kMaxCode = 448.f;
-constexpr float kValueSpan = 0x1p80f, kLogSpan = 80.f, kMaxSum = 0x1p100f;
+constexpr float kOverFirst = 0x1p-16f, kMaxOver = 0x1p80f, kLogOver = 80.f, kMinOver = 0x1p-96f, kLogUnder = 96.f;
+constexpr float kMaxSum = 0x1p104f, kHugeTerm = 0x1p126f;
 constexpr float kMinVScale = 0x1p-120f;
 constexpr float kMinM = -3e38f;       // m stays finite, so that a score of -inf gives probability 0
 
@@ -153,9 +155,9 @@ struct AttnState {
   float nm[NG][GP];            // -m of each group (log2 units), 0 before a unit's first tile
   float ninf[GP];              // -inf: the row of -m that an entry without a token reads
   float part[NG][4][GP];       // [group][warp]: a tile's maxima over m; a unit's sums
-  float resc[NG][GP];          // a new maximum: 2^-(what m grows by)
+  float resc[NG][GP];          // a new maximum: 2^-(half of what m grows by, which may be 200)
   float fac[NG][GP];           // a unit's end: factor of the accumulator
-  float xm[NG][GP], xl[NG][GP];  // cluster: the group's maximum and sum per head
+  float xl[NG][GP];            // cluster: log2 of the group's sum per head, its maximum included
   float wvs[NG][4];            // a tile's largest value scales
   float qf[QB];                // [query buffer]: 2^-e of the query's scaling
   uint32_t spread[QB];         // whether its heads have factors
@@ -851,8 +853,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
               }
             }
             ptx::fence_proxy_async_smem();  // (before the vote, which hides some of its wait)
-            again = fabsf(w) > kTopCode * kValueSpan || !__hble2(top, __floats2half2_rn(kMaxCode, kMaxCode));
-            if (valid && !(fabsf(w) * kValueSpan >= kTopCode)) {  // a scale so small (or NaN) that P does not bound the sums
+            again = fabsf(w) > kTopCode * kMaxOver || !__hble2(top, __floats2half2_rn(kMaxCode, kMaxCode));
+            if (valid && !(fabsf(w) >= kTopCode * kMinOver)) {  // a scale so small (or NaN) that P does not bound the sums
               float sum = 0.f;
 #pragma unroll
               for (int j = 0; j < GP / 2; ++j) sum = fmaxf(sum, fmaxf(l2[j].x, l2[j].y));
@@ -872,11 +874,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
           const float last_cref = cref;
           {
             const float m = fmaxf(fmaxf(stt.wvs[g][0], stt.wvs[g][1]), fmaxf(stt.wvs[g][2], stt.wvs[g][3]));
-            if (!has_o || m > kValueSpan * cref) cref = fmaxf(m, kMinVScale);
+            if (!has_o || m > kMaxOver * cref) cref = fmaxf(m * kOverFirst, kMinVScale);
             wref = kTopCode / cref;
           }
           {
-            const float lv = fminf(fmaxf(__log2f(fabsf(vs)) - __log2f(cref), -kLogSpan), kLogSpan);
+            const float lv = fminf(fmaxf(__log2f(fabsf(vs)) - __log2f(cref), -kLogUnder), kLogOver);
             float v[GP];
 #pragma unroll
             for (int b = 0; b < GP; b += 16) {
@@ -891,7 +893,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
 #pragma unroll
               for (int j = 0; j < GP / 2; ++j) {
                 const float ex = ex2(v[2 * j]), ey = ex2(v[2 * j + 1]);
-                l2[j] = make_float2(ex < 0x1p125f ? l2[j].x - ex : 0.f, ey < 0x1p125f ? l2[j].y - ey : 0.f);
+                l2[j] = make_float2(ex < kHugeTerm ? l2[j].x - ex : 0.f, ey < kHugeTerm ? l2[j].y - ey : 0.f);
               }
             }
 #pragma unroll
@@ -904,7 +906,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
             const float d = fmaxf(fmaxf(fmaxf(stt.part[g][0][tg], stt.part[g][1][tg]),
                                         fmaxf(stt.part[g][2][tg], stt.part[g][3][tg])),
                                   has_o ? 0.f : kMinM);
-            stt.resc[g][tg] = ex2(-d);
+            stt.resc[g][tg] = ex2(-0.5f * d);
             stt.nm[g][tg] -= d;
           }
           ptx::bar_sync(bar_id, 128);
@@ -913,7 +915,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
 #pragma unroll
             for (int j = 0; j < GP / 2; ++j) {
               const float2 f = *reinterpret_cast<const float2*>(&stt.resc[g][2 * j]);
-              l2[j] = make_float2(l2[j].x * f.x, l2[j].y * f.y);
+              l2[j] = make_float2(l2[j].x * f.x * f.x, l2[j].y * f.y * f.y);
             }
             const float cf = last_cref / cref;
 #pragma unroll 1
@@ -923,7 +925,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
               ptx::tmem_wait_ld_n(v);
               const float* f = &stt.resc[g][b % GP];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * (f[j] * cf));
+              for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f[j] * f[j] * cf);
               ptx::tmem_st_32x32b_x16(o_tm + b, v);
             }
             ptx::tmem_wait_st();
@@ -951,16 +953,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       const int nh = pl.heads;
       if (tg < GP) {
         const float sum = (stt.part[g][0][tg] + stt.part[g][1][tg]) + (stt.part[g][2][tg] + stt.part[g][3][tg]);
-        const float m = has_o ? -stt.nm[g][tg] : kMinM;
+        const float log_sum = sum == 0.f ? -INFINITY : log2f(sum) - stt.nm[g][tg];
         stt.nm[g][tg] = 0.f;
         stt.fac[g][tg] = sum == 0.f ? 0.f : cref / (sum * kTopCode);
-        if constexpr (CLUSTER) {
-          stt.xm[g][tg] = m;
-          stt.xl[g][tg] = sum;
-        } else if (p.lse != nullptr && tg < nh) {
-          p.lse[pl.lse + tg] =
-              sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
-        }
+        if constexpr (CLUSTER)
+          stt.xl[g][tg] = log_sum;
+        else if (p.lse != nullptr && tg < nh)
+          p.lse[pl.lse + tg] = log_sum * 0.6931471805599453f;
       }
       if (has_o) wait_outputs();
       if constexpr (CLUSTER) {  // the outputs go where the tiles were: both groups are done with them
@@ -1018,16 +1017,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       // thread (head, r), r fastest: the factor of partial result r
       if (threadIdx.x < GP * NG) {
         const int r = static_cast<int>(threadIdx.x) % R, h = first + static_cast<int>(threadIdx.x) / R;
-        const float m_r = *cl.map_shared_rank(&stt.xm[r % NG][h], r / NG);
         const float l_r = *cl.map_shared_rank(&stt.xl[r % NG][h], r / NG);
         const uint32_t lanes = GP * NG < 32 ? (1u << (GP * NG % 32)) - 1u : kFull;
-        float m = m_r;
-        bool nan = m_r != m_r;
-        for (int d = R / 2; d > 0; d >>= 1) {
-          m = fmaxf(m, __shfl_xor_sync(lanes, m, d));
-          nan |= __shfl_xor_sync(lanes, nan, d);
-        }
-        const float f = nan ? NAN : ex2(m_r - m) * l_r;
+        float m = fmaxf(l_r, kMinM);
+        for (int d = R / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, d));
+        const float f = ex2(l_r - m);  // (NaN for a partial result that is)
         float sum = f;
         for (int d = R / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(lanes, sum, d);
         (&stt.fac[0][0])[threadIdx.x] = sum == 0.f ? 0.f : __fdividef(f, sum);

@@ -179,7 +179,7 @@ def test_all_values_zero(fp8idx):
 
 
 @pytest.mark.parametrize("where", [0, 200, 599])
-@pytest.mark.parametrize("score", [30.0, 50.0, 150.0])
+@pytest.mark.parametrize("score", [30.0, 50.0, 70.0, 150.0])
 def test_entries_without_values_bound_no_sum(fp8idx, score, where):
     """Zero values with a score so far above the others' that the
     exponentials over a reference made of the others would overflow."""
@@ -197,6 +197,35 @@ def test_first_tile_of_other_values(fp8idx, first):
     gain = np.where(np.arange(600) < 256, first, 1.0)
     for slope in (0.0, 48.0 if first > 1 else 0.0):
         spread_rows(fp8idx, rng, 1, 20, 128, 600, rng.standard_normal(600) + slope * (np.arange(600) >= 256), gain)
+
+
+@pytest.mark.parametrize("ctas", [1, 2])
+def test_partial_sums_over_far_apart_references(fp8idx, ctas):
+    """Tiles without values on one of a row's pipelines; on the other, values
+    that grow by 2^60 under falling scores: their references lie 2^130 apart,
+    their weights do not."""
+    rng = np.random.default_rng(46)
+    tile = np.arange(1024) // 128
+    score = np.where((tile == 3) | (tile == 7), -25.0, 0.0) + 0.1 * rng.standard_normal(1024)
+    gain = np.array([0.0, 1.0, 0.0, 2.0**60, 0.0, 1.0, 0.0, 2.0**60])[tile]
+    q, cache, tables = setup(rng, 1, 1, 6, 1, 128, 16, 1024, extra=0, spread=0.2)
+    q[:] = 1.0 / 128
+    aligned_keys(cache, tables, 16, 128, score, 1024)
+    sc, put = scales_of(cache, 16, 128)
+    for i in range(1024):
+        b, o = at(tables, i, 16)
+        sc[b, :, o, 1] *= np.float32(gain[i])
+    put()
+    attend(fp8idx, q, cache, np.arange(1024, dtype=np.int32)[None], tables, 16, 1.0, ctas=ctas)
+
+
+def test_a_reference_that_rises_by_more_than_a_float_holds(fp8idx):
+    """Little values of no weight, then weight without values, then values:
+    the reference rises by 2^127 at once over sums that stay in range."""
+    rng = np.random.default_rng(47)
+    tile = np.arange(768) // 128
+    score = np.array([-130.0, -130.0, 24.0, 24.0, 22.4, 22.4])[tile] + 0.1 * rng.standard_normal(768)
+    spread_rows(fp8idx, rng, 1, 6, 128, 768, score, np.array([2.0**-17, 2.0**-17, 0.0, 0.0, 1.0, 1.0])[tile])
 
 
 def test_a_scale_past_the_span_becomes_the_reference(fp8idx):
