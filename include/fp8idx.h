@@ -514,7 +514,8 @@ fp8idx_status fp8_paged_store(const fp8idx_tensor* k, const fp8idx_tensor* v,
  * while the value scales that a row selects (but for zeros) lie within 2^64 of
  * one another and its largest product is no less than 2^-110 of its largest
  * probability times its largest value scale; past that products have fewer
- * bits.
+ * bits.  Scores are below 10^7 in size (an f32 steps by 1 there; the
+ * outputs of rows with larger ones are unspecified).
  * A NaN or an infinity in q makes its head's outputs NaN; a NaN in a key, value
  * or scale, and an infinite value scale, reaches the rows that select it, no
  * others.

@@ -925,7 +925,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
               ptx::tmem_wait_ld_n(v);
               const float* f = &stt.resc[g][b % GP];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f[j] * f[j] * cf);
+              for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * (f[j] * f[j] * cf));
               ptx::tmem_st_32x32b_x16(o_tm + b, v);
             }
             ptx::tmem_wait_st();
@@ -953,13 +953,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) sparse_attn_kernel(const __gr
       const int nh = pl.heads;
       if (tg < GP) {
         const float sum = (stt.part[g][0][tg] + stt.part[g][1][tg]) + (stt.part[g][2][tg] + stt.part[g][3][tg]);
-        const float log_sum = sum == 0.f ? -INFINITY : log2f(sum) - stt.nm[g][tg];
+        const float m = has_o ? -stt.nm[g][tg] : kMinM;
         stt.nm[g][tg] = 0.f;
         stt.fac[g][tg] = sum == 0.f ? 0.f : cref / (sum * kTopCode);
         if constexpr (CLUSTER)
-          stt.xl[g][tg] = log_sum;
+          stt.xl[g][tg] = sum == 0.f ? -INFINITY : m + log2f(sum);
         else if (p.lse != nullptr && tg < nh)
-          p.lse[pl.lse + tg] = log_sum * 0.6931471805599453f;
+          p.lse[pl.lse + tg] =
+              sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
       }
       if (has_o) wait_outputs();
       if constexpr (CLUSTER) {  // the outputs go where the tiles were: both groups are done with them
