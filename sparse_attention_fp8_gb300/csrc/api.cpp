@@ -1059,7 +1059,7 @@ fp8idx_status sparse_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, 
   TRY(check_tensor(bt, "block_tables", FP8IDX_I32, 2));
   if (bt->shape[1] > 1 && bt->stride[1] != 1) return fail(FP8IDX_ERR_INVALID, "block_tables rows must be contiguous");
   if (!prefill && bt->shape[0] != B) return fail(FP8IDX_ERR_INVALID, "block_tables must be [batch, max_blocks]");
-  if (bt->shape[1] < 1 || (prefill && bt->shape[0] < 1)) return fail(FP8IDX_ERR_INVALID, "empty block table");
+  if (R > 0 && (bt->shape[1] < 1 || (prefill && bt->shape[0] < 1))) return fail(FP8IDX_ERR_INVALID, "empty block table");
   if (bt->shape[1] * bs >= (1ll << 31)) return fail(FP8IDX_ERR_UNSUPPORTED, "positions must stay below 2^31");
   if (prefill) {
     if (bt->shape[0] > kMaxBatch)

@@ -299,3 +299,15 @@ def test_binding_of_the_logits_calls_refuses_16_bit_types(monkeypatch, dtype):
         fp8idx.fp8_paged_topk(t[0], i, 1, 4, 2, i, stream=0)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     assert len(_native._descs(OnDevice(t, 1))) == 1
+
+
+def test_attention_of_no_rows(lib):
+    """No rows, and no requests that they could belong to: nothing to do."""
+    kv = _t(U8, (9, 2, 16 * 264), 0x100000)
+    for reqs, blocks in ((2, 5), (0, 5), (0, 0)):
+        assert lib.fp8_mqa_sparse_attn_paged(
+            R(_t(BF16, (0, 8, 128))), R(kv), R(_t(I32, (reqs, blocks))), R(_t(I32, (reqs + 1,))), R(_t(I32, (0, 50))), 1.0,
+            R(_t(BF16, (0, 8, 128))), R(_t(F32, (0, 8))), None, None) == fp8idx.FP8IDX_OK, lib.fp8idx_last_error()
+    for blocks in (5, 0):
+        assert lib.fp8_paged_sparse_attn(*attn_args(q=_t(BF16, (0, 3, 8, 128)), kv=kv, idx=_t(I32, (0, 50)),
+                                                    bt=_t(I32, (0, blocks)))) == fp8idx.FP8IDX_OK, lib.fp8idx_last_error()
