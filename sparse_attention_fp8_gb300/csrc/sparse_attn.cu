@@ -45,13 +45,13 @@
 // tiles of the busiest SM, is decided on the host (api.cpp).
 //
 // What bounds it: with many query heads per key head, the softmax's latency (a
-// tile of 32 heads takes a warpgroup 2600 clocks, 1150 of them arithmetic, the
+// tile of 32 heads takes a warpgroup about 2500 clocks, 1150 of them arithmetic, the
 // rest waits, the vote and fences between roles; half of the issue slots are
 // filled, the tensor cores are busy 14% of the time).  4096 prompt rows of 32
 // heads and 2048 entries: 328 us, 419 TFLOP/s; a verify step of 96 such rows
 // 22 us; 128 heads on one key head 21 us (500 to 600 GB/s through the gather).
 // 8 heads a key head over pages of one token: the scattered rows, 1.3 GB through
-// L2 in 242 us (182 us if the pages lie in order, 137 us with pages of 64
+// L2 in 244 us (182 us if the pages lie in order, 137 us with pages of 64
 // tokens).  One decode row: latency, 9.2 us, of which two dependent loads before
 // the first copy take 1.4 and the meeting of the cluster 2.
 // Every wait is bounded (common.cuh).  After a wait has run out the group
