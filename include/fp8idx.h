@@ -540,6 +540,141 @@ fp8idx_status fp8_mqa_sparse_attn_paged(const fp8idx_tensor* q,
                                         const fp8idx_options* opts,
                                         void* stream);
 
+/*
+ * The norms of the heads' queries and keys and the rotation of their
+ * positions, in one pass: fp8idx_head_norm_rope.
+ * Each row x (one head of one token, head_dim values) becomes
+ *   y = x                                              (norm 0)
+ *   y = x / sqrt(mean(x^2) + eps) * weight + bias      (norm 1)
+ *   y = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * weight + bias (2)
+ * and then, in its rotated part (rot = 2 * len(inv_freq) elements from
+ * rot_start on), each pair (a, b) with index i becomes
+ *   ((a cos - b sin) * rope_scale, (b cos + a sin) * rope_scale),
+ * cos and sin of positions[token] * inv_freq[i], to within 1e-7 at every
+ * position.  Pair i is elements (i, i + rot/2) of the rotated part, or with
+ * `interleaved` (2i, 2i + 1).  Sums are f32, rounded once at the end.  A token
+ * with a negative position is not written.
+ *
+ *  q, k          [tokens, heads, head_dim] and [tokens, kv_heads, head_dim]
+ *                BF16, F16 or F32 (the same), unit inner stride, rows 16-byte
+ *                aligned; head_dim a multiple of 8, at most 256.  k may be
+ *                NULL (then out_k is).
+ *  positions     [tokens] I32, contiguous.
+ *  inv_freq      [rot / 2] F32, contiguous, below 2^16 in size; rot a multiple
+ *                of 16 (interleaved: of 8; 0: no rotation), rot_start of 8.
+ *  q_weight, q_bias, k_weight, k_bias  [head_dim] F32, contiguous, or NULL (1
+ *                and 0); NULL with norm 0.
+ *  opts          NULL: no norm, halves, rot_start 0, eps 1e-6, rope_scale 1.
+ *  out_q, out_k  shape and type of q and k, the same rules; rows that overlap
+ *                no others.  out_q may be q itself and out_k k itself; other
+ *                overlaps with inputs or one another are refused.
+ * One kernel on `stream`.
+ */
+typedef struct {
+  int32_t norm;        /* 0 none, 1 root mean square, 2 layer norm   */
+  int32_t interleaved; /* rotated pairs: 0 (i, i + rot/2), 1 (2i, 2i + 1) */
+  int32_t rot_start;   /* first rotated element                      */
+  float eps;
+  float rope_scale;    /* factor of the rotated part                 */
+} fp8idx_norm_rope_options;
+fp8idx_status fp8idx_head_norm_rope(
+    const fp8idx_tensor* q, const fp8idx_tensor* k,
+    const fp8idx_tensor* positions, const fp8idx_tensor* inv_freq,
+    const fp8idx_tensor* q_weight, const fp8idx_tensor* q_bias,
+    const fp8idx_tensor* k_weight, const fp8idx_tensor* k_bias,
+    const fp8idx_norm_rope_options* opts, const fp8idx_tensor* out_q,
+    const fp8idx_tensor* out_k, void* stream);
+
+/*
+ * A key/value cache whose blocks share a scale: kv_cache [num_blocks,
+ * kv_heads, page] U8, where a page holds one head's block_size tokens:
+ * block_size rows of 2*D bytes (the token's key row, then its value row,
+ * e4m3), then the f32 scale of the keys and that of the values, then 8 bytes
+ * without meaning.  A key's value is code * scale.  block_size 16, 32, 64 or
+ * 128.
+ */
+
+/* Bytes of one head's page: block_size*2*head_dim + 16 (0 for a block_size or
+ * head_dim that is not implemented).  Pure host function. */
+int64_t fp8idx_kv_block_page_bytes(int32_t block_size, int32_t head_dim);
+
+/*
+ * The quantising write into such a cache: fp8_paged_block_store.
+ * Token t goes to slot s = slot_mapping[t]: token s % block_size of block
+ * s / block_size; a slot that is negative or past the cache is skipped.
+ * Consecutive rows with consecutive slots of one block are a run; a call has
+ * at most one run for a block (what fp8idx_paged_step_tables gives; with more,
+ * or a slot twice, what remains of that block is unspecified).  For each run,
+ * head and part (keys, values), with A the largest |x| of its rows and
+ * need = A / 448 (f32):
+ *   a run that starts at the block's first token sets scale = need;
+ *   else the block holds tokens before it, whose scale s is kept if it is at
+ *   least need, set to need if it is 0, and otherwise becomes s * 2^k, k the
+ *   smallest that reaches need: the codes written before become
+ *   e4m3(code * 2^-k).
+ * The run's codes are e4m3(clamp(x / scale, -448, 448)), rounded to nearest
+ * even, and 0 where the scale is 0.  NaN and infinities do not count in A and
+ * get a NaN code.  What lies past the run in its block is left as it is and
+ * has no meaning any more.
+ *
+ *  k, v          [tokens, kv_heads, head_dim], BF16, F16 or F32 (the same),
+ *                unit inner stride, rows 16-byte aligned; head_dim 64 or 128.
+ *  slot_mapping  [tokens] I32, contiguous.
+ *  kv_cache      as above (any block and head strides that are multiples of
+ *                16 bytes; pages contiguous); 16-byte aligned;
+ *                num_blocks*block_size < 2^31; shares no bytes with k, v or
+ *                slot_mapping.
+ * One kernel on `stream`.
+ */
+fp8idx_status fp8_paged_block_store(const fp8idx_tensor* k,
+                                    const fp8idx_tensor* v,
+                                    const fp8idx_tensor* slot_mapping,
+                                    const fp8idx_tensor* kv_cache,
+                                    void* stream);
+
+/*
+ * Attention over every position of such a cache, for a step's rows of any mix
+ * of prompt chunks and decode rows: fp8_paged_block_attn.
+ * Rows cu_new_lens[b] <= t < cu_new_lens[b+1] belong to request b and are the
+ * last ones of its context_lens[b] positions: row t stands at position
+ * p = context_lens[b] - cu_new_lens[b+1] + t.  With query head h, key head
+ * g = h / (heads/kv_heads), over the positions j with 0 <= j <= p, j > p -
+ * window (window 0: no such bound) and j < max_blocks*block_size whose block
+ * (block_tables[b][j / block_size]) lies in the cache:
+ *   s_j = softmax_scale * <q[t,h], K[g, j]>,
+ *   out[t,h] = sum_j exp(s_j) V[g, j] / sum_j exp(s_j),
+ *   lse[t,h] = ln sum_j exp(s_j).
+ * A row without positions gets out 0 and lse -inf; rows from
+ * cu_new_lens[batch] on are not written.
+ *
+ *  q             [rows, heads, head_dim] BF16, unit inner stride, rows 16-byte
+ *                aligned; head_dim 64 or 128; heads a multiple of kv_heads,
+ *                heads/kv_heads <= 128.
+ *  kv_cache      as for fp8_paged_block_store; scales not negative.
+ *  block_tables  [batch, max_blocks] I32, rows contiguous, batch <= 4096,
+ *                max_blocks*block_size < 2^31 - 256.
+ *  context_lens  [batch] I32; cu_new_lens [batch + 1] I32, a prefix sum, at
+ *                most `rows`: both as fp8idx_paged_step_tables makes them.
+ *  out           shape and type of q, the same rules; rows that overlap
+ *                nothing.
+ *  lse           [rows, heads] F32, contiguous, or NULL.
+ *  workspace     device scratch of at least
+ *                fp8idx_paged_block_attn_workspace(head_dim) bytes, 256-byte
+ *                aligned, owned by the caller; its contents on entry do not
+ *                matter.  Two calls in flight at once (two captured graphs,
+ *                too) need two workspaces.
+ */
+size_t fp8idx_paged_block_attn_workspace(int32_t head_dim);
+fp8idx_status fp8_paged_block_attn(const fp8idx_tensor* q,
+                                   const fp8idx_tensor* kv_cache,
+                                   const fp8idx_tensor* block_tables,
+                                   const fp8idx_tensor* context_lens,
+                                   const fp8idx_tensor* cu_new_lens,
+                                   float softmax_scale, int32_t window,
+                                   const fp8idx_tensor* out,
+                                   const fp8idx_tensor* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 /* Support gates, after the pages' is_supported(num_heads, head_dim,
  * kv_block_size) (aiter PR 5047, Technical Details) and is_supported(
  * num_heads, head_dim) (aiter PR 5046, Technical Details): 1 if the shape is

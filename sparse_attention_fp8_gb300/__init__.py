@@ -33,6 +33,14 @@ The operators around them in a serving step:
   fp8_mqa_sparse_attn_paged(q, kv_cache, block_tables, cu_seq_lens, indices,
                             softmax_scale, out, lse=None, stream=None,
                             options=None)
+  head_norm_rope(q, k, positions, inv_freq, out_q, out_k=None, norm=None,
+                 q_weight=None, q_bias=None, k_weight=None, k_bias=None,
+                 eps=1e-6, interleaved=False, rot_start=0, rope_scale=1.0,
+                 stream=None), with rope_frequencies(...) for inv_freq
+  fp8_paged_block_store(k, v, slot_mapping, kv_cache, stream=None)
+  fp8_paged_block_attn(q, kv_cache, block_tables, context_lens, cu_new_lens,
+                       softmax_scale, out, lse=None, window=0,
+                       workspace=None, stream=None)
 """
 from ._native import (  # noqa: F401
     FP8IDX_ERR_CUDA,
@@ -49,21 +57,27 @@ from ._native import (  # noqa: F401
     fp8_mqa_logits_paged,
     fp8_mqa_sparse_attn_paged,
     fp8_mqa_topk,
+    fp8_paged_block_attn,
+    fp8_paged_block_store,
     fp8_paged_mqa_logits,
     fp8_paged_mqa_topk,
     fp8_paged_sparse_attn,
     fp8_paged_store,
     fp8_paged_topk,
+    head_norm_rope,
     is_supported,
+    kv_block_page_bytes,
     kv_page_bytes,
     library,
     library_path,
+    paged_block_attn_workspace,
     paged_mqa_topk_workspace,
     paged_is_supported,
     paged_step_tables,
     plan_paged,
     plan_prefill,
     prefill_is_supported,
+    rope_frequencies,
     version,
     watchdog_selftest,
 )

@@ -17,8 +17,8 @@ OBJ_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfp8idx.so")
 SOURCES = ["api.cpp", "paged_logits.cu", "mqa_logits.cu", "topk.cu", "noalloc.cu", "step_tables.cu",
-           "paged_store.cu", "sparse_attn.cu"]
-HEADERS = ["ptx.cuh", "common.cuh", "kernels.h", "operators.h"]
+           "paged_store.cu", "sparse_attn.cu", "norm_rope.cu", "block_store.cu", "block_attn.cu"]
+HEADERS = ["ptx.cuh", "common.cuh", "kernels.h", "operators.h", "rows.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -47,6 +47,11 @@ class _Options(ctypes.Structure):
                 ("reverse_rows", ctypes.c_int32), ("block_m", ctypes.c_int32), ("clean_logits", ctypes.c_int32)]
 
 
+class _NormRopeOptions(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("rot_start", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("rope_scale", ctypes.c_float)]
+
+
 class _Plan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("grid", "threads", "smem_bytes", "stages", "tile_n", "block_m",
                                                "split_n", "reverse_rows", "tmem_cols", "gather")]
@@ -126,8 +131,17 @@ def library():
             lib.fp8_paged_store.argtypes = [T, T, T, T, V]
             lib.fp8_paged_sparse_attn.argtypes = [T, T, T, T, ctypes.c_float, T, T, P(_Options), V]
             lib.fp8_mqa_sparse_attn_paged.argtypes = [T, T, T, T, T, ctypes.c_float, T, T, P(_Options), V]
+            lib.fp8idx_kv_block_page_bytes.argtypes = [ctypes.c_int32] * 2
+            lib.fp8idx_kv_block_page_bytes.restype = ctypes.c_int64
+            lib.fp8idx_paged_block_attn_workspace.argtypes = [ctypes.c_int32]
+            lib.fp8idx_paged_block_attn_workspace.restype = ctypes.c_size_t
+            lib.fp8idx_head_norm_rope.argtypes = [T] * 8 + [P(_NormRopeOptions), T, T, V]
+            lib.fp8_paged_block_store.argtypes = [T, T, T, T, V]
+            lib.fp8_paged_block_attn.argtypes = [T, T, T, T, T, ctypes.c_float, ctypes.c_int32, T, T, V,
+                                                 ctypes.c_size_t, V]
             for f in ("fp8idx_paged_step_tables", "fp8_paged_store", "fp8_paged_sparse_attn",
-                      "fp8_mqa_sparse_attn_paged"):
+                      "fp8_mqa_sparse_attn_paged", "fp8idx_head_norm_rope", "fp8_paged_block_store",
+                      "fp8_paged_block_attn"):
                 getattr(lib, f).restype = ctypes.c_int
             for f in ("fp8_paged_mqa_logits", "fp8_paged_mqa_logits_ex", "fp8_mqa_logits", "fp8_mqa_logits_ex",
                       "fp8_mqa_logits_paged", "fp8_paged_topk", "fp8_mqa_topk", "fp8_paged_topk_ex",
@@ -418,6 +432,113 @@ def fp8_mqa_sparse_attn_paged(q, kv_cache, block_tables, cu_seq_lens, indices, s
     oc = options._c() if options is not None else None
     _check(library().fp8_mqa_sparse_attn_paged(*d[:5], float(softmax_scale), *d[5:],
                                                ctypes.byref(oc) if oc is not None else None, _stream(stream, q)))
+    return out
+
+
+_NORMS = {None: 0, "none": 0, "rms": 1, "layer": 2}
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_len=None, beta_fast=32.0,
+                     beta_slow=1.0):
+    """The angles per position, inv_freq [rot_dim / 2] (an f32 CPU tensor),
+    and the factor rope_scale that head_norm_rope takes.  scaling, for
+    contexts ``factor`` times as long as the ones trained on:
+      None      base ** (-2 i / rot_dim);
+      "linear"  positions divided by factor;
+      "ntk"     the base times factor ** (rot_dim / (rot_dim - 2)), so that the
+                lowest frequency is divided by factor and the highest kept;
+      "yarn"    frequencies with fewer than beta_slow turns in original_len
+                positions divided by factor, those with more than beta_fast
+                kept, a ramp between; rope_scale 0.1 ln(factor) + 1."""
+    import math
+
+    import torch
+    rot_dim, factor = int(rot_dim), float(factor)
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even, at least 2")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must exceed 1 and factor be at least 1")
+    scale = 1.0
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk needs a rot_dim of 4 or more")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freq = [base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+    if scaling == "linear":
+        freq = [f / factor for f in freq]
+    elif scaling == "yarn":
+        if not original_len or not beta_fast > beta_slow > 0:
+            raise ValueError("yarn needs original_len and beta_fast > beta_slow > 0")
+
+        def index_of(turns):  # the index (a real number) of the frequency with so many turns in original_len
+            return rot_dim * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo = max(math.floor(index_of(beta_fast)), 0)
+        hi = min(math.ceil(index_of(beta_slow)), rot_dim - 1)
+        for i, f in enumerate(freq):
+            slow = min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0)  # share of the divided frequency
+            freq[i] = f * (1 - slow) + f / factor * slow
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return torch.tensor(freq, dtype=torch.float64).float(), scale
+
+
+def head_norm_rope(q, k, positions, inv_freq, out_q, out_k=None, norm=None, q_weight=None, q_bias=None, k_weight=None,
+                   k_bias=None, eps=1e-6, interleaved=False, rot_start=0, rope_scale=1.0, stream=None):
+    """Norm of every head of q [tokens, heads, D] and k [tokens, kv_heads, D]
+    (or None) and rotation of its elements rot_start .. rot_start + 2 *
+    len(inv_freq) by positions * inv_freq, in one pass, into out_q and out_k
+    (which may be q and k themselves).  norm: None, "rms" or "layer", with f32
+    weights and biases [D] or None; interleaved: pairs (2i, 2i+1) instead of
+    the halves' (i, i + half).  Rows with a negative position are not written."""
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be None, 'rms' or 'layer', not {norm!r}")
+    d = _descs(q, k, positions, inv_freq, q_weight, q_bias, k_weight, k_bias, out_q, out_k)
+    oc = _NormRopeOptions(_NORMS[norm], int(bool(interleaved)), int(rot_start), float(eps), float(rope_scale))
+    _check(library().fp8idx_head_norm_rope(*d[:8], ctypes.byref(oc), *d[8:], _stream(stream, q)))
+    return out_q, out_k
+
+
+def kv_block_page_bytes(block_size, head_dim) -> int:
+    """Bytes of one head's page of a key/value cache whose blocks share a
+    scale (0 if not implemented)."""
+    return int(library().fp8idx_kv_block_page_bytes(int(block_size), int(head_dim)))
+
+
+def fp8_paged_block_store(k, v, slot_mapping, kv_cache, stream=None):
+    """Quantises k and v [tokens, kv_heads, D] to e4m3 with an f32 scale for
+    each block, head and part, and writes them at their slots (a negative slot
+    is skipped).  A block's rows are consecutive; a block that holds tokens
+    keeps its scale or doubles it as often as the new ones need."""
+    d = _descs(k, v, slot_mapping, kv_cache)
+    _check(library().fp8_paged_block_store(*d, _stream(stream, k)))
+    return kv_cache
+
+
+def paged_block_attn_workspace(head_dim) -> int:
+    """Bytes of workspace fp8_paged_block_attn needs."""
+    return int(library().fp8idx_paged_block_attn_workspace(int(head_dim)))
+
+
+def fp8_paged_block_attn(q, kv_cache, block_tables, context_lens, cu_new_lens, softmax_scale, out, lse=None, window=0,
+                         workspace=None, stream=None):
+    """Causal attention of q [rows, heads, D] over a paged key/value cache
+    whose blocks share a scale, into ``out``, and the log-sum-exp of the scores
+    into ``lse``.  Rows cu_new_lens[b] .. cu_new_lens[b+1] are the last
+    positions of request b's context_lens[b]; window: positions that a row
+    sees, its own included (0: all).  workspace: a uint8 CUDA tensor of at
+    least paged_block_attn_workspace(D) bytes (allocated here if None)."""
+    import torch
+    if workspace is None:
+        workspace = torch.empty(paged_block_attn_workspace(q.shape[-1]) + 256, dtype=torch.uint8, device=q.device)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    d = _descs(q, kv_cache, block_tables, context_lens, cu_new_lens, out, lse, workspace)
+    base = workspace.data_ptr()
+    off = (-base) % 256
+    _check(library().fp8_paged_block_attn(*d[:5], float(softmax_scale), int(window), d[5], d[6],
+                                          ctypes.c_void_p(base + off),
+                                          ctypes.c_size_t(max(workspace.numel() - off, 0)), _stream(stream, q)))
     return out
 
 

@@ -764,6 +764,7 @@ fp8idx_status topk_impl(int mode, const fp8idx_tensor* logits, const fp8idx_tens
 bool block_size_ok(int64_t bs) { return bs == 1 || bs == 16 || bs == 32 || bs == 64 || bs == 128; }
 bool row_dim_ok(int64_t d) { return d == 64 || d == 128; }
 int64_t kv_page_bytes(int64_t bs, int64_t d) { return (bs * (2 * d + 8) + 15) / 16 * 16; }
+int64_t kv_block_page_bytes(int64_t bs, int64_t d) { return bs * 2 * d + 16; }
 
 fp8idx_status check_vector(const fp8idx_tensor* t, const char* name, int64_t n) {
   TRY(check_tensor(t, name, FP8IDX_I32, 1));
@@ -924,16 +925,10 @@ fp8idx_status step_tables_impl(const fp8idx_tensor* old_lens, const fp8idx_tenso
   return ok();
 }
 
-// A key/value cache [num_blocks, kv_heads, page]: its strides, and the block
-// size that its page has for head_dim D.
-fp8idx_status check_kv_cache(const fp8idx_tensor* kv, int64_t D, int64_t* block_size) {
-  TRY(check_tensor(kv, "kv_cache", FP8IDX_U8, 3));
-  const int64_t page = kv->shape[2], bs = page / (2 * D + 8);
-  if (bs < 1 || kv_page_bytes(bs, D) != page)
-    return fail(FP8IDX_ERR_INVALID, "kv_cache: a page of %lld bytes is not fp8idx_kv_page_bytes(block_size, %lld)",
-                (long long)page, (long long)D);
-  if (!block_size_ok(bs))
-    return fail(FP8IDX_ERR_UNSUPPORTED, "kv_cache: block_size %lld not in {1, 16, 32, 64, 128}", (long long)bs);
+// A cache of keys and values [num_blocks, kv_heads, page] with pages for
+// `bs` tokens: its strides and size.
+fp8idx_status check_kv_pages(const fp8idx_tensor* kv, int64_t bs) {
+  const int64_t page = kv->shape[2];
   if (kv->shape[0] < 1 || kv->shape[1] < 1) return fail(FP8IDX_ERR_INVALID, "kv_cache: empty");
   if (kv->stride[2] != 1) return fail(FP8IDX_ERR_INVALID, "kv_cache: pages must be contiguous");
   const bool one_block = kv->shape[0] == 1, one_head = kv->shape[1] == 1;
@@ -947,8 +942,276 @@ fp8idx_status check_kv_cache(const fp8idx_tensor* kv, int64_t D, int64_t* block_
   if (kv->shape[0] * bs >= (1ll << 31))
     return fail(FP8IDX_ERR_UNSUPPORTED, "kv_cache: %lld blocks of %lld tokens (slots must stay below 2^31)",
                 (long long)kv->shape[0], (long long)bs);
+  return FP8IDX_OK;
+}
+
+// A key/value cache [num_blocks, kv_heads, page]: its strides, and the block
+// size that its page has for head_dim D.
+fp8idx_status check_kv_cache(const fp8idx_tensor* kv, int64_t D, int64_t* block_size) {
+  TRY(check_tensor(kv, "kv_cache", FP8IDX_U8, 3));
+  const int64_t page = kv->shape[2], bs = page / (2 * D + 8);
+  if (bs < 1 || kv_page_bytes(bs, D) != page)
+    return fail(FP8IDX_ERR_INVALID, "kv_cache: a page of %lld bytes is not fp8idx_kv_page_bytes(block_size, %lld)",
+                (long long)page, (long long)D);
+  if (!block_size_ok(bs))
+    return fail(FP8IDX_ERR_UNSUPPORTED, "kv_cache: block_size %lld not in {1, 16, 32, 64, 128}", (long long)bs);
+  TRY(check_kv_pages(kv, bs));
   *block_size = bs;
   return FP8IDX_OK;
+}
+
+// The same for a cache whose blocks share a scale.
+fp8idx_status check_kv_block_cache(const fp8idx_tensor* kv, int64_t D, int64_t* block_size) {
+  TRY(check_tensor(kv, "kv_cache", FP8IDX_U8, 3));
+  const int64_t page = kv->shape[2], bs = (page - 16) / (2 * D);
+  if (bs < 1 || kv_block_page_bytes(bs, D) != page)
+    return fail(FP8IDX_ERR_INVALID, "kv_cache: a page of %lld bytes is not fp8idx_kv_block_page_bytes(block_size, %lld)",
+                (long long)page, (long long)D);
+  if (bs == 1 || !block_size_ok(bs))
+    return fail(FP8IDX_ERR_UNSUPPORTED, "kv_cache: block_size %lld not in {16, 32, 64, 128}", (long long)bs);
+  TRY(check_kv_pages(kv, bs));
+  *block_size = bs;
+  return FP8IDX_OK;
+}
+
+// The type of rows of values, or a refusal.
+fp8idx_status row_type(const fp8idx_tensor* x, const char* name, int* type) {
+  if (!x) return fail(FP8IDX_ERR_INVALID, "%s: null descriptor", name);
+  *type = x->dtype == FP8IDX_BF16 ? kRowBf16 : x->dtype == FP8IDX_F16 ? kRowF16 : x->dtype == FP8IDX_F32 ? kRowF32 : -1;
+  if (*type < 0) return fail(FP8IDX_ERR_INVALID, "%s: wrong dtype %d", name, x->dtype);
+  return FP8IDX_OK;
+}
+
+// Rows [tokens, heads, D] that are read or written 16 bytes at a time: unit
+// inner stride, and the byte strides of tokens and heads.
+fp8idx_status check_rows(const fp8idx_tensor* x, const char* name, int64_t* token_stride, int64_t* head_stride) {
+  if (x->shape[2] > 1 && x->stride[2] != 1) return fail(FP8IDX_ERR_INVALID, "%s: rows must have unit inner stride", name);
+  const int64_t item = element_bytes(x->dtype);
+  *token_stride = x->shape[0] > 1 ? x->stride[0] * item : 0;
+  *head_stride = x->shape[1] > 1 ? x->stride[1] * item : 0;
+  if (!aligned16(x->data) || *token_stride % 16 != 0 || *head_stride % 16 != 0)
+    return fail(FP8IDX_ERR_INVALID, "%s: rows must be 16-byte aligned", name);
+  if (*token_stride < 0 || *head_stride < 0) return fail(FP8IDX_ERR_INVALID, "%s: negative stride", name);
+  return FP8IDX_OK;
+}
+
+// The same bytes, element for element.
+bool same_view(const fp8idx_tensor* a, const fp8idx_tensor* b) {
+  if (a->data != b->data) return false;
+  for (int i = 0; i < a->ndim; ++i)
+    if (a->shape[i] != b->shape[i] || (a->shape[i] > 1 && a->stride[i] != b->stride[i])) return false;
+  return true;
+}
+
+fp8idx_status head_norm_rope_impl(const fp8idx_tensor* q, const fp8idx_tensor* k, const fp8idx_tensor* positions,
+                                  const fp8idx_tensor* inv_freq, const fp8idx_tensor* q_weight,
+                                  const fp8idx_tensor* q_bias, const fp8idx_tensor* k_weight,
+                                  const fp8idx_tensor* k_bias, const fp8idx_norm_rope_options* opts,
+                                  const fp8idx_tensor* out_q, const fp8idx_tensor* out_k, void* stream) {
+  g_last_error.clear();
+  const fp8idx_norm_rope_options o = opts ? *opts : fp8idx_norm_rope_options{0, 0, 0, 1e-6f, 1.f};
+  int type = -1;
+  TRY(row_type(q, "q", &type));
+  TRY(check_tensor(q, "q", q->dtype, 3));
+  const int64_t T = q->shape[0], D = q->shape[2];
+  if ((k == nullptr) != (out_k == nullptr)) return fail(FP8IDX_ERR_INVALID, "k and out_k go together");
+  if (!k && (k_weight || k_bias)) return fail(FP8IDX_ERR_INVALID, "k_weight or k_bias without k");
+  NormRopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  const fp8idx_tensor *xs[2] = {q, k}, *ys[2] = {out_q, out_k};
+  const fp8idx_tensor *weights[2] = {q_weight, k_weight}, *biases[2] = {q_bias, k_bias};
+  const char *xn[2] = {"q", "k"}, *yn[2] = {"out_q", "out_k"};
+  const char *wn[2] = {"q_weight", "k_weight"}, *bn[2] = {"q_bias", "k_bias"};
+  if (o.norm != kNormNone && o.norm != kNormRms && o.norm != kNormLayer)
+    return fail(FP8IDX_ERR_INVALID, "norm: %d (0 none, 1 root mean square, 2 layer)", o.norm);
+  if (!std::isfinite(o.eps) || o.eps < 0.f) return fail(FP8IDX_ERR_INVALID, "eps must be finite and not negative");
+  if (!std::isfinite(o.rope_scale)) return fail(FP8IDX_ERR_INVALID, "rope_scale must be finite");
+  for (int i = 0; i < (k ? 2 : 1); ++i) {
+    TRY(check_tensor(xs[i], xn[i], q->dtype, 3));
+    TRY(check_tensor(ys[i], yn[i], q->dtype, 3));
+    if (xs[i]->shape[0] != T || xs[i]->shape[2] != D) return fail(FP8IDX_ERR_INVALID, "k must have the tokens and head_dim of q");
+    for (int d = 0; d < 3; ++d)
+      if (ys[i]->shape[d] != xs[i]->shape[d]) return fail(FP8IDX_ERR_INVALID, "%s must have the shape of %s", yn[i], xn[i]);
+    TRY(check_rows(xs[i], xn[i], &p.x_token[i], &p.x_head[i]));
+    TRY(check_rows(ys[i], yn[i], &p.y_token[i], &p.y_head[i]));
+    if (Extent(ys[i]).overlaps_itself()) return fail(FP8IDX_ERR_INVALID, "%s: rows overlap", yn[i]);
+    p.x[i] = xs[i]->data;
+    p.y[i] = ys[i]->data;
+    p.heads[i] = (int32_t)std::min<int64_t>(xs[i]->shape[1], 1 << 30);
+    const fp8idx_tensor* vs[2] = {weights[i], biases[i]};
+    for (int j = 0; j < 2; ++j) {
+      if (!vs[j]) continue;
+      if (o.norm == kNormNone) return fail(FP8IDX_ERR_INVALID, "%s without a norm", j ? bn[i] : wn[i]);
+      TRY(check_tensor(vs[j], j ? bn[i] : wn[i], FP8IDX_F32, 1));
+      if (vs[j]->shape[0] != D || (D > 1 && vs[j]->stride[0] != 1))
+        return fail(FP8IDX_ERR_INVALID, "%s: expected contiguous [%lld]", j ? bn[i] : wn[i], (long long)D);
+      (j ? p.bias : p.weight)[i] = static_cast<const float*>(vs[j]->data);
+    }
+  }
+  if (D < 8 || D > kNormRopeMaxDim || D % 8 != 0)
+    return fail(FP8IDX_ERR_UNSUPPORTED, "head_norm_rope: head_dim %lld (a multiple of 8, 8 to %d)", (long long)D, kNormRopeMaxDim);
+  TRY(check_vector(positions, "positions", T));
+  TRY(check_tensor(inv_freq, "inv_freq", FP8IDX_F32, 1));
+  if (inv_freq->shape[0] > 1 && inv_freq->stride[0] != 1) return fail(FP8IDX_ERR_INVALID, "inv_freq must be contiguous");
+  const int64_t rot = 2 * inv_freq->shape[0], unit = o.interleaved ? 8 : 16;
+  if (o.rot_start < 0 || o.rot_start + rot > D)
+    return fail(FP8IDX_ERR_INVALID, "the rotated part [%d, %lld) lies outside the head", o.rot_start, (long long)(o.rot_start + rot));
+  if (rot % unit != 0 || o.rot_start % 8 != 0)
+    return fail(FP8IDX_ERR_UNSUPPORTED, "head_norm_rope: %lld rotated elements from %d on (multiples of %lld and 8)",
+                (long long)rot, o.rot_start, (long long)unit);
+  const int64_t H = q->shape[1] + (k ? k->shape[1] : 0);
+  if (T >= (1ll << 31) || H >= (1ll << 31) || T * H >= (1ll << 31) - 4096)
+    return fail(FP8IDX_ERR_UNSUPPORTED, "head_norm_rope: %lld tokens of %lld heads in one call", (long long)T, (long long)H);
+  if (T == 0 || H == 0) return ok();
+  for (int i = 0; i < (k ? 2 : 1); ++i) {
+    const fp8idx_tensor* ins[] = {q, k, positions, inv_freq, q_weight, q_bias, k_weight, k_bias};
+    for (const fp8idx_tensor* in : ins)
+      if (in && !(in == xs[i] && same_view(in, ys[i])) && tensors_overlap(ys[i], in))
+        return fail(FP8IDX_ERR_INVALID, "%s overlaps an input (only its own rows may be the same tensor)", yn[i]);
+  }
+  if (k && tensors_overlap(out_q, out_k)) return fail(FP8IDX_ERR_INVALID, "out_q and out_k overlap");
+  p.positions = static_cast<const int32_t*>(positions->data);
+  p.inv_freq = static_cast<const float*>(inv_freq->data);
+  p.tokens = (int32_t)T;
+  p.dim = (int32_t)D;
+  p.rot = (int32_t)rot;
+  p.rot_start = o.rot_start;
+  p.norm = o.norm;
+  p.eps = o.eps;
+  p.inv_dim = 1.f / (float)D;
+  p.rope_scale = o.rope_scale;
+  DeviceInfo dev;
+  TRY(device_info(&dev));
+  cudaError_t e = launch_norm_rope(p, type, o.interleaved != 0, dev.sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(FP8IDX_ERR_CUDA, "head_norm_rope launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+fp8idx_status block_store_impl(const fp8idx_tensor* k, const fp8idx_tensor* v, const fp8idx_tensor* slots,
+                               const fp8idx_tensor* kv, void* stream) {
+  g_last_error.clear();
+  int type = -1;
+  TRY(row_type(k, "k", &type));
+  BlockStoreParams p;
+  std::memset(&p, 0, sizeof(p));
+  const fp8idx_tensor* xs[2] = {k, v};
+  const char* names[2] = {"k", "v"};
+  for (int i = 0; i < 2; ++i) {
+    TRY(check_tensor(xs[i], names[i], k->dtype, 3));
+    for (int d = 0; d < 3; ++d)
+      if (xs[i]->shape[d] != k->shape[d]) return fail(FP8IDX_ERR_INVALID, "v must have the shape of k");
+    TRY(check_rows(xs[i], names[i], &p.token_stride[i], &p.head_stride[i]));
+    p.x[i] = xs[i]->data;
+  }
+  const int64_t T = k->shape[0], H = k->shape[1], D = k->shape[2];
+  TRY(check_vector(slots, "slot_mapping", T));
+  if (!row_dim_ok(D)) return fail(FP8IDX_ERR_UNSUPPORTED, "block store: head_dim %lld (64 or 128)", (long long)D);
+  int64_t bs = 0;
+  TRY(check_kv_block_cache(kv, D, &bs));
+  if (kv->shape[1] != H) return fail(FP8IDX_ERR_INVALID, "kv_cache has %lld heads, k has %lld", (long long)kv->shape[1], (long long)H);
+  if (T >= (1ll << 31) || T * H >= (1ll << 30) - 4096)
+    return fail(FP8IDX_ERR_UNSUPPORTED, "block store: %lld tokens of %lld heads in one call", (long long)T, (long long)H);
+  if (T == 0) return ok();
+  if (tensors_overlap(kv, k) || tensors_overlap(kv, v) || tensors_overlap(kv, slots))
+    return fail(FP8IDX_ERR_INVALID, "block store: the cache overlaps an input");
+  p.slots = static_cast<const int32_t*>(slots->data);
+  p.cache = static_cast<uint8_t*>(kv->data);
+  p.block_stride = kv->shape[0] > 1 ? kv->stride[0] : 0;
+  p.cache_head_stride = H > 1 ? kv->stride[1] : 0;
+  p.num_slots = (int32_t)(kv->shape[0] * bs);
+  p.tokens = (int32_t)T;
+  p.heads = (int32_t)H;
+  while ((1 << p.block_shift) < bs) ++p.block_shift;
+  DeviceInfo dev;
+  TRY(device_info(&dev));
+  cudaError_t e = launch_block_store(p, type, (int)D, dev.sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(FP8IDX_ERR_CUDA, "block store launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+fp8idx_status block_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, const fp8idx_tensor* bt,
+                              const fp8idx_tensor* ctx, const fp8idx_tensor* cu, float softmax_scale, int32_t window,
+                              const fp8idx_tensor* out, const fp8idx_tensor* lse, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  TRY(check_tensor(q, "q", FP8IDX_BF16, 3));
+  TRY(check_tensor(out, "out", FP8IDX_BF16, 3));
+  const int64_t R = q->shape[0], H = q->shape[1], D = q->shape[2];
+  for (int i = 0; i < 3; ++i)
+    if (out->shape[i] != q->shape[i]) return fail(FP8IDX_ERR_INVALID, "out must have the shape of q");
+  if (!row_dim_ok(D)) return fail(FP8IDX_ERR_UNSUPPORTED, "block attention: head_dim %lld (64 or 128)", (long long)D);
+  int64_t q_token, q_head, out_token, out_head;
+  TRY(check_rows(q, "q", &q_token, &q_head));
+  TRY(check_rows(out, "out", &out_token, &out_head));
+  if (Extent(out).overlaps_itself()) return fail(FP8IDX_ERR_INVALID, "out: rows overlap");
+  if (H < 1) return fail(FP8IDX_ERR_INVALID, "q has no heads");
+  int64_t bs = 0;
+  TRY(check_kv_block_cache(kv, D, &bs));
+  const int64_t HK = kv->shape[1];
+  if (H % HK != 0) return fail(FP8IDX_ERR_INVALID, "%lld heads are no multiple of %lld kv_heads", (long long)H, (long long)HK);
+  if (H / HK > kBlockAttnMaxGroup)
+    return fail(FP8IDX_ERR_UNSUPPORTED, "block attention: %lld heads per key head (at most %d)", (long long)(H / HK), kBlockAttnMaxGroup);
+  TRY(check_tensor(bt, "block_tables", FP8IDX_I32, 2));
+  const int64_t B = bt->shape[0];
+  if (bt->shape[1] > 1 && bt->stride[1] != 1) return fail(FP8IDX_ERR_INVALID, "block_tables rows must be contiguous");
+  if (B > 1 && bt->stride[0] < 0) return fail(FP8IDX_ERR_INVALID, "block_tables: negative stride");
+  if (B > kMaxBatch) return fail(FP8IDX_ERR_UNSUPPORTED, "block attention: %lld requests > %d", (long long)B, kMaxBatch);
+  if (bt->shape[1] * bs >= (1ll << 31) - 256) return fail(FP8IDX_ERR_UNSUPPORTED, "positions must stay below 2^31 - 256");
+  TRY(check_vector(ctx, "context_lens", B));
+  TRY(check_vector(cu, "cu_new_lens", B + 1));
+  if (window < 0) return fail(FP8IDX_ERR_INVALID, "window must not be negative (0: every position up to the row's own)");
+  if (lse) {
+    TRY(check_tensor(lse, "lse", FP8IDX_F32, 2));
+    if (lse->shape[0] != R || lse->shape[1] != H || !contiguous(lse))
+      return fail(FP8IDX_ERR_INVALID, "lse must be contiguous [rows, heads]");
+  }
+  if (!std::isfinite(softmax_scale * 1.4426950408889634f)) return fail(FP8IDX_ERR_INVALID, "softmax_scale must be finite (times log2 e, too)");
+  if (R >= (1ll << 31) || R * H >= (1ll << 31) - 4096) return fail(FP8IDX_ERR_UNSUPPORTED, "block attention: rows*heads must stay below 2^31");
+  const size_t need = block_attn_workspace((int)D);
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+    return fail(FP8IDX_ERR_INVALID, "workspace must be 256-byte aligned device memory");
+  if (workspace_bytes < need)
+    return fail(FP8IDX_ERR_INVALID, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  if (R == 0 || B == 0) return ok();
+  if (bt->shape[1] < 1) return fail(FP8IDX_ERR_INVALID, "empty block table");
+  const fp8idx_tensor ws{workspace, FP8IDX_U8, 1, {(int64_t)need, 0, 0, 0}, {1, 0, 0, 0}};
+  const fp8idx_tensor* ins[] = {q, kv, bt, ctx, cu};
+  for (const fp8idx_tensor* in : ins)
+    if (tensors_overlap(out, in) || (lse && tensors_overlap(lse, in)) || tensors_overlap(&ws, in))
+      return fail(FP8IDX_ERR_INVALID, "block attention: an output or the workspace overlaps an input");
+  if ((lse && (tensors_overlap(out, lse) || tensors_overlap(&ws, lse))) || tensors_overlap(&ws, out))
+    return fail(FP8IDX_ERR_INVALID, "block attention: out, lse and workspace overlap");
+  BlockAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = q->data;
+  p.out = out->data;
+  p.lse = lse ? static_cast<float*>(lse->data) : nullptr;
+  p.kv = static_cast<const uint8_t*>(kv->data);
+  p.block_tables = static_cast<const int32_t*>(bt->data);
+  p.context_lens = static_cast<const int32_t*>(ctx->data);
+  p.cu_new = static_cast<const int32_t*>(cu->data);
+  p.block_stride = kv->shape[0] > 1 ? kv->stride[0] : 0;
+  p.head_stride = HK > 1 ? kv->stride[1] : 0;
+  p.q_row_stride = q_token / 2;
+  p.q_head_stride = q_head / 2;
+  p.out_row_stride = out_token / 2;
+  p.out_head_stride = out_head / 2;
+  p.bt_stride = B > 1 ? bt->stride[0] : 0;
+  p.rows = (int32_t)R;
+  p.heads = (int32_t)H;
+  p.kv_heads = (int32_t)HK;
+  p.group = (int32_t)(H / HK);
+  while ((1 << p.block_shift) < bs) ++p.block_shift;
+  p.max_blocks = (int32_t)bt->shape[1];
+  p.num_blocks = (int32_t)kv->shape[0];
+  p.n_req = (int32_t)B;
+  p.window = window;
+  p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
+  DeviceInfo dev;
+  TRY(device_info(&dev));
+  cudaError_t e = launch_block_attn(p, (int)D, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(FP8IDX_ERR_CUDA, "block attention launch: %s", cudaGetErrorString(e));
+  return ok();
 }
 
 fp8idx_status paged_store_impl(const fp8idx_tensor* k, const fp8idx_tensor* v, const fp8idx_tensor* slots,
@@ -1261,6 +1524,36 @@ fp8idx_status fp8idx_paged_step_tables(const fp8idx_tensor* old_lens, const fp8i
 fp8idx_status fp8_paged_store(const fp8idx_tensor* k, const fp8idx_tensor* v, const fp8idx_tensor* slot_mapping,
                               const fp8idx_tensor* kv_cache, void* stream) {
   return paged_store_impl(k, v, slot_mapping, kv_cache, stream);
+}
+
+int64_t fp8idx_kv_block_page_bytes(int32_t block_size, int32_t head_dim) {
+  return block_size > 1 && block_size_ok(block_size) && row_dim_ok(head_dim) ? kv_block_page_bytes(block_size, head_dim) : 0;
+}
+
+fp8idx_status fp8idx_head_norm_rope(const fp8idx_tensor* q, const fp8idx_tensor* k, const fp8idx_tensor* positions,
+                                    const fp8idx_tensor* inv_freq, const fp8idx_tensor* q_weight,
+                                    const fp8idx_tensor* q_bias, const fp8idx_tensor* k_weight,
+                                    const fp8idx_tensor* k_bias, const fp8idx_norm_rope_options* opts,
+                                    const fp8idx_tensor* out_q, const fp8idx_tensor* out_k, void* stream) {
+  return head_norm_rope_impl(q, k, positions, inv_freq, q_weight, q_bias, k_weight, k_bias, opts, out_q, out_k, stream);
+}
+
+fp8idx_status fp8_paged_block_store(const fp8idx_tensor* k, const fp8idx_tensor* v, const fp8idx_tensor* slot_mapping,
+                                    const fp8idx_tensor* kv_cache, void* stream) {
+  return block_store_impl(k, v, slot_mapping, kv_cache, stream);
+}
+
+size_t fp8idx_paged_block_attn_workspace(int32_t head_dim) {
+  return row_dim_ok(head_dim) ? block_attn_workspace(head_dim) : 0;
+}
+
+fp8idx_status fp8_paged_block_attn(const fp8idx_tensor* q, const fp8idx_tensor* kv_cache,
+                                   const fp8idx_tensor* block_tables, const fp8idx_tensor* context_lens,
+                                   const fp8idx_tensor* cu_new_lens, float softmax_scale, int32_t window,
+                                   const fp8idx_tensor* out, const fp8idx_tensor* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  return block_attn_impl(q, kv_cache, block_tables, context_lens, cu_new_lens, softmax_scale, window, out, lse,
+                         workspace, workspace_bytes, stream);
 }
 
 fp8idx_status fp8_paged_sparse_attn(const fp8idx_tensor* q, const fp8idx_tensor* kv_cache,

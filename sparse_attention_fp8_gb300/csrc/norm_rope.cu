@@ -1,0 +1,241 @@
+// Norms of the heads' queries and keys and the rotation of their positions in
+// one pass (fp8idx_head_norm_rope).
+//
+// A row is one head of one token.  D/8 lanes hold it, eight values each: sums
+// are butterflies among them, and the value that a rotation pairs with another
+// one is in the same lane (neighbouring pairs) or in the lane rot/16 further on
+// (halves), which takes one exchange.  A warp keeps to one token and walks its
+// heads, so the token's sines and cosines are made once, in the registers of
+// the lanes that need them, and no table of them is read.
+//
+// Angles of far positions: position * inv_freq has up to 55 bits, of which the
+// whole turns do not matter.  inv_freq / 2 pi becomes a 64-bit fraction of a
+// turn (a product of the float's significand with 1/(2 pi) in whole numbers),
+// its product with the position wraps at whole turns by itself, and the upper
+// 32 bits are the angle to 2^-32 turns, exactly reduced to an eighth of a turn
+// around zero, where the Taylor series of sine and cosine to x^9 and x^10 are
+// good to 2e-9.  (In 32-bit floats the product alone would be off by 0.004 at
+// position 100000; 64-bit floats run at a sixty-fourth of the rate here.)
+// DRAM bound: every value is read and written once.
+#include <cuda_runtime.h>
+
+#include "rows.cuh"
+
+namespace fp8idx {
+namespace {
+
+constexpr int kNormRopeThreads = 128;
+constexpr uint32_t kFull = 0xffffffffu;
+
+// f / (2 pi) turns as a fraction of 2^64, whole turns dropped.
+__device__ __forceinline__ uint64_t turn_fraction(float f) {
+  // 1 / (2 pi) * 2^66 (its first two bits are zeros), and 64 more bits
+  constexpr uint64_t kHi = 0xA2F9836E4E441529ull, kLo = 0xFC2757D1F534DDC0ull;
+  const uint32_t bits = __float_as_uint(f), field = bits >> 23 & 0xFFu;
+  const uint64_t m = (bits & 0x7FFFFFu) | (field ? 0x800000u : 0u);
+  // m * 1/(2 pi) * 2^66, below 2^88, times 2^(exponent - 2)
+  const uint64_t carry = __umul64hi(m, kLo), low = m * kHi + carry;
+  const uint64_t high = __umul64hi(m, kHi) + (low < carry ? 1u : 0u);
+  const int right = 152 - static_cast<int>(field ? field : 1u);  // 2 - (field - 150)
+  uint64_t t;
+  if (right >= 128)
+    t = 0;
+  else if (right >= 64)
+    t = high >> (right - 64);
+  else if (right > 0)
+    t = high << (64 - right) | low >> right;
+  else
+    t = right > -64 ? low << -right : 0;
+  return bits >> 31 ? 0 - t : t;
+}
+
+// cosine and sine of `position` times `turn` 2^-64 turns, times `mul`.
+__device__ __forceinline__ void rotation(int32_t position, float inv_freq, float mul, float* c, float* s) {
+  const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(position)) * turn_fraction(inv_freq);
+  const uint32_t phase = static_cast<uint32_t>((at + 0x80000000ull) >> 32);
+  const uint32_t quarter = (phase + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int32_t>(phase - (quarter << 30))) * 1.46291807926716e-9f;  // 2 pi / 2^32
+  const float x2 = x * x;
+  float sn = fmaf(x2, 2.75573192e-6f, -1.98412698e-4f);
+  sn = fmaf(x2, sn, 8.33333333e-3f);
+  sn = fmaf(x2, sn, -1.66666667e-1f);
+  sn = fmaf(x2 * x, sn, x);
+  float cs = fmaf(x2, -2.75573192e-7f, 2.48015873e-5f);
+  cs = fmaf(x2, cs, -1.38888889e-3f);
+  cs = fmaf(x2, cs, 4.16666667e-2f);
+  cs = fmaf(x2, cs, -0.5f);
+  cs = fmaf(x2, cs, 1.f);
+  const float a = quarter & 1u ? sn : cs, b = quarter & 1u ? cs : sn;
+  *c = ((quarter + 1u) & 2u ? -a : a) * mul;
+  *s = (quarter & 2u ? -b : b) * mul;
+}
+
+template <int TYPE>
+__device__ __forceinline__ void store8(uint8_t* dst, const float (&y)[8]) {
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  if constexpr (TYPE == kRowF32) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __stcs(d + i, make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]),
+                               __float_as_uint(y[4 * i + 3])));
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (TYPE == kRowBf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+      } else {
+        const __half2 v = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+    __stcs(d, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+}
+
+template <int L>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+  return v;
+}
+
+}  // namespace
+
+// L lanes a row (8, 16 or 32; those past D/8 idle); PAIRS: neighbouring pairs
+// are rotated, else halves of the rotated part.
+template <int TYPE, int L, bool PAIRS>
+__global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(const NormRopeParams p) {
+  constexpr int kRows = 32 / L, kBatch = 4;  // rows that a warp holds side by side, and of those in flight
+  constexpr int kItem = TYPE == kRowF32 ? 4 : 2;
+  const int lane = threadIdx.x & 31, sub = lane % L;
+  const uint32_t warp = blockIdx.x * (kNormRopeThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t per_token = static_cast<uint32_t>(p.chunks[0] + p.chunks[1]);
+  const uint32_t t = warp / per_token;
+  if (t >= static_cast<uint32_t>(p.tokens)) return;
+  int chunk = static_cast<int>(warp - t * per_token);
+  const int side = chunk >= p.chunks[0] ? 1 : 0;
+  chunk -= side ? p.chunks[0] : 0;
+  const int32_t position = __ldg(p.positions + t);
+  if (position < 0) return;
+  const bool live = sub < p.dim / 8;
+  const int first = chunk * p.per * kRows + lane / L, heads = p.heads[side];
+  const uint8_t* x = static_cast<const uint8_t*>(p.x[side]) + t * p.x_token[side] + sub * 8 * kItem;
+  uint8_t* y = static_cast<uint8_t*>(p.y[side]) + t * p.y_token[side] + sub * 8 * kItem;
+
+  // The rotation of this lane's values: its first value's place in the rotated part.
+  const int rel = sub * 8 - p.rot_start, half = p.rot / 2;
+  const bool turns = live && rel >= 0 && rel < p.rot;
+  constexpr int kAngles = PAIRS ? 4 : 8;
+  float cs[kAngles], sn[kAngles];
+  int partner = lane;
+  if constexpr (PAIRS) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      rotation(position, turns ? __ldg(p.inv_freq + rel / 2 + i) : 0.f, p.rope_scale, &cs[i], &sn[i]);
+  } else {
+    // a lane and its partner have the same eight angles: each makes four
+    const bool upper = turns && rel >= half;
+    if (turns) partner = lane + (upper ? -half : half) / 8;
+    float c4[4], s4[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      rotation(position, turns ? __ldg(p.inv_freq + (upper ? rel - half + 4 : rel) + i) : 0.f, p.rope_scale, &c4[i], &s4[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float c = __shfl_sync(kFull, c4[i], partner), s = __shfl_sync(kFull, s4[i], partner);
+      cs[i] = upper ? c : c4[i];
+      cs[i + 4] = upper ? c4[i] : c;
+      sn[i] = upper ? s : -s4[i];
+      sn[i + 4] = upper ? s4[i] : -s;
+    }
+  }
+  float w[8], b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w[i] = live && p.weight[side] ? __ldg(p.weight[side] + sub * 8 + i) : 1.f;
+    b[i] = live && p.bias[side] ? __ldg(p.bias[side] + sub * 8 + i) : 0.f;
+  }
+#pragma unroll 1
+  for (int at = 0; at < p.per; at += kBatch) {
+    Raw8<TYPE> raw[kBatch] = {};
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = first + (at + i) * kRows;
+      if (live && at + i < p.per && h < heads) raw[i].load(x + h * p.x_head[side]);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = first + (at + i) * kRows;
+      if (at + i >= p.per || first - lane / L + (at + i) * kRows >= heads) break;  // (the same for the whole warp)
+      float v[8];
+      raw[i].values(v);
+      if (p.norm == kNormLayer) {
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += v[j];
+        const float mean = row_sum<L>(sum) * p.inv_dim;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = live ? v[j] - mean : 0.f;
+      }
+      if (p.norm != kNormNone) {
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
+        const float r = rsqrtf(fmaf(row_sum<L>(sum), p.inv_dim, p.eps));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j] * r, w[j], b[j]);
+      }
+      float out[8];
+      if constexpr (PAIRS) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float a = v[2 * j], c = v[2 * j + 1];
+          out[2 * j] = turns ? fmaf(a, cs[j], -(c * sn[j])) : a;
+          out[2 * j + 1] = turns ? fmaf(c, cs[j], a * sn[j]) : c;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float other = __shfl_sync(kFull, v[j], partner);
+          out[j] = turns ? fmaf(v[j], cs[j], other * sn[j]) : v[j];
+        }
+      }
+      if (live && h < heads) store8<TYPE>(y + h * p.y_head[side], out);
+    }
+  }
+}
+
+namespace {
+using NormRopeKernel = void (*)(NormRopeParams);
+template <int TYPE, int L>
+NormRopeKernel norm_rope_instance(bool pairs) {
+  return pairs ? norm_rope_kernel<TYPE, L, true> : norm_rope_kernel<TYPE, L, false>;
+}
+template <int TYPE>
+NormRopeKernel norm_rope_instance(int lanes, bool pairs) {
+  return lanes == 8 ? norm_rope_instance<TYPE, 8>(pairs)
+         : lanes == 16 ? norm_rope_instance<TYPE, 16>(pairs) : norm_rope_instance<TYPE, 32>(pairs);
+}
+}  // namespace
+
+cudaError_t launch_norm_rope(NormRopeParams& p, int row_type, bool pairs, int sms, cudaStream_t stream) {
+  const int lanes = p.dim <= 64 ? 8 : p.dim <= 128 ? 16 : 32, rows = 32 / lanes;
+  const int groups[2] = {(p.heads[0] + rows - 1) / rows, (p.heads[1] + rows - 1) / rows};
+  // Heads that a warp walks: all of a token's once that leaves every SM 64 warps.
+  const int64_t all = static_cast<int64_t>(p.tokens) * (groups[0] + groups[1]);
+  const int most = groups[0] > groups[1] ? groups[0] : groups[1];
+  const int64_t per = all / (64 * sms);
+  p.per = static_cast<int32_t>(per < 1 ? 1 : per > most ? most : per);
+  for (int i = 0; i < 2; ++i) p.chunks[i] = (groups[i] + p.per - 1) / p.per;
+  const int64_t warps = static_cast<int64_t>(p.tokens) * (p.chunks[0] + p.chunks[1]);
+  const NormRopeKernel kern = row_type == kRowBf16  ? norm_rope_instance<kRowBf16>(lanes, pairs)
+                              : row_type == kRowF16 ? norm_rope_instance<kRowF16>(lanes, pairs)
+                                                    : norm_rope_instance<kRowF32>(lanes, pairs);
+  constexpr int kWarps = kNormRopeThreads / 32;
+  kern<<<static_cast<unsigned>((warps + kWarps - 1) / kWarps), kNormRopeThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace fp8idx

@@ -1,5 +1,6 @@
 // Parameter blocks and launchers of the operators around the indexer: the
-// step tables, the quantising paged store and the sparse attention.
+// step tables, the norms and rotations of the heads, the quantising paged
+// stores, the sparse and the dense attention.
 #pragma once
 
 #include <cstdint>
@@ -53,6 +54,66 @@ struct PagedStoreParams {
   int32_t div_shift;           // -1: the divisor is 1
 };
 cudaError_t launch_paged_store(const PagedStoreParams& p, int row_type, int head_dim, int sms, cudaStream_t stream);
+
+// ------------------------------------------------- head norms and rotation
+enum HeadNorm : int { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };
+constexpr int kNormRopeMaxDim = 256;
+struct NormRopeParams {
+  const void* x[2];            // queries, keys (or null)
+  void* y[2];
+  int64_t x_token[2], x_head[2], y_token[2], y_head[2];  // bytes
+  const int32_t* positions;
+  const float* inv_freq;
+  const float* weight[2];      // or null
+  const float* bias[2];        // or null
+  int32_t tokens, dim, rot, rot_start, norm;
+  int32_t heads[2];
+  float eps, inv_dim, rope_scale;
+  // set by the launcher: groups of heads side by side that a warp walks, and
+  // warps per token
+  int32_t per, chunks[2];
+};
+cudaError_t launch_norm_rope(NormRopeParams& p, int row_type, bool pairs, int sms, cudaStream_t stream);
+
+// ----------------------------------------------------- block-scaled store
+struct BlockStoreParams {
+  const void* x[2];            // keys, values
+  int64_t token_stride[2];     // bytes
+  int64_t head_stride[2];      // bytes
+  const int32_t* slots;
+  uint8_t* cache;
+  int64_t block_stride;        // bytes between blocks
+  int64_t cache_head_stride;   // bytes between heads
+  int32_t num_slots, tokens, heads, block_shift;
+  int32_t window;              // set by the launcher: rows of a CTA
+};
+cudaError_t launch_block_store(BlockStoreParams& p, int row_type, int head_dim, int sms, cudaStream_t stream);
+
+// --------------------------------------------------------- dense attention
+struct BlockAttnParams {
+  const void* q;
+  void* out;
+  float* lse;                  // [rows][heads] or null
+  const uint8_t* kv;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* cu_new;       // [n_req + 1]
+  int64_t block_stride, head_stride;                                     // bytes
+  int64_t q_row_stride, q_head_stride, out_row_stride, out_head_stride;  // elements
+  int64_t bt_stride;
+  int32_t rows, heads, kv_heads, group;  // group: query heads per key head
+  int32_t block_shift, max_blocks, num_blocks, n_req;
+  int32_t window;              // positions a row sees, its own included (0: all)
+  float scale_log2;            // softmax_scale * log2(e)
+};
+constexpr int kBlockAttnMaxGroup = 128;
+// Partial results of rows whose positions several CTAs share: at most two
+// pieces a CTA, of 256 rows with D outputs, a reference and a sum each.
+constexpr int kBlockAttnMaxCtas = 160, kBlockAttnLanes = 256;
+constexpr size_t block_attn_workspace(int head_dim) {
+  return static_cast<size_t>(kBlockAttnMaxCtas) * (2 * kBlockAttnLanes * (head_dim + 2) * 4 + 64);
+}
+cudaError_t launch_block_attn(const BlockAttnParams& p, int head_dim, cudaStream_t stream);
 
 // ------------------------------------------------------- sparse attention
 struct SparseAttnParams {

@@ -18,54 +18,14 @@
 // are spread over more warps.  16384 tokens of 8 heads, keys and values: 22.0 us,
 // 4.6 TB/s of the 102 MB that have to move (68% of a copy's rate); 4096 index
 // keys 1.9 us, 96 of them 1.5 us.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
-#include "operators.h"
+#include "rows.cuh"
 
 namespace fp8idx {
 namespace {
 
 constexpr int kStoreThreads = 128;  // (256: 23.8 us where this takes 22.0; the registers then hold fewer warps)
-
-// Eight values as they lie in memory: one or two 16-byte pieces.
-template <int TYPE>
-struct Raw8 {
-  uint4 v[TYPE == kRowF32 ? 2 : 1];
-  __device__ __forceinline__ void load(const uint8_t* src) {
-#pragma unroll
-    for (int i = 0; i < (TYPE == kRowF32 ? 2 : 1); ++i) v[i] = __ldcs(reinterpret_cast<const uint4*>(src) + i);
-  }
-  __device__ __forceinline__ void values(float (&x)[8]) const {
-    if constexpr (TYPE == kRowF32) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x[4 * i] = __uint_as_float(v[i].x), x[4 * i + 1] = __uint_as_float(v[i].y);
-        x[4 * i + 2] = __uint_as_float(v[i].z), x[4 * i + 3] = __uint_as_float(v[i].w);
-      }
-    } else {
-      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float2 f;
-        if constexpr (TYPE == kRowBf16)
-          f = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-        else
-          f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-      }
-    }
-  }
-};
-
-// a / b for r = RN(1 / b) (see above), divided where a step could underflow.
-__device__ __forceinline__ float rounded_quotient(float a, float b, float r) {
-  const float q = a * r;
-  return a > 0x1p-80f && a < 0x1p120f ? fmaf(fmaf(-q, b, a), r, q) : __fdiv_rn(a, b);
-}
 
 }  // namespace
 
@@ -116,40 +76,25 @@ __global__ void __launch_bounds__(kStoreThreads) paged_store_kernel(const PagedS
     if (page[i] == nullptr) continue;  // (after the exchange: other rows' lanes take part in it)
     const float scale = rounded_quotient(amax, 448.f, 1.f / 448.f);
     const float r = __frcp_rn(scale);
-    const bool divide = !(scale > 0x1p-90f && scale < 0x1p90f) || (__float_as_uint(scale) & 0x7FFFFFu) == 0x7FFFFFu;
+    const bool divide = has_to_divide(scale);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       float x[8], y[8];
       raw[i][half].values(x);
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {  // two at a time
-        const float2 v = make_float2(x[j], x[j + 1]), r2 = make_float2(r, r);
-        const float2 q = __fmul2_rn(v, r2);
-        const float2 e = __ffma2_rn(make_float2(-q.x, -q.y), make_float2(scale, scale), v);
-        const float2 z = __ffma2_rn(e, r2, q);
-        y[j] = copysignf(z.x, x[j]);  // (-0 / scale is -0)
-        y[j + 1] = copysignf(z.y, x[j + 1]);
-      }
+      quotients8(x, scale, r, y);
       if (divide) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)  // (amax is 0 for a row of zeros and NaN, too: the NaN stay)
           y[j] = amax != 0.f ? __fdiv_rn(x[j], scale) : x[j] == 0.f ? 0.f : x[j];
       }
-      uint32_t codes[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        // (saturating: max|x| / scale can round to just above 448)
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * k], y[4 * k + 1]), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * k + 2], y[4 * k + 3]), __NV_SATFINITE, __NV_E4M3);
-        codes[k] = lo | hi << 16;
-      }
+      const uint2 codes = e4m3_codes8(y);
       uint32_t* dst = reinterpret_cast<uint32_t*>(page[i] + off[i] * D + half * (D / 2) + sub * 8);
       // rows of the co-packed token cache (132 or 68 bytes) are only 4-byte aligned
       if (PARTS == 2 || p.block_shift > 0) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(codes[0], codes[1]);
+        *reinterpret_cast<uint2*>(dst) = codes;
       } else {
-        dst[0] = codes[0];
-        dst[1] = codes[1];
+        dst[0] = codes.x;
+        dst[1] = codes.y;
       }
     }
     if (sub == 0) reinterpret_cast<float*>(page[i] + (PARTS * D << p.block_shift))[off[i]] = scale;
