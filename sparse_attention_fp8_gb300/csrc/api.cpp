@@ -1205,11 +1205,29 @@ fp8idx_status block_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, c
   p.max_blocks = (int32_t)bt->shape[1];
   p.num_blocks = (int32_t)kv->shape[0];
   p.n_req = (int32_t)B;
+  p.half_positions = kBlockAttnLanes / 2 / p.group;
   p.window = window;
-  p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
+  p.negative = softmax_scale < 0.f;
+  p.scale_log2 = (float)(std::fabs((double)softmax_scale) * 1.4426950408889634);
+  p.partial = static_cast<float*>(workspace);
+  p.meta = reinterpret_cast<BlockAttnMeta*>(p.partial + 2ll * kBlockAttnMaxCtas * block_attn_piece_floats((int)D));
   DeviceInfo dev;
   TRY(device_info(&dev));
-  cudaError_t e = launch_block_attn(p, (int)D, static_cast<cudaStream_t>(stream));
+  if (block_attn_smem((int)D) > dev.smem_optin)
+    return fail(FP8IDX_ERR_UNSUPPORTED, "block attention: shared memory too small");
+  const int64_t page = kv->shape[2];
+  const uint64_t dims[4] = {(uint64_t)(2 * D), (uint64_t)bs, (uint64_t)HK, (uint64_t)kv->shape[0]};
+  const uint64_t strides[3] = {(uint64_t)(2 * D), (uint64_t)(HK > 1 ? kv->stride[1] : page),
+                               (uint64_t)(kv->shape[0] > 1 ? kv->stride[0] : HK * page)};
+  const uint32_t box[4] = {128u, (uint32_t)bs, 1u, 1u};
+  if (strides[1] >= 1ull << 40 || strides[2] >= 1ull << 40)
+    return fail(FP8IDX_ERR_UNSUPPORTED, "kv_cache: strides of 2^40 bytes or more");
+  CUtensorMap tm;
+  TRY(encode(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, kv->data, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, "kv_cache"));
+  // One CTA an SM, as far as the call can have steps (of 128 positions at least) for them.
+  const int64_t units = (R / (2 * p.half_positions) + B) * HK, steps = (bt->shape[1] * bs + kTileTokens - 1) / kTileTokens;
+  const int grid = (int)std::min<int64_t>(std::min(dev.sms, kBlockAttnMaxCtas), units * steps);
+  cudaError_t e = launch_block_attn(tm, p, (int)D, grid, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(FP8IDX_ERR_CUDA, "block attention launch: %s", cudaGetErrorString(e));
   return ok();
 }
@@ -1630,14 +1648,16 @@ fp8idx_status fp8idx_host_mapped_pointer(const void* host_ptr, void** device_ptr
 
 fp8idx_status fp8idx_device_status(int32_t clear) {
   g_last_error.clear();
-  unsigned int a = 0, b = 0, c = 0, d = 0;
+  unsigned int a = 0, b = 0, c = 0, d = 0, e = 0;
   if (read_paged_watchdog(&a, clear != 0) != cudaSuccess || read_prefill_watchdog(&b, clear != 0) != cudaSuccess ||
-      read_topk_watchdog(&c, clear != 0) != cudaSuccess || read_attn_watchdog(&d, clear != 0) != cudaSuccess)
+      read_topk_watchdog(&c, clear != 0) != cudaSuccess || read_attn_watchdog(&d, clear != 0) != cudaSuccess ||
+      read_block_attn_watchdog(&e, clear != 0) != cudaSuccess)
     return fail(FP8IDX_ERR_CUDA, "reading the device watchdog failed");
-  if (a | b | c | d)
+  if (a | b | c | d | e)
     return fail(FP8IDX_ERR_TIMEOUT,
-                "device wait timed out (decode sites 0x%x, prefill sites 0x%x, top-k sites 0x%x, attention sites 0x%x)",
-                a, b, c, d);
+                "device wait timed out (decode sites 0x%x, prefill sites 0x%x, top-k sites 0x%x, attention sites 0x%x, "
+                "block attention sites 0x%x)",
+                a, b, c, d, e);
   return FP8IDX_OK;
 }
 

@@ -1,72 +1,1117 @@
 // Dense attention over a paged e4m3 cache whose blocks share one scale
-// (fp8_paged_block_attn).
+// (fp8_paged_block_attn) for sm_103a.
 //
-// A warp takes one query row and head; its lanes hold the channels and walk
-// the row's positions one after the other.
+//   s[r, j] = softmax_scale * <q[r], K[j]>,  out[r] = sum_j softmax(s)[r, j] V[j]
+//
+// A unit is one key head and up to 256 query rows (positions x its query heads)
+// of one request; its positions are taken in tiles of 128.  Both products run
+// on the tensor cores with a query row per accumulator lane:
+//   S [128 rows x 128 tokens] = [Qh | Ql] * [K | K]^T     (e4m3: the cache's bytes)
+//   O [128 rows x D]         += P * V                     (f16: P from tensor memory)
+// A query is split once a unit into two e4m3 values, x 2^e = h + l, which hold
+// bf16's 8 bits; both products go into one accumulator.  P has 11 bits as f16,
+// and V's codes become f16, exactly, in shared memory: a conversion for each
+// value byte and 256 rows, where splitting P as well would cost four for each
+// score.
+//
+// A CTA (16 warps) walks its units with
+//  * two softmax warpgroups, one accumulator of scores and one of outputs each;
+//    a thread has one row, so its maximum and sum need no other thread.  More
+//    than 128 rows: each group has half of the rows and both see every tile.
+//    Up to 128: both have the same rows and take the tiles in turn; up to 64 or
+//    32, the rows stand in a tile's lanes twice or four times, and each copy
+//    takes that share of the tile's tokens: its other probabilities are zeros.
+//    The copies' results meet through shared memory at the unit's end.
+//  * a converting warpgroup: V's codes to f16, NaN codes to zeros and a mask of
+//    their tokens, so that they reach the rows that see them and no others.
+//  * a warp that loads pages by TMA and the blocks' scales, two tiles ahead of
+//    them their table entries; one that issues the products; one that walks the
+//    units.
+// The units' steps (a tile for both groups, or two tiles) are dealt out evenly:
+// every CTA takes an equal range of them, from lengths on the device.  A unit
+// that several CTAs share leaves its pieces in the workspace, and a second
+// kernel joins them.
+// The running maximum of a row goes by the products 2^t * vscale (t the score in
+// log2 units), so that P, which is multiplied with codes, keeps its bits; it is
+// raised when a P exceeds 2^8.  Sums are of unrounded f32 exponentials.
+// Every wait is bounded (common.cuh); a role whose wait has run out leaves, and
+// then so do the others.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "common.cuh"
 #include "operators.h"
 
 namespace fp8idx {
+
+static __device__ unsigned int g_block_attn_watchdog;
+
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kThreads = 512;
+constexpr int kTile = 128;
+constexpr int kConvWarp0 = 8, kLoadWarp = 12, kMmaWarp = 13, kPlanWarp = 14;
+// Registers a thread: 256 * 192 + 128 * 72 + 128 * 48 <= 512 * 128.
+constexpr int kSoftmaxRegs = 192, kConvRegs = 72, kOtherRegs = 48;
+constexpr float kMinM = -3e38f;   // m stays finite, so that a score of -inf gives probability 0
+constexpr float kRaise = 8.f;     // P may reach 2^8 before m is raised
+constexpr float kNoScaleLog = -64.f;
+constexpr int kUnitSlots = 8, kScaleSlots = 8;
+
+// A CTA's share of a unit.
+struct Piece {
+  int32_t row0;        // first row; -1: no more pieces
+  int32_t positions;   // rows / heads per key head
+  int32_t head;        // key head
+  int32_t req;
+  int32_t pos0;        // position of the first row
+  int32_t len;         // positions that exist
+  int32_t ta, tb;      // tiles
+  int32_t shared;      // both groups see every tile
+  int32_t slot;        // -1: the whole unit, else the workspace piece
+};
+
+// Scales of a tile: per 16 tokens the keys' (times the softmax's), log2 of the
+// values' over `ref` and its inverse; bits of groups of 16 tokens without
+// values (0-7), with values that are NaN (8-15), in the cache (16-23).
+struct TileScales {
+  float key[8], vlog[8], vinv[8];
+  float ref;
+  uint32_t flags;
+  uint32_t pad[6];
+};
+static_assert(sizeof(TileScales) == 128, "a scale slot");
 
 template <int D>
-__global__ void __launch_bounds__(128) block_attn_kernel(const BlockAttnParams p) {
-  constexpr int kPer = D / 32;  // channels of a lane
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int64_t row = unit / p.heads;
-  const int h = static_cast<int>(unit - row * p.heads);
-  if (row >= p.rows || row >= __ldg(p.cu_new + p.n_req)) return;
-  int a = 0, b = p.n_req;
-  while (b - a > 1) {
-    const int mid = (a + b) >> 1;
-    if (__ldg(p.cu_new + mid) <= row) a = mid; else b = mid;
-  }
-  const int32_t ctx = __ldg(p.context_lens + a);
-  const int64_t pos = static_cast<int64_t>(ctx) - __ldg(p.cu_new + a + 1) + row;
-  const int64_t hi = min(min(pos + 1, static_cast<int64_t>(ctx)), static_cast<int64_t>(p.max_blocks) << p.block_shift);
-  const int64_t lo = p.window > 0 ? max(pos - p.window + 1, static_cast<int64_t>(0)) : 0;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row * p.q_row_stride + h * p.q_head_stride;
-  float qv[kPer], o[kPer] = {};
-  for (int i = 0; i < kPer; ++i) qv[i] = __bfloat162float(q[lane * kPer + i]);
-  float m = -3e38f, l = 0.f;
-  const int bs = 1 << p.block_shift;
-  for (int64_t at = lo; at < hi; ++at) {
-    const int32_t block = __ldg(p.block_tables + a * p.bt_stride + (at >> p.block_shift));
-    if (block < 0 || block >= p.num_blocks) continue;
-    const uint8_t* page = p.kv + block * p.block_stride + h / p.group * p.head_stride;
-    const float2 scales = *reinterpret_cast<const float2*>(page + 2 * D * bs);
-    const uint8_t* kr = page + (at & (bs - 1)) * 2 * D;
-    float s = 0.f, v[kPer];
-    for (int i = 0; i < kPer; ++i) {
-      s += qv[i] * __half2float(__half(__nv_cvt_fp8_to_halfraw(kr[lane * kPer + i], __NV_E4M3)));
-      v[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(kr[D + lane * kPer + i], __NV_E4M3)));
+struct Smem {
+  static constexpr int kStages = D == 128 ? 3 : 6;       // tiles in flight
+  static constexpr uint32_t kHalf = kTile * 128u;         // a tile's keys or values (D 64: both)
+  static constexpr uint32_t q = 0;                        // [group]; group 1's is also where copies meet
+  static constexpr uint32_t qBytes = 2u * kHalf;          // of a group (the meeting takes 32 KB)
+  static constexpr uint32_t k = q + 2 * qBytes;
+  static constexpr uint32_t v = k + (D == 128 ? kStages * kHalf : 0);
+  static constexpr uint32_t v16 = v + kStages * kHalf;    // two tiles of f16 values
+  static constexpr uint32_t kV16 = kTile * D * 2u;
+  static constexpr uint32_t scales = v16 + 2 * kV16;
+  static constexpr uint32_t units = scales + kScaleSlots * sizeof(TileScales);
+  static constexpr uint32_t nan = units + kUnitSlots * 64u;   // [v16 buffer][4 words]
+  static constexpr uint32_t bars = nan + 32u;
+  // barriers
+  static constexpr uint32_t kFullB = bars, kEmptyB = kFullB + 8 * kStages;
+  static constexpr uint32_t vFullB = kEmptyB + 8 * kStages, vEmptyB = vFullB + 8 * kStages;
+  static constexpr uint32_t v16FullB = vEmptyB + 8 * kStages, v16EmptyB = v16FullB + 16;
+  static constexpr uint32_t qFullB = v16EmptyB + 16, sFullB = qFullB + 16, pFullB = sFullB + 16, oFullB = pFullB + 16;
+  static constexpr uint32_t unitFullB = oFullB + 16, unitEmptyB = unitFullB + 8 * kUnitSlots;
+  static constexpr uint32_t meetB = unitEmptyB + 8 * kUnitSlots, drainB = meetB + 8;
+  static constexpr uint32_t misc = drainB + 8;            // tensor memory's address, abort flag
+  static constexpr uint32_t total = misc + 16 + 1024;     // and the alignment
+};
+static_assert(Smem<128>::total <= kMaxSmem && Smem<64>::total <= kMaxSmem, "shared memory");
+static_assert(sizeof(Piece) <= 64, "a unit slot");
+// The plan's prefix sums lie where the f16 values and the scales will.
+static_assert((kMaxBatch + 1) * 8 <= 2 * Smem<64>::kV16 + kScaleSlots * sizeof(TileScales), "prefix sums");
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t site) {
+  bool ok = ptx::mbar_test_wait(bar, parity);
+  if (!ok) {
+    const uint64_t since = ptx::globaltimer_ns();
+#pragma unroll 1
+    while (!(ok = ptx::mbar_try_wait(bar, parity))) {
+      if (*abort_flag) break;
+      if (ptx::globaltimer_ns() - since > kWaitTimeoutNs) {
+        *abort_flag = 1u;
+        atomicOr(&g_block_attn_watchdog, site);
+        break;
+      }
     }
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-    s *= scales.x * p.scale_log2;
-    const float top = fmaxf(m, s), f = exp2f(m - top), e = exp2f(s - top);
-    l = l * f + e;
-    for (int i = 0; i < kPer; ++i) o[i] = o[i] * f + e * scales.y * v[i];
-    m = top;
   }
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.out_row_stride + h * p.out_head_stride;
-  for (int i = 0; i < kPer; ++i) out[lane * kPer + i] = __float2bfloat16(l == 0.f ? 0.f : o[i] / l);
-  if (p.lse && lane == 0) p.lse[row * p.heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  return __all_sync(kFull, ok);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ------------------------------------------------------------------- the plan
+// A request's rows and positions.  (Clamped: lengths that are no prefix sums
+// must not lead out of the tensors.)
+struct Request {
+  int32_t row0, rows;  // rows
+  int64_t pos0;        // of the first row
+  int32_t len;         // positions that exist
+  __device__ __forceinline__ Request(const BlockAttnParams& p, int b) {
+    const int32_t a = __ldg(p.cu_new + b), e = __ldg(p.cu_new + b + 1), ctx = __ldg(p.context_lens + b);
+    row0 = min(max(a, 0), p.rows);
+    rows = max(min(e, p.rows) - row0, 0);
+    pos0 = static_cast<int64_t>(ctx) - e + row0;
+    len = static_cast<int32_t>(min(static_cast<int64_t>(max(ctx, 0)), static_cast<int64_t>(p.max_blocks) << p.block_shift));
+  }
+};
+// Unit u of a request: its positions (rows / heads), tiles and steps.
+struct Unit {
+  int32_t at, positions, pos0, ta, tb, steps;
+  bool shared;
+  __device__ __forceinline__ Unit(const BlockAttnParams& p, const Request& r, int u) {
+    const int half = p.half_positions;
+    at = u * 2 * half;
+    positions = min(2 * half, r.rows - at);
+    shared = positions > half;
+    const int64_t first = r.pos0 + at, last = first + positions - 1;
+    const int32_t hi = static_cast<int32_t>(min(max(last + 1, static_cast<int64_t>(0)), static_cast<int64_t>(r.len)));
+    const int32_t lo = p.window > 0 ? static_cast<int32_t>(min(max(first - p.window + 1, static_cast<int64_t>(0)),
+                                                               static_cast<int64_t>(r.len)))
+                                    : 0;
+    ta = lo / kTile;
+    tb = max((hi + kTile - 1) / kTile, ta + 1);  // (rows that see nothing take one tile, all masked)
+    steps = shared ? tb - ta : (tb - ta + 1) / 2;
+    pos0 = static_cast<int32_t>(min(max(first, static_cast<int64_t>(-(1 << 30))), static_cast<int64_t>(0x7fffffff - 1024)));
+  }
+};
+__device__ __forceinline__ int unit_count(const BlockAttnParams& p, const Request& r) {
+  return (r.rows + 2 * p.half_positions - 1) / (2 * p.half_positions);
+}
+
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t u = __shfl_up_sync(kFull, v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+// --------------------------------------------------------------- the softmax
+// Which of the 32 columns from `col` on (of the tile at `tile0`) a row at
+// position pos sees.
+__device__ __forceinline__ uint32_t seen32(int pos, int window, int len, int tile0, int col, uint32_t in_cache) {
+  const int hi = min(pos + 1, len) - tile0 - col;
+  const int lo = window > 0 ? pos - window + 1 - tile0 - col : 0;
+  uint32_t m = hi <= 0 ? 0u : hi >= 32 ? kFull : (1u << hi) - 1u;
+  if (lo > 0) m &= lo >= 32 ? 0u : kFull << lo;
+  if (!(in_cache >> (col / 16) & 1u)) m &= 0xFFFF0000u;
+  if (!(in_cache >> (col / 16 + 1) & 1u)) m &= 0x0000FFFFu;
+  return m;
+}
+
+struct RowState {
+  float m = kMinM, l = 0.f;
+  bool bad = false;  // sees a value that is NaN
+};
+
+// A tile's scores to probabilities, 32 * NCH columns from column col0 on; the
+// rest of the probabilities are zeros.
+template <int NCH, int D>
+__device__ __forceinline__ void softmax_tile(uint32_t s_tm, uint32_t o_tm, const TileScales& sc, const uint32_t* nan_words,
+                                             int chunk0, bool masked, int pos, int window, int len, int tile0,
+                                             float row_scale, bool first, RowState& st) {
+  uint32_t r[NCH][32];
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) ptx::tmem_ld_32x32b_x32(s_tm + (chunk0 + k) * 32, r[k]);
+  float c[2 * NCH], o[2 * NCH];
+  const int g0 = 2 * chunk0;
+#pragma unroll
+  for (int i = 0; i < 2 * NCH; ++i) {
+    c[i] = sc.key[g0 + i] * row_scale;
+    o[i] = sc.vlog[g0 + i];
+  }
+  const uint32_t flags = sc.flags;
+  ptx::tmem_wait_ld_regs(r[0]);
+#pragma unroll
+  for (int k = 1; k < NCH; ++k) ptx::reg_fence(r[k]);
+  if (masked) {
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const uint32_t see = seen32(pos, window, len, tile0, (chunk0 + k) * 32, flags >> 16);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float x = fmaf(__uint_as_float(r[k][j]), c[2 * k + j / 16], o[2 * k + j / 16]);
+        r[k][j] = __float_as_uint(see >> j & 1u ? x : -INFINITY);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * NCH; ++i) c[i] = 1.f, o[i] = 0.f;
+  }
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 2 * NCH; ++i) {
+    const uint32_t* v = &r[i / 2][i % 2 * 16];
+    float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]);
+#pragma unroll
+    for (int j = 2; j < 16; j += 4) {
+      a = fmaxf(fmaxf(a, __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
+      if (j + 2 < 16) b = fmaxf(fmaxf(b, __uint_as_float(v[j + 2])), __uint_as_float(v[j + 3]));
+    }
+    top = fmaxf(top, fmaf(fmaxf(a, b), c[i], o[i]));
+  }
+  if (__any_sync(kFull, top > st.m + kRaise)) {
+    const float m = fmaxf(st.m, top), f = ex2(st.m - m);
+    st.l *= f;
+    st.m = m;
+    if (!first) {  // (the products before this tile are done: its scores were issued after them)
+#pragma unroll 1
+      for (int k = 0; k < D; k += 32) {
+        uint32_t a[32];
+        ptx::tmem_ld_32x32b_x32(o_tm + k, a);
+        ptx::tmem_wait_ld_regs(a);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
+        ptx::tmem_st_32x32b_x32(o_tm + k, a);
+      }
+    }
+  }
+  if constexpr (NCH < 4) {
+    const uint32_t zeros[16] = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < chunk0 || k >= chunk0 + NCH) ptx::tmem_st_32x32b_x16(s_tm + k * 16, zeros);
+  }
+  const float m = st.m;
+  float l = st.l;
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    uint32_t h[16];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const float2 cc = make_float2(c[2 * k + g], c[2 * k + g]);
+      const float off = o[2 * k + g] - m;
+      const float2 oo = make_float2(off, off);
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) {
+        const uint32_t* v = &r[k][g * 16 + j];
+        const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), cc, oo);
+        const float2 e = make_float2(ex2(x.x), ex2(x.y));
+        sum = __fadd2_rn(sum, e);
+        const __half2 hv = __floats2half2_rn(e.x, e.y);
+        h[g * 8 + j / 2] = *reinterpret_cast<const uint32_t*>(&hv);
+      }
+      l = fmaf(sum.x + sum.y, sc.vinv[g0 + 2 * k + g], l);
+    }
+    ptx::tmem_st_32x32b_x16(s_tm + (chunk0 + k) * 16, h);
+  }
+  st.l = l;
+  if ((nan_words[0] | nan_words[1] | nan_words[2] | nan_words[3]) != 0u) {
+#pragma unroll
+    for (int k = 0; k < NCH; ++k)
+      st.bad |= (nan_words[chunk0 + k] & seen32(pos, window, len, tile0, (chunk0 + k) * 32, flags >> 16)) != 0u;
+  }
+}
+
+// ------------------------------------------------------------------ queries
+// The 2^e that puts a row's largest finite element, with the bits `top`, into
+// [128, 256).
+__device__ __forceinline__ int query_exponent(uint32_t top) {
+  const int e = 134 - static_cast<int>(top >> 7);
+  return top == 0u ? 0 : min(max(e, -120), 120);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// Two values as e4m3 pairs h and l with x = h + l.
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t* h, uint32_t* l) {
+  const __half2 x = __floats2half2_rn(a, b);
+  const __nv_fp8x2_storage_t hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+  const __half2 back(__nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3));
+  *h = hi;
+  *l = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, back)), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Row r of a group's queries: reads it (zeros where q is null), writes both parts if
+// `write`, and returns 2^-e.  D 128: h in rows of 128 bytes, l in a second tile;
+// D 64: h and l in one row.  `sign` flips every element.
+template <int D>
+__device__ __forceinline__ float load_query(uint8_t* dst, int r, const __nv_bfloat16* q, bool write, uint32_t sign) {
+  uint4 v[D / 8];
+  uint32_t top2 = 0, odd = 0;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (q) v[i] = __ldg(reinterpret_cast<const uint4*>(q) + i);
+  }
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t m = w[k] & 0x7FFF7FFFu, special = __vcmpgeu2(m, 0x7F807F80u);  // infinities and NaN do not count
+      odd |= special;
+      top2 = __vmaxu2(top2, m & ~special);
+    }
+  }
+  const int e = query_exponent(max(top2 >> 16, top2 & 0xFFFFu));
+  if (write) {
+    const float mul = __uint_as_float(__float_as_uint(power_of_two(e)) | sign);
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t h[8], l[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4& p = v[2 * c + i / 4];
+        uint32_t w = i % 4 == 0 ? p.x : i % 4 == 1 ? p.y : i % 4 == 2 ? p.z : p.w;
+        // an infinity becomes NaN: as a code it would be the largest value
+        if (odd) w |= __vcmpeq2(w & 0x7FFF7FFFu, 0x7F807F80u) & 0x7FFF7FFFu;
+        split_pair(__uint_as_float(w << 16) * mul, __uint_as_float(w & 0xFFFF0000u) * mul, &h[i], &l[i]);
+      }
+      const int ch = c, cl = D == 64 ? c + 4 : c;
+      uint8_t* const hrow = dst + r * 128;
+      uint8_t* const lrow = hrow + (D == 64 ? 0 : kTile * 128);
+      *reinterpret_cast<uint4*>(hrow + ((ch ^ (r & 7)) << 4)) =
+          make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+      *reinterpret_cast<uint4*>(lrow + ((cl ^ (r & 7)) << 4)) =
+          make_uint4(l[0] | l[1] << 16, l[2] | l[3] << 16, l[4] | l[5] << 16, l[6] | l[7] << 16);
+    }
+  }
+  return power_of_two(-e);
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 }  // namespace
 
-cudaError_t launch_block_attn(const BlockAttnParams& p, int head_dim, cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(p.rows) * p.heads;
-  (head_dim == 128 ? block_attn_kernel<128> : block_attn_kernel<64>)
-      <<<static_cast<unsigned>((units + 3) / 4), 128, 0, stream>>>(p);
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    block_attn_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ BlockAttnParams p) {
+  using L = Smem<D>;
+  constexpr int S = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = align_up_1024(smem_raw);
+  const uint32_t base = ptx::smem_u32(smem);
+  uint32_t* const misc = reinterpret_cast<uint32_t*>(smem + L::misc);
+  volatile uint32_t* const abort_flag = misc + 1;
+  TileScales* const tile_scales = reinterpret_cast<TileScales*>(smem + L::scales);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const auto bar = [&](uint32_t at, int i = 0) { return base + at + 8u * i; };
+
+  if (threadIdx.x == 0) {
+    misc[1] = 0u;
+    for (int s = 0; s < S; ++s) {
+      ptx::mbar_init(bar(L::kFullB, s), 1u);
+      ptx::mbar_init(bar(L::kEmptyB, s), D == 128 ? 1u : 5u);  // the score MMA (and the converting warps)
+      ptx::mbar_init(bar(L::vFullB, s), 1u);
+      ptx::mbar_init(bar(L::vEmptyB, s), 4u);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar(L::v16FullB, i), 4u);
+      ptx::mbar_init(bar(L::v16EmptyB, i), 1u);
+      ptx::mbar_init(bar(L::qFullB, i), 4u);
+      ptx::mbar_init(bar(L::sFullB, i), 1u);
+      ptx::mbar_init(bar(L::pFullB, i), 4u);
+      ptx::mbar_init(bar(L::oFullB, i), 1u);
+    }
+    for (int i = 0; i < kUnitSlots; ++i) {
+      ptx::mbar_init(bar(L::unitFullB, i), 1u);
+      ptx::mbar_init(bar(L::unitEmptyB, i), 1u + 1u + 4u + 8u);
+    }
+    ptx::mbar_init(bar(L::meetB), 8u);
+    ptx::mbar_init(bar(L::drainB), 1u);
+    ptx::fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(ptx::smem_u32(misc), 512);
+    ptx::tmem_relinquish();
+  }
+  if (warp == kLoadWarp && lane == 0) ptx::prefetch_tmap(&tm_kv);
+
+  // ---- This CTA's range of steps: a key head's steps of each request, summed up.
+  int64_t* const warp_sum = reinterpret_cast<int64_t*>(smem + L::q);
+  int64_t* const cum = reinterpret_cast<int64_t*>(smem + L::v16);  // [n_req + 1], per key head
+  {
+    const int per = (p.n_req + kThreads - 1) / kThreads;
+    int64_t mine = 0;
+    for (int i = 0; i < per; ++i) {
+      const int b = threadIdx.x * per + i;
+      if (b >= p.n_req) break;
+      const Request r(p, b);
+      const int n = unit_count(p, r);
+      int64_t steps = 0;
+      if (n <= 16) {
+        for (int u = 0; u < n; ++u) steps += Unit(p, r, u).steps;
+      } else {
+        steps = -1;  // many units: a warp's work
+      }
+      cum[b + 1] = steps;
+    }
+    __syncthreads();
+    for (int b = warp; b < p.n_req; b += kThreads / 32) {
+      if (cum[b + 1] >= 0) continue;
+      const Request r(p, b);
+      const int n = unit_count(p, r);
+      int64_t steps = 0;
+      for (int u = lane; u < n; u += 32) steps += Unit(p, r, u).steps;
+      steps = __shfl_sync(kFull, warp_scan(steps, lane), 31);
+      __syncwarp();
+      if (lane == 0) cum[b + 1] = steps;
+    }
+    __syncthreads();
+    for (int i = 0; i < per; ++i) {
+      const int b = threadIdx.x * per + i;
+      if (b < p.n_req) mine += cum[b + 1];
+    }
+    const int64_t scan = warp_scan(mine, lane);
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+    int64_t before = scan - mine;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    for (int i = 0; i < per; ++i) {
+      const int b = threadIdx.x * per + i;
+      if (b >= p.n_req) break;
+      before += cum[b + 1];
+      cum[b + 1] = before;
+    }
+    if (threadIdx.x == 0) cum[0] = 0;
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = misc[0];
+
+  // The plan warp finds the start of the range before the sums are overwritten.
+  int64_t at = 0, end = 0, per_cta = 1;
+  int req = 0, head = 0, unit = 0;
+  int32_t skip = 0;  // steps of the first unit that earlier CTAs have
+  if (warp == kPlanWarp) {
+    const int64_t all = cum[p.n_req] * p.kv_heads;
+    per_cta = max((all + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(1));
+    at = min(blockIdx.x * per_cta, all);
+    end = min(at + per_cta, all);
+    if (at < end) {
+      int hi = p.n_req;
+      while (hi - req > 1) {
+        const int mid = (req + hi) >> 1;
+        if (cum[mid] * p.kv_heads <= at) req = mid; else hi = mid;
+      }
+      const int64_t steps = cum[req + 1] - cum[req], in = at - cum[req] * p.kv_heads;
+      head = static_cast<int>(in / steps);
+      int64_t rest = in - head * steps;
+      const Request r(p, req);
+      const int n = unit_count(p, r);
+      for (unit = 0; unit < n; unit += 32) {  // 32 units at a time
+        const int u = unit + lane;
+        const int64_t sum = warp_scan(u < n ? Unit(p, r, u).steps : 0, lane);
+        const uint32_t over = __ballot_sync(kFull, sum > rest);
+        if (over) {
+          const int l = __ffs(over) - 1;
+          const int64_t prev = __shfl_sync(kFull, sum, max(l - 1, 0));
+          rest -= l > 0 ? prev : 0;
+          unit += l;
+          break;
+        }
+        rest -= __shfl_sync(kFull, sum, 31);
+      }
+      skip = static_cast<int32_t>(rest);
+    }
+  }
+  __syncthreads();
+
+  const auto slot_of = [&](uint32_t n) { return reinterpret_cast<Piece*>(smem + L::units + 64u * (n % kUnitSlots)); };
+  // Reads piece n, once it is there.
+  const auto get_piece = [&](uint32_t n, Piece* out) {
+    if (!wait(bar(L::unitFullB, n % kUnitSlots), (n / kUnitSlots) & 1u, abort_flag, kSiteQEmpty)) return false;
+    *out = *slot_of(n);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar(L::unitEmptyB, n % kUnitSlots));
+    return out->row0 >= 0;
+  };
+
+  if (warp >= kLoadWarp) {
+    reg_dec<kOtherRegs>();
+    if (warp == kPlanWarp) {
+      // ============================ the plan ============================
+      BlockAttnMeta meta = {};
+      if (at < end) {
+        Request r(p, req);
+        int n_units = unit_count(p, r);
+        uint32_t n = 0;
+        bool ok = true;
+#pragma unroll 1
+        while (ok) {
+          Piece out;
+          out.row0 = -1;
+          if (at < end) {
+            const Unit u(p, r, unit);
+            const int32_t stop = static_cast<int32_t>(min(static_cast<int64_t>(u.steps), skip + (end - at)));
+            out.row0 = r.row0 + u.at;
+            out.positions = u.positions;
+            out.head = head;
+            out.req = req;
+            out.pos0 = u.pos0;
+            out.len = r.len;
+            out.shared = u.shared;
+            out.ta = u.ta + (u.shared ? skip : 2 * skip);
+            out.tb = min(u.ta + (u.shared ? stop : 2 * stop), u.tb);
+            out.slot = skip > 0 ? 0 : stop < u.steps ? 1 : -1;
+            if (out.slot == 1) {
+              meta.row0 = out.row0;
+              meta.positions = out.positions;
+              meta.head = head;
+              meta.last = static_cast<int32_t>((at + u.steps - 1) / per_cta);
+              meta.shared = out.shared;
+            }
+            at += stop - skip;
+            skip = 0;
+          }
+          ok = wait(bar(L::unitEmptyB, n % kUnitSlots), ((n / kUnitSlots) & 1u) ^ 1u, abort_flag, kSiteAccEmpty);
+          if (!ok) break;
+          if (lane == 0) {
+            *slot_of(n) = out;
+            ptx::mbar_arrive(bar(L::unitFullB, n % kUnitSlots));
+          }
+          __syncwarp();
+          ++n;
+          if (out.row0 < 0) break;
+          if (at < end && ++unit == n_units) {
+            unit = 0;
+            if (++head == p.kv_heads) {
+              head = 0;
+              do {  // (there is one: steps are left)
+                r = Request(p, ++req);
+                n_units = unit_count(p, r);
+              } while (n_units == 0 && req + 1 < p.n_req);
+            }
+          }
+        }
+      } else {
+        if (lane == 0) {
+          slot_of(0)->row0 = -1;
+          ptx::mbar_arrive(bar(L::unitFullB, 0));
+        }
+      }
+      if (lane == 0) p.meta[blockIdx.x] = meta;
+    } else if (warp == kLoadWarp) {
+      // ============================ the loads ============================
+      // Lane l < 8 has the 16 tokens l of a tile: its block's table entry two
+      // tiles ahead, its scales one.
+      struct Ahead {
+        int32_t block = -1, head = 0, first = 0, live = 0;
+      };
+      const int shift = p.block_shift;
+      Piece piece;
+      uint32_t n_piece = 0;
+      int32_t t = 0;
+      bool more = get_piece(n_piece++, &piece);
+      if (more) t = piece.ta;
+      const auto ahead = [&](Ahead* a) {  // the next tile's table entry
+        a->live = more;
+        if (!more) return;
+        a->head = piece.head;
+        a->first = t == piece.ta;
+        const int64_t j = (static_cast<int64_t>(t) * kTile + lane * 16) >> shift;
+        a->block = -1;
+        if (lane < 8 && j < p.max_blocks) a->block = __ldg(p.block_tables + piece.req * p.bt_stride + j);
+        if (++t == piece.tb) {
+          more = get_piece(n_piece++, &piece);
+          if (more) t = piece.ta;
+        }
+      };
+      const auto in_cache = [&](const Ahead& a) { return a.block >= 0 && a.block < p.num_blocks; };
+      const auto scales_of = [&](const Ahead& a) {
+        float2 s = make_float2(0.f, 0.f);
+        if (a.live && lane < 8 && in_cache(a))
+          s = __ldg(reinterpret_cast<const float2*>(p.kv + a.block * p.block_stride + a.head * p.head_stride +
+                                                    (2 * D << shift)));
+        return s;
+      };
+      Ahead a0, a1;
+      ahead(&a0);
+      float2 s0 = scales_of(a0);
+      ahead(&a1);
+      uint32_t j = 0, stage = 0, phase = 0;
+      float ref = 1.f;
+#pragma unroll 1
+      while (a0.live) {
+        const float2 s1 = scales_of(a1);
+        Ahead a2;
+        ahead(&a2);
+        if (!wait(bar(L::kEmptyB, stage), phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
+        // scales, by the lanes that have them
+        const bool here = lane < 8 && in_cache(a0);
+        const bool zero = s0.y == 0.f, bad = !(fabsf(s0.y) < INFINITY);
+        const float own = here && !zero && !bad ? s0.y : 0.f;
+        const float top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(own, 0.f))));
+        if (a0.first) ref = top > 0.f ? top : 1.f;
+        const float toplog = top > 0.f ? log2f(top / ref) : 0.f;
+        const float vlog = own > 0.f ? log2f(own / ref) : toplog + kNoScaleLog;
+        const uint32_t flags = __ballot_sync(kFull, here && zero) | __ballot_sync(kFull, here && bad) << 8 |
+                               __ballot_sync(kFull, here) << 16;
+        TileScales& sc = tile_scales[j % kScaleSlots];
+        if (lane < 8) {
+          sc.key[lane] = s0.x * p.scale_log2;
+          sc.vlog[lane] = vlog;
+          sc.vinv[lane] = ex2(-vlog);
+          if (lane == 0) {
+            sc.ref = ref;
+            sc.flags = flags;
+          }
+        }
+        __syncwarp();
+        const bool leader = lane < 8 && (lane * 16 & ((1 << shift) - 1)) == 0;
+        const int32_t block = here ? a0.block : p.num_blocks;  // (outside: zeros)
+        const uint32_t rows = lane * 16 * 128u;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar(L::kFullB, stage), L::kHalf);
+        __syncwarp();
+        if (leader)
+          ptx::tma_load_4d(base + L::k + stage * L::kHalf + rows, &tm_kv, bar(L::kFullB, stage), 0, 0, a0.head, block);
+        if constexpr (D == 128) {
+          if (!wait(bar(L::vEmptyB, stage), phase ^ 1u, abort_flag, kSiteStageEmpty)) {
+            ++j;
+            break;
+          }
+          if (lane == 0) ptx::mbar_arrive_expect_tx(bar(L::vFullB, stage), L::kHalf);
+          __syncwarp();
+          if (leader)
+            ptx::tma_load_4d(base + L::v + stage * L::kHalf + rows, &tm_kv, bar(L::vFullB, stage), D, 0, a0.head, block);
+        }
+        ++j;
+        if (++stage == S) stage = 0, phase ^= 1u;
+        a0 = a1;
+        s0 = s1;
+        a1 = a2;
+      }
+      __syncwarp();
+      if (*abort_flag && lane == 0) {  // copies in flight must land before the memory is given back
+        for (uint32_t i = j > S ? j - S : 0; i < j; ++i) {
+          wait_drain(bar(L::kFullB, i % S), (i / S) & 1u, &g_block_attn_watchdog);
+          if (D == 128) wait_drain(bar(L::vFullB, i % S), (i / S) & 1u, &g_block_attn_watchdog);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // =========================== the products ===========================
+      constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(128, kTile);
+      constexpr uint32_t kIdescO = ptx::idesc_f16_f32(128, D) | ptx::kIdescMnMajorB;
+      const uint64_t q0 = ptx::smem_desc_sw128(base + L::q), k0 = ptx::smem_desc_sw128(base + L::k);
+      const uint64_t v0 = ptx::smem_desc_mn16(base + L::v16, kTile * 128u);
+      uint32_t j0 = 0;                  // tiles before this piece
+      uint32_t np[2] = {0u, 0u};        // products of each group so far
+      uint32_t nq[2] = {0u, 0u};
+      Piece piece;
+      bool ok = true;
+#pragma unroll 1
+      for (uint32_t n = 0; ok && get_piece(n, &piece); ++n) {
+        const int tiles = piece.tb - piece.ta;
+        const bool shared = piece.shared != 0;
+        const int count[2] = {shared ? tiles : (tiles + 1) / 2, shared ? tiles : tiles / 2};
+        const auto tile_of = [&](int g, int i) { return j0 + static_cast<uint32_t>(shared ? i : 2 * i + g); };
+        const auto scores = [&](int g, int i) {
+          const uint32_t j = tile_of(g, i), st = j % S;
+          if (!wait(bar(L::kFullB, st), (j / S) & 1u, abort_flag, kSiteStageFull)) return false;
+          ptx::tc_fence_after();
+          const uint64_t a = q0 + static_cast<uint64_t>((shared ? g : 0) * (L::qBytes >> 4));
+          const uint64_t b = k0 + static_cast<uint64_t>(st * (L::kHalf >> 4));
+          if (ptx::elect_one()) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                ptx::mma_f8f6f4(tmem + g * kTile, a + part * (D == 128 ? L::kHalf >> 4 : 4u) + 2ull * kk, b + 2ull * kk,
+                                kIdescS, part + kk > 0 ? 1u : 0u);
+            ptx::mma_commit(bar(L::sFullB, g));
+            if (!shared || g == 1) ptx::mma_commit(bar(L::kEmptyB, st));
+          }
+          __syncwarp();
+          return true;
+        };
+        const auto outputs = [&](int g, int i) {
+          const uint32_t j = tile_of(g, i), buf = j & 1u;
+          if (!wait(bar(L::pFullB, g), np[g] & 1u, abort_flag, kSiteAccEmpty) ||
+              !wait(bar(L::v16FullB, buf), (j >> 1) & 1u, abort_flag, kSiteStageFull))
+            return false;
+          ++np[g];
+          ptx::tc_fence_after();
+          const uint64_t b = v0 + static_cast<uint64_t>(buf * (L::kV16 >> 4));
+          if (ptx::elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              ptx::mma_f16_ts(tmem + 2 * kTile + g * 128, tmem + g * kTile + 8 * kk, b + static_cast<uint64_t>(kk * (2048 >> 4)),
+                              kIdescO, i + kk > 0 ? 1u : 0u);
+            if (!shared || g == 1) ptx::mma_commit(bar(L::v16EmptyB, buf));
+            if (i + 1 == count[g]) ptx::mma_commit(bar(L::oFullB, g));
+          }
+          __syncwarp();
+          return true;
+        };
+        ok = wait(bar(L::qFullB, 0), nq[0] & 1u, abort_flag, kSiteQFull);
+        ++nq[0];
+        if (ok && shared) {
+          ok = wait(bar(L::qFullB, 1), nq[1] & 1u, abort_flag, kSiteQFull);
+          ++nq[1];
+        }
+        ok = ok && scores(0, 0) && (count[1] == 0 || scores(1, 0));
+#pragma unroll 1
+        for (int i = 0; ok && i < count[0]; ++i) {
+          ok = outputs(0, i) && (i + 1 >= count[0] || scores(0, i + 1));
+          if (ok && i < count[1]) ok = outputs(1, i) && (i + 1 >= count[1] || scores(1, i + 1));
+        }
+        j0 += tiles;
+      }
+      __syncwarp();
+      if (*abort_flag && lane == 0) {
+        ptx::mma_commit(bar(L::drainB));
+        wait_drain(bar(L::drainB), 0, &g_block_attn_watchdog);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kConvWarp0) {
+    // ========================= values to f16 =========================
+    reg_dec<kConvRegs>();
+    const int w = warp - kConvWarp0;  // its 32 tokens of a tile
+    // Eight lanes convert 64 codes of two tokens whose rows differ in bits 0 and
+    // 2: neither their reads nor their writes share banks.
+    const int piece_in = lane & 3, other = lane >> 2 & 1, quarter = lane >> 3;
+    uint32_t j = 0, stage = 0, phase = 0;
+    Piece piece;
+    bool ok = true;
+#pragma unroll 1
+    for (uint32_t n = 0; ok && get_piece(n, &piece); ++n) {
+#pragma unroll 1
+      for (int t = piece.ta; t < piece.tb; ++t) {
+        const uint32_t buf = j & 1u;
+        ok = wait(bar(L::v16EmptyB, buf), ((j >> 1) & 1u) ^ 1u, abort_flag, kSiteAccFull) &&
+             wait(bar(D == 128 ? L::vFullB : L::kFullB, stage), phase, abort_flag, kSiteStageFull);
+        if (!ok) break;
+        const uint32_t flags = tile_scales[j % kScaleSlots].flags;
+        const uint8_t* const src = smem + L::v + stage * L::kHalf;
+        uint8_t* const dst = smem + L::v16 + buf * L::kV16;
+        uint32_t nan_rows = 0;
+        constexpr int kPanels = D / 64, kTimes = 4 * kPanels;
+        uint4 codes[kTimes];
+        const auto row_of = [&](int i) {  // combination i * 4 + quarter: panel, rows
+          const int pair = (i * 4 + quarter) / kPanels;
+          return 32 * w + 8 * (pair >> 2) + ((pair & 3) ^ (other * 5));
+        };
+        const auto panel_of = [&](int i) { return (i * 4 + quarter) % kPanels; };
+#pragma unroll
+        for (int i = 0; i < kTimes; ++i) {
+          const int r = row_of(i), c = (D == 64 ? 4 : panel_of(i) * 4) + piece_in;
+          codes[i] = *reinterpret_cast<const uint4*>(src + r * 128 + ((c ^ (r & 7)) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < kTimes; ++i) {
+          const int r = row_of(i);
+          uint32_t x[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w}, odd = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) odd |= __vcmpeq4(x[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          if ((flags & 0xFFFFu) != 0u || odd != 0u) {
+            const uint32_t group = static_cast<uint32_t>(r) >> 4;
+            if (odd != 0u || (flags >> (8 + group) & 1u)) nan_rows |= 1u << (r & 31);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[k] &= ~__vcmpeq4(x[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+              if ((flags | flags >> 8) >> group & 1u) x[k] = 0u;
+            }
+          }
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2(
+                static_cast<__nv_fp8x2_storage_t>(x[k / 2] >> (16 * (k % 2)) & 0xFFFFu), __NV_E4M3);
+            h[k] = static_cast<uint32_t>(v.x) | static_cast<uint32_t>(v.y) << 16;
+          }
+          uint8_t* const row = dst + panel_of(i) * (kTile * 128) + r * 128;
+          *reinterpret_cast<uint4*>(row + (((2 * piece_in) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(row + (((2 * piece_in + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        nan_rows = __reduce_or_sync(kFull, nan_rows);
+        if (lane == 0) reinterpret_cast<uint32_t*>(smem + L::nan)[buf * 4 + w] = nan_rows;
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(L::v16FullB, buf));
+          ptx::mbar_arrive(bar(D == 128 ? L::vEmptyB : L::kEmptyB, stage));
+        }
+        ++j;
+        if (++stage == S) stage = 0, phase ^= 1u;
+      }
+    }
+  } else {
+    // ============================ the softmax ============================
+    reg_inc<kSoftmaxRegs>();
+    const int g = warp >> 2, quad = warp & 3;
+    const int i = threadIdx.x & 127;  // lane of the accumulators
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t s_tm = tmem + g * kTile + lane_off, o_tm = tmem + 2 * kTile + g * 128 + lane_off;
+    const uint32_t sign = p.negative ? 0x80000000u : 0u;
+    uint32_t j0 = 0, n_tiles = 0, n_outs = 0, n_meet = 0;
+    const auto meet = [&] {  // the two groups
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(L::meetB));
+      return wait(bar(L::meetB), n_meet++ & 1u, abort_flag, kSiteAccFull);
+    };
+    Piece piece;
+#pragma unroll 1
+    for (uint32_t n = 0; get_piece(n, &piece); ++n) {
+      const bool shared = piece.shared != 0;
+      const int tiles = piece.tb - piece.ta, half = p.half_positions;
+      const int rows = shared ? kTile : piece.positions * p.group;   // rows in use of a tile's lanes
+      const int copy_lanes = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;  // lanes of a copy of the rows
+      const int r = i & (copy_lanes - 1);
+      const int index = r / p.group, h = r - index * p.group;        // position (of this group's), head
+      const int position = index + (shared ? g * half : 0);
+      const bool live = index < half && position < piece.positions;
+      const int count = shared ? tiles : (tiles - g + 1) / 2;
+      const int64_t row = static_cast<int64_t>(piece.row0) + position;
+      const __nv_bfloat16* const q = static_cast<const __nv_bfloat16*>(p.q) + row * p.q_row_stride +
+                                     (piece.head * p.group + h) * p.q_head_stride;
+      const bool write = shared || g == 0;
+      const float row_scale = load_query<D>(smem + L::q + g * L::qBytes, i, live ? q : nullptr, write, sign);
+      if (write) {
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(L::qFullB, g));
+      }
+      const int pos = live ? max(piece.pos0 + position, -1) : -1;
+      const int full_to = min(piece.pos0 + 1, piece.len);            // positions below are seen by every row,
+      const int full_from = p.window > 0 ? max(piece.pos0 + piece.positions - 1, -1) - p.window + 1 : 0;  // from here on
+      const int chunk0 = quad / (copy_lanes / 32) * (copy_lanes / 32);
+      RowState st;
+      float ref = 1.f;
+#pragma unroll 1
+      for (int k = 0; k < count; ++k) {
+        const uint32_t j = j0 + static_cast<uint32_t>(shared ? k : 2 * k + g);
+        const int tile0 = (piece.ta + (shared ? k : 2 * k + g)) * kTile;
+        if (!wait(bar(L::v16FullB, j & 1u), (j >> 1) & 1u, abort_flag, kSiteStageFull) ||
+            !wait(bar(L::sFullB, g), n_tiles & 1u, abort_flag, kSiteAccFull))
+          goto out;
+        ++n_tiles;
+        ptx::tc_fence_after();
+        {
+          const TileScales& sc = tile_scales[j % kScaleSlots];
+          const uint32_t* const nan_words = reinterpret_cast<const uint32_t*>(smem + L::nan) + (j & 1u) * 4;
+          ref = sc.ref;
+          const bool masked = tile0 + kTile > full_to || tile0 < full_from || (sc.flags >> 16) != 0xFFu;
+          if (copy_lanes == 128)
+            softmax_tile<4, D>(s_tm, o_tm, sc, nan_words, 0, masked, pos, p.window, piece.len, tile0, row_scale, k == 0, st);
+          else if (copy_lanes == 64)
+            softmax_tile<2, D>(s_tm, o_tm, sc, nan_words, chunk0, masked, pos, p.window, piece.len, tile0, row_scale, k == 0, st);
+          else
+            softmax_tile<1, D>(s_tm, o_tm, sc, nan_words, chunk0, masked, pos, p.window, piece.len, tile0, row_scale, k == 0, st);
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(L::pFullB, g));
+      }
+      j0 += tiles;
+      if (count > 0) {
+        if (!wait(bar(L::oFullB, g), n_outs & 1u, abort_flag, kSiteAccFull)) goto out;
+        ++n_outs;
+        ptx::tc_fence_after();
+      }
+      {
+        // Where the results go: out, or the workspace.
+        float* const ws = p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + piece.slot) * block_attn_piece_floats(D);
+        if (shared) {
+          const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
+          const int64_t head = piece.head * p.group + h;
+          __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + row * p.out_row_stride + head * p.out_head_stride;
+          const int wrow = g * kTile + i;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t a[32];
+            ptx::tmem_ld_32x32b_x32(o_tm + c, a);
+            ptx::tmem_wait_ld_regs(a);
+            if (!live) continue;
+            if (st.bad) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) a[k] = 0x7FC00000u;
+            }
+            if (piece.slot < 0) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  w[x] = bf16_pair(__uint_as_float(a[k + 2 * x]) * inv * ref, __uint_as_float(a[k + 2 * x + 1]) * inv * ref);
+                *reinterpret_cast<uint4*>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                __stcg(reinterpret_cast<uint4*>(ws + wrow * D + c + k), make_uint4(a[k], a[k + 1], a[k + 2], a[k + 3]));
+            }
+          }
+          if (live) {
+            if (piece.slot >= 0)
+              __stcg(reinterpret_cast<float4*>(ws + kBlockAttnLanes * D) + wrow, make_float4(st.m, st.l, ref, 0.f));
+            else if (p.lse)
+              p.lse[row * p.heads + head] = st.l == 0.f ? -INFINITY : (st.m + log2f(st.l)) * 0.6931471805599453f;
+          }
+        } else {
+          // The copies of a row meet: their maxima and sums first, then 32
+          // channels at a time.
+          float* const stage = reinterpret_cast<float*>(smem + L::q + L::qBytes);
+          const int copies = 2 * kTile / copy_lanes, copy = (g * kTile + i) / copy_lanes;
+          float4* const sums = reinterpret_cast<float4*>(stage);
+          sums[g * kTile + i] = make_float4(st.m, st.l, ref, 0.f);
+          if (!meet()) goto out;
+          float m = kMinM, l = 0.f;
+#pragma unroll 1
+          for (int k = 0; k < copies; ++k) m = fmaxf(m, sums[k * copy_lanes + r].x);
+#pragma unroll 1
+          for (int k = 0; k < copies; ++k) {
+            const float4 v = sums[k * copy_lanes + r];
+            l = fmaf(v.y, ex2(v.x - m), l);
+          }
+          ref = sums[0].z;  // (group 0 has a tile of every piece)
+          const float f = ex2(st.m - m);
+          // Outputs of a row, 32 channels: copy_lanes / 8 of them a thread.
+          const int share = copy_lanes / 8, tid = threadIdx.x;
+          const int to_row = tid / (256 / copy_lanes), to_col = tid % (256 / copy_lanes) * share;
+          const int to_index = to_row / p.group, to_head = piece.head * p.group + to_row - to_index * p.group;
+          const bool to_live = to_row < rows;
+          // (the row that this thread puts out is another one than its own: its sum through the stage)
+          if (!meet()) goto out;
+          if (copy == 0) sums[r] = make_float4(m, l, ref, 0.f);
+          if (!meet()) goto out;
+          const float4 to_ml = sums[to_row];
+          const float inv = to_ml.y == 0.f ? 0.f : 1.f / to_ml.y;
+          const int64_t out_row = static_cast<int64_t>(piece.row0) + to_index;
+          __nv_bfloat16* const out =
+              static_cast<__nv_bfloat16*>(p.out) + out_row * p.out_row_stride + to_head * p.out_head_stride;
+          if (to_live && to_col == 0) {
+            if (piece.slot >= 0)
+              __stcg(reinterpret_cast<float4*>(ws + kBlockAttnLanes * D) + to_row, make_float4(to_ml.x, to_ml.y, ref, 0.f));
+            else if (p.lse)
+              p.lse[out_row * p.heads + to_head] =
+                  to_ml.y == 0.f ? -INFINITY : (to_ml.x + log2f(to_ml.y)) * 0.6931471805599453f;
+          }
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t a[32];
+            if (count > 0) {
+              ptx::tmem_ld_32x32b_x32(o_tm + c, a);
+              ptx::tmem_wait_ld_regs(a);
+            }
+            if (!meet()) goto out;  // (what stood there has been read)
+            float* const mine = stage + (g * kTile + i) * 32;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (count > 0)
+                v = make_float4(__uint_as_float(a[4 * k]) * f, __uint_as_float(a[4 * k + 1]) * f,
+                                __uint_as_float(a[4 * k + 2]) * f, __uint_as_float(a[4 * k + 3]) * f);
+              if (st.bad) v = make_float4(NAN, NAN, NAN, NAN);
+              *reinterpret_cast<float4*>(mine + ((k ^ (i & 7)) << 2)) = v;
+            }
+            if (!meet()) goto out;
+            if (to_live) {
+#pragma unroll 1
+              for (int x = to_col; x < to_col + share; x += 4) {
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                for (int k = 0; k < copies; ++k) {
+                  const float4 v = *reinterpret_cast<const float4*>(stage + (k * copy_lanes + to_row) * 32 +
+                                                                    (((x >> 2) ^ (to_row & 7)) << 2));
+                  sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                }
+                if (piece.slot >= 0)
+                  __stcg(reinterpret_cast<float4*>(ws + to_row * D + c + x), sum);
+                else
+                  *reinterpret_cast<uint2*>(out + c + x) =
+                      make_uint2(bf16_pair(sum.x * inv * ref, sum.y * inv * ref), bf16_pair(sum.z * inv * ref, sum.w * inv * ref));
+              }
+            }
+          }
+          if (!meet()) goto out;  // (group 1's queries may come where the copies met)
+        }
+        // the accumulator is read before the next piece's products overwrite it
+        ptx::tc_fence_before();
+      }
+    }
+  out:;
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of the units that several CTAs shared: a warp a row.
+template <int D>
+__global__ void __launch_bounds__(256) block_attn_join_kernel(const BlockAttnParams p) {
+  const BlockAttnMeta meta = p.meta[blockIdx.x];
+  if (meta.positions == 0) return;
+  const int lane = threadIdx.x & 31, half = p.half_positions;
+  constexpr int kPer = D / 32;
+  const int rows = meta.shared ? kBlockAttnLanes : meta.positions * p.group;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
+    const int g = meta.shared ? r / kTile : 0, index = (r - g * kTile) / p.group;
+    const int position = index + g * half, head = meta.head * p.group + (r - g * kTile) - index * p.group;
+    if ((meta.shared && index >= half) || position >= meta.positions) continue;
+    float top = kMinM, l = 0.f;
+    float4 ml = make_float4(kMinM, 0.f, 1.f, 0.f);
+    const auto piece = [&](int c) {
+      return p.partial + (static_cast<int64_t>(c) * 2 + (c == static_cast<int>(blockIdx.x) ? 1 : 0)) * block_attn_piece_floats(D);
+    };
+    for (int c = blockIdx.x; c <= meta.last; ++c)
+      top = fmaxf(top, __ldcg(reinterpret_cast<const float4*>(piece(c) + kBlockAttnLanes * D) + r).x);
+    for (int c = blockIdx.x; c <= meta.last; ++c) {
+      ml = __ldcg(reinterpret_cast<const float4*>(piece(c) + kBlockAttnLanes * D) + r);
+      l = fmaf(ml.y, ex2(ml.x - top), l);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    float o[kPer] = {};
+    for (int c = blockIdx.x; c <= meta.last; ++c) {
+      const float* ws = piece(c);
+      ml = __ldcg(reinterpret_cast<const float4*>(ws + kBlockAttnLanes * D) + r);
+      const float f = ex2(ml.x - top) * inv;
+#pragma unroll
+      for (int k = 0; k < kPer; k += 2) {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(ws + r * D + lane * kPer + k));
+        o[k] = fmaf(v.x * f, ml.z, o[k]);
+        o[k + 1] = fmaf(v.y * f, ml.z, o[k + 1]);
+      }
+    }
+    const int64_t row = static_cast<int64_t>(meta.row0) + position;
+    __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + row * p.out_row_stride + head * p.out_head_stride;
+#pragma unroll
+    for (int k = 0; k < kPer; k += 2) *reinterpret_cast<uint32_t*>(out + lane * kPer + k) = bf16_pair(o[k], o[k + 1]);
+    if (p.lse && lane == 0) p.lse[row * p.heads + head] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+namespace {
+template <int D>
+cudaError_t launch(const CUtensorMap& tm, const BlockAttnParams& p, int grid, cudaStream_t stream) {
+  const int smem = static_cast<int>(Smem<D>::total);
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(block_attn_kernel<D>), smem);
+  if (e != cudaSuccess) return e;
+  block_attn_kernel<D><<<grid, kThreads, smem, stream>>>(tm, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  block_attn_join_kernel<D><<<dim3(grid, 8), 256, 0, stream>>>(p);
   return cudaGetLastError();
+}
+}  // namespace
+
+int block_attn_smem(int head_dim) { return static_cast<int>(head_dim == 128 ? Smem<128>::total : Smem<64>::total); }
+
+cudaError_t launch_block_attn(const CUtensorMap& tm, const BlockAttnParams& p, int head_dim, int grid, cudaStream_t stream) {
+  return head_dim == 128 ? launch<128>(tm, p, grid, stream) : launch<64>(tm, p, grid, stream);
+}
+
+cudaError_t read_block_attn_watchdog(unsigned int* value, bool clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_block_attn_watchdog, sizeof(unsigned int));
+  if (e != cudaSuccess || !clear) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_block_attn_watchdog, &zero, sizeof(unsigned int));
 }
 
 }  // namespace fp8idx

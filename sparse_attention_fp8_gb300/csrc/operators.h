@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "kernels.h"
@@ -90,6 +91,14 @@ struct BlockStoreParams {
 cudaError_t launch_block_store(BlockStoreParams& p, int row_type, int head_dim, int sms, cudaStream_t stream);
 
 // --------------------------------------------------------- dense attention
+// A unit that several CTAs share, by the CTA that has its first piece.
+struct BlockAttnMeta {
+  int32_t row0, positions;     // first row; rows / heads per key head (0: no unit)
+  int32_t head;                // key head
+  int32_t last;                // CTA of the last piece
+  int32_t shared;              // rows in two tiles of 128 lanes
+  int32_t pad[3];
+};
 struct BlockAttnParams {
   const void* q;
   void* out;
@@ -98,22 +107,32 @@ struct BlockAttnParams {
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* cu_new;       // [n_req + 1]
+  float* partial;              // workspace: two pieces a CTA
+  BlockAttnMeta* meta;         // workspace: one a CTA
   int64_t block_stride, head_stride;                                     // bytes
   int64_t q_row_stride, q_head_stride, out_row_stride, out_head_stride;  // elements
   int64_t bt_stride;
   int32_t rows, heads, kv_heads, group;  // group: query heads per key head
+  int32_t half_positions;      // positions of 128 lanes: 128 / group
   int32_t block_shift, max_blocks, num_blocks, n_req;
   int32_t window;              // positions a row sees, its own included (0: all)
-  float scale_log2;            // softmax_scale * log2(e)
+  int32_t negative;            // the softmax scale's sign
+  float scale_log2;            // |softmax_scale| * log2(e)
 };
 constexpr int kBlockAttnMaxGroup = 128;
 // Partial results of rows whose positions several CTAs share: at most two
-// pieces a CTA, of 256 rows with D outputs, a reference and a sum each.
+// pieces a CTA (one that began in an earlier CTA, one that ends in a later
+// one), of 256 rows with D outputs, a reference, a sum and a scale each.
 constexpr int kBlockAttnMaxCtas = 160, kBlockAttnLanes = 256;
+__host__ __device__ constexpr int block_attn_piece_floats(int head_dim) { return kBlockAttnLanes * (head_dim + 4); }
 constexpr size_t block_attn_workspace(int head_dim) {
-  return static_cast<size_t>(kBlockAttnMaxCtas) * (2 * kBlockAttnLanes * (head_dim + 2) * 4 + 64);
+  return static_cast<size_t>(kBlockAttnMaxCtas) * (2 * 4 * block_attn_piece_floats(head_dim) + sizeof(BlockAttnMeta));
 }
-cudaError_t launch_block_attn(const BlockAttnParams& p, int head_dim, cudaStream_t stream);
+// tm: the cache as [block][head][token][2 * head_dim bytes], boxes of a block's
+// tokens by 128 bytes, 128-byte swizzle.
+cudaError_t launch_block_attn(const CUtensorMap& tm, const BlockAttnParams& p, int head_dim, int grid, cudaStream_t stream);
+int block_attn_smem(int head_dim);
+cudaError_t read_block_attn_watchdog(unsigned int* value, bool clear);
 
 // ------------------------------------------------------- sparse attention
 struct SparseAttnParams {
