@@ -54,12 +54,13 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kThreads = 512;
 constexpr int kTile = 128;
 constexpr int kConvWarp0 = 8, kLoadWarp = 12, kMmaWarp = 13, kPlanWarp = 14;
-// Registers a thread: 256 * 192 + 128 * 72 + 128 * 48 <= 512 * 128.
-constexpr int kSoftmaxRegs = 192, kConvRegs = 72, kOtherRegs = 48;
+// Registers a thread: 256 * 184 + 128 * 80 + 128 * 64 = 512 * 128.
+constexpr int kSoftmaxRegs = 184, kConvRegs = 80, kOtherRegs = 64;
 constexpr float kMinM = -3e38f;   // m stays finite, so that a score of -inf gives probability 0
 constexpr float kRaise = 8.f;     // P may reach 2^8 before m is raised
 constexpr float kNoScaleLog = -64.f;
 constexpr int kUnitSlots = 8, kScaleSlots = 8;
+constexpr int kUnitCost = 3;      // a unit's start and end, in steps
 
 // A CTA's share of a unit.
 struct Piece {
@@ -80,8 +81,8 @@ struct Piece {
 struct TileScales {
   float key[8], vlog[8], vinv[8];
   float ref;
-  uint32_t flags;
-  uint32_t pad[6];
+  uint32_t flags, pad[2];
+  uint4 nan;           // (by the converting warps) tokens with a NaN among their values
 };
 static_assert(sizeof(TileScales) == 128, "a scale slot");
 
@@ -97,12 +98,12 @@ struct Smem {
   static constexpr uint32_t kV16 = kTile * D * 2u;
   static constexpr uint32_t scales = v16 + 2 * kV16;
   static constexpr uint32_t units = scales + kScaleSlots * sizeof(TileScales);
-  static constexpr uint32_t nan = units + kUnitSlots * 64u;   // [v16 buffer][4 words]
-  static constexpr uint32_t bars = nan + 32u;
+  static constexpr uint32_t bars = units + kUnitSlots * 64u;
   // barriers
   static constexpr uint32_t kFullB = bars, kEmptyB = kFullB + 8 * kStages;
   static constexpr uint32_t vFullB = kEmptyB + 8 * kStages, vEmptyB = vFullB + 8 * kStages;
-  static constexpr uint32_t v16FullB = vEmptyB + 8 * kStages, v16EmptyB = v16FullB + 16;
+  static constexpr uint32_t scaleFullB = vEmptyB + 8 * kStages, v16FullB = scaleFullB + 8 * kScaleSlots;  // by tile % kScaleSlots
+  static constexpr uint32_t v16EmptyB = v16FullB + 8 * kScaleSlots;
   static constexpr uint32_t qFullB = v16EmptyB + 16, sFullB = qFullB + 16, pFullB = sFullB + 16, oFullB = pFullB + 16;
   static constexpr uint32_t unitFullB = oFullB + 16, unitEmptyB = unitFullB + 8 * kUnitSlots;
   static constexpr uint32_t meetB = unitEmptyB + 8 * kUnitSlots, drainB = meetB + 8;
@@ -212,50 +213,95 @@ struct RowState {
   bool bad = false;  // sees a value that is NaN
 };
 
-// A tile's scores to probabilities, 32 * NCH columns from column col0 on; the
-// rest of the probabilities are zeros.
-template <int NCH, int D>
-__device__ __forceinline__ void softmax_tile(uint32_t s_tm, uint32_t o_tm, const TileScales& sc, const uint32_t* nan_words,
-                                             int chunk0, bool masked, int pos, int window, int len, int tile0,
-                                             float row_scale, bool first, RowState& st) {
-  uint32_t r[NCH][32];
-#pragma unroll
-  for (int k = 0; k < NCH; ++k) ptx::tmem_ld_32x32b_x32(s_tm + (chunk0 + k) * 32, r[k]);
-  float c[2 * NCH], o[2 * NCH];
-  const int g0 = 2 * chunk0;
-#pragma unroll
-  for (int i = 0; i < 2 * NCH; ++i) {
-    c[i] = sc.key[g0 + i] * row_scale;
-    o[i] = sc.vlog[g0 + i];
-  }
-  const uint32_t flags = sc.flags;
-  ptx::tmem_wait_ld_regs(r[0]);
-#pragma unroll
-  for (int k = 1; k < NCH; ++k) ptx::reg_fence(r[k]);
-  if (masked) {
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      const uint32_t see = seen32(pos, window, len, tile0, (chunk0 + k) * 32, flags >> 16);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float x = fmaf(__uint_as_float(r[k][j]), c[2 * k + j / 16], o[2 * k + j / 16]);
-        r[k][j] = __float_as_uint(see >> j & 1u ? x : -INFINITY);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 2 * NCH; ++i) c[i] = 1.f, o[i] = 0.f;
-  }
+// The largest of 32 columns (two groups of 16) of scores times c[] plus o[].
+__device__ __forceinline__ float chunk_max(const uint32_t (&r)[32], const float (&c)[2], const float (&o)[2]) {
   float top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 2 * NCH; ++i) {
-    const uint32_t* v = &r[i / 2][i % 2 * 16];
+  for (int g = 0; g < 2; ++g) {
+    const uint32_t* v = &r[16 * g];
     float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]);
 #pragma unroll
     for (int j = 2; j < 16; j += 4) {
       a = fmaxf(fmaxf(a, __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
       if (j + 2 < 16) b = fmaxf(fmaxf(b, __uint_as_float(v[j + 2])), __uint_as_float(v[j + 3]));
     }
-    top = fmaxf(top, fmaf(fmaxf(a, b), c[i], o[i]));
+    top = fmaxf(top, fmaf(fmaxf(a, b), c[g], o[g]));
+  }
+  return top;
+}
+// Probabilities of 32 columns into tensor memory; adds their sum to l.
+__device__ __forceinline__ void chunk_exp(const uint32_t (&r)[32], const float (&c)[2], const float (&o)[2], const float* vinv,
+                                          float m, uint32_t p_tm, float& l) {
+  uint32_t h[16];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const float off = o[g] - m;
+    const float2 cc = make_float2(c[g], c[g]), oo = make_float2(off, off);
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[16 * g + j]), __uint_as_float(r[16 * g + j + 1])), cc, oo);
+      const float2 e = make_float2(ex2(x.x), ex2(x.y));
+      sum = __fadd2_rn(sum, e);
+      const __half2 hv = __floats2half2_rn(e.x, e.y);
+      h[g * 8 + j / 2] = *reinterpret_cast<const uint32_t*>(&hv);
+    }
+    l = fmaf(sum.x + sum.y, vinv[g], l);
+  }
+  ptx::tmem_st_32x32b_x16(p_tm, h);
+}
+
+// A tile's scores to probabilities, `chunks` (1, 2 or 4) times 32 columns from
+// chunk0 on; the rest of the probabilities are zeros.  Probabilities lie over
+// the scores (16 columns for 32), written in order, so those of a chunk
+// overwrite scores that have been read.  The loops are rolled, and the scores
+// loaded twice: unrolled they wait for their instructions (the roles' loops
+// together do not fit the instruction cache then: 924 us where this takes 861).
+template <int D>
+__device__ __forceinline__ void softmax_tile(uint32_t s_tm, uint32_t o_tm, const TileScales& sc, int chunk0, int chunks,
+                                             bool masked, int pos, int window, int len, int tile0, float row_scale, bool first,
+                                             RowState& st) {
+  uint32_t r0[32], r1[32];
+  const auto scales = [&](int k, float (&c)[2], float (&o)[2]) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      c[g] = masked ? 1.f : sc.key[2 * k + g] * row_scale;
+      o[g] = masked ? 0.f : sc.vlog[2 * k + g];
+    }
+  };
+  const int end = chunk0 + chunks;
+  if (masked) {  // log2 probabilities, -inf where the row sees nothing, in the scores' place
+#pragma unroll 1
+    for (int k = chunk0; k < end; ++k) {
+      ptx::tmem_ld_32x32b_x32(s_tm + k * 32, r0);
+      const uint32_t see = seen32(pos, window, len, tile0, k * 32, sc.flags >> 16);
+      ptx::tmem_wait_ld_regs(r0);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float x = fmaf(__uint_as_float(r0[j]), sc.key[2 * k + j / 16] * row_scale, sc.vlog[2 * k + j / 16]);
+        r0[j] = __float_as_uint(see >> j & 1u ? x : -INFINITY);
+      }
+      ptx::tmem_st_32x32b_x32(s_tm + k * 32, r0);
+    }
+    ptx::tmem_wait_st();
+  }
+  float top = -INFINITY, c[2], o[2];
+  const auto top_of = [&](const uint32_t (&r)[32], int k) {
+    scales(k, c, o);
+    top = fmaxf(top, chunk_max(r, c, o));
+  };
+  const auto exp_of = [&](const uint32_t (&r)[32], int k) {
+    scales(k, c, o);
+    chunk_exp(r, c, o, sc.vinv + 2 * k, st.m, s_tm + k * 16, st.l);
+  };
+#pragma unroll 1
+  for (int k = chunk0; k < end; k += 2) {
+    ptx::tmem_ld_32x32b_x32(s_tm + k * 32, r0);
+    if (k + 1 < end) ptx::tmem_ld_32x32b_x32(s_tm + (k + 1) * 32, r1);
+    ptx::tmem_wait_ld_regs(r0);
+    ptx::reg_fence(r1);
+    top_of(r0, k);
+    if (k + 1 < end) top_of(r1, k + 1);
   }
   if (__any_sync(kFull, top > st.m + kRaise)) {
     const float m = fmaxf(st.m, top), f = ex2(st.m - m);
@@ -264,50 +310,28 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_tm, uint32_t o_tm, const
     if (!first) {  // (the products before this tile are done: its scores were issued after them)
 #pragma unroll 1
       for (int k = 0; k < D; k += 32) {
-        uint32_t a[32];
-        ptx::tmem_ld_32x32b_x32(o_tm + k, a);
-        ptx::tmem_wait_ld_regs(a);
+        ptx::tmem_ld_32x32b_x32(o_tm + k, r0);
+        ptx::tmem_wait_ld_regs(r0);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) * f);
-        ptx::tmem_st_32x32b_x32(o_tm + k, a);
+        for (int j = 0; j < 32; ++j) r0[j] = __float_as_uint(__uint_as_float(r0[j]) * f);
+        ptx::tmem_st_32x32b_x32(o_tm + k, r0);
       }
     }
   }
-  if constexpr (NCH < 4) {
+#pragma unroll 1
+  for (int k = chunk0; k < end; k += 2) {
+    ptx::tmem_ld_32x32b_x32(s_tm + k * 32, r0);
+    if (k + 1 < end) ptx::tmem_ld_32x32b_x32(s_tm + (k + 1) * 32, r1);
+    ptx::tmem_wait_ld_regs(r0);
+    ptx::reg_fence(r1);
+    exp_of(r0, k);
+    if (k + 1 < end) exp_of(r1, k + 1);
+  }
+  if (chunks < 4) {
     const uint32_t zeros[16] = {};
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < 4; ++k)
-      if (k < chunk0 || k >= chunk0 + NCH) ptx::tmem_st_32x32b_x16(s_tm + k * 16, zeros);
-  }
-  const float m = st.m;
-  float l = st.l;
-#pragma unroll
-  for (int k = 0; k < NCH; ++k) {
-    uint32_t h[16];
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const float2 cc = make_float2(c[2 * k + g], c[2 * k + g]);
-      const float off = o[2 * k + g] - m;
-      const float2 oo = make_float2(off, off);
-      float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        const uint32_t* v = &r[k][g * 16 + j];
-        const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), cc, oo);
-        const float2 e = make_float2(ex2(x.x), ex2(x.y));
-        sum = __fadd2_rn(sum, e);
-        const __half2 hv = __floats2half2_rn(e.x, e.y);
-        h[g * 8 + j / 2] = *reinterpret_cast<const uint32_t*>(&hv);
-      }
-      l = fmaf(sum.x + sum.y, sc.vinv[g0 + 2 * k + g], l);
-    }
-    ptx::tmem_st_32x32b_x16(s_tm + (chunk0 + k) * 16, h);
-  }
-  st.l = l;
-  if ((nan_words[0] | nan_words[1] | nan_words[2] | nan_words[3]) != 0u) {
-#pragma unroll
-    for (int k = 0; k < NCH; ++k)
-      st.bad |= (nan_words[chunk0 + k] & seen32(pos, window, len, tile0, (chunk0 + k) * 32, flags >> 16)) != 0u;
+      if (k < chunk0 || k >= end) ptx::tmem_st_32x32b_x16(s_tm + k * 16, zeros);
   }
 }
 
@@ -334,47 +358,70 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t* h, uint32
 // D 64: h and l in one row.  `sign` flips every element.
 template <int D>
 __device__ __forceinline__ float load_query(uint8_t* dst, int r, const __nv_bfloat16* q, bool write, uint32_t sign) {
-  uint4 v[D / 8];
+  const uint4* const piece = reinterpret_cast<const uint4*>(q);
   uint32_t top2 = 0, odd = 0;
+  if (q) {
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (q) v[i] = __ldg(reinterpret_cast<const uint4*>(q) + i);
-  }
+    for (int i = 0; i < D / 8; ++i) {
+      const uint4 v = __ldg(piece + i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t m = w[k] & 0x7FFF7FFFu, special = __vcmpgeu2(m, 0x7F807F80u);  // infinities and NaN do not count
-      odd |= special;
-      top2 = __vmaxu2(top2, m & ~special);
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t m = w[k] & 0x7FFF7FFFu, special = __vcmpgeu2(m, 0x7F807F80u);  // infinities and NaN do not count
+        odd |= special;
+        top2 = __vmaxu2(top2, m & ~special);
+      }
     }
   }
   const int e = query_exponent(max(top2 >> 16, top2 & 0xFFFFu));
   if (write) {
     const float mul = __uint_as_float(__float_as_uint(power_of_two(e)) | sign);
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < D / 16; ++c) {
+      uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      if (q) v[0] = __ldg(piece + 2 * c), v[1] = __ldg(piece + 2 * c + 1);
       uint32_t h[8], l[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint4& p = v[2 * c + i / 4];
-        uint32_t w = i % 4 == 0 ? p.x : i % 4 == 1 ? p.y : i % 4 == 2 ? p.z : p.w;
+        const uint4& x = v[i / 4];
+        uint32_t w = i % 4 == 0 ? x.x : i % 4 == 1 ? x.y : i % 4 == 2 ? x.z : x.w;
         // an infinity becomes NaN: as a code it would be the largest value
         if (odd) w |= __vcmpeq2(w & 0x7FFF7FFFu, 0x7F807F80u) & 0x7FFF7FFFu;
         split_pair(__uint_as_float(w << 16) * mul, __uint_as_float(w & 0xFFFF0000u) * mul, &h[i], &l[i]);
       }
-      const int ch = c, cl = D == 64 ? c + 4 : c;
+      const int cl = D == 64 ? c + 4 : c;
       uint8_t* const hrow = dst + r * 128;
       uint8_t* const lrow = hrow + (D == 64 ? 0 : kTile * 128);
-      *reinterpret_cast<uint4*>(hrow + ((ch ^ (r & 7)) << 4)) =
+      *reinterpret_cast<uint4*>(hrow + ((c ^ (r & 7)) << 4)) =
           make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
       *reinterpret_cast<uint4*>(lrow + ((cl ^ (r & 7)) << 4)) =
           make_uint4(l[0] | l[1] << 16, l[2] | l[3] << 16, l[4] | l[5] << 16, l[6] | l[7] << 16);
     }
   }
   return power_of_two(-e);
+}
+
+// Sixteen values of a token (row r of a tile): NaN codes become zeros, and all
+// of them do where the group's scale is zero or none.  Returns the token's bit
+// of 32 where there was a NaN.
+__device__ __noinline__ uint32_t clear_values(uint4* codes, int r, uint32_t flags) {
+  const int group = r >> 4;
+  uint32_t* const x = reinterpret_cast<uint32_t*>(codes);
+  uint32_t any = flags >> (8 + group) & 1u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t n = __vcmpeq4(x[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    any |= n;
+    x[k] = (flags | flags >> 8) >> group & 1u ? 0u : x[k] & ~n;
+  }
+  return any != 0u ? 1u << (r & 31) : 0u;
+}
+
+// Four e4m3 codes as f16.
+__device__ __forceinline__ void half_pairs(uint32_t codes, uint32_t* lo, uint32_t* hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(*lo), "=r"(*hi)
+      : "r"(codes));
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
@@ -407,12 +454,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(bar(L::vEmptyB, s), 4u);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(bar(L::v16FullB, i), 4u);
       ptx::mbar_init(bar(L::v16EmptyB, i), 1u);
       ptx::mbar_init(bar(L::qFullB, i), 4u);
       ptx::mbar_init(bar(L::sFullB, i), 1u);
       ptx::mbar_init(bar(L::pFullB, i), 4u);
       ptx::mbar_init(bar(L::oFullB, i), 1u);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      ptx::mbar_init(bar(L::scaleFullB, i), 1u);
+      ptx::mbar_init(bar(L::v16FullB, i), 4u);
     }
     for (int i = 0; i < kUnitSlots; ++i) {
       ptx::mbar_init(bar(L::unitFullB, i), 1u);
@@ -441,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = unit_count(p, r);
       int64_t steps = 0;
       if (n <= 16) {
-        for (int u = 0; u < n; ++u) steps += Unit(p, r, u).steps;
+        for (int u = 0; u < n; ++u) steps += Unit(p, r, u).steps + kUnitCost;
       } else {
         steps = -1;  // many units: a warp's work
       }
@@ -453,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Request r(p, b);
       const int n = unit_count(p, r);
       int64_t steps = 0;
-      for (int u = lane; u < n; u += 32) steps += Unit(p, r, u).steps;
+      for (int u = lane; u < n; u += 32) steps += Unit(p, r, u).steps + kUnitCost;
       steps = __shfl_sync(kFull, warp_scan(steps, lane), 31);
       __syncwarp();
       if (lane == 0) cum[b + 1] = steps;
@@ -503,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = unit_count(p, r);
       for (unit = 0; unit < n; unit += 32) {  // 32 units at a time
         const int u = unit + lane;
-        const int64_t sum = warp_scan(u < n ? Unit(p, r, u).steps : 0, lane);
+        const int64_t sum = warp_scan(u < n ? Unit(p, r, u).steps + kUnitCost : 0, lane);
         const uint32_t over = __ballot_sync(kFull, sum > rest);
         if (over) {
           const int l = __ffs(over) - 1;
@@ -543,9 +593,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok) {
           Piece out;
           out.row0 = -1;
+          bool empty = false;
           if (at < end) {
             const Unit u(p, r, unit);
-            const int32_t stop = static_cast<int32_t>(min(static_cast<int64_t>(u.steps), skip + (end - at)));
+            const int32_t all = u.steps + kUnitCost;
+            const int32_t stop = static_cast<int32_t>(min(static_cast<int64_t>(all), skip + (end - at)));
+            // (the unit's cost stands before its steps)
+            const int32_t from = max(skip - kUnitCost, 0), to = max(stop - kUnitCost, 0);
+            empty = from == to;
             out.row0 = r.row0 + u.at;
             out.positions = u.positions;
             out.head = head;
@@ -553,27 +608,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             out.pos0 = u.pos0;
             out.len = r.len;
             out.shared = u.shared;
-            out.ta = u.ta + (u.shared ? skip : 2 * skip);
-            out.tb = min(u.ta + (u.shared ? stop : 2 * stop), u.tb);
-            out.slot = skip > 0 ? 0 : stop < u.steps ? 1 : -1;
-            if (out.slot == 1) {
+            out.ta = u.ta + (u.shared ? from : 2 * from);
+            out.tb = min(u.ta + (u.shared ? to : 2 * to), u.tb);
+            out.slot = from > 0 ? 0 : to < u.steps ? 1 : -1;
+            if (out.slot == 1 && !empty) {
               meta.row0 = out.row0;
               meta.positions = out.positions;
               meta.head = head;
-              meta.last = static_cast<int32_t>((at + u.steps - 1) / per_cta);
+              meta.last = static_cast<int32_t>((at - skip + all - 1) / per_cta);
               meta.shared = out.shared;
             }
             at += stop - skip;
             skip = 0;
           }
-          ok = wait(bar(L::unitEmptyB, n % kUnitSlots), ((n / kUnitSlots) & 1u) ^ 1u, abort_flag, kSiteAccEmpty);
-          if (!ok) break;
-          if (lane == 0) {
-            *slot_of(n) = out;
-            ptx::mbar_arrive(bar(L::unitFullB, n % kUnitSlots));
+          if (!empty) {
+            ok = wait(bar(L::unitEmptyB, n % kUnitSlots), ((n / kUnitSlots) & 1u) ^ 1u, abort_flag, kSiteAccEmpty);
+            if (!ok) break;
+            if (lane == 0) {
+              *slot_of(n) = out;
+              ptx::mbar_arrive(bar(L::unitFullB, n % kUnitSlots));
+            }
+            __syncwarp();
+            ++n;
           }
-          __syncwarp();
-          ++n;
           if (out.row0 < 0) break;
           if (at < end && ++unit == n_units) {
             unit = 0;
@@ -663,7 +720,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool leader = lane < 8 && (lane * 16 & ((1 << shift) - 1)) == 0;
         const int32_t block = here ? a0.block : p.num_blocks;  // (outside: zeros)
         const uint32_t rows = lane * 16 * 128u;
-        if (lane == 0) ptx::mbar_arrive_expect_tx(bar(L::kFullB, stage), L::kHalf);
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(L::scaleFullB, j % kScaleSlots));
+          ptx::mbar_arrive_expect_tx(bar(L::kFullB, stage), L::kHalf);
+        }
         __syncwarp();
         if (leader)
           ptx::tma_load_4d(base + L::k + stage * L::kHalf + rows, &tm_kv, bar(L::kFullB, stage), 0, 0, a0.head, block);
@@ -698,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t q0 = ptx::smem_desc_sw128(base + L::q), k0 = ptx::smem_desc_sw128(base + L::k);
       const uint64_t v0 = ptx::smem_desc_mn16(base + L::v16, kTile * 128u);
       uint32_t j0 = 0;                  // tiles before this piece
-      uint32_t np[2] = {0u, 0u};        // products of each group so far
+      uint32_t np0 = 0, np1 = 0;        // outputs of each group so far
       uint32_t nq[2] = {0u, 0u};
       Piece piece;
       bool ok = true;
@@ -710,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto tile_of = [&](int g, int i) { return j0 + static_cast<uint32_t>(shared ? i : 2 * i + g); };
         const auto scores = [&](int g, int i) {
           const uint32_t j = tile_of(g, i), st = j % S;
-          if (!wait(bar(L::kFullB, st), (j / S) & 1u, abort_flag, kSiteStageFull)) return false;
+          if ((!shared || g == 0) && !wait(bar(L::kFullB, st), (j / S) & 1u, abort_flag, kSiteStageFull)) return false;
           ptx::tc_fence_after();
           const uint64_t a = q0 + static_cast<uint64_t>((shared ? g : 0) * (L::qBytes >> 4));
           const uint64_t b = k0 + static_cast<uint64_t>(st * (L::kHalf >> 4));
@@ -727,12 +787,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           return true;
         };
-        const auto outputs = [&](int g, int i) {
+        const auto outputs = [&](int g, int i, int n_g) {
           const uint32_t j = tile_of(g, i), buf = j & 1u;
-          if (!wait(bar(L::pFullB, g), np[g] & 1u, abort_flag, kSiteAccEmpty) ||
-              !wait(bar(L::v16FullB, buf), (j >> 1) & 1u, abort_flag, kSiteStageFull))
+          if ((!shared || g == 0) &&
+              !wait(bar(L::v16FullB, j % kScaleSlots), (j / kScaleSlots) & 1u, abort_flag, kSiteStageFull))
             return false;
-          ++np[g];
+          if (!wait(bar(L::pFullB, g), (g ? np1 : np0) & 1u, abort_flag, kSiteAccEmpty)) return false;
+          if (g) ++np1; else ++np0;
           ptx::tc_fence_after();
           const uint64_t b = v0 + static_cast<uint64_t>(buf * (L::kV16 >> 4));
           if (ptx::elect_one()) {
@@ -741,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::mma_f16_ts(tmem + 2 * kTile + g * 128, tmem + g * kTile + 8 * kk, b + static_cast<uint64_t>(kk * (2048 >> 4)),
                               kIdescO, i + kk > 0 ? 1u : 0u);
             if (!shared || g == 1) ptx::mma_commit(bar(L::v16EmptyB, buf));
-            if (i + 1 == count[g]) ptx::mma_commit(bar(L::oFullB, g));
+            if (i + 1 == n_g) ptx::mma_commit(bar(L::oFullB, g));
           }
           __syncwarp();
           return true;
@@ -752,11 +813,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(bar(L::qFullB, 1), nq[1] & 1u, abort_flag, kSiteQFull);
           ++nq[1];
         }
-        ok = ok && scores(0, 0) && (count[1] == 0 || scores(1, 0));
+        // A group's outputs of a tile, then its scores of the next.
 #pragma unroll 1
-        for (int i = 0; ok && i < count[0]; ++i) {
-          ok = outputs(0, i) && (i + 1 >= count[0] || scores(0, i + 1));
-          if (ok && i < count[1]) ok = outputs(1, i) && (i + 1 >= count[1] || scores(1, i + 1));
+        for (int i = -1; ok && i < count[0]; ++i) {
+#pragma unroll 1
+          for (int g = 0; ok && g < 2; ++g) {
+            const int n_g = g ? count[1] : count[0];
+            if (i >= 0 && i < n_g) ok = outputs(g, i, n_g);
+            if (ok && i + 1 < n_g) ok = scores(g, i + 1);
+          }
         }
         j0 += tiles;
       }
@@ -790,51 +855,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* const dst = smem + L::v16 + buf * L::kV16;
         uint32_t nan_rows = 0;
         constexpr int kPanels = D / 64, kTimes = 4 * kPanels;
-        uint4 codes[kTimes];
-        const auto row_of = [&](int i) {  // combination i * 4 + quarter: panel, rows
-          const int pair = (i * 4 + quarter) / kPanels;
-          return 32 * w + 8 * (pair >> 2) + ((pair & 3) ^ (other * 5));
-        };
-        const auto panel_of = [&](int i) { return (i * 4 + quarter) % kPanels; };
+#pragma unroll 1
+        for (int i = 0; i < kTimes; i += 2) {
+          uint4 codes[2];
+          int r[2], panel[2];
+          uint32_t odd = flags & 0xFFFFu;
 #pragma unroll
-        for (int i = 0; i < kTimes; ++i) {
-          const int r = row_of(i), c = (D == 64 ? 4 : panel_of(i) * 4) + piece_in;
-          codes[i] = *reinterpret_cast<const uint4*>(src + r * 128 + ((c ^ (r & 7)) << 4));
-        }
-#pragma unroll
-        for (int i = 0; i < kTimes; ++i) {
-          const int r = row_of(i);
-          uint32_t x[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w}, odd = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) odd |= __vcmpeq4(x[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-          if ((flags & 0xFFFFu) != 0u || odd != 0u) {
-            const uint32_t group = static_cast<uint32_t>(r) >> 4;
-            if (odd != 0u || (flags >> (8 + group) & 1u)) nan_rows |= 1u << (r & 31);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              x[k] &= ~__vcmpeq4(x[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-              if ((flags | flags >> 8) >> group & 1u) x[k] = 0u;
-            }
+          for (int x = 0; x < 2; ++x) {
+            // the combination of a panel and a pair of rows that these eight lanes have
+            const int combo = (i + x) * 4 + quarter, pair = combo / kPanels;
+            panel[x] = combo % kPanels;
+            r[x] = 32 * w + 8 * (pair >> 2) + ((pair & 3) ^ (other * 5));
+            const int c = (D == 64 ? 4 : panel[x] * 4) + piece_in;
+            codes[x] = *reinterpret_cast<const uint4*>(src + r[x] * 128 + ((c ^ (r[x] & 7)) << 4));
           }
-          uint32_t h[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2(
-                static_cast<__nv_fp8x2_storage_t>(x[k / 2] >> (16 * (k % 2)) & 0xFFFFu), __NV_E4M3);
-            h[k] = static_cast<uint32_t>(v.x) | static_cast<uint32_t>(v.y) << 16;
+          for (int x = 0; x < 2; ++x)  // NaN codes (0x7F and 0xFF): adding one to the lower seven bits reaches the eighth
+            odd |= ((codes[x].x & 0x7F7F7F7Fu) + 0x01010101u | (codes[x].y & 0x7F7F7F7Fu) + 0x01010101u |
+                    (codes[x].z & 0x7F7F7F7Fu) + 0x01010101u | (codes[x].w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+          if (__any_sync(kFull, odd != 0u)) {
+            nan_rows |= clear_values(&codes[0], r[0], flags);
+            nan_rows |= clear_values(&codes[1], r[1], flags);
           }
-          uint8_t* const row = dst + panel_of(i) * (kTile * 128) + r * 128;
-          *reinterpret_cast<uint4*>(row + (((2 * piece_in) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(row + (((2 * piece_in + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t h[8];
+            half_pairs(codes[x].x, &h[0], &h[1]);
+            half_pairs(codes[x].y, &h[2], &h[3]);
+            half_pairs(codes[x].z, &h[4], &h[5]);
+            half_pairs(codes[x].w, &h[6], &h[7]);
+            uint8_t* const row = dst + panel[x] * (kTile * 128) + r[x] * 128;
+            *reinterpret_cast<uint4*>(row + (((2 * piece_in) ^ (r[x] & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(row + (((2 * piece_in + 1) ^ (r[x] & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+          }
         }
+        __syncwarp();
+        // the codes have been read: the stage may be filled again
+        if (lane == 0) ptx::mbar_arrive(bar(D == 128 ? L::vEmptyB : L::kEmptyB, stage));
         nan_rows = __reduce_or_sync(kFull, nan_rows);
-        if (lane == 0) reinterpret_cast<uint32_t*>(smem + L::nan)[buf * 4 + w] = nan_rows;
+        if (lane == 0) reinterpret_cast<uint32_t*>(&tile_scales[j % kScaleSlots].nan)[w] = nan_rows;
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(bar(L::v16FullB, buf));
-          ptx::mbar_arrive(bar(D == 128 ? L::vEmptyB : L::kEmptyB, stage));
-        }
+        if (lane == 0) ptx::mbar_arrive(bar(L::v16FullB, j % kScaleSlots));
         ++j;
         if (++stage == S) stage = 0, phase ^= 1u;
       }
@@ -846,79 +908,100 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = threadIdx.x & 127;  // lane of the accumulators
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_tm = tmem + g * kTile + lane_off, o_tm = tmem + 2 * kTile + g * 128 + lane_off;
-    const uint32_t sign = p.negative ? 0x80000000u : 0u;
     uint32_t j0 = 0, n_tiles = 0, n_outs = 0, n_meet = 0;
     const auto meet = [&] {  // the two groups
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(L::meetB));
       return wait(bar(L::meetB), n_meet++ & 1u, abort_flag, kSiteAccFull);
     };
-    Piece piece;
 #pragma unroll 1
-    for (uint32_t n = 0; get_piece(n, &piece); ++n) {
+    for (uint32_t n = 0;; ++n) {
+      // (the piece stays in its slot: the registers are for the scores)
+      if (!wait(bar(L::unitFullB, n % kUnitSlots), (n / kUnitSlots) & 1u, abort_flag, kSiteQEmpty)) goto out;
+      const Piece& piece = *slot_of(n);
+      if (piece.row0 < 0) break;
       const bool shared = piece.shared != 0;
-      const int tiles = piece.tb - piece.ta, half = p.half_positions;
-      const int rows = shared ? kTile : piece.positions * p.group;   // rows in use of a tile's lanes
-      const int copy_lanes = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;  // lanes of a copy of the rows
-      const int r = i & (copy_lanes - 1);
-      const int index = r / p.group, h = r - index * p.group;        // position (of this group's), head
-      const int position = index + (shared ? g * half : 0);
-      const bool live = index < half && position < piece.positions;
-      const int count = shared ? tiles : (tiles - g + 1) / 2;
-      const int64_t row = static_cast<int64_t>(piece.row0) + position;
-      const __nv_bfloat16* const q = static_cast<const __nv_bfloat16*>(p.q) + row * p.q_row_stride +
-                                     (piece.head * p.group + h) * p.q_head_stride;
-      const bool write = shared || g == 0;
-      const float row_scale = load_query<D>(smem + L::q + g * L::qBytes, i, live ? q : nullptr, write, sign);
-      if (write) {
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(L::qFullB, g));
+      const int half = p.half_positions;
+      // lanes of a copy of the rows, and this thread's row
+      const int rows = shared ? kTile : piece.positions * p.group;
+      const int copy_lanes = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+      float row_scale;
+      int pos = -1;
+      {
+        const int r = i & (copy_lanes - 1), index = r / p.group, h = r - index * p.group;  // position (of this group's), head
+        const int position = index + (shared ? g * half : 0);
+        const bool live = index < half && position < piece.positions;
+        const __nv_bfloat16* const q = static_cast<const __nv_bfloat16*>(p.q) +
+                                       (static_cast<int64_t>(piece.row0) + position) * p.q_row_stride +
+                                       (piece.head * p.group + h) * p.q_head_stride;
+        const bool write = shared || g == 0;
+        row_scale = load_query<D>(smem + L::q + g * L::qBytes, i, live ? q : nullptr, write, p.negative ? 0x80000000u : 0u);
+        if (write) {
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(L::qFullB, g));
+        }
+        if (live) pos = max(piece.pos0 + position, -1);
       }
-      const int pos = live ? max(piece.pos0 + position, -1) : -1;
-      const int full_to = min(piece.pos0 + 1, piece.len);            // positions below are seen by every row,
+      const int len = piece.len;
+      const int full_to = min(piece.pos0 + 1, len);                  // positions below are seen by every row,
       const int full_from = p.window > 0 ? max(piece.pos0 + piece.positions - 1, -1) - p.window + 1 : 0;  // from here on
       const int chunk0 = quad / (copy_lanes / 32) * (copy_lanes / 32);
+      const int step = shared ? 1 : 2, first = shared ? 0 : g;
+      const int count = (piece.tb - piece.ta - first + step - 1) / step;
       RowState st;
       float ref = 1.f;
+      uint32_t j = j0 + first;
+      int tile0 = (piece.ta + first) * kTile;
+      j0 += piece.tb - piece.ta;
+      // Whether the row sees a NaN among the values of a tile whose products have been issued.
+      const auto see_nan = [&](uint32_t jj, int at) {
+        if (!wait(bar(L::v16FullB, jj % kScaleSlots), (jj / kScaleSlots) & 1u, abort_flag, kSiteStageFull)) return false;
+        const uint4 words = tile_scales[jj % kScaleSlots].nan;
+        if ((words.x | words.y | words.z | words.w) != 0u) {
+          const uint32_t in_cache = tile_scales[jj % kScaleSlots].flags >> 16;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c >= chunk0 && c < chunk0 + copy_lanes / 32)
+              st.bad |= ((c == 0 ? words.x : c == 1 ? words.y : c == 2 ? words.z : words.w) &
+                         seen32(pos, p.window, len, at, c * 32, in_cache)) != 0u;
+        }
+        return true;
+      };
 #pragma unroll 1
-      for (int k = 0; k < count; ++k) {
-        const uint32_t j = j0 + static_cast<uint32_t>(shared ? k : 2 * k + g);
-        const int tile0 = (piece.ta + (shared ? k : 2 * k + g)) * kTile;
-        if (!wait(bar(L::v16FullB, j & 1u), (j >> 1) & 1u, abort_flag, kSiteStageFull) ||
+      for (int k = 0; k < count; ++k, j += step, tile0 += step * kTile) {
+        if (!wait(bar(L::scaleFullB, j % kScaleSlots), (j / kScaleSlots) & 1u, abort_flag, kSiteStageFull) ||
             !wait(bar(L::sFullB, g), n_tiles & 1u, abort_flag, kSiteAccFull))
           goto out;
         ++n_tiles;
         ptx::tc_fence_after();
         {
           const TileScales& sc = tile_scales[j % kScaleSlots];
-          const uint32_t* const nan_words = reinterpret_cast<const uint32_t*>(smem + L::nan) + (j & 1u) * 4;
           ref = sc.ref;
           const bool masked = tile0 + kTile > full_to || tile0 < full_from || (sc.flags >> 16) != 0xFFu;
-          if (copy_lanes == 128)
-            softmax_tile<4, D>(s_tm, o_tm, sc, nan_words, 0, masked, pos, p.window, piece.len, tile0, row_scale, k == 0, st);
-          else if (copy_lanes == 64)
-            softmax_tile<2, D>(s_tm, o_tm, sc, nan_words, chunk0, masked, pos, p.window, piece.len, tile0, row_scale, k == 0, st);
-          else
-            softmax_tile<1, D>(s_tm, o_tm, sc, nan_words, chunk0, masked, pos, p.window, piece.len, tile0, row_scale, k == 0, st);
+          softmax_tile<D>(s_tm, o_tm, sc, chunk0, copy_lanes / 32, masked, pos, p.window, len, tile0, row_scale, k == 0, st);
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(L::pFullB, g));
+        if (k > 0 && !see_nan(j - step, tile0 - step * kTile)) goto out;
       }
-      j0 += tiles;
       if (count > 0) {
-        if (!wait(bar(L::oFullB, g), n_outs & 1u, abort_flag, kSiteAccFull)) goto out;
+        if (!wait(bar(L::oFullB, g), n_outs & 1u, abort_flag, kSiteAccFull) || !see_nan(j - step, tile0 - step * kTile))
+          goto out;
         ++n_outs;
         ptx::tc_fence_after();
       }
       {
         // Where the results go: out, or the workspace.
+        const int r = i & (copy_lanes - 1);
         float* const ws = p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + piece.slot) * block_attn_piece_floats(D);
         if (shared) {
           const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
-          const int64_t head = piece.head * p.group + h;
+          const int index = r / p.group, position = index + g * half;
+          const bool live = index < half && position < piece.positions;
+          const int64_t row = static_cast<int64_t>(piece.row0) + position, head = piece.head * p.group + r - index * p.group;
           __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + row * p.out_row_stride + head * p.out_head_stride;
           const int wrow = g * kTile + i;
 #pragma unroll 1
@@ -1032,6 +1115,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the accumulator is read before the next piece's products overwrite it
         ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(L::unitEmptyB, n % kUnitSlots));
       }
     }
   out:;
