@@ -115,21 +115,24 @@ static_assert(sizeof(Piece) <= 64, "a unit slot");
 // The plan's prefix sums lie where the f16 values and the scales will.
 static_assert((kMaxBatch + 1) * 8 <= 2 * Smem<64>::kV16 + kScaleSlots * sizeof(TileScales), "prefix sums");
 
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t site) {
-  bool ok = ptx::mbar_test_wait(bar, parity);
-  if (!ok) {
-    const uint64_t since = ptx::globaltimer_ns();
+// One warp-collective bounded wait.
+__device__ __forceinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t site) {
+  bool ok;
+  const uint64_t since = ptx::globaltimer_ns();
 #pragma unroll 1
-    while (!(ok = ptx::mbar_try_wait(bar, parity))) {
-      if (*abort_flag) break;
-      if (ptx::globaltimer_ns() - since > kWaitTimeoutNs) {
-        *abort_flag = 1u;
-        atomicOr(&g_block_attn_watchdog, site);
-        break;
-      }
+  while (!(ok = ptx::mbar_try_wait(bar, parity))) {
+    if (*abort_flag) break;
+    if (ptx::globaltimer_ns() - since > kWaitTimeoutNs) {
+      *abort_flag = 1u;
+      atomicOr(&g_block_attn_watchdog, site);
+      break;
     }
   }
   return __all_sync(kFull, ok);
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t site) {
+  if (__all_sync(kFull, ptx::mbar_test_wait(bar, parity))) return true;
+  return wait_longer(bar, parity, abort_flag, site);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -251,6 +254,40 @@ __device__ __forceinline__ void chunk_exp(const uint32_t (&r)[32], const float (
   ptx::tmem_st_32x32b_x16(p_tm, h);
 }
 
+// Of a tile that not every row sees in full: log2 probabilities, -inf where the
+// row sees nothing, in the scores' place.
+__device__ __noinline__ void mask_tile(uint32_t s_tm, const TileScales* sc, int chunk0, int end, int pos, int window, int len,
+                                       int tile0, float row_scale) {
+#pragma unroll 1
+  for (int k = chunk0; k < end; ++k) {
+    uint32_t r[32];
+    ptx::tmem_ld_32x32b_x32(s_tm + k * 32, r);
+    const uint32_t see = seen32(pos, window, len, tile0, k * 32, sc->flags >> 16);
+    ptx::tmem_wait_ld_regs(r);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float x = fmaf(__uint_as_float(r[j]), sc->key[2 * k + j / 16] * row_scale, sc->vlog[2 * k + j / 16]);
+      r[j] = __float_as_uint(see >> j & 1u ? x : -INFINITY);
+    }
+    ptx::tmem_st_32x32b_x32(s_tm + k * 32, r);
+  }
+  ptx::tmem_wait_st();
+}
+
+// A row's outputs times f.
+template <int D>
+__device__ __noinline__ void scale_outputs(uint32_t o_tm, float f) {
+#pragma unroll 1
+  for (int k = 0; k < D; k += 32) {
+    uint32_t r[32];
+    ptx::tmem_ld_32x32b_x32(o_tm + k, r);
+    ptx::tmem_wait_ld_regs(r);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
+    ptx::tmem_st_32x32b_x32(o_tm + k, r);
+  }
+}
+
 // A tile's scores to probabilities, `chunks` (1, 2 or 4) times 32 columns from
 // chunk0 on; the rest of the probabilities are zeros.  Probabilities lie over
 // the scores (16 columns for 32), written in order, so those of a chunk
@@ -270,21 +307,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_tm, uint32_t o_tm, const
     }
   };
   const int end = chunk0 + chunks;
-  if (masked) {  // log2 probabilities, -inf where the row sees nothing, in the scores' place
-#pragma unroll 1
-    for (int k = chunk0; k < end; ++k) {
-      ptx::tmem_ld_32x32b_x32(s_tm + k * 32, r0);
-      const uint32_t see = seen32(pos, window, len, tile0, k * 32, sc.flags >> 16);
-      ptx::tmem_wait_ld_regs(r0);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float x = fmaf(__uint_as_float(r0[j]), sc.key[2 * k + j / 16] * row_scale, sc.vlog[2 * k + j / 16]);
-        r0[j] = __float_as_uint(see >> j & 1u ? x : -INFINITY);
-      }
-      ptx::tmem_st_32x32b_x32(s_tm + k * 32, r0);
-    }
-    ptx::tmem_wait_st();
-  }
+  if (masked) mask_tile(s_tm, &sc, chunk0, end, pos, window, len, tile0, row_scale);
   float top = -INFINITY, c[2], o[2];
   const auto top_of = [&](const uint32_t (&r)[32], int k) {
     scales(k, c, o);
@@ -307,16 +330,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_tm, uint32_t o_tm, const
     const float m = fmaxf(st.m, top), f = ex2(st.m - m);
     st.l *= f;
     st.m = m;
-    if (!first) {  // (the products before this tile are done: its scores were issued after them)
-#pragma unroll 1
-      for (int k = 0; k < D; k += 32) {
-        ptx::tmem_ld_32x32b_x32(o_tm + k, r0);
-        ptx::tmem_wait_ld_regs(r0);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) r0[j] = __float_as_uint(__uint_as_float(r0[j]) * f);
-        ptx::tmem_st_32x32b_x32(o_tm + k, r0);
-      }
-    }
+    if (!first) scale_outputs<D>(o_tm, f);  // (the products before this tile are done: its scores were issued after them)
   }
 #pragma unroll 1
   for (int k = chunk0; k < end; k += 2) {
