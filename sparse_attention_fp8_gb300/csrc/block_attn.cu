@@ -326,6 +326,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_tm, uint32_t o_tm, const
     top_of(r0, k);
     if (k + 1 < end) top_of(r1, k + 1);
   }
+  ptx::tmem_ld_32x32b_x32(s_tm + chunk0 * 32, r0);
+  if (chunks > 1) ptx::tmem_ld_32x32b_x32(s_tm + (chunk0 + 1) * 32, r1);
   if (__any_sync(kFull, top > st.m + kRaise)) {
     const float m = fmaxf(st.m, top), f = ex2(st.m - m);
     st.l *= f;
@@ -334,12 +336,12 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_tm, uint32_t o_tm, const
   }
 #pragma unroll 1
   for (int k = chunk0; k < end; k += 2) {
-    ptx::tmem_ld_32x32b_x32(s_tm + k * 32, r0);
-    if (k + 1 < end) ptx::tmem_ld_32x32b_x32(s_tm + (k + 1) * 32, r1);
     ptx::tmem_wait_ld_regs(r0);
     ptx::reg_fence(r1);
     exp_of(r0, k);
+    if (k + 2 < end) ptx::tmem_ld_32x32b_x32(s_tm + (k + 2) * 32, r0);
     if (k + 1 < end) exp_of(r1, k + 1);
+    if (k + 2 < end) ptx::tmem_ld_32x32b_x32(s_tm + (k + 3) * 32, r1);
   }
   if (chunks < 4) {
     const uint32_t zeros[16] = {};
@@ -415,27 +417,67 @@ __device__ __forceinline__ float load_query(uint8_t* dst, int r, const __nv_bflo
   return power_of_two(-e);
 }
 
-// Sixteen values of a token (row r of a tile): NaN codes become zeros, and all
-// of them do where the group's scale is zero or none.  Returns the token's bit
-// of 32 where there was a NaN.
-__device__ __noinline__ uint32_t clear_values(uint4* codes, int r, uint32_t flags) {
-  const int group = r >> 4;
-  uint32_t* const x = reinterpret_cast<uint32_t*>(codes);
-  uint32_t any = flags >> (8 + group) & 1u;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t n = __vcmpeq4(x[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    any |= n;
-    x[k] = (flags | flags >> 8) >> group & 1u ? 0u : x[k] & ~n;
-  }
-  return any != 0u ? 1u << (r & 31) : 0u;
-}
-
 // Four e4m3 codes as f16.
 __device__ __forceinline__ void half_pairs(uint32_t codes, uint32_t* lo, uint32_t* hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(*lo), "=r"(*hi)
       : "r"(codes));
+}
+
+// Where a lane's codes of a tile lie: eight lanes convert 64 codes of two
+// tokens whose rows differ in bits 0 and 2, so that neither their reads nor
+// their writes share banks.  Combination i * 4 + quarter of a panel of 64
+// channels and a pair of rows.
+template <int D>
+struct ConvPlace {
+  static constexpr int kPanels = D / 64, kTimes = 4 * kPanels;
+  int w, piece, other, quarter;  // w: the warp's 32 tokens of a tile
+  __device__ __forceinline__ ConvPlace(int warp, int lane)
+      : w(warp), piece(lane & 3), other(lane >> 2 & 1), quarter(lane >> 3) {}
+  __device__ __forceinline__ int panel(int i) const { return (i * 4 + quarter) % kPanels; }
+  __device__ __forceinline__ int row(int i) const {
+    const int pair = (i * 4 + quarter) / kPanels;
+    return 32 * w + 8 * (pair >> 2) + ((pair & 3) ^ (other * 5));
+  }
+  __device__ __forceinline__ uint4 load(const uint8_t* src, int i) const {
+    const int r = row(i), c = (D == 64 ? 4 : panel(i) * 4) + piece;
+    return *reinterpret_cast<const uint4*>(src + r * 128 + ((c ^ (r & 7)) << 4));
+  }
+  __device__ __forceinline__ void store(uint8_t* dst, int i, const uint4& codes) const {
+    const int r = row(i);
+    uint32_t h[8];
+    half_pairs(codes.x, &h[0], &h[1]);
+    half_pairs(codes.y, &h[2], &h[3]);
+    half_pairs(codes.z, &h[4], &h[5]);
+    half_pairs(codes.w, &h[6], &h[7]);
+    uint8_t* const at = dst + panel(i) * (kTile * 128) + r * 128;
+    *reinterpret_cast<uint4*>(at + (((2 * piece) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(at + (((2 * piece + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+};
+
+// A tile once more, with zeros for codes that are NaN and for groups of tokens
+// whose scale is zero or NaN (flags).  Returns the warp's tokens with a NaN.
+template <int D>
+__device__ __noinline__ uint32_t convert_odd(uint8_t* dst, const uint8_t* src, int warp, int lane, uint32_t flags) {
+  const ConvPlace<D> at(warp, lane);
+  uint32_t nan_rows = 0;
+#pragma unroll 1
+  for (int i = 0; i < ConvPlace<D>::kTimes; ++i) {
+    const uint4 x = at.load(src, i);
+    const int r = at.row(i);
+    const uint32_t group = flags >> (r >> 4);
+    const bool none = ((group | group >> 8) & 1u) != 0u;
+    uint32_t any = group >> 8 & 1u;
+    const auto clear = [&](uint32_t v) {
+      const uint32_t n = __vcmpeq4(v & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+      any |= n;
+      return none ? 0u : v & ~n;
+    };
+    at.store(dst, i, make_uint4(clear(x.x), clear(x.y), clear(x.z), clear(x.w)));
+    if (any != 0u) nan_rows |= 1u << (r & 31);
+  }
+  return __reduce_or_sync(kFull, nan_rows);
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
@@ -850,9 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ========================= values to f16 =========================
     reg_dec<kConvRegs>();
     const int w = warp - kConvWarp0;  // its 32 tokens of a tile
-    // Eight lanes convert 64 codes of two tokens whose rows differ in bits 0 and
-    // 2: neither their reads nor their writes share banks.
-    const int piece_in = lane & 3, other = lane >> 2 & 1, quarter = lane >> 3;
+    const ConvPlace<D> at(w, lane);
     uint32_t j = 0, stage = 0, phase = 0;
     Piece piece;
     bool ok = true;
@@ -867,46 +907,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t flags = tile_scales[j % kScaleSlots].flags;
         const uint8_t* const src = smem + L::v + stage * L::kHalf;
         uint8_t* const dst = smem + L::v16 + buf * L::kV16;
-        uint32_t nan_rows = 0;
-        constexpr int kPanels = D / 64, kTimes = 4 * kPanels;
-#pragma unroll 1
-        for (int i = 0; i < kTimes; i += 2) {
-          uint4 codes[2];
-          int r[2], panel[2];
-          uint32_t odd = flags & 0xFFFFu;
+        uint32_t odd = flags & 0xFFFFu, nan_rows = 0;
+        uint4 next[2] = {at.load(src, 0), at.load(src, 1)};
+#pragma unroll 2
+        for (int i = 0; i < ConvPlace<D>::kTimes; i += 2) {
+          const uint4 codes[2] = {next[0], next[1]};
+          if (i + 2 < ConvPlace<D>::kTimes) next[0] = at.load(src, i + 2), next[1] = at.load(src, i + 3);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            // the combination of a panel and a pair of rows that these eight lanes have
-            const int combo = (i + x) * 4 + quarter, pair = combo / kPanels;
-            panel[x] = combo % kPanels;
-            r[x] = 32 * w + 8 * (pair >> 2) + ((pair & 3) ^ (other * 5));
-            const int c = (D == 64 ? 4 : panel[x] * 4) + piece_in;
-            codes[x] = *reinterpret_cast<const uint4*>(src + r[x] * 128 + ((c ^ (r[x] & 7)) << 4));
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x)  // NaN codes (0x7F and 0xFF): adding one to the lower seven bits reaches the eighth
+            // NaN codes (0x7F and 0xFF): adding one to the lower seven bits reaches the eighth
             odd |= ((codes[x].x & 0x7F7F7F7Fu) + 0x01010101u | (codes[x].y & 0x7F7F7F7Fu) + 0x01010101u |
                     (codes[x].z & 0x7F7F7F7Fu) + 0x01010101u | (codes[x].w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-          if (__any_sync(kFull, odd != 0u)) {
-            nan_rows |= clear_values(&codes[0], r[0], flags);
-            nan_rows |= clear_values(&codes[1], r[1], flags);
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t h[8];
-            half_pairs(codes[x].x, &h[0], &h[1]);
-            half_pairs(codes[x].y, &h[2], &h[3]);
-            half_pairs(codes[x].z, &h[4], &h[5]);
-            half_pairs(codes[x].w, &h[6], &h[7]);
-            uint8_t* const row = dst + panel[x] * (kTile * 128) + r[x] * 128;
-            *reinterpret_cast<uint4*>(row + (((2 * piece_in) ^ (r[x] & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(row + (((2 * piece_in + 1) ^ (r[x] & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+            at.store(dst, i + x, codes[x]);
           }
         }
-        __syncwarp();
+        if (__any_sync(kFull, odd != 0u)) nan_rows = convert_odd<D>(dst, src, w, lane, flags);
         // the codes have been read: the stage may be filled again
         if (lane == 0) ptx::mbar_arrive(bar(D == 128 ? L::vEmptyB : L::kEmptyB, stage));
-        nan_rows = __reduce_or_sync(kFull, nan_rows);
         if (lane == 0) reinterpret_cast<uint32_t*>(&tile_scales[j % kScaleSlots].nan)[w] = nan_rows;
         ptx::fence_proxy_async_smem();
         __syncwarp();
