@@ -31,9 +31,10 @@
 // every CTA takes an equal range of them, from lengths on the device.  A unit
 // that several CTAs share leaves its pieces in the workspace, and a second
 // kernel joins them.
-// The running maximum of a row goes by the products 2^t * vscale (t the score in
-// log2 units), so that P, which is multiplied with codes, keeps its bits; it is
-// raised when a P exceeds 2^8.  Sums are of unrounded f32 exponentials.
+// The reference of a row goes by the products 2^t * vscale (t the score in log2
+// units), so that P, which is multiplied with codes, keeps its bits: the largest
+// one of its first tile, raised when one could exceed 2^15 times that.  Sums are
+// of unrounded f32 exponentials.
 // Every wait is bounded (common.cuh); a role whose wait has run out leaves, and
 // then so do the others.
 #include <cuda_bf16.h>
@@ -57,7 +58,6 @@ constexpr int kConvWarp0 = 8, kLoadWarp = 12, kMmaWarp = 13, kPlanWarp = 14;
 // Registers a thread: 256 * 184 + 128 * 80 + 128 * 64 = 512 * 128.
 constexpr int kSoftmaxRegs = 184, kConvRegs = 80, kOtherRegs = 64;
 constexpr float kMinM = -3e38f;   // m stays finite, so that a score of -inf gives probability 0
-constexpr float kRaise = 8.f;     // P may reach 2^8 before m is raised
 constexpr float kNoScaleLog = -64.f;
 constexpr int kUnitSlots = 8, kScaleSlots = 8;
 constexpr int kUnitCost = 3;      // a unit's start and end, in steps
@@ -216,8 +216,18 @@ struct RowState {
   bool bad = false;  // sees a value that is NaN
 };
 
-// The largest of 32 columns (two groups of 16) of scores times c[] plus o[].
-__device__ __forceinline__ float chunk_max(const uint32_t (&r)[32], const float (&c)[2], const float (&o)[2]) {
+// What turns 32 scores (two groups of 16) into log2 probabilities x c + o, and
+// the groups' inverse value scales.  Masked scores are log2 probabilities.
+struct ChunkScale {
+  float2 c, o, vinv;
+  __device__ __forceinline__ ChunkScale(const TileScales& sc, int k, bool masked, float row_scale) {
+    const float2 key = reinterpret_cast<const float2*>(sc.key)[k];
+    c = masked ? make_float2(1.f, 1.f) : make_float2(key.x * row_scale, key.y * row_scale);
+    o = masked ? make_float2(0.f, 0.f) : reinterpret_cast<const float2*>(sc.vlog)[k];
+    vinv = reinterpret_cast<const float2*>(sc.vinv)[k];
+  }
+};
+__device__ __forceinline__ float chunk_max(const uint32_t (&r)[32], const ChunkScale& cs) {
   float top = -INFINITY;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
@@ -228,18 +238,19 @@ __device__ __forceinline__ float chunk_max(const uint32_t (&r)[32], const float 
       a = fmaxf(fmaxf(a, __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
       if (j + 2 < 16) b = fmaxf(fmaxf(b, __uint_as_float(v[j + 2])), __uint_as_float(v[j + 3]));
     }
-    top = fmaxf(top, fmaf(fmaxf(a, b), c[g], o[g]));
+    top = fmaxf(top, fmaf(fmaxf(a, b), g ? cs.c.y : cs.c.x, g ? cs.o.y : cs.o.x));
   }
   return top;
 }
-// Probabilities of 32 columns into tensor memory; adds their sum to l.
-__device__ __forceinline__ void chunk_exp(const uint32_t (&r)[32], const float (&c)[2], const float (&o)[2], const float* vinv,
-                                          float m, uint32_t p_tm, float& l) {
-  uint32_t h[16];
+// Probabilities of 32 scores over 2^m, as f16 pairs; the larger group's sum into
+// `most`.  Returns the sum over the value scales.
+__device__ __forceinline__ float chunk_exp(const uint32_t (&r)[32], const ChunkScale& cs, float m, uint32_t (&h)[16],
+                                           float& most) {
+  float l = 0.f;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const float off = o[g] - m;
-    const float2 cc = make_float2(c[g], c[g]), oo = make_float2(off, off);
+    const float c = g ? cs.c.y : cs.c.x, o = (g ? cs.o.y : cs.o.x) - m;
+    const float2 cc = make_float2(c, c), oo = make_float2(o, o);
     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
@@ -249,9 +260,11 @@ __device__ __forceinline__ void chunk_exp(const uint32_t (&r)[32], const float (
       const __half2 hv = __floats2half2_rn(e.x, e.y);
       h[g * 8 + j / 2] = *reinterpret_cast<const uint32_t*>(&hv);
     }
-    l = fmaf(sum.x + sum.y, vinv[g], l);
+    const float s = sum.x + sum.y;
+    most += s;
+    l = fmaf(s, g ? cs.vinv.y : cs.vinv.x, l);
   }
-  ptx::tmem_st_32x32b_x16(p_tm, h);
+  return l;
 }
 
 // Of a tile that not every row sees in full: log2 probabilities, -inf where the
@@ -288,64 +301,87 @@ __device__ __noinline__ void scale_outputs(uint32_t o_tm, float f) {
   }
 }
 
+// Raises a row's reference to the largest log2 probability of the chunks k to
+// end, rounded up (so that factors are powers of two), and scales what goes by
+// the old one: the outputs (if there are any) and the tile's probabilities
+// before chunk k.  Returns the new reference.
+template <int D>
+__device__ __noinline__ float raise_reference(uint32_t s_tm, uint32_t o_tm, const TileScales* sc, int chunk0, int k, int end,
+                                              bool masked, float row_scale, bool outputs, float m) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int i = k; i < end; ++i) {
+    uint32_t r[32];
+    ptx::tmem_ld_32x32b_x32(s_tm + i * 32, r);
+    ptx::tmem_wait_ld_regs(r);
+    top = fmaxf(top, chunk_max(r, ChunkScale(*sc, i, masked, row_scale)));
+  }
+  const float now = fmaxf(m, ceilf(top)), f = ex2(m - now);
+#pragma unroll 1
+  for (int i = chunk0; i < k; ++i) {
+    uint32_t h[16];
+    ptx::tmem_ld_32x32b_x16(s_tm + i * 16, h);
+    ptx::tmem_wait_ld_n(h);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+      const __half2 w = __floats2half2_rn(v.x * f, v.y * f);
+      h[j] = *reinterpret_cast<const uint32_t*>(&w);
+    }
+    ptx::tmem_st_32x32b_x16(s_tm + i * 16, h);
+  }
+  if (outputs) scale_outputs<D>(o_tm, f);
+  ptx::tmem_wait_st();
+  return now;
+}
+
 // A tile's scores to probabilities, `chunks` (1, 2 or 4) times 32 columns from
 // chunk0 on; the rest of the probabilities are zeros.  Probabilities lie over
 // the scores (16 columns for 32), written in order, so those of a chunk
-// overwrite scores that have been read.  The loops are rolled, and the scores
-// loaded twice: unrolled they wait for their instructions (the roles' loops
-// together do not fit the instruction cache then: 924 us where this takes 861).
+// overwrite scores that have been read.  No maximum is looked for: the sum of a
+// pair of chunks shows whether its probabilities stay within f16 (each below
+// 2^15); where one does not, and at a row's first tile, the reference is raised
+// and the pair done over.  (A pass for the maximum took a third of the
+// instructions.)  The loop is rolled: unrolled it waits for its instructions,
+// as the roles' loops together do not fit the instruction cache then.
 template <int D>
 __device__ __forceinline__ void softmax_tile(uint32_t s_tm, uint32_t o_tm, const TileScales& sc, int chunk0, int chunks,
                                              bool masked, int pos, int window, int len, int tile0, float row_scale, bool first,
                                              RowState& st) {
-  uint32_t r0[32], r1[32];
-  const auto scales = [&](int k, float (&c)[2], float (&o)[2]) {
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      c[g] = masked ? 1.f : sc.key[2 * k + g] * row_scale;
-      o[g] = masked ? 0.f : sc.vlog[2 * k + g];
-    }
-  };
   const int end = chunk0 + chunks;
   if (masked) mask_tile(s_tm, &sc, chunk0, end, pos, window, len, tile0, row_scale);
-  float top = -INFINITY, c[2], o[2];
-  const auto top_of = [&](const uint32_t (&r)[32], int k) {
-    scales(k, c, o);
-    top = fmaxf(top, chunk_max(r, c, o));
-  };
-  const auto exp_of = [&](const uint32_t (&r)[32], int k) {
-    scales(k, c, o);
-    chunk_exp(r, c, o, sc.vinv + 2 * k, st.m, s_tm + k * 16, st.l);
-  };
+  bool raised = false;
 #pragma unroll 1
-  for (int k = chunk0; k < end; k += 2) {
-    ptx::tmem_ld_32x32b_x32(s_tm + k * 32, r0);
-    if (k + 1 < end) ptx::tmem_ld_32x32b_x32(s_tm + (k + 1) * 32, r1);
-    ptx::tmem_wait_ld_regs(r0);
-    ptx::reg_fence(r1);
-    top_of(r0, k);
-    if (k + 1 < end) top_of(r1, k + 1);
-  }
-  ptx::tmem_ld_32x32b_x32(s_tm + chunk0 * 32, r0);
-  if (chunks > 1) ptx::tmem_ld_32x32b_x32(s_tm + (chunk0 + 1) * 32, r1);
-  if (__any_sync(kFull, top > st.m + kRaise)) {
-    const float m = fmaxf(st.m, top), f = ex2(st.m - m);
-    st.l *= f;
-    st.m = m;
-    if (!first) scale_outputs<D>(o_tm, f);  // (the products before this tile are done: its scores were issued after them)
-  }
-#pragma unroll 1
-  for (int k = chunk0; k < end; k += 2) {
-    ptx::tmem_wait_ld_regs(r0);
-    ptx::reg_fence(r1);
-    exp_of(r0, k);
-    if (k + 2 < end) ptx::tmem_ld_32x32b_x32(s_tm + (k + 2) * 32, r0);
-    if (k + 1 < end) exp_of(r1, k + 1);
-    if (k + 2 < end) ptx::tmem_ld_32x32b_x32(s_tm + (k + 3) * 32, r1);
+  for (int k = chunk0; k < end;) {
+    uint32_t r[32], h0[16], h1[16];
+    float most = 0.f, l;
+    ptx::tmem_ld_32x32b_x32(s_tm + k * 32, r);
+    {
+      const ChunkScale cs(sc, k, masked, row_scale);
+      ptx::tmem_wait_ld_regs(r);
+      l = chunk_exp(r, cs, st.m, h0, most);
+    }
+    if (k + 1 < end) {
+      ptx::tmem_ld_32x32b_x32(s_tm + (k + 1) * 32, r);
+      const ChunkScale cs(sc, k + 1, masked, row_scale);
+      ptx::tmem_wait_ld_regs(r);
+      l += chunk_exp(r, cs, st.m, h1, most);
+    }
+    if (__any_sync(kFull, !(most < 32768.f)) && !raised) {
+      const float m = raise_reference<D>(s_tm, o_tm, &sc, chunk0, k, end, masked, row_scale, !first, st.m);
+      st.l *= ex2(st.m - m);
+      st.m = m;
+      raised = true;
+      continue;
+    }
+    st.l += l;
+    ptx::tmem_st_32x32b_x16(s_tm + k * 16, h0);
+    if (k + 1 < end) ptx::tmem_st_32x32b_x16(s_tm + (k + 1) * 16, h1);
+    k += 2;
   }
   if (chunks < 4) {
     const uint32_t zeros[16] = {};
-#pragma unroll 1
+#pragma unroll
     for (int k = 0; k < 4; ++k)
       if (k < chunk0 || k >= end) ptx::tmem_st_32x32b_x16(s_tm + k * 16, zeros);
   }
