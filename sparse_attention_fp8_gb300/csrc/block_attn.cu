@@ -351,33 +351,53 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_tm, uint32_t o_tm, const
   const int end = chunk0 + chunks;
   if (masked) mask_tile(s_tm, &sc, chunk0, end, pos, window, len, tile0, row_scale);
   bool raised = false;
+  const auto raise = [&](int k) {
+    const float m = raise_reference<D>(s_tm, o_tm, &sc, chunk0, k, end, masked, row_scale, !first, st.m);
+    st.l *= ex2(st.m - m);
+    st.m = m;
+    raised = true;
+  };
+  if (chunks > 1) {
 #pragma unroll 1
-  for (int k = chunk0; k < end;) {
-    uint32_t r[32], h0[16], h1[16];
-    float most = 0.f, l;
-    ptx::tmem_ld_32x32b_x32(s_tm + k * 32, r);
-    {
-      const ChunkScale cs(sc, k, masked, row_scale);
-      ptx::tmem_wait_ld_regs(r);
-      l = chunk_exp(r, cs, st.m, h0, most);
-    }
-    if (k + 1 < end) {
+    for (int k = chunk0; k < end;) {
+      uint32_t r[32], h0[16], h1[16];
+      float most = 0.f, l;
+      ptx::tmem_ld_32x32b_x32(s_tm + k * 32, r);
+      {
+        const ChunkScale cs(sc, k, masked, row_scale);
+        ptx::tmem_wait_ld_regs(r);
+        l = chunk_exp(r, cs, st.m, h0, most);
+      }
       ptx::tmem_ld_32x32b_x32(s_tm + (k + 1) * 32, r);
-      const ChunkScale cs(sc, k + 1, masked, row_scale);
-      ptx::tmem_wait_ld_regs(r);
-      l += chunk_exp(r, cs, st.m, h1, most);
+      {
+        const ChunkScale cs(sc, k + 1, masked, row_scale);
+        ptx::tmem_wait_ld_regs(r);
+        l += chunk_exp(r, cs, st.m, h1, most);
+      }
+
+      if (__any_sync(kFull, !(most < 32768.f)) && !raised) {
+        raise(k);
+        continue;
+      }
+      st.l += l;
+      ptx::tmem_st_32x32b_x16(s_tm + k * 16, h0);
+      ptx::tmem_st_32x32b_x16(s_tm + (k + 1) * 16, h1);
+      k += 2;
     }
-    if (__any_sync(kFull, !(most < 32768.f)) && !raised) {
-      const float m = raise_reference<D>(s_tm, o_tm, &sc, chunk0, k, end, masked, row_scale, !first, st.m);
-      st.l *= ex2(st.m - m);
-      st.m = m;
-      raised = true;
-      continue;
+  } else {
+    uint32_t r[32], h[16];
+    float l, most;
+    while (true) {
+      most = 0.f;
+      ptx::tmem_ld_32x32b_x32(s_tm + chunk0 * 32, r);
+      const ChunkScale cs(sc, chunk0, masked, row_scale);
+      ptx::tmem_wait_ld_regs(r);
+      l = chunk_exp(r, cs, st.m, h, most);
+      if (!__any_sync(kFull, !(most < 32768.f)) || raised) break;
+      raise(chunk0);
     }
     st.l += l;
-    ptx::tmem_st_32x32b_x16(s_tm + k * 16, h0);
-    if (k + 1 < end) ptx::tmem_st_32x32b_x16(s_tm + (k + 1) * 16, h1);
-    k += 2;
+    ptx::tmem_st_32x32b_x16(s_tm + chunk0 * 16, h);
   }
   if (chunks < 4) {
     const uint32_t zeros[16] = {};
