@@ -135,6 +135,12 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile uin
   return wait_longer(bar, parity, abort_flag, site);
 }
 
+// The same for a thread alone.
+__device__ __forceinline__ bool wait_alone(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t site) {
+  if (ptx::mbar_test_wait(bar, parity)) return true;
+  return wait_bounded(bar, parity, abort_flag, &g_block_attn_watchdog, site);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -448,10 +454,12 @@ __device__ __forceinline__ float load_query(uint8_t* dst, int r, const __nv_bflo
   const int e = query_exponent(max(top2 >> 16, top2 & 0xFFFFu));
   if (write) {
     const float mul = __uint_as_float(__float_as_uint(power_of_two(e)) | sign);
+    uint4 next[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    if (q) next[0] = __ldg(piece), next[1] = __ldg(piece + 1);
 #pragma unroll 1
     for (int c = 0; c < D / 16; ++c) {
-      uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-      if (q) v[0] = __ldg(piece + 2 * c), v[1] = __ldg(piece + 2 * c + 1);
+      const uint4 v[2] = {next[0], next[1]};
+      if (q && c + 1 < D / 16) next[0] = __ldg(piece + 2 * c + 2), next[1] = __ldg(piece + 2 * c + 3);
       uint32_t h[8], l[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -865,82 +873,86 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == kMmaWarp) {
       // =========================== the products ===========================
+      // One thread waits for and issues all of them.
       constexpr uint32_t kIdescS = ptx::idesc_e4m3_f32(128, kTile);
       constexpr uint32_t kIdescO = ptx::idesc_f16_f32(128, D) | ptx::kIdescMnMajorB;
       const uint64_t q0 = ptx::smem_desc_sw128(base + L::q), k0 = ptx::smem_desc_sw128(base + L::k);
       const uint64_t v0 = ptx::smem_desc_mn16(base + L::v16, kTile * 128u);
-      uint32_t j0 = 0;                  // tiles before this piece
-      uint32_t np0 = 0, np1 = 0;        // outputs of each group so far
-      uint32_t nq[2] = {0u, 0u};
-      Piece piece;
-      bool ok = true;
+      if (ptx::elect_one()) {
+        Ring ks{0u, 0u, static_cast<uint32_t>(S)}, vs{0u, 0u, static_cast<uint32_t>(kScaleSlots)}, us{0u, 0u, static_cast<uint32_t>(kUnitSlots)};
+        uint32_t buf = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;  // f16 buffer; queries and probabilities of each group so far
+        bool ok = true;
 #pragma unroll 1
-      for (uint32_t n = 0; ok && get_piece(n, &piece); ++n) {
-        const int tiles = piece.tb - piece.ta;
-        const bool shared = piece.shared != 0;
-        const int count[2] = {shared ? tiles : (tiles + 1) / 2, shared ? tiles : tiles / 2};
-        const auto tile_of = [&](int g, int i) { return j0 + static_cast<uint32_t>(shared ? i : 2 * i + g); };
-        const auto scores = [&](int g, int i) {
-          const uint32_t j = tile_of(g, i), st = j % S;
-          if ((!shared || g == 0) && !wait(bar(L::kFullB, st), (j / S) & 1u, abort_flag, kSiteStageFull)) return false;
-          ptx::tc_fence_after();
-          const uint64_t a = q0 + static_cast<uint64_t>((shared ? g : 0) * (L::qBytes >> 4));
-          const uint64_t b = k0 + static_cast<uint64_t>(st * (L::kHalf >> 4));
-          if (ptx::elect_one()) {
+        while (true) {
+          if (!wait_alone(bar(L::unitFullB, us.idx), us.phase, abort_flag, kSiteQEmpty)) break;
+          const Piece& piece = *slot_of(us.idx);
+          const int tiles = piece.tb - piece.ta;
+          const bool shared = piece.shared != 0, last = piece.row0 < 0;
+          ptx::mbar_arrive(bar(L::unitEmptyB, us.idx));
+          us.next();
+          if (last) break;
+          const int count0 = shared ? tiles : (tiles + 1) / 2, count1 = shared ? tiles : tiles / 2;
+          // Scores of group g's next tile; its tile's place is free after both groups' (its own) scores.
+          const auto scores = [&](int g) {
+            if ((!shared || g == 0) && !wait_alone(bar(L::kFullB, ks.idx), ks.phase, abort_flag, kSiteStageFull)) return false;
+            ptx::tc_fence_after();
+            const uint64_t a = q0 + static_cast<uint64_t>((shared ? g : 0) * (L::qBytes >> 4));
+            const uint64_t b = k0 + static_cast<uint64_t>(ks.idx * (L::kHalf >> 4));
+            const uint32_t d = tmem + g * kTile;
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
               for (int kk = 0; kk < D / 32; ++kk)
-                ptx::mma_f8f6f4(tmem + g * kTile, a + part * (D == 128 ? L::kHalf >> 4 : 4u) + 2ull * kk, b + 2ull * kk,
-                                kIdescS, part + kk > 0 ? 1u : 0u);
+                ptx::mma_f8f6f4(d, a + part * (D == 128 ? L::kHalf >> 4 : 4u) + 2ull * kk, b + 2ull * kk, kIdescS,
+                                part + kk > 0 ? 1u : 0u);
             ptx::mma_commit(bar(L::sFullB, g));
-            if (!shared || g == 1) ptx::mma_commit(bar(L::kEmptyB, st));
-          }
-          __syncwarp();
-          return true;
-        };
-        const auto outputs = [&](int g, int i, int n_g) {
-          const uint32_t j = tile_of(g, i), buf = j & 1u;
-          if ((!shared || g == 0) &&
-              !wait(bar(L::v16FullB, j % kScaleSlots), (j / kScaleSlots) & 1u, abort_flag, kSiteStageFull))
-            return false;
-          if (!wait(bar(L::pFullB, g), (g ? np1 : np0) & 1u, abort_flag, kSiteAccEmpty)) return false;
-          if (g) ++np1; else ++np0;
-          ptx::tc_fence_after();
-          const uint64_t b = v0 + static_cast<uint64_t>(buf * (L::kV16 >> 4));
-          if (ptx::elect_one()) {
+            if (!shared || g == 1) {
+              ptx::mma_commit(bar(L::kEmptyB, ks.idx));
+              ks.next();
+            }
+            return true;
+          };
+          // Outputs of group g's oldest tile, the i-th of n_g.
+          const auto outputs = [&](int g, int i, int n_g) {
+            if ((!shared || g == 0) && !wait_alone(bar(L::v16FullB, vs.idx), vs.phase, abort_flag, kSiteStageFull)) return false;
+            if (!wait_alone(bar(L::pFullB, g), (g ? np1 : np0) & 1u, abort_flag, kSiteAccEmpty)) return false;
+            if (g) ++np1; else ++np0;
+            ptx::tc_fence_after();
+            const uint64_t b = v0 + static_cast<uint64_t>(buf * (L::kV16 >> 4));
+            const uint32_t d = tmem + 2 * kTile + g * 128, a = tmem + g * kTile;
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
-              ptx::mma_f16_ts(tmem + 2 * kTile + g * 128, tmem + g * kTile + 8 * kk, b + static_cast<uint64_t>(kk * (2048 >> 4)),
-                              kIdescO, i + kk > 0 ? 1u : 0u);
-            if (!shared || g == 1) ptx::mma_commit(bar(L::v16EmptyB, buf));
+              ptx::mma_f16_ts(d, a + 8 * kk, b + static_cast<uint64_t>(kk * (2048 >> 4)), kIdescO, i + kk > 0 ? 1u : 0u);
+            if (!shared || g == 1) {
+              ptx::mma_commit(bar(L::v16EmptyB, buf));
+              buf ^= 1u;
+              vs.next();
+            }
             if (i + 1 == n_g) ptx::mma_commit(bar(L::oFullB, g));
+            return true;
+          };
+          ok = wait_alone(bar(L::qFullB, 0), nq0 & 1u, abort_flag, kSiteQFull);
+          ++nq0;
+          if (ok && shared) {
+            ok = wait_alone(bar(L::qFullB, 1), nq1 & 1u, abort_flag, kSiteQFull);
+            ++nq1;
           }
-          __syncwarp();
-          return true;
-        };
-        ok = wait(bar(L::qFullB, 0), nq[0] & 1u, abort_flag, kSiteQFull);
-        ++nq[0];
-        if (ok && shared) {
-          ok = wait(bar(L::qFullB, 1), nq[1] & 1u, abort_flag, kSiteQFull);
-          ++nq[1];
-        }
-        // A group's outputs of a tile, then its scores of the next.
+          // A group's outputs of a tile, then its scores of the next.
 #pragma unroll 1
-        for (int i = -1; ok && i < count[0]; ++i) {
+          for (int i = -1; ok && i < count0; ++i) {
 #pragma unroll 1
-          for (int g = 0; ok && g < 2; ++g) {
-            const int n_g = g ? count[1] : count[0];
-            if (i >= 0 && i < n_g) ok = outputs(g, i, n_g);
-            if (ok && i + 1 < n_g) ok = scores(g, i + 1);
+            for (int g = 0; ok && g < 2; ++g) {
+              const int n_g = g ? count1 : count0;
+              if (i >= 0 && i < n_g) ok = outputs(g, i, n_g);
+              if (ok && i + 1 < n_g) ok = scores(g);
+            }
           }
+          if (!ok) break;
         }
-        j0 += tiles;
-      }
-      __syncwarp();
-      if (*abort_flag && lane == 0) {
-        ptx::mma_commit(bar(L::drainB));
-        wait_drain(bar(L::drainB), 0, &g_block_attn_watchdog);
+        if (*abort_flag) {  // products in flight must end before the memory is given back
+          ptx::mma_commit(bar(L::drainB));
+          wait_drain(bar(L::drainB), 0, &g_block_attn_watchdog);
+        }
       }
       __syncwarp();
     }
@@ -1096,25 +1108,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t a[32];
             ptx::tmem_ld_32x32b_x32(o_tm + c, a);
             ptx::tmem_wait_ld_regs(a);
-            if (!live) continue;
-            if (st.bad) {
+            if (live) {
+              if (st.bad) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) a[k] = 0x7FC00000u;
-            }
-            if (piece.slot < 0) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 8) {
-                uint32_t w[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  w[x] = bf16_pair(__uint_as_float(a[k + 2 * x]) * inv * ref, __uint_as_float(a[k + 2 * x + 1]) * inv * ref);
-                *reinterpret_cast<uint4*>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int k = 0; k < 32; ++k) a[k] = 0x7FC00000u;
               }
-            } else {
+              if (piece.slot < 0) {
 #pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                __stcg(reinterpret_cast<uint4*>(ws + wrow * D + c + k), make_uint4(a[k], a[k + 1], a[k + 2], a[k + 3]));
+                for (int k = 0; k < 32; k += 8) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int x = 0; x < 4; ++x)
+                    w[x] = bf16_pair(__uint_as_float(a[k + 2 * x]) * inv * ref, __uint_as_float(a[k + 2 * x + 1]) * inv * ref);
+                  *reinterpret_cast<uint4*>(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 32; k += 4)
+                  __stcg(reinterpret_cast<uint4*>(ws + wrow * D + c + k), make_uint4(a[k], a[k + 1], a[k + 2], a[k + 3]));
+              }
             }
+            __syncwarp();  // (the next load is the whole warp's)
           }
           if (live) {
             if (piece.slot >= 0)
@@ -1140,9 +1154,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ref = sums[0].z;  // (group 0 has a tile of every piece)
           const float f = ex2(st.m - m);
-          // Outputs of a row, 32 channels: copy_lanes / 8 of them a thread.
-          const int share = copy_lanes / 8, tid = threadIdx.x;
-          const int to_row = tid / (256 / copy_lanes), to_col = tid % (256 / copy_lanes) * share;
+          // A round takes as many channels as 32 KB hold of all copies' rows in use,
+          // and a thread puts out `share` of them for one row.
+          const int pad = D == 128 && rows <= 8 ? 8 : rows <= 16 ? 16 : copy_lanes;  // (at most D channels)
+          const int width = 32 * copy_lanes / pad, share = copy_lanes / 8, tid = threadIdx.x;
+          const int to_row = tid / (256 / pad), to_col = tid % (256 / pad) * share;
           const int to_index = to_row / p.group, to_head = piece.head * p.group + to_row - to_index * p.group;
           const bool to_live = to_row < rows;
           // (the row that this thread puts out is another one than its own: its sum through the stage)
@@ -1162,32 +1178,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                   to_ml.y == 0.f ? -INFINITY : (to_ml.x + log2f(to_ml.y)) * 0.6931471805599453f;
           }
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t a[32];
-            if (count > 0) {
-              ptx::tmem_ld_32x32b_x32(o_tm + c, a);
-              ptx::tmem_wait_ld_regs(a);
-            }
+          for (int c = 0; c < D; c += width) {
             if (!meet()) goto out;  // (what stood there has been read)
-            float* const mine = stage + (g * kTile + i) * 32;
+#pragma unroll 1
+            for (int x = 0; x < width; x += 32) {
+              uint32_t a[32];
+              if (count > 0) {
+                ptx::tmem_ld_32x32b_x32(o_tm + c + x, a);
+                ptx::tmem_wait_ld_regs(a);
+              }
+              if (r < pad) {
+                float* const mine = stage + (copy * pad + r) * width + x;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (count > 0)
-                v = make_float4(__uint_as_float(a[4 * k]) * f, __uint_as_float(a[4 * k + 1]) * f,
-                                __uint_as_float(a[4 * k + 2]) * f, __uint_as_float(a[4 * k + 3]) * f);
-              if (st.bad) v = make_float4(NAN, NAN, NAN, NAN);
-              *reinterpret_cast<float4*>(mine + ((k ^ (i & 7)) << 2)) = v;
+                for (int k = 0; k < 8; ++k) {
+                  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                  if (count > 0)
+                    v = make_float4(__uint_as_float(a[4 * k]) * f, __uint_as_float(a[4 * k + 1]) * f,
+                                    __uint_as_float(a[4 * k + 2]) * f, __uint_as_float(a[4 * k + 3]) * f);
+                  if (st.bad) v = make_float4(NAN, NAN, NAN, NAN);
+                  *reinterpret_cast<float4*>(mine + ((k ^ (r & 7)) << 2)) = v;
+                }
+              }
+              __syncwarp();  // (the next load is the whole warp's)
             }
             if (!meet()) goto out;
             if (to_live) {
 #pragma unroll 1
               for (int x = to_col; x < to_col + share; x += 4) {
+                const float* const from = stage + to_row * width + (x & ~31) + (((x >> 2 & 7) ^ (to_row & 7)) << 2);
                 float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
+#pragma unroll 2
                 for (int k = 0; k < copies; ++k) {
-                  const float4 v = *reinterpret_cast<const float4*>(stage + (k * copy_lanes + to_row) * 32 +
-                                                                    (((x >> 2) ^ (to_row & 7)) << 2));
+                  const float4 v = *reinterpret_cast<const float4*>(from + k * pad * width);
                   sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
                 }
                 if (piece.slot >= 0)
