@@ -19,6 +19,8 @@
 // DRAM bound: every value is read and written once.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "rows.cuh"
 
 namespace fp8idx {
@@ -107,22 +109,28 @@ __device__ __forceinline__ float row_sum(float v) {
 // are rotated, else halves of the rotated part.
 template <int TYPE, int L, bool PAIRS>
 __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(const NormRopeParams p) {
-  constexpr int kRows = 32 / L, kBatch = 4;  // rows that a warp holds side by side, and of those in flight
+  constexpr int kRows = 32 / L, kBatch = 2;  // rows that a warp holds side by side, and of those in flight
   constexpr int kItem = TYPE == kRowF32 ? 4 : 2;
   const int lane = threadIdx.x & 31, sub = lane % L;
   const uint32_t warp = blockIdx.x * (kNormRopeThreads / 32) + (threadIdx.x >> 5);
-  const uint32_t per_token = static_cast<uint32_t>(p.chunks[0] + p.chunks[1]);
-  const uint32_t t = warp / per_token;
+  const uint32_t t = warp / static_cast<uint32_t>(p.chunks);
   if (t >= static_cast<uint32_t>(p.tokens)) return;
-  int chunk = static_cast<int>(warp - t * per_token);
-  const int side = chunk >= p.chunks[0] ? 1 : 0;
-  chunk -= side ? p.chunks[0] : 0;
   const int32_t position = __ldg(p.positions + t);
   if (position < 0) return;
   const bool live = sub < p.dim / 8;
-  const int first = chunk * p.per * kRows + lane / L, heads = p.heads[side];
-  const uint8_t* x = static_cast<const uint8_t*>(p.x[side]) + t * p.x_token[side] + sub * 8 * kItem;
-  uint8_t* y = static_cast<uint8_t*>(p.y[side]) + t * p.y_token[side] + sub * 8 * kItem;
+  // The warp's groups of rows (queries', then keys').
+  const int chunk = static_cast<int>(warp - t * p.chunks), from = chunk * p.per, to = min(from + p.per, p.groups[0] + p.groups[1]);
+  Raw8<TYPE> raw[kBatch] = {};
+  const auto load = [&](int side, int at, int end) {
+    const uint8_t* const x = static_cast<const uint8_t*>(p.x[side]) + t * p.x_token[side] + sub * 8 * kItem;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = (at + i) * kRows + lane / L;
+      if (live && at + i < end && h < p.heads[side]) raw[i].load(x + h * p.x_head[side]);
+    }
+  };
+  const int first_side = from >= p.groups[0] ? 1 : 0;
+  load(first_side, first_side ? from - p.groups[0] : from, first_side ? to - p.groups[0] : min(to, p.groups[0]));
 
   // The rotation of this lane's values: its first value's place in the rotated part.
   const int rel = sub * 8 - p.rot_start, half = p.rot / 2;
@@ -151,58 +159,184 @@ __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(const NormR
       sn[i + 4] = upper ? s4[i] : -s;
     }
   }
-  float w[8], b[8];
+#pragma unroll 1
+  for (int side = first_side; side < 2; ++side) {
+    const int base = side ? p.groups[0] : 0, end = min(to - base, p.groups[side]), begin = max(from - base, 0);
+    if (begin >= end) continue;
+    float w[8], b[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    w[i] = live && p.weight[side] ? __ldg(p.weight[side] + sub * 8 + i) : 1.f;
-    b[i] = live && p.bias[side] ? __ldg(p.bias[side] + sub * 8 + i) : 0.f;
+    for (int i = 0; i < 8; ++i) {
+      w[i] = live && p.weight[side] ? __ldg(p.weight[side] + sub * 8 + i) : 1.f;
+      b[i] = live && p.bias[side] ? __ldg(p.bias[side] + sub * 8 + i) : 0.f;
+    }
+    uint8_t* const y = static_cast<uint8_t*>(p.y[side]) + t * p.y_token[side] + sub * 8 * kItem;
+#pragma unroll 1
+    for (int at = begin; at < end; at += kBatch) {
+      if (at > begin || side != first_side) load(side, at, end);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (at + i >= end) break;  // (the same for the whole warp)
+        const int h = (at + i) * kRows + lane / L;
+        float v[8];
+        raw[i].values(v);
+        if (p.norm == kNormLayer) {
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum += v[j];
+          const float mean = row_sum<L>(sum) * p.inv_dim;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = live ? v[j] - mean : 0.f;
+        }
+        if (p.norm != kNormNone) {
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
+          const float r = rsqrtf(fmaf(row_sum<L>(sum), p.inv_dim, p.eps));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j] * r, w[j], b[j]);
+        }
+        float out[8];
+        if constexpr (PAIRS) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float a = v[2 * j], c = v[2 * j + 1];
+            out[2 * j] = turns ? fmaf(a, cs[j], -(c * sn[j])) : a;
+            out[2 * j + 1] = turns ? fmaf(c, cs[j], a * sn[j]) : c;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float other = __shfl_sync(kFull, v[j], partner);
+            out[j] = turns ? fmaf(v[j], cs[j], other * sn[j]) : v[j];
+          }
+        }
+        if (live && h < p.heads[side]) store8<TYPE>(y + h * p.y_head[side], out);
+      }
+    }
+  }
+}
+
+namespace {
+// Four values as they lie in memory.
+template <int TYPE>
+struct Raw4 {
+  using Word = typename std::conditional<TYPE == kRowF32, uint4, uint2>::type;
+  Word v;
+  __device__ __forceinline__ void load(const uint8_t* src) { v = __ldcs(reinterpret_cast<const Word*>(src)); }
+  __device__ __forceinline__ void values(float2 (&x)[2]) const {
+    if constexpr (TYPE == kRowF32) {
+      x[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+      x[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+    } else if constexpr (TYPE == kRowBf16) {
+      x[0] = make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+      x[1] = make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+    } else {
+      x[0] = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+      x[1] = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+    }
+  }
+  __device__ __forceinline__ void set(const float2 (&x)[2]) {
+    if constexpr (TYPE == kRowF32) {
+      v = make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x), __float_as_uint(x[1].y));
+    } else if constexpr (TYPE == kRowBf16) {
+      const __nv_bfloat162 a = __float22bfloat162_rn(x[0]), b = __float22bfloat162_rn(x[1]);
+      v = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+      const __half2 a = __float22half2_rn(x[0]), b = __float22half2_rn(x[1]);
+      v = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+  }
+};
+__device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 minus(float2 v) { return make_float2(-v.x, -v.y); }
+}  // namespace
+
+// Halves of the whole head, 8 * L elements: a lane has four values of each half,
+// so pairs meet in it, and arithmetic goes two values an instruction.
+template <int TYPE, int L>
+__global__ void __launch_bounds__(kNormRopeThreads) norm_rope_whole_kernel(const NormRopeParams p) {
+  constexpr int kRows = 32 / L, kBatch = 4;
+  constexpr int kPiece = TYPE == kRowF32 ? 16 : 8, kHalf = L * kPiece;  // bytes of four values, of half a row
+  const int lane = threadIdx.x & 31, sub = lane % L;
+  const uint32_t warp = blockIdx.x * (kNormRopeThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t t = warp / static_cast<uint32_t>(p.chunks);
+  if (t >= static_cast<uint32_t>(p.tokens)) return;
+  const int32_t position = __ldg(p.positions + t);
+  if (position < 0) return;
+  const int chunk = static_cast<int>(warp - t * p.chunks), from = chunk * p.per, to = min(from + p.per, p.groups[0] + p.groups[1]);
+  float2 cs[2], sn[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    rotation(position, __ldg(p.inv_freq + sub * 4 + 2 * i), p.rope_scale, &cs[i].x, &sn[i].x);
+    rotation(position, __ldg(p.inv_freq + sub * 4 + 2 * i + 1), p.rope_scale, &cs[i].y, &sn[i].y);
   }
 #pragma unroll 1
-  for (int at = 0; at < p.per; at += kBatch) {
-    Raw8<TYPE> raw[kBatch] = {};
+  for (int side = from >= p.groups[0] ? 1 : 0; side < 2; ++side) {
+    const int base = side ? p.groups[0] : 0, end = min(to - base, p.groups[side]), begin = max(from - base, 0);
+    if (begin >= end) continue;
+    float2 w[2][2], b[2][2];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int h = first + (at + i) * kRows;
-      if (live && at + i < p.per && h < heads) raw[i].load(x + h * p.x_head[side]);
+    for (int i = 0; i < 8; ++i) {
+      const int e = (i / 4) * 4 * L + sub * 4 + i % 4;
+      const float wi = p.weight[side] ? __ldg(p.weight[side] + e) : 1.f, bi = p.bias[side] ? __ldg(p.bias[side] + e) : 0.f;
+      float2 &w2 = w[i / 4][i % 4 / 2], &b2 = b[i / 4][i % 4 / 2];
+      (i % 2 ? w2.y : w2.x) = wi;
+      (i % 2 ? b2.y : b2.x) = bi;
     }
+    const int heads = p.heads[side];
+    const uint8_t* x = static_cast<const uint8_t*>(p.x[side]) + t * p.x_token[side] + sub * kPiece;
+    uint8_t* y = static_cast<uint8_t*>(p.y[side]) + t * p.y_token[side] + sub * kPiece;
+    int h = begin * kRows + lane / L;
+    x += h * p.x_head[side];
+    y += h * p.y_head[side];
+    const int64_t x_step = kRows * p.x_head[side], y_step = kRows * p.y_head[side];
+#pragma unroll 1
+    for (int at = begin; at < end; at += kBatch) {
+      Raw4<TYPE> raw[kBatch][2] = {};
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int h = first + (at + i) * kRows;
-      if (at + i >= p.per || first - lane / L + (at + i) * kRows >= heads) break;  // (the same for the whole warp)
-      float v[8];
-      raw[i].values(v);
-      if (p.norm == kNormLayer) {
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum += v[j];
-        const float mean = row_sum<L>(sum) * p.inv_dim;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = live ? v[j] - mean : 0.f;
-      }
-      if (p.norm != kNormNone) {
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
-        const float r = rsqrtf(fmaf(row_sum<L>(sum), p.inv_dim, p.eps));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j] * r, w[j], b[j]);
-      }
-      float out[8];
-      if constexpr (PAIRS) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float a = v[2 * j], c = v[2 * j + 1];
-          out[2 * j] = turns ? fmaf(a, cs[j], -(c * sn[j])) : a;
-          out[2 * j + 1] = turns ? fmaf(c, cs[j], a * sn[j]) : c;
+      for (int i = 0; i < kBatch; ++i)
+        if (at + i < end && h + i * kRows < heads) {
+          raw[i][0].load(x + i * x_step);
+          raw[i][1].load(x + i * x_step + kHalf);
         }
-      } else {
+      x += kBatch * x_step;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float other = __shfl_sync(kFull, v[j], partner);
-          out[j] = turns ? fmaf(v[j], cs[j], other * sn[j]) : v[j];
+      for (int i = 0; i < kBatch; ++i) {
+        if (at + i >= end) break;  // (the same for the whole warp)
+        float2 v[2][2];
+        raw[i][0].values(v[0]);
+        raw[i][1].values(v[1]);
+        if (p.norm == kNormLayer) {
+          const float2 sum = __fadd2_rn(__fadd2_rn(v[0][0], v[0][1]), __fadd2_rn(v[1][0], v[1][1]));
+          const float2 mean = twice(-row_sum<L>(sum.x + sum.y) * p.inv_dim);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j / 2][j % 2] = __fadd2_rn(v[j / 2][j % 2], mean);
         }
+        if (p.norm != kNormNone) {
+          float2 sum = __fmul2_rn(v[0][0], v[0][0]);
+#pragma unroll
+          for (int j = 1; j < 4; ++j) sum = __ffma2_rn(v[j / 2][j % 2], v[j / 2][j % 2], sum);
+          const float2 r = twice(rsqrtf(fmaf(row_sum<L>(sum.x + sum.y), p.inv_dim, p.eps)));
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[j / 2][j % 2] = __ffma2_rn(__fmul2_rn(v[j / 2][j % 2], r), w[j / 2][j % 2], b[j / 2][j % 2]);
+        }
+        float2 out[2][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          out[0][j] = __ffma2_rn(v[0][j], cs[j], minus(__fmul2_rn(v[1][j], sn[j])));
+          out[1][j] = __ffma2_rn(v[1][j], cs[j], __fmul2_rn(v[0][j], sn[j]));
+        }
+        if (h < heads) {
+          Raw4<TYPE> o;
+          o.set(out[0]);
+          __stcs(reinterpret_cast<typename Raw4<TYPE>::Word*>(y), o.v);
+          o.set(out[1]);
+          __stcs(reinterpret_cast<typename Raw4<TYPE>::Word*>(y + kHalf), o.v);
+        }
+        h += kRows;
+        y += y_step;
       }
-      if (live && h < heads) store8<TYPE>(y + h * p.y_head[side], out);
     }
   }
 }
@@ -214,7 +348,9 @@ NormRopeKernel norm_rope_instance(bool pairs) {
   return pairs ? norm_rope_kernel<TYPE, L, true> : norm_rope_kernel<TYPE, L, false>;
 }
 template <int TYPE>
-NormRopeKernel norm_rope_instance(int lanes, bool pairs) {
+NormRopeKernel norm_rope_instance(int lanes, bool pairs, bool whole) {
+  if (whole && !pairs)
+    return lanes == 8 ? norm_rope_whole_kernel<TYPE, 8> : lanes == 16 ? norm_rope_whole_kernel<TYPE, 16> : norm_rope_whole_kernel<TYPE, 32>;
   return lanes == 8 ? norm_rope_instance<TYPE, 8>(pairs)
          : lanes == 16 ? norm_rope_instance<TYPE, 16>(pairs) : norm_rope_instance<TYPE, 32>(pairs);
 }
@@ -222,17 +358,17 @@ NormRopeKernel norm_rope_instance(int lanes, bool pairs) {
 
 cudaError_t launch_norm_rope(NormRopeParams& p, int row_type, bool pairs, int sms, cudaStream_t stream) {
   const int lanes = p.dim <= 64 ? 8 : p.dim <= 128 ? 16 : 32, rows = 32 / lanes;
-  const int groups[2] = {(p.heads[0] + rows - 1) / rows, (p.heads[1] + rows - 1) / rows};
-  // Heads that a warp walks: all of a token's once that leaves every SM 64 warps.
-  const int64_t all = static_cast<int64_t>(p.tokens) * (groups[0] + groups[1]);
-  const int most = groups[0] > groups[1] ? groups[0] : groups[1];
-  const int64_t per = all / (64 * sms);
-  p.per = static_cast<int32_t>(per < 1 ? 1 : per > most ? most : per);
-  for (int i = 0; i < 2; ++i) p.chunks[i] = (groups[i] + p.per - 1) / p.per;
-  const int64_t warps = static_cast<int64_t>(p.tokens) * (p.chunks[0] + p.chunks[1]);
-  const NormRopeKernel kern = row_type == kRowBf16  ? norm_rope_instance<kRowBf16>(lanes, pairs)
-                              : row_type == kRowF16 ? norm_rope_instance<kRowF16>(lanes, pairs)
-                                                    : norm_rope_instance<kRowF32>(lanes, pairs);
+  for (int i = 0; i < 2; ++i) p.groups[i] = (p.heads[i] + rows - 1) / rows;
+  // Groups that a warp walks: a whole token's once that leaves every SM 64 warps.
+  const int groups = p.groups[0] + p.groups[1];
+  const int64_t per = static_cast<int64_t>(p.tokens) * groups / (64 * sms);
+  p.per = static_cast<int32_t>(per < 1 ? 1 : per > groups ? groups : per);
+  p.chunks = (groups + p.per - 1) / p.per;
+  const int64_t warps = static_cast<int64_t>(p.tokens) * p.chunks;
+  const bool whole = p.rot == p.dim && p.dim == 8 * lanes;
+  const NormRopeKernel kern = row_type == kRowBf16  ? norm_rope_instance<kRowBf16>(lanes, pairs, whole)
+                              : row_type == kRowF16 ? norm_rope_instance<kRowF16>(lanes, pairs, whole)
+                                                    : norm_rope_instance<kRowF32>(lanes, pairs, whole);
   constexpr int kWarps = kNormRopeThreads / 32;
   kern<<<static_cast<unsigned>((warps + kWarps - 1) / kWarps), kNormRopeThreads, 0, stream>>>(p);
   return cudaGetLastError();

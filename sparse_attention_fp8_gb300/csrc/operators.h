@@ -70,9 +70,9 @@ struct NormRopeParams {
   int32_t tokens, dim, rot, rot_start, norm;
   int32_t heads[2];
   float eps, inv_dim, rope_scale;
-  // set by the launcher: groups of heads side by side that a warp walks, and
-  // warps per token
-  int32_t per, chunks[2];
+  // set by the launcher: groups of heads side by side, how many of them a warp
+  // walks, and warps per token
+  int32_t groups[2], per, chunks;
 };
 cudaError_t launch_norm_rope(NormRopeParams& p, int row_type, bool pairs, int sms, cudaStream_t stream);
 
