@@ -359,9 +359,9 @@ NormRopeKernel norm_rope_instance(int lanes, bool pairs, bool whole) {
 cudaError_t launch_norm_rope(NormRopeParams& p, int row_type, bool pairs, int sms, cudaStream_t stream) {
   const int lanes = p.dim <= 64 ? 8 : p.dim <= 128 ? 16 : 32, rows = 32 / lanes;
   for (int i = 0; i < 2; ++i) p.groups[i] = (p.heads[i] + rows - 1) / rows;
-  // Groups that a warp walks: a whole token's once that leaves every SM 64 warps.
+  // Groups that a warp walks: a whole token's once that leaves every SM 24 warps.
   const int groups = p.groups[0] + p.groups[1];
-  const int64_t per = static_cast<int64_t>(p.tokens) * groups / (64 * sms);
+  const int64_t per = static_cast<int64_t>(p.tokens) * groups / (24 * sms);
   p.per = static_cast<int32_t>(per < 1 ? 1 : per > groups ? groups : per);
   p.chunks = (groups + p.per - 1) / p.per;
   const int64_t warps = static_cast<int64_t>(p.tokens) * p.chunks;
