@@ -1,6 +1,7 @@
 """Plain CPU definitions of the operators around the indexer: step tables,
-the quantising paged store and the attention over selected positions
-(numpy, 64 bits, loops where they are clearest).  Test infrastructure only.
+head norms with rotation, the quantising paged stores, the attention over
+selected positions and over all of them (numpy, 64 bits, loops where they are
+clearest).  Test infrastructure only.
 """
 from __future__ import annotations
 
@@ -158,4 +159,137 @@ def sparse_attention(q, cache, indices, block_tables, block_size, scale, next_n=
                 most = (w * np.abs(sc[:, 1])).max() if by_product else w.max() * np.abs(sc[:, 1]).max()
                 floor[r, h] = most * np.abs(codes[:, D:]).sum(0)
                 sabs[r, h] = (np.abs(scale) * (np.abs(key) @ np.abs(q[r, h]))).max()
+    return out, lse, mag, floor, sabs
+
+
+def head_norm_rope(x, positions, inv_freq, norm=None, weight=None, bias=None, eps=1e-6, interleaved=False, rot_start=0,
+                   rope_scale=1.0):
+    """x [T, heads, D] -> [T, heads, D] f64 (rows with a negative position are
+    as if at position 0), and the sum of |terms| of each output."""
+    y = np.asarray(x, np.float64).copy()
+    D = y.shape[-1]
+    if norm == "layer":
+        y -= y.mean(-1, keepdims=True)
+    if norm is not None:
+        y /= np.sqrt((y**2).mean(-1, keepdims=True) + eps)
+    terms = np.abs(y)
+    if weight is not None:
+        y, terms = y * weight, terms * np.abs(weight)
+    if bias is not None:
+        y, terms = y + bias, terms + np.abs(bias)
+    half = len(inv_freq)
+    angle = np.maximum(np.asarray(positions, np.float64), 0)[:, None] * np.asarray(inv_freq, np.float64)
+    c, s = np.cos(angle) * rope_scale, np.sin(angle) * rope_scale
+    for i in range(half):
+        a, b = (rot_start + 2 * i, rot_start + 2 * i + 1) if interleaved else (rot_start + i, rot_start + half + i)
+        assert b < D
+        ya, yb, ta, tb = (z[..., j].copy() for z in (y, terms) for j in (a, b))
+        ci, si = c[:, i, None], s[:, i, None]
+        y[..., a], y[..., b] = ya * ci - yb * si, yb * ci + ya * si
+        terms[..., a], terms[..., b] = (ta + tb) * abs(rope_scale), (tb + ta) * abs(rope_scale)
+    return y, terms
+
+
+def block_page_bytes(block_size, dim):
+    return block_size * 2 * dim + 16
+
+
+def _e4m3(y):
+    """f32 values -> codes (rounded to nearest even, saturating, NaN kept)."""
+    y = np.ascontiguousarray(np.clip(np.asarray(y, np.float32), -448, 448))
+    return torch.from_numpy(y).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+
+
+def block_runs(slots, num_slots, block_size):
+    """(first row, rows) of each run of consecutive slots in one block."""
+    out, t = [], 0
+    while t < len(slots):
+        if not 0 <= slots[t] < num_slots:
+            t += 1
+            continue
+        n = 1
+        while (t + n < len(slots) and slots[t + n] == slots[t] + n and slots[t + n] % block_size != 0
+               and slots[t + n] < num_slots):
+            n += 1
+        out.append((t, n))
+        t += n
+    return out
+
+
+def store_blocks(cache, slots, k, v, block_size):
+    """cache [num_blocks, kv_heads, page] u8, changed in place; k, v [T, kv_heads, D] f32."""
+    D, values = k.shape[-1], e4m3_values().astype(np.float32)
+    for t, n in block_runs([int(s) for s in slots], cache.shape[0] * block_size, block_size):
+        b, o = divmod(int(slots[t]), block_size)
+        for h in range(cache.shape[1]):
+            page = cache[b, h]
+            rows = page[: block_size * 2 * D].reshape(block_size, 2, D)
+            at = block_size * 2 * D
+            scales = page[at: at + 8].copy().view(np.float32)
+            for part, src in enumerate((k, v)):
+                x = np.asarray(src[t: t + n, h], np.float32)
+                fine = np.isfinite(x)
+                top = np.abs(x[fine]).max() if fine.any() else np.float32(0)
+                need = np.float32(top) / np.float32(448)
+                scale = need
+                if o > 0 and scales[part] != 0:
+                    scale = scales[part]
+                    shift = 0
+                    while scale < need:
+                        scale, shift = np.float32(scale * 2), shift + 1
+                    if shift:
+                        rows[:o, part] = _e4m3(values[rows[:o, part]].astype(np.float64) * 2.0**-shift)
+                with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
+                    y = np.where(fine, x / scale if scale != 0 else np.float32(0), np.float32(np.nan)).astype(np.float32)
+                rows[o: o + n, part] = _e4m3(y)
+                scales[part] = scale
+            page[at: at + 8] = scales.view(np.uint8)
+
+
+def block_attention(q, cache, block_tables, context_lens, cu_new, block_size, scale, window=0):
+    """q [R, H, D] f64 over a cache whose blocks share a scale.  Returns out,
+    lse and the figures of sparse_attention (floor by product), rows past
+    cu_new[-1] NaN."""
+    R, H, D = q.shape
+    HK = cache.shape[1]
+    G = H // HK
+    table = e4m3_values()
+    out, lse = np.full((R, H, D), np.nan), np.full((R, H), np.nan)
+    mag, floor, sabs = np.zeros((R, H, D)), np.zeros((R, H, D)), np.zeros((R, H))
+    cap = block_tables.shape[1] * block_size
+    for b in range(len(context_lens)):
+        lo, hi = int(cu_new[b]), int(cu_new[b + 1])
+        if lo == hi:
+            continue
+        out[lo:hi], lse[lo:hi] = 0.0, -np.inf
+        n = min(max(int(context_lens[b]), 0), cap)
+        blocks = block_tables[b, : -(-n // block_size)]
+        j = np.arange(n)
+        there = (blocks >= 0) & (blocks < cache.shape[0])
+        there = there[j // block_size] if n else np.zeros(0, bool)
+        pos = int(context_lens[b]) - hi + np.arange(lo, hi)
+        seen = (j <= pos[:, None]) & there & ((j > pos[:, None] - window) if window else True)
+        for g in range(HK):
+            pages = cache[np.where((blocks >= 0) & (blocks < cache.shape[0]), blocks, 0), g]
+            codes = table[pages[:, : block_size * 2 * D].reshape(-1, 2, D)[:n]]
+            at = block_size * 2 * D
+            sc = np.ascontiguousarray(pages[:, at: at + 8]).view(np.float32).astype(np.float64)[j // block_size]
+            any_seen = seen.any(0)  # (what no row sees may hold anything)
+            codes, sc = np.where(any_seen[:, None, None], codes, 0), np.where(any_seen[:, None], sc, 0)
+            key, val = codes[:, 0] * sc[:, :1], codes[:, 1] * sc[:, 1:]
+            for h in range(g * G, (g + 1) * G):
+                for r in range(lo, hi):
+                    m = seen[r - lo]
+                    if not m.any():
+                        continue
+                    s = scale * (key[m] @ q[r, h])
+                    top = s.max()
+                    w = np.exp(s - top)
+                    z = w.sum()
+                    w /= z
+                    lse[r, h] = top + np.log(z)
+                    out[r, h] = w @ val[m]
+                    mag[r, h] = w @ np.abs(val[m])
+                    floor[r, h] = (w * sc[m, 1]).max() * np.abs(codes[m, 1]).sum(0)
+                    sabs[r, h] = (np.abs(scale) * (np.abs(key[m]) @ np.abs(q[r, h]))).max()
     return out, lse, mag, floor, sabs

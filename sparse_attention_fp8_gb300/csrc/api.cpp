@@ -995,6 +995,13 @@ fp8idx_status check_rows(const fp8idx_tensor* x, const char* name, int64_t* toke
   return FP8IDX_OK;
 }
 
+// Whether rows of an output [tokens, heads, D] share bytes.
+bool rows_overlap(const fp8idx_tensor* y) {
+  for (int i = 0; i < 2; ++i)
+    if (y->shape[i] > 1 && y->stride[i] < y->shape[2]) return true;
+  return Extent(y).overlaps_itself();
+}
+
 // The same bytes, element for element.
 bool same_view(const fp8idx_tensor* a, const fp8idx_tensor* b) {
   if (a->data != b->data) return false;
@@ -1034,7 +1041,7 @@ fp8idx_status head_norm_rope_impl(const fp8idx_tensor* q, const fp8idx_tensor* k
       if (ys[i]->shape[d] != xs[i]->shape[d]) return fail(FP8IDX_ERR_INVALID, "%s must have the shape of %s", yn[i], xn[i]);
     TRY(check_rows(xs[i], xn[i], &p.x_token[i], &p.x_head[i]));
     TRY(check_rows(ys[i], yn[i], &p.y_token[i], &p.y_head[i]));
-    if (Extent(ys[i]).overlaps_itself()) return fail(FP8IDX_ERR_INVALID, "%s: rows overlap", yn[i]);
+    if (rows_overlap(ys[i])) return fail(FP8IDX_ERR_INVALID, "%s: rows overlap", yn[i]);
     p.x[i] = xs[i]->data;
     p.y[i] = ys[i]->data;
     p.heads[i] = (int32_t)std::min<int64_t>(xs[i]->shape[1], 1 << 30);
@@ -1143,8 +1150,8 @@ fp8idx_status block_attn_impl(const fp8idx_tensor* q, const fp8idx_tensor* kv, c
   int64_t q_token, q_head, out_token, out_head;
   TRY(check_rows(q, "q", &q_token, &q_head));
   TRY(check_rows(out, "out", &out_token, &out_head));
-  if (Extent(out).overlaps_itself()) return fail(FP8IDX_ERR_INVALID, "out: rows overlap");
   if (H < 1) return fail(FP8IDX_ERR_INVALID, "q has no heads");
+  if (rows_overlap(out)) return fail(FP8IDX_ERR_INVALID, "out: rows overlap");
   int64_t bs = 0;
   TRY(check_kv_block_cache(kv, D, &bs));
   const int64_t HK = kv->shape[1];
