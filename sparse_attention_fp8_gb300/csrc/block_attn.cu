@@ -60,7 +60,7 @@ constexpr int kSoftmaxRegs = 184, kConvRegs = 80, kOtherRegs = 64;
 constexpr float kMinM = -3e38f;   // m stays finite, so that a score of -inf gives probability 0
 constexpr float kNoScaleLog = -64.f;
 constexpr int kUnitSlots = 8, kScaleSlots = 8;
-constexpr int kUnitCost = 3;      // a unit's start and end, in steps
+constexpr int kUnitCost = 4;      // a unit's start and end, in steps (3 to 8 are within 2% of one another)
 
 // A CTA's share of a unit.
 struct Piece {
@@ -215,6 +215,20 @@ __device__ __forceinline__ uint32_t seen32(int pos, int window, int len, int til
   if (!(in_cache >> (col / 16) & 1u)) m &= 0xFFFF0000u;
   if (!(in_cache >> (col / 16 + 1) & 1u)) m &= 0x0000FFFFu;
   return m;
+}
+
+// Whether a row sees a NaN in the chunks chunk0 .. end of the last n tiles (each
+// `step` after the other) before tile j, which starts at tile0.
+__device__ __noinline__ bool sees_nan(const TileScales* scales, uint32_t j, int tile0, int step, int n, int chunk0, int end,
+                                      int pos, int window, int len) {
+  uint32_t seen = 0;
+#pragma unroll 1
+  for (int back = 1; back <= n; ++back) {
+    const uint32_t* const words = reinterpret_cast<const uint32_t*>(&scales[(j - back * step) % kScaleSlots].nan);
+#pragma unroll 1
+    for (int c = chunk0; c < end; ++c) seen |= words[c] & seen32(pos, window, len, tile0 - back * step * kTile, c * 32, 0xFFu);
+  }
+  return seen != 0u;
 }
 
 struct RowState {
@@ -561,12 +575,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = ptx::smem_u32(smem);
   uint32_t* const misc = reinterpret_cast<uint32_t*>(smem + L::misc);
   volatile uint32_t* const abort_flag = misc + 1;
+  volatile uint32_t* const odd_values = misc + 2;  // a tile had a NaN among its values
   TileScales* const tile_scales = reinterpret_cast<TileScales*>(smem + L::scales);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const auto bar = [&](uint32_t at, int i = 0) { return base + at + 8u * i; };
 
   if (threadIdx.x == 0) {
-    misc[1] = 0u;
+    misc[1] = misc[2] = 0u;
     for (int s = 0; s < S; ++s) {
       ptx::mbar_init(bar(L::kFullB, s), 1u);
       ptx::mbar_init(bar(L::kEmptyB, s), D == 128 ? 1u : 5u);  // the score MMA (and the converting warps)
@@ -989,7 +1004,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             at.store(dst, i + x, codes[x]);
           }
         }
-        if (__any_sync(kFull, odd != 0u)) nan_rows = convert_odd<D>(dst, src, w, lane, flags);
+        if (__any_sync(kFull, odd != 0u)) {
+          nan_rows = convert_odd<D>(dst, src, w, lane, flags);
+          if (nan_rows != 0u && lane == 0) *odd_values = 1u;
+        }
         // the codes have been read: the stage may be filled again
         if (lane == 0) ptx::mbar_arrive(bar(D == 128 ? L::vEmptyB : L::kEmptyB, stage));
         if (lane == 0) reinterpret_cast<uint32_t*>(&tile_scales[j % kScaleSlots].nan)[w] = nan_rows;
@@ -1053,19 +1071,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t j = j0 + first;
       int tile0 = (piece.ta + first) * kTile;
       j0 += piece.tb - piece.ta;
-      // Whether the row sees a NaN among the values of a tile whose products have been issued.
-      const auto see_nan = [&](uint32_t jj, int at) {
-        if (!wait(bar(L::v16FullB, jj % kScaleSlots), (jj / kScaleSlots) & 1u, abort_flag, kSiteStageFull)) return false;
-        const uint4 words = tile_scales[jj % kScaleSlots].nan;
-        if ((words.x | words.y | words.z | words.w) != 0u) {
-          const uint32_t in_cache = tile_scales[jj % kScaleSlots].flags >> 16;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c >= chunk0 && c < chunk0 + copy_lanes / 32)
-              st.bad |= ((c == 0 ? words.x : c == 1 ? words.y : c == 2 ? words.z : words.w) &
-                         seen32(pos, p.window, len, at, c * 32, in_cache)) != 0u;
-        }
-        return true;
+      // Whether the row sees a NaN among the values of this group's last n tiles
+      // before tile jj, which starts at `at`.  (Their scores' successors, which
+      // this group has waited for, were issued after their products, and those
+      // after their values had been converted: flag and masks are there.  They
+      // stay until the third tile of the group after them is through.)
+      const auto see_nan = [&](uint32_t jj, int at, int n) {
+        if (*odd_values != 0u)
+          st.bad |= sees_nan(tile_scales, jj, at, step, n, chunk0, chunk0 + copy_lanes / 32, pos, p.window, len);
       };
 #pragma unroll 1
       for (int k = 0; k < count; ++k, j += step, tile0 += step * kTile) {
@@ -1084,11 +1097,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(L::pFullB, g));
-        if (k > 0 && !see_nan(j - step, tile0 - step * kTile)) goto out;
+        if ((k & 1) == 0 && k > 0) see_nan(j, tile0, 2);
       }
       if (count > 0) {
-        if (!wait(bar(L::oFullB, g), n_outs & 1u, abort_flag, kSiteAccFull) || !see_nan(j - step, tile0 - step * kTile))
-          goto out;
+        if (!wait(bar(L::oFullB, g), n_outs & 1u, abort_flag, kSiteAccFull)) goto out;
+        see_nan(j, tile0, (count & 1) != 0 ? 1 : 2);
         ++n_outs;
         ptx::tc_fence_after();
       }
