@@ -130,6 +130,15 @@ def test_one_long_request(fp8idx, heads):
     check(fp8idx, setup(rng, [30011], [1], heads, 1, 64, 16))
 
 
+@pytest.mark.parametrize("H,new", [(100, 2), (100, 1), (7, 30), (127, 3), (64, 2), (43, 5), (3, 60)])
+def test_units_that_are_cut(fp8idx, H, new):
+    """Every kind of unit in pieces: lanes between the heads of the last position
+    and a tile's end, one tile of rows and two."""
+    rng = np.random.default_rng(H)
+    check(fp8idx, setup(rng, [9000, 700], [new, 1], H, 1, 128, 64))
+    check(fp8idx, setup(rng, [4000], [new], H, 1, 64, 32), window=3000)
+
+
 def test_context_past_the_table(fp8idx):
     """Positions past the block table are not attended, by any row."""
     rng = np.random.default_rng(8)
