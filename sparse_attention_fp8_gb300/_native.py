@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 import re
 import struct
@@ -38,6 +39,7 @@ class _Tensor(ctypes.Structure):
 _TENSOR_PACK = struct.Struct("=qii4q4q")
 assert _TENSOR_PACK.size == ctypes.sizeof(_Tensor)
 _PACK_1D, _PACK_2D = struct.Struct("=qiiq24xq24x"), struct.Struct("=qiiqq16xqq16x")
+_PACK_3D = struct.Struct("=qiiqqq8xqqq8x")
 _PAD = (0, 0, 0, 0)
 _dtype_codes = _row_codes = None
 
@@ -353,10 +355,10 @@ def _descs(*tensors):
     """The packed descriptors of a call (None stays None).  The library
     launches on the current device: every tensor has to be there (a kernel
     cannot be sent after the data of another device).  One pass over the
-    tensors with vectors and matrices spelt out: a step's tables have twelve
+    tensors with one to three dimensions spelt out: a step's tables have twelve
     descriptors, which costs 5 us this way and 13 us tensor by tensor."""
     import torch
-    codes, pack_1d, pack_2d = _codes(rows=True), _PACK_1D.pack, _PACK_2D.pack
+    codes, pack_1d, pack_2d, pack_3d = _codes(rows=True), _PACK_1D.pack, _PACK_2D.pack, _PACK_3D.pack
     dev = None
     out = []
     for t in tensors:
@@ -378,6 +380,8 @@ def _descs(*tensors):
             rows, cols = t.shape
             step, inner = t.stride()
             out.append(pack_2d(t.data_ptr(), dt, 2, rows, cols, step, inner))
+        elif n == 3 and dt is not None:
+            out.append(pack_3d(t.data_ptr(), dt, 3, *t.shape, *t.stride()))
         else:
             out.append(_pack(t, t.data_ptr(), rows=True))
     return out
@@ -438,6 +442,12 @@ def fp8_mqa_sparse_attn_paged(q, kv_cache, block_tables, cu_seq_lens, indices, s
 _NORMS = {None: 0, "none": 0, "rms": 1, "layer": 2}
 
 
+@functools.lru_cache(maxsize=64)
+def _norm_rope_options(norm, interleaved, rot_start, eps, rope_scale):
+    """The options of a call (a model has a few)."""
+    return ctypes.byref(_NormRopeOptions(_NORMS[norm], interleaved, rot_start, eps, rope_scale))
+
+
 def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_len=None, beta_fast=32.0,
                      beta_slow=1.0):
     """The angles per position, inv_freq [rot_dim / 2] (an f32 CPU tensor),
@@ -494,8 +504,8 @@ def head_norm_rope(q, k, positions, inv_freq, out_q, out_k=None, norm=None, q_we
     if norm not in _NORMS:
         raise ValueError(f"norm must be None, 'rms' or 'layer', not {norm!r}")
     d = _descs(q, k, positions, inv_freq, q_weight, q_bias, k_weight, k_bias, out_q, out_k)
-    oc = _NormRopeOptions(_NORMS[norm], int(bool(interleaved)), int(rot_start), float(eps), float(rope_scale))
-    _check(library().fp8idx_head_norm_rope(*d[:8], ctypes.byref(oc), *d[8:], _stream(stream, q)))
+    oc = _norm_rope_options(norm, int(bool(interleaved)), int(rot_start), float(eps), float(rope_scale))
+    _check(library().fp8idx_head_norm_rope(*d[:8], oc, *d[8:], _stream(stream, q)))
     return out_q, out_k
 
 
