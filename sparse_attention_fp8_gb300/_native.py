@@ -246,6 +246,19 @@ def _stream(stream, like):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _scratch(nbytes, like, stream):
+    """Workspace for one call, allocated as the launching stream's: the caching
+    allocator hands it on in that stream's order, not in the current one's."""
+    import torch
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=like.device) if stream
+                  else torch.cuda.default_stream(like.device))
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
 def fp8_paged_mqa_logits(q_fp8, kv_cache, weights, context_lens, block_tables, max_model_len, out,
                          stream=None, options: Options | None = None):
     """Decode logits into ``out`` (only the causal windows are written).
@@ -333,12 +346,11 @@ def fp8_paged_mqa_topk(q_fp8, kv_cache, weights, context_lens, block_tables, max
     row are never written): indices [batch*next_n, k] as fp8_paged_topk gives
     on the decode logits.  workspace: a uint8 CUDA tensor of at least
     paged_mqa_topk_workspace(...) bytes (allocated here if None)."""
-    import torch
     lib = library()
     B, n = q_fp8.shape[0], q_fp8.shape[1]
     need = paged_mqa_topk_workspace(B, n, max_model_len, k)
     if workspace is None:
-        workspace = torch.empty(need + 256, dtype=torch.uint8, device=q_fp8.device)
+        workspace = _scratch(need + 256, q_fp8, stream)
     base = workspace.data_ptr()
     off = (-base) % 256
     args = [_desc(q_fp8), _desc(kv_cache), _desc(weights), _desc(context_lens), _desc(block_tables)]
@@ -540,7 +552,7 @@ def fp8_paged_block_attn(q, kv_cache, block_tables, context_lens, cu_new_lens, s
     least paged_block_attn_workspace(D) bytes (allocated here if None)."""
     import torch
     if workspace is None:
-        workspace = torch.empty(paged_block_attn_workspace(q.shape[-1]) + 256, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(paged_block_attn_workspace(q.shape[-1]) + 256, q, stream)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     d = _descs(q, kv_cache, block_tables, context_lens, cu_new_lens, out, lse, workspace)

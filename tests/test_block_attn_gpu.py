@@ -409,3 +409,29 @@ def test_lengths_that_are_no_prefix_sums(fp8idx):
     torch.cuda.synchronize()
     assert fp8idx.device_status() == fp8idx.FP8IDX_OK
     assert torch.isnan(guard[:32]).all() and torch.isnan(guard[-32:]).all()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_own_workspace_on_another_stream(fp8idx, monkeypatch, handle):
+    """The workspace that a call allocates belongs to the stream it runs on:
+    what the current stream allocates next is other memory."""
+    from sparse_attention_fp8_gb300 import _native
+    rng = np.random.default_rng(29)
+    x = setup(rng, [700, 300], [1, 1], 8, 2, 128, 64)
+    d = {n: torch.from_numpy(x[n]).cuda() for n in ("cache", "tables", "ctx", "cu")}
+    q = torch.from_numpy(x["q"]).to(torch.bfloat16).cuda()
+    out, want = torch.empty_like(q), torch.empty_like(q)
+    nbytes = fp8idx.paged_block_attn_workspace(128) + 256
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    held = []
+    monkeypatch.setattr(_native, "_scratch", lambda *a, f=_native._scratch: held.append(w := f(*a)) or w)
+    fp8idx.fp8_paged_block_attn(q, d["cache"], d["tables"], d["ctx"], d["cu"], 0.1, out,
+                                stream=s.cuda_stream if handle else s)
+    used = held.pop().data_ptr()  # (the last reference: the allocator has the memory back)
+    other = torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")
+    assert other.data_ptr() != used
+    torch.cuda.synchronize()
+    fp8idx.fp8_paged_block_attn(q, d["cache"], d["tables"], d["ctx"], d["cu"], 0.1, want)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and fp8idx.device_status() == fp8idx.FP8IDX_OK
