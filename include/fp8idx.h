@@ -650,7 +650,8 @@ fp8idx_status fp8_paged_block_store(const fp8idx_tensor* k,
  *  q             [rows, heads, head_dim] BF16, unit inner stride, rows 16-byte
  *                aligned; head_dim 64 or 128; heads a multiple of kv_heads,
  *                heads/kv_heads <= 128.
- *  kv_cache      as for fp8_paged_block_store; scales not negative.
+ *  kv_cache      as for fp8_paged_block_store; a value scale below zero, which
+ *                no store writes, counts as NaN.
  *  block_tables  [batch, max_blocks] I32, rows contiguous, batch <= 4096,
  *                max_blocks*block_size < 2^31 - 256.
  *  context_lens  [batch] I32; cu_new_lens [batch + 1] I32, a prefix sum, at

@@ -838,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(bar(L::kEmptyB, stage), phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
         // scales, by the lanes that have them
         const bool here = lane < 8 && in_cache(a0);
-        const bool zero = s0.y == 0.f, bad = !(fabsf(s0.y) < INFINITY);
+        const bool zero = s0.y == 0.f, bad = !(s0.y >= 0.f && s0.y < INFINITY);
         const float own = here && !zero && !bad ? s0.y : 0.f;
         const float top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(own, 0.f))));
         if (a0.first) ref = top > 0.f ? top : 1.f;

@@ -435,3 +435,22 @@ def test_own_workspace_on_another_stream(fp8idx, monkeypatch, handle):
     fp8idx.fp8_paged_block_attn(q, d["cache"], d["tables"], d["ctx"], d["cu"], 0.1, want)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and fp8idx.device_status() == fp8idx.FP8IDX_OK
+
+
+def test_negative_value_scales(fp8idx):
+    """A value scale below zero, which no store writes, counts as no number."""
+    rng = np.random.default_rng(30)
+    x = setup(rng, [256, 200], [1, 40], 4, 2, 128, 32)
+    scales = scales_of(x["cache"], 32, 128).copy()
+    block = x["tables"][0, 3]
+    scales[block, 1, 1] *= -1
+    set_scales(x["cache"], 32, 128, scales)
+    out, lse = call(fp8idx, x, 0.1)
+    scales[block, 1, 1] *= -1
+    set_scales(x["cache"], 32, 128, scales)
+    want = ref.block_attention(x["q"].astype(np.float64), x["cache"], x["tables"], x["ctx"], x["cu"], 32, 0.1, 0)
+    hit = np.zeros(x["q"].shape[:2], bool)
+    hit[0, 2:] = True  # (the heads of key head 1, in the request that has the block)
+    assert torch.isnan(out[0, 2:]).all()
+    check_rows(out, lse, want, ~hit)
+    assert np.abs(lse.cpu().numpy() - want[1])[hit].max() < 2.0**-16 * (1 + want[4][hit]).max()
