@@ -16,7 +16,9 @@
 // around zero, where the Taylor series of sine and cosine to x^9 and x^10 are
 // good to 2e-9.  (In 32-bit floats the product alone would be off by 0.004 at
 // position 100000; 64-bit floats run at a sixty-fourth of the rate here.)
-// DRAM bound: every value is read and written once.
+// DRAM bound: every value is read and written once.  16384 tokens of 32 + 8 bf16
+// heads of 128 take 55.3 us, 6.07 TB/s of the 6.68 that a copy reaches; one
+// token 3.3 us, a launch.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -109,7 +111,9 @@ __device__ __forceinline__ float row_sum(float v) {
 // are rotated, else halves of the rotated part.
 template <int TYPE, int L, bool PAIRS>
 __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_kernel(const NormRopeParams p) {
-  constexpr int kRows = 32 / L, kBatch = 2;  // rows that a warp holds side by side, and of those in flight
+  // Rows that a warp holds side by side, and of those in flight (4099 tokens of
+  // 24 f32 heads of 64: 15.8 us with 2, 13.9 with 3, 14.8 with 4, 18.0 with 8).
+  constexpr int kRows = 32 / L, kBatch = 3;
   constexpr int kItem = TYPE == kRowF32 ? 4 : 2;
   const int lane = threadIdx.x & 31, sub = lane % L;
   const uint32_t warp = blockIdx.x * (kNormRopeThreads / 32) + (threadIdx.x >> 5);
@@ -252,10 +256,11 @@ __device__ __forceinline__ float2 minus(float2 v) { return make_float2(-v.x, -v.
 }  // namespace
 
 // Halves of the whole head, 8 * L elements: a lane has four values of each half,
-// so pairs meet in it, and arithmetic goes two values an instruction.
+// so pairs meet in it, and arithmetic goes two values an instruction (16384
+// tokens of 40 heads: 55 us, where the kernel above takes 110).
 template <int TYPE, int L>
 __global__ void __launch_bounds__(kNormRopeThreads) norm_rope_whole_kernel(const NormRopeParams p) {
-  constexpr int kRows = 32 / L, kBatch = 4;
+  constexpr int kRows = 32 / L, kBatch = 4;  // (2: 62.9 us, 8: 58.7)
   constexpr int kPiece = TYPE == kRowF32 ? 16 : 8, kHalf = L * kPiece;  // bytes of four values, of half a row
   const int lane = threadIdx.x & 31, sub = lane % L;
   const uint32_t warp = blockIdx.x * (kNormRopeThreads / 32) + (threadIdx.x >> 5);
@@ -359,7 +364,10 @@ NormRopeKernel norm_rope_instance(int lanes, bool pairs, bool whole) {
 cudaError_t launch_norm_rope(NormRopeParams& p, int row_type, bool pairs, int sms, cudaStream_t stream) {
   const int lanes = p.dim <= 64 ? 8 : p.dim <= 128 ? 16 : 32, rows = 32 / lanes;
   for (int i = 0; i < 2; ++i) p.groups[i] = (p.heads[i] + rows - 1) / rows;
-  // Groups that a warp walks: a whole token's once that leaves every SM 24 warps.
+  // Groups that a warp walks: a whole token's once that leaves every SM 24 warps
+  // (4099 tokens of 7 groups: 13.9 us; pieces of a token, at 32 or 64 warps,
+  // 16.6 and 18.6: each makes the token's angles again), fewer below (96 tokens
+  // of 20 groups: 3.7 us where a warp for a token takes longer than all of them).
   const int groups = p.groups[0] + p.groups[1];
   const int64_t per = static_cast<int64_t>(p.tokens) * groups / (24 * sms);
   p.per = static_cast<int32_t>(per < 1 ? 1 : per > groups ? groups : per);
