@@ -43,6 +43,48 @@ struct Raw8 {
   }
 };
 
+// The largest magnitude of values, from their bits: ordered like the numbers,
+// infinities and NaN behind them, two 16-bit values or two f32 an instruction.
+template <int TYPE>
+struct Magnitude {
+  static constexpr uint32_t kInf = TYPE == kRowF32 ? 0x7F800000u : TYPE == kRowBf16 ? 0x7F80u : 0x7C00u;
+  uint32_t m = 0;
+  __device__ __forceinline__ void add(const Raw8<TYPE>& x) {
+    if constexpr (TYPE == kRowF32) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m = __vimax3_u32(m, x.v[i].x & 0x7FFFFFFFu, x.v[i].y & 0x7FFFFFFFu);
+        m = __vimax3_u32(m, x.v[i].z & 0x7FFFFFFFu, x.v[i].w & 0x7FFFFFFFu);
+      }
+    } else {
+      m = __vimax3_u16x2(m, x.v[0].x & 0x7FFF7FFFu, x.v[0].y & 0x7FFF7FFFu);
+      m = __vimax3_u16x2(m, x.v[0].z & 0x7FFF7FFFu, x.v[0].w & 0x7FFF7FFFu);
+    }
+  }
+  __device__ __forceinline__ uint32_t top() const { return TYPE == kRowF32 ? m : max(m & 0xFFFFu, m >> 16); }
+  // (of finite values)
+  __device__ __forceinline__ float value() const {
+    const uint32_t t = top();
+    if constexpr (TYPE == kRowF32) return __uint_as_float(t);
+    if constexpr (TYPE == kRowBf16) return __uint_as_float(t << 16);
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(t)));
+  }
+};
+
+// The signs of eight values, where their codes have theirs.
+template <int TYPE>
+__device__ __forceinline__ uint2 code_signs(const Raw8<TYPE>& x) {
+  uint2 s;
+  if constexpr (TYPE == kRowF32) {
+    s.x = __byte_perm(__byte_perm(x.v[0].x, x.v[0].y, 0x73), __byte_perm(x.v[0].z, x.v[0].w, 0x73), 0x5410);
+    s.y = __byte_perm(__byte_perm(x.v[1].x, x.v[1].y, 0x73), __byte_perm(x.v[1].z, x.v[1].w, 0x73), 0x5410);
+  } else {
+    s.x = __byte_perm(x.v[0].x, x.v[0].y, 0x7531);
+    s.y = __byte_perm(x.v[0].z, x.v[0].w, 0x7531);
+  }
+  return make_uint2(s.x & 0x80808080u, s.y & 0x80808080u);
+}
+
 // a / b for r = RN(1 / b) by Markstein's method (see paged_store.cu), divided
 // where a step could underflow.
 __device__ __forceinline__ float rounded_quotient(float a, float b, float r) {
@@ -58,16 +100,18 @@ __device__ __forceinline__ bool has_to_divide(float scale) {
 }
 
 // The correctly rounded quotients x / scale of eight values (r = RN(1/scale),
-// which has_to_divide does not hold for).
+// which has_to_divide does not hold for).  SIGNED: -0 / scale is -0, else 0; no
+// other quotient lacks its value's sign.
+template <bool SIGNED = true>
 __device__ __forceinline__ void quotients8(const float (&x)[8], float scale, float r, float (&y)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {  // two at a time
     const float2 v = make_float2(x[j], x[j + 1]), r2 = make_float2(r, r);
     const float2 q = __fmul2_rn(v, r2);
-    const float2 e = __ffma2_rn(make_float2(-q.x, -q.y), make_float2(scale, scale), v);
+    const float2 e = __ffma2_rn(q, make_float2(-scale, -scale), v);
     const float2 z = __ffma2_rn(e, r2, q);
-    y[j] = copysignf(z.x, x[j]);  // (-0 / scale is -0)
-    y[j + 1] = copysignf(z.y, x[j + 1]);
+    y[j] = SIGNED ? copysignf(z.x, x[j]) : z.x;
+    y[j + 1] = SIGNED ? copysignf(z.y, x[j + 1]) : z.y;
   }
 }
 
