@@ -552,8 +552,9 @@ fp8idx_status fp8_mqa_sparse_attn_paged(const fp8idx_tensor* q,
  *   ((a cos - b sin) * rope_scale, (b cos + a sin) * rope_scale),
  * cos and sin of positions[token] * inv_freq[i], to within 1e-7 at every
  * position.  Pair i is elements (i, i + rot/2) of the rotated part, or with
- * `interleaved` (2i, 2i + 1).  Sums are f32, rounded once at the end.  A token
- * with a negative position is not written.
+ * `interleaved` (2i, 2i + 1).  Sums are f32, rounded once at the end (with a
+ * norm, the mean square has to be an f32 number: values below 2^60 in size).  A
+ * token with a negative position is not written.
  *
  *  q, k          [tokens, heads, head_dim] and [tokens, kv_heads, head_dim]
  *                BF16, F16 or F32 (the same), unit inner stride, rows 16-byte
@@ -664,6 +665,22 @@ fp8idx_status fp8_paged_block_store(const fp8idx_tensor* k,
  *                aligned, owned by the caller; its contents on entry do not
  *                matter.  Two calls in flight at once (two captured graphs,
  *                too) need two workspaces.
+ *
+ * Precision: a query element is exact, but for those below 2^-10 of its head's
+ * largest one, which are off by up to 2^-17 of that.  Products and sums are
+ * f32.  What is multiplied with a value's code is probability * value scale as
+ * f16 (2^-11 of itself, and 2^-24 of the row's largest one); value scales other
+ * than 0 should lie within 2^64 of one another, scores (times log2 e) below
+ * 10^7.  The sum of the probabilities is not rounded to f16.  out is rounded
+ * once to BF16.
+ * NaN and infinities: in a query they make its head's out and lse NaN; a NaN
+ * key code or key scale, the out and lse of the rows that see the key; a NaN
+ * value code, or a value scale that is NaN, infinite or negative, every channel
+ * of the out of the rows that see it, not their lse.  What no row sees does not
+ * matter.  A scale of 0 stands for zeros.
+ * A call gives the same bits on every run; how a row's sums are split, and so
+ * their rounding, depends on the whole step's lengths and the number of SMs.
+ * Two kernels on `stream`.
  */
 size_t fp8idx_paged_block_attn_workspace(int32_t head_dim);
 fp8idx_status fp8_paged_block_attn(const fp8idx_tensor* q,

@@ -37,6 +37,27 @@
 // of unrounded f32 exponentials.
 // Every wait is bounded (common.cuh); a role whose wait has run out leaves, and
 // then so do the others.
+//
+// What bounds it, measured with replayed graphs (the join included):
+//  * 32 requests of one row, 64 / 8 heads, 32768 positions: 338 us, 5.4 TB/s of
+//    cache, 81% of a copy's rate.  A tile's 32 KB take 1420 clocks of an SM's
+//    share of that rate, its products 1024 of the tensor pipe, for 8 rows as for
+//    128, and its softmax and conversion have to stay below as well.
+//  * 16 requests of 6 rows, 32 heads on one key head, 131072 positions: 198 us,
+//    895 TFLOP/s; 4 requests of 2048 prompt rows, 32 / 8 heads, 8192 positions:
+//    577 us, 1135 TFLOP/s, 58% of a bf16 product's rate.  The 1024 clocks of a
+//    tile and 128 rows are half scores (e4m3, but twice: both parts of a query)
+//    and half outputs (f16); the tensor pipe is busy 47% and the issue slots 44%
+//    of the time (2 x 1024 rows): the chain of a tile - scores, softmax,
+//    probabilities, outputs - is what takes the time, with two in flight.  The
+//    code of the roles' inner loops has to stay within the instruction cache:
+//    loops are rolled and what is rare is out of line (unrolled softmax 924 us
+//    where the rolled one took 861).
+//  * one row of 1024 positions: 15.2 us, 2.5 of it the join: launch, plan, table
+//    entry, scales, tile, one step and the meeting are one chain.
+// Queries in tensor memory with scores in halves of a tile (887 us where this
+// took 802), all scores of a tile held in registers (1203 against 820) and both
+// chunks loaded ahead (717 against 640) were slower.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -59,6 +80,8 @@ constexpr int kConvWarp0 = 8, kLoadWarp = 12, kMmaWarp = 13, kPlanWarp = 14;
 constexpr int kSoftmaxRegs = 184, kConvRegs = 80, kOtherRegs = 64;
 constexpr float kMinM = -3e38f;   // m stays finite, so that a score of -inf gives probability 0
 constexpr float kNoScaleLog = -64.f;
+// (Scale slots outnumber the tiles in flight: a tile's masks of NaN stay behind it
+// until its group has looked, two of its tiles later.)
 constexpr int kUnitSlots = 8, kScaleSlots = 8;
 constexpr int kUnitCost = 4;      // a unit's start and end, in steps (3 to 8 are within 2% of one another)
 
@@ -110,6 +133,7 @@ struct Smem {
   static constexpr uint32_t misc = drainB + 8;            // tensor memory's address, abort flag
   static constexpr uint32_t total = misc + 16 + 1024;     // and the alignment
 };
+static_assert(Smem<128>::kStages < kScaleSlots && Smem<64>::kStages < kScaleSlots, "scale slots");
 static_assert(Smem<128>::total <= kMaxSmem && Smem<64>::total <= kMaxSmem, "shared memory");
 static_assert(sizeof(Piece) <= 64, "a unit slot");
 // The plan's prefix sums lie where the f16 values and the scales will.
@@ -262,8 +286,8 @@ __device__ __forceinline__ float chunk_max(const uint32_t (&r)[32], const ChunkS
   }
   return top;
 }
-// Probabilities of 32 scores over 2^m, as f16 pairs; the larger group's sum into
-// `most`.  Returns the sum over the value scales.
+// Probabilities of 32 scores over 2^m, as f16 pairs; their sum is added to `most`.
+// Returns the sum over the value scales.
 __device__ __forceinline__ float chunk_exp(const uint32_t (&r)[32], const ChunkScale& cs, float m, uint32_t (&h)[16],
                                            float& most) {
   float l = 0.f;
@@ -394,7 +418,6 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_tm, uint32_t o_tm, const
         ptx::tmem_wait_ld_regs(r);
         l += chunk_exp(r, cs, st.m, h1, most);
       }
-
       if (__any_sync(kFull, !(most < 32768.f)) && !raised) {
         raise(k);
         continue;
@@ -1044,7 +1067,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (piece.row0 < 0) break;
       const bool shared = piece.shared != 0;
       const int half = p.half_positions;
-      // lanes of a copy of the rows, and this thread's row
+      // Lanes of a copy of the rows, and this thread's row.  (Two copies at least:
+      // 350 us for 32 requests of 8 rows a key head, 17.0 for one of 4; one a
+      // group: 376 and 17.7; four and eight, as here: 337 and 15.2.)
       const int rows = shared ? kTile : piece.positions * p.group;
       const int copy_lanes = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
       float row_scale;

@@ -367,7 +367,7 @@ cudaError_t launch_norm_rope(NormRopeParams& p, int row_type, bool pairs, int sm
   // Groups that a warp walks: a whole token's once that leaves every SM 24 warps
   // (4099 tokens of 7 groups: 13.9 us; pieces of a token, at 32 or 64 warps,
   // 16.6 and 18.6: each makes the token's angles again), fewer below (96 tokens
-  // of 20 groups: 3.7 us where a warp for a token takes longer than all of them).
+  // of 20 groups: 3.7 us, with a warp for a token 6.8).
   const int groups = p.groups[0] + p.groups[1];
   const int64_t per = static_cast<int64_t>(p.tokens) * groups / (24 * sms);
   p.per = static_cast<int32_t>(per < 1 ? 1 : per > groups ? groups : per);
