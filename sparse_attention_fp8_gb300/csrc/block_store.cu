@@ -17,11 +17,12 @@
 // values an instruction, and tell NaN and infinities, too.
 //
 // Read once and written once.  12288 bf16 rows of 8 heads of 128 in blocks of 64
-// take 17.1 us, 4.4 TB/s: the chain slots - rows - maximum - codes of a CTA, of
-// which five are on an SM, and the arithmetic (about 8 instructions a value; with
-// floating-point maxima and signs value by value 19.2 us).  More CTAs an SM
-// (16.9 us, and 4.4 instead of 4.1 us for f32 rows of 64) and rows fetched into
-// L2 before their slots are known (17.3) do not pay.  A decode step of 96 rows
+// take 17.1 us, 4.4 TB/s: the chain slots - rows - maximum - codes of a CTA, with
+// eight CTAs of 64 registers on an SM (loads are what most warps wait for), and
+// the arithmetic (with floating-point maxima and signs value by value, 92
+// registers, 19.2 us).  Fewer registers for f32 rows (4.4 us instead of 4.1 for
+// 3 heads of 64) and rows fetched into L2 before their slots are known (17.3) do
+// not pay.  A decode step of 96 rows
 // takes 3.5 us, a launch.
 #include <cuda_runtime.h>
 
