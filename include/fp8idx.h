@@ -677,7 +677,9 @@ fp8idx_status fp8_paged_block_store(const fp8idx_tensor* k,
  * key code or key scale, the out and lse of the rows that see the key; a NaN
  * value code, or a value scale that is NaN, infinite or negative, every channel
  * of the out of the rows that see it, not their lse.  What no row sees does not
- * matter.  A scale of 0 stands for zeros.
+ * matter: table entries past a request's positions or before its window, and the
+ * codes and scales of their blocks, may be anything.  A scale of 0 stands for
+ * zeros.
  * A call gives the same bits on every run; how a row's sums are split, and so
  * their rounding, depends on the whole step's lengths and the number of SMs.
  * Two kernels on `stream`.

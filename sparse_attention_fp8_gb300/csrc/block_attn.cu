@@ -816,28 +816,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kLoadWarp) {
       // ============================ the loads ============================
       // Lane l < 8 has the 16 tokens l of a tile: its block's table entry two
-      // tiles ahead, its scales one.
+      // tiles ahead, its scales one.  A block that no row of the unit sees (past
+      // its positions or before its window) counts as one outside the cache: its
+      // bytes and scales may be anything.
       struct Ahead {
         int32_t block = -1, head = 0, first = 0, live = 0;
       };
       const int shift = p.block_shift;
       Piece piece;
       uint32_t n_piece = 0;
-      int32_t t = 0;
-      bool more = get_piece(n_piece++, &piece);
-      if (more) t = piece.ta;
+      int32_t t = 0, from = 0, to = 0;  // tile; blocks that some row sees
+      bool more = true;
+      const auto next_piece = [&] {
+        more = get_piece(n_piece++, &piece);
+        if (!more) return;
+        t = piece.ta;
+        to = (min(piece.pos0 + piece.positions, piece.len) - 1 >> shift) + 1;
+        from = p.window > 0 ? max(max(piece.pos0, -1) - p.window + 1, 0) >> shift : 0;
+      };
+      next_piece();
       const auto ahead = [&](Ahead* a) {  // the next tile's table entry
         a->live = more;
         if (!more) return;
         a->head = piece.head;
         a->first = t == piece.ta;
-        const int64_t j = (static_cast<int64_t>(t) * kTile + lane * 16) >> shift;
+        const int32_t j = (t * kTile + (lane & 7) * 16) >> shift;
         a->block = -1;
-        if (lane < 8 && j < p.max_blocks) a->block = __ldg(p.block_tables + piece.req * p.bt_stride + j);
-        if (++t == piece.tb) {
-          more = get_piece(n_piece++, &piece);
-          if (more) t = piece.ta;
-        }
+        if (lane < 8 && j < to && j >= from)
+          a->block = __ldg(p.block_tables + piece.req * p.bt_stride + j);
+        if (++t == piece.tb) next_piece();
       };
       const auto in_cache = [&](const Ahead& a) { return a.block >= 0 && a.block < p.num_blocks; };
       const auto scales_of = [&](const Ahead& a) {
@@ -858,17 +865,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 s1 = scales_of(a1);
         Ahead a2;
         ahead(&a2);
-        if (!wait(bar(L::kEmptyB, stage), phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
-        // scales, by the lanes that have them
+        // Scales, by the lanes that have them; made before the stage is free (after the wait
+        // they hold up the copies: 32 x 32768 decode 3 % slower).
         const bool here = lane < 8 && in_cache(a0);
         const bool zero = s0.y == 0.f, bad = !(s0.y >= 0.f && s0.y < INFINITY);
         const float own = here && !zero && !bad ? s0.y : 0.f;
         const float top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(own, 0.f))));
         if (a0.first) ref = top > 0.f ? top : 1.f;
         const float toplog = top > 0.f ? log2f(top / ref) : 0.f;
-        const float vlog = own > 0.f ? log2f(own / ref) : toplog + kNoScaleLog;
+        const float vlog = own > 0.f ? log2f(own / ref) : here ? toplog + kNoScaleLog : 0.f;
         const uint32_t flags = __ballot_sync(kFull, here && zero) | __ballot_sync(kFull, here && bad) << 8 |
                                __ballot_sync(kFull, here) << 16;
+        if (!wait(bar(L::kEmptyB, stage), phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
         TileScales& sc = tile_scales[j % kScaleSlots];
         if (lane < 8) {
           sc.key[lane] = s0.x * p.scale_log2;

@@ -454,3 +454,27 @@ def test_negative_value_scales(fp8idx):
     assert torch.isnan(out[0, 2:]).all()
     check_rows(out, lse, want, ~hit)
     assert np.abs(lse.cpu().numpy() - want[1])[hit].max() < 2.0**-16 * (1 + want[4][hit]).max()
+
+
+@pytest.mark.parametrize("size", [1e-45, 1e-42, 1e30, 3e38])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scales_where_nobody_looks(fp8idx, D, size):
+    """Scales of blocks that no row sees may be any number: table entries past a
+    request's positions (in a tile with seen ones, first and only or last) and
+    before a window, with seen blocks of scale 0 in the same tiles and without."""
+    rng = np.random.default_rng(31)
+    bs = 16
+    ctx, new = [75, 300, 20, 700], [30, 2, 1, 200]
+    for window in (0, 40):
+        x = setup(rng, ctx, new, 4, 2, D, bs, max_blocks=50)
+        seen = np.zeros(x["cache"].shape[0], bool)
+        for b, (n, m) in enumerate(zip(ctx, new)):
+            seen[x["tables"][b, (max(n - m - window + 1, 0) if window else 0) // bs: -(-n // bs)]] = True
+        sc = scales_of(x["cache"], bs, D)
+        sc[~seen] = size
+        for zeros in (False, True):
+            if zeros:
+                for b in (1, 3):
+                    sc[x["tables"][b, (ctx[b] - 1) // bs], :, 1] = 0
+            set_scales(x["cache"], bs, D, sc)
+            check(fp8idx, x, window=window, what=f"window {window}, zeros {zeros}")
