@@ -669,10 +669,11 @@ fp8idx_status fp8_paged_block_store(const fp8idx_tensor* k,
  * Precision: a query element is exact, but for those below 2^-10 of its head's
  * largest one, which are off by up to 2^-17 of that.  Products and sums are
  * f32.  What is multiplied with a value's code is probability * value scale as
- * f16 (2^-11 of itself, and 2^-24 of the row's largest one); value scales other
- * than 0 should lie within 2^64 of one another, scores (times log2 e) below
- * 10^7.  The sum of the probabilities is not rounded to f16.  out is rounded
- * once to BF16.
+ * f16 (2^-11 of itself, and 2^-24 of the row's largest one, where a scale of 0
+ * counts as 2^-64 of the largest one); value scales other than 0 should lie
+ * within 2^64 of one another (values far below that count as next to nothing,
+ * their weights as they are), scores (times log2 e) below 10^7.  The sum of the
+ * probabilities is not rounded to f16.  out is rounded once to BF16.
  * NaN and infinities: in a query they make its head's out and lse NaN; a NaN
  * key code or key scale, the out and lse of the rows that see the key; a NaN
  * value code, or a value scale that is NaN, infinite or negative, every channel

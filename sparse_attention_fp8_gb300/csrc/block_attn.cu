@@ -79,7 +79,12 @@ constexpr int kConvWarp0 = 8, kLoadWarp = 12, kMmaWarp = 13, kPlanWarp = 14;
 // Registers a thread: 256 * 184 + 128 * 80 + 128 * 64 = 512 * 128.
 constexpr int kSoftmaxRegs = 184, kConvRegs = 80, kOtherRegs = 64;
 constexpr float kMinM = -3e38f;   // m stays finite, so that a score of -inf gives probability 0
+// A group of scale 0 (or NaN) has weights and no values: log2 of its scale counts as this far below the
+// largest one of the piece so far, where its exponentials neither vanish beside the others' (below 2^-126)
+// nor raise the reference over them.
 constexpr float kNoScaleLog = -64.f;
+// Bounds of the logarithms, so that their inverses and sums stay finite.
+constexpr float kMinScaleLog = -100.f, kMaxScaleLog = 126.f;
 // (Scale slots outnumber the tiles in flight: a tile's masks of NaN stay behind it
 // until its group has looked, two of its tiles later.)
 constexpr int kUnitSlots = 8, kScaleSlots = 8;
@@ -859,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 s0 = scales_of(a0);
       ahead(&a1);
       uint32_t j = 0, stage = 0, phase = 0;
-      float ref = 1.f;
+      float ref = 1.f, most = 0.f;  // the first tile's largest value scale; log2 of the largest so far over it
 #pragma unroll 1
       while (a0.live) {
         const float2 s1 = scales_of(a1);
@@ -871,9 +876,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool zero = s0.y == 0.f, bad = !(s0.y >= 0.f && s0.y < INFINITY);
         const float own = here && !zero && !bad ? s0.y : 0.f;
         const float top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(own, 0.f))));
-        if (a0.first) ref = top > 0.f ? top : 1.f;
-        const float toplog = top > 0.f ? log2f(top / ref) : 0.f;
-        const float vlog = own > 0.f ? log2f(own / ref) : here ? toplog + kNoScaleLog : 0.f;
+        if (a0.first) ref = top > 0.f ? top : 1.f, most = 0.f;
+        most = fmaxf(most, fminf(log2f(top / ref), kMaxScaleLog));
+        const float vlog = own > 0.f ? fminf(fmaxf(log2f(own / ref), kMinScaleLog), kMaxScaleLog)
+                           : here    ? most + kNoScaleLog
+                                     : 0.f;
         const uint32_t flags = __ballot_sync(kFull, here && zero) | __ballot_sync(kFull, here && bad) << 8 |
                                __ballot_sync(kFull, here) << 16;
         if (!wait(bar(L::kEmptyB, stage), phase ^ 1u, abort_flag, kSiteStageEmpty)) break;

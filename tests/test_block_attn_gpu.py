@@ -478,3 +478,35 @@ def test_scales_where_nobody_looks(fp8idx, D, size):
                     sc[x["tables"][b, (ctx[b] - 1) // bs], :, 1] = 0
             set_scales(x["cache"], bs, D, sc)
             check(fp8idx, x, window=window, what=f"window {window}, zeros {zeros}")
+
+
+@pytest.mark.parametrize("far", [2.0**-64, 2.0**-63, 2.0**63, 2.0**64])
+@pytest.mark.parametrize("new", [1, 40, 130])
+def test_value_scales_of_zero_beside_far_ones(fp8idx, new, far):
+    """Blocks of scale 0 keep their weight (every score is the same) next to
+    scales at the far end of the range, before them and after them."""
+    rng = np.random.default_rng(32)
+    bs, D = 16, 128
+    x = setup(rng, [560], [new], 2, 1, D, bs)
+    sc = scales_of(x["cache"], bs, D)
+    sc[..., 0] = 0
+    sc[..., 1] = 1
+    table = x["tables"][0]
+    sc[table[8:16], :, 1] = far  # the second tile
+    sc[table[[3, 9, 11, 18, 30]], :, 1] = 0
+    set_scales(x["cache"], bs, D, sc)
+    check(fp8idx, x)
+    check(fp8idx, x, window=200)
+
+
+def test_value_scales_farther_apart_than_the_range(fp8idx):
+    """A block of tiny values (a scale that a store of them writes) next to
+    ordinary ones: its values do not count, its weights do."""
+    rng = np.random.default_rng(33)
+    bs, D = 16, 128
+    for new in (1, 40, 130):
+        x = setup(rng, [560], [new], 2, 1, D, bs)
+        sc = scales_of(x["cache"], bs, D)
+        sc[x["tables"][0, [2, 9, 20]], :, 1] = [[1e-42], [1e-45], [2e-38]]
+        set_scales(x["cache"], bs, D, sc)
+        check(fp8idx, x)
