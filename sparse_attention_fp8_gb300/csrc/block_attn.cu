@@ -1309,7 +1309,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) block_attn_join_kernel(const 
   const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), g = meta.shared ? r / kTile : 0;
   const int index = (r - g * kTile) / p.group, position = index + g * half;
   if ((meta.shared && index >= half) || position >= meta.positions) return;
-  float top = kMinM, l = 0.f, o[kPer] = {};
+  // (outputs go by the first piece's value scale: their sums may be 2^15 times the mean)
+  float top = kMinM, l = 0.f, ref = 0.f, o[kPer] = {};
 #pragma unroll 4
   for (int c = blockIdx.x; c <= meta.last; ++c) {
     const float* const ws =
@@ -1321,10 +1322,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) block_attn_join_kernel(const 
     const float now = fmaxf(top, ml.x), f = ex2(top - now), e = ex2(ml.x - now);
     l = fmaf(ml.y, e, l * f);
     top = now;
+    if (c == static_cast<int>(blockIdx.x)) ref = ml.z;
+    const float by = ml.z / ref;
 #pragma unroll
     for (int i = 0; i < kPer / 2; ++i) {
-      o[2 * i] = fmaf(v[i].x * e, ml.z, o[2 * i] * f);
-      o[2 * i + 1] = fmaf(v[i].y * e, ml.z, o[2 * i + 1] * f);
+      o[2 * i] = fmaf(v[i].x * e, by, o[2 * i] * f);
+      o[2 * i + 1] = fmaf(v[i].y * e, by, o[2 * i + 1] * f);
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1333,7 +1336,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) block_attn_join_kernel(const 
   __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + row * p.out_row_stride + head * p.out_head_stride;
 #pragma unroll
   for (int i = 0; i < kPer; i += 2)
-    *reinterpret_cast<uint32_t*>(out + lane * kPer + i) = bf16_pair(o[i] * inv, o[i + 1] * inv);
+    *reinterpret_cast<uint32_t*>(out + lane * kPer + i) = bf16_pair(o[i] * inv * ref, o[i + 1] * inv * ref);
   if (p.lse && lane == 0)
     p.lse[row * p.heads + head] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }

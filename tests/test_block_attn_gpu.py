@@ -510,3 +510,20 @@ def test_value_scales_farther_apart_than_the_range(fp8idx):
         sc[x["tables"][0, [2, 9, 20]], :, 1] = [[1e-42], [1e-45], [2e-38]]
         set_scales(x["cache"], bs, D, sc)
         check(fp8idx, x)
+
+
+@pytest.mark.parametrize("size", [1e-38, 1e36, 3e38])
+def test_value_scales_at_the_ends_of_f32(fp8idx, size):
+    """Whole units and units in pieces, whose sums are larger than their means."""
+    rng = np.random.default_rng(38)
+    bs, D = 32, 128
+    for ctx, new in ((100, 1), (3000, 2), (3000, 130)):
+        x = setup(rng, [ctx], [new], 2, 1, D, bs)
+        codes = x["cache"][..., : bs * 2 * D].reshape(-1, bs, 2, D)
+        codes[:, :, 1] = codes[:, :, 1] & 0x87 | 0x30  # values of 0.5 to 0.94
+        sc = scales_of(x["cache"], bs, D)
+        sc[..., 0] = 0.01
+        sc[..., 1] = size
+        set_scales(x["cache"], bs, D, sc)
+        out, _ = check(fp8idx, x, what=f"{ctx} positions, {new} rows")
+        assert (out.abs() > 0).any()
