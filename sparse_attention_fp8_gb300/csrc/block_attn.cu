@@ -864,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 s0 = scales_of(a0);
       ahead(&a1);
       uint32_t j = 0, stage = 0, phase = 0;
-      float ref = 1.f, most = 0.f;  // the first tile's largest value scale; log2 of the largest so far over it
+      float ref = 0.f, most = 0.f;  // largest value scales: of the first tile that has one, of all so far
 #pragma unroll 1
       while (a0.live) {
         const float2 s1 = scales_of(a1);
@@ -875,14 +875,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool here = lane < 8 && in_cache(a0);
         const bool zero = s0.y == 0.f, bad = !(s0.y >= 0.f && s0.y < INFINITY);
         const float own = here && !zero && !bad ? s0.y : 0.f;
-        const float top = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(fmaxf(own, 0.f))));
-        if (a0.first) ref = top > 0.f ? top : 1.f, most = 0.f;
-        most = fmaxf(most, fminf(log2f(top / ref), kMaxScaleLog));
-        const float vlog = own > 0.f ? fminf(fmaxf(log2f(own / ref), kMinScaleLog), kMaxScaleLog)
-                           : here    ? most + kNoScaleLog
-                                     : 0.f;
         const uint32_t flags = __ballot_sync(kFull, here && zero) | __ballot_sync(kFull, here && bad) << 8 |
                                __ballot_sync(kFull, here) << 16;
+        if (a0.first) ref = most = 0.f;
+        most = fmaxf(most, own);
+        if (ref == 0.f || (flags & 0xFFFFu) != 0u) {  // (a tile without scales of zero needs the largest one at first only)
+          most = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(most)));
+          if (ref == 0.f) ref = most;  // (until a tile has values their scale is 0, like theirs)
+        }
+        float vlog = 0.f;
+        if (own > 0.f)
+          vlog = fminf(fmaxf(log2f(own / ref), kMinScaleLog), kMaxScaleLog);
+        else if (here)
+          vlog = (ref > 0.f ? fminf(log2f(most / ref), kMaxScaleLog) : 0.f) + kNoScaleLog;
         if (!wait(bar(L::kEmptyB, stage), phase ^ 1u, abort_flag, kSiteStageEmpty)) break;
         TileScales& sc = tile_scales[j % kScaleSlots];
         if (lane < 8) {
@@ -1113,7 +1118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int step = shared ? 1 : 2, first = shared ? 0 : g;
       const int count = (piece.tb - piece.ta - first + step - 1) / step;
       RowState st;
-      float ref = 1.f;
+      float ref = 0.f;
       uint32_t j = j0 + first;
       int tile0 = (piece.ta + first) * kTile;
       j0 += piece.tb - piece.ta;
@@ -1211,7 +1216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float4 v = sums[k * copy_lanes + r];
             l = fmaf(v.y, ex2(v.x - m), l);
           }
-          ref = sums[0].z;  // (group 0 has a tile of every piece)
+          ref = fmaxf(sums[0].z, sums[kTile].z);  // (0 before the first tile with values)
           const float f = ex2(st.m - m);
           // A round takes as many channels as 32 KB hold of all copies' rows in use,
           // and a thread puts out `share` of them for one row.
@@ -1309,8 +1314,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) block_attn_join_kernel(const 
   const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), g = meta.shared ? r / kTile : 0;
   const int index = (r - g * kTile) / p.group, position = index + g * half;
   if ((meta.shared && index >= half) || position >= meta.positions) return;
-  // (outputs go by the first piece's value scale: their sums may be 2^15 times the mean)
-  float top = kMinM, l = 0.f, ref = 0.f, o[kPer] = {};
+  // Outputs go by the power of two below the first value scale: their sums may be 2^15 times the mean.
+  float top = kMinM, l = 0.f, over = 0.f, o[kPer] = {};
 #pragma unroll 4
   for (int c = blockIdx.x; c <= meta.last; ++c) {
     const float* const ws =
@@ -1322,21 +1327,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) block_attn_join_kernel(const 
     const float now = fmaxf(top, ml.x), f = ex2(top - now), e = ex2(ml.x - now);
     l = fmaf(ml.y, e, l * f);
     top = now;
-    if (c == static_cast<int>(blockIdx.x)) ref = ml.z;
-    const float by = ml.z / ref;
+    if (over == 0.f && ml.z > 0.f)  // (0: a piece without values)
+      over = power_of_two(127 - min(max(static_cast<int>(__float_as_uint(ml.z) >> 23), 1), 253));
+    const float by = e * (ml.z * over);
 #pragma unroll
     for (int i = 0; i < kPer / 2; ++i) {
-      o[2 * i] = fmaf(v[i].x * e, by, o[2 * i] * f);
-      o[2 * i + 1] = fmaf(v[i].y * e, by, o[2 * i + 1] * f);
+      o[2 * i] = fmaf(v[i].x, by, o[2 * i] * f);
+      o[2 * i + 1] = fmaf(v[i].y, by, o[2 * i + 1] * f);
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : 1.f / l, under = over > 0.f ? 1.f / over : 0.f;
   const int64_t row = static_cast<int64_t>(meta.row0) + position;
   const int head = meta.head * p.group + (r - g * kTile) - index * p.group;
   __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + row * p.out_row_stride + head * p.out_head_stride;
 #pragma unroll
   for (int i = 0; i < kPer; i += 2)
-    *reinterpret_cast<uint32_t*>(out + lane * kPer + i) = bf16_pair(o[i] * inv * ref, o[i + 1] * inv * ref);
+    *reinterpret_cast<uint32_t*>(out + lane * kPer + i) = bf16_pair(o[i] * inv * under, o[i + 1] * inv * under);
   if (p.lse && lane == 0)
     p.lse[row * p.heads + head] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }

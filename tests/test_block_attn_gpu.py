@@ -527,3 +527,22 @@ def test_value_scales_at_the_ends_of_f32(fp8idx, size):
         set_scales(x["cache"], bs, D, sc)
         out, _ = check(fp8idx, x, what=f"{ctx} positions, {new} rows")
         assert (out.abs() > 0).any()
+
+
+@pytest.mark.parametrize("size", [1e-38, 1.0, 3e38])
+@pytest.mark.parametrize("D", [64, 128])
+def test_first_tiles_without_values(fp8idx, D, size):
+    """Value scales of any size after tiles whose blocks all have scale 0, in
+    either group's tiles."""
+    rng = np.random.default_rng(34)
+    bs = 32
+    for ctx, new, zeros in ((200, 1, 4), (300, 1, 4), (300, 1, 8), (513, 3, 12), (300, 130, 4), (700, 260, 8), (140, 140, 4)):
+        x = setup(rng, [ctx], [new], 2, 1, D, bs)
+        codes = x["cache"][..., : bs * 2 * D].reshape(-1, bs, 2, D)
+        codes[:, :, 1] = codes[:, :, 1] & 0x87 | 0x30  # values of 0.5 to 0.94
+        sc = scales_of(x["cache"], bs, D)
+        sc[..., 0] = 0.01
+        sc[..., 1] = size
+        sc[x["tables"][0, :zeros], :, 1] = 0
+        set_scales(x["cache"], bs, D, sc)
+        check(fp8idx, x, what=f"{ctx} positions, {new} rows")
