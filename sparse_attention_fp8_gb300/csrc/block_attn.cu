@@ -276,18 +276,25 @@ struct ChunkScale {
     vinv = reinterpret_cast<const float2*>(sc.vinv)[k];
   }
 };
+// The largest log2 probability: of the largest score, or (a negative key scale) the smallest one.
 __device__ __forceinline__ float chunk_max(const uint32_t (&r)[32], const ChunkScale& cs) {
   float top = -INFINITY;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     const uint32_t* v = &r[16 * g];
+    const float c = g ? cs.c.y : cs.c.x;
     float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]);
 #pragma unroll
     for (int j = 2; j < 16; j += 4) {
       a = fmaxf(fmaxf(a, __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
       if (j + 2 < 16) b = fmaxf(fmaxf(b, __uint_as_float(v[j + 2])), __uint_as_float(v[j + 3]));
     }
-    top = fmaxf(top, fmaf(fmaxf(a, b), g ? cs.c.y : cs.c.x, g ? cs.o.y : cs.o.x));
+    a = fmaxf(a, b);
+    if (c < 0.f) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) a = fminf(a, __uint_as_float(v[j]));
+    }
+    top = fmaxf(top, fmaf(a, c, g ? cs.o.y : cs.o.x));
   }
   return top;
 }

@@ -546,3 +546,19 @@ def test_first_tiles_without_values(fp8idx, D, size):
         sc[x["tables"][0, :zeros], :, 1] = 0
         set_scales(x["cache"], bs, D, sc)
         check(fp8idx, x, what=f"{ctx} positions, {new} rows")
+
+
+@pytest.mark.parametrize("softmax_scale", [0.1, 1.0, -1.0])
+def test_negative_key_scales(fp8idx, softmax_scale):
+    """A key is code * scale whatever the scale's sign."""
+    rng = np.random.default_rng(35)
+    bs, D = 16, 128
+    for new in (1, 20, 200):
+        x = setup(rng, [900], [new], 2, 1, D, bs)
+        sc = scales_of(x["cache"], bs, D)
+        sc[rng.random(sc.shape[0]) < 0.5, :, 0] *= -1
+        set_scales(x["cache"], bs, D, sc)
+        check(fp8idx, x, scale=softmax_scale)
+        sc[..., 0] = -np.abs(sc[..., 0])
+        set_scales(x["cache"], bs, D, sc)
+        check(fp8idx, x, scale=softmax_scale)
