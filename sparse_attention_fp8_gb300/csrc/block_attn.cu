@@ -217,7 +217,7 @@ struct Unit {
     ta = lo / kTile;
     tb = max((hi + kTile - 1) / kTile, ta + 1);  // (rows that see nothing take one tile, all masked)
     steps = shared ? tb - ta : (tb - ta + 1) / 2;
-    pos0 = static_cast<int32_t>(min(max(first, static_cast<int64_t>(-(1 << 30))), static_cast<int64_t>(0x7fffffff - 1024)));
+    pos0 = static_cast<int32_t>(max(first, static_cast<int64_t>(-(1 << 30))));  // (none reaches context_lens[b])
   }
 };
 __device__ __forceinline__ int unit_count(const BlockAttnParams& p, const Request& r) {
@@ -237,8 +237,8 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
 // Which of the 32 columns from `col` on (of the tile at `tile0`) a row at
 // position pos sees.
 __device__ __forceinline__ uint32_t seen32(int pos, int window, int len, int tile0, int col, uint32_t in_cache) {
-  const int hi = min(pos + 1, len) - tile0 - col;
-  const int lo = window > 0 ? pos - window + 1 - tile0 - col : 0;
+  const int past = pos + 1 - tile0 - col, hi = min(past, len - tile0 - col);
+  const int lo = window > 0 ? max(past, 0) - window : 0;  // (no difference leaves 32 bits)
   uint32_t m = hi <= 0 ? 0u : hi >= 32 ? kFull : (1u << hi) - 1u;
   if (lo > 0) m &= lo >= 32 ? 0u : kFull << lo;
   if (!(in_cache >> (col / 16) & 1u)) m &= 0xFFFF0000u;

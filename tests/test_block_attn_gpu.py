@@ -562,3 +562,20 @@ def test_negative_key_scales(fp8idx, softmax_scale):
         sc[..., 0] = -np.abs(sc[..., 0])
         set_scales(x["cache"], bs, D, sc)
         check(fp8idx, x, scale=softmax_scale)
+
+
+@pytest.mark.parametrize("ctx,window", [(2**31 - 389, 300), (2**31 - 384, 100), (2**31 - 1, 700), (2**31 - 700, 2000)])
+def test_positions_near_two_to_the_31(fp8idx, ctx, window):
+    """The last positions that a table may hold, and a row's position past them:
+    the same as at the start, with as many blocks less."""
+    rng = np.random.default_rng(36)
+    bs, D, blocks = 128, 128, 24
+    per = 2**24 - 3  # 2^31 - 384 positions
+    less = per - blocks
+    x = setup(rng, [blocks * bs], [3], 4, 2, D, bs)
+    tables = torch.zeros((1, per), dtype=torch.int32, device="cuda")
+    tables[:, less:] = torch.from_numpy(x["tables"]).cuda()
+    d = {"cache": torch.from_numpy(x["cache"]).cuda(), "tables": tables,
+         "ctx": torch.tensor([ctx], dtype=torch.int32, device="cuda"), "cu": torch.from_numpy(x["cu"]).cuda()}
+    x["ctx"] = np.array([ctx - less * bs])
+    check(fp8idx, x, window=window, d=d)
