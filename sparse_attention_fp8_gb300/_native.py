@@ -246,6 +246,14 @@ def _stream(stream, like):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _int32(name, value):
+    """A whole number as the library's int32 (ctypes would drop its upper bits)."""
+    value = int(value)
+    if not -(1 << 31) <= value < 1 << 31:
+        raise ValueError(f"{name} does not fit 32 bits: {value}")
+    return value
+
+
 def _scratch(nbytes, like, stream):
     """Workspace for one call, allocated as the launching stream's: the caching
     allocator hands it on in that stream's order, not in the current one's."""
@@ -516,7 +524,7 @@ def head_norm_rope(q, k, positions, inv_freq, out_q, out_k=None, norm=None, q_we
     if norm not in _NORMS:
         raise ValueError(f"norm must be None, 'rms' or 'layer', not {norm!r}")
     d = _descs(q, k, positions, inv_freq, q_weight, q_bias, k_weight, k_bias, out_q, out_k)
-    oc = _norm_rope_options(norm, int(bool(interleaved)), int(rot_start), float(eps), float(rope_scale))
+    oc = _norm_rope_options(norm, int(bool(interleaved)), _int32("rot_start", rot_start), float(eps), float(rope_scale))
     _check(library().fp8idx_head_norm_rope(*d[:8], oc, *d[8:], _stream(stream, q)))
     return out_q, out_k
 
@@ -524,7 +532,7 @@ def head_norm_rope(q, k, positions, inv_freq, out_q, out_k=None, norm=None, q_we
 def kv_block_page_bytes(block_size, head_dim) -> int:
     """Bytes of one head's page of a key/value cache whose blocks share a
     scale (0 if not implemented)."""
-    return int(library().fp8idx_kv_block_page_bytes(int(block_size), int(head_dim)))
+    return int(library().fp8idx_kv_block_page_bytes(_int32("block_size", block_size), _int32("head_dim", head_dim)))
 
 
 def fp8_paged_block_store(k, v, slot_mapping, kv_cache, stream=None):
@@ -539,7 +547,7 @@ def fp8_paged_block_store(k, v, slot_mapping, kv_cache, stream=None):
 
 def paged_block_attn_workspace(head_dim) -> int:
     """Bytes of workspace fp8_paged_block_attn needs."""
-    return int(library().fp8idx_paged_block_attn_workspace(int(head_dim)))
+    return int(library().fp8idx_paged_block_attn_workspace(_int32("head_dim", head_dim)))
 
 
 def fp8_paged_block_attn(q, kv_cache, block_tables, context_lens, cu_new_lens, softmax_scale, out, lse=None, window=0,
@@ -551,6 +559,7 @@ def fp8_paged_block_attn(q, kv_cache, block_tables, context_lens, cu_new_lens, s
     sees, its own included (0: all).  workspace: a uint8 CUDA tensor of at
     least paged_block_attn_workspace(D) bytes (allocated here if None)."""
     import torch
+    window = _int32("window", min(int(window), 0x7FFFFFFF))  # (no two positions lie farther apart)
     if workspace is None:
         workspace = _scratch(paged_block_attn_workspace(q.shape[-1]) + 256, q, stream)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
@@ -558,7 +567,7 @@ def fp8_paged_block_attn(q, kv_cache, block_tables, context_lens, cu_new_lens, s
     d = _descs(q, kv_cache, block_tables, context_lens, cu_new_lens, out, lse, workspace)
     base = workspace.data_ptr()
     off = (-base) % 256
-    _check(library().fp8_paged_block_attn(*d[:5], float(softmax_scale), int(window), d[5], d[6],
+    _check(library().fp8_paged_block_attn(*d[:5], float(softmax_scale), window, d[5], d[6],
                                           ctypes.c_void_p(base + off),
                                           ctypes.c_size_t(max(workspace.numel() - off, 0)), _stream(stream, q)))
     return out

@@ -579,3 +579,12 @@ def test_positions_near_two_to_the_31(fp8idx, ctx, window):
          "ctx": torch.tensor([ctx], dtype=torch.int32, device="cuda"), "cu": torch.from_numpy(x["cu"]).cuda()}
     x["ctx"] = np.array([ctx - less * bs])
     check(fp8idx, x, window=window, d=d)
+
+
+@pytest.mark.parametrize("window", [2**31, 2**32 + 5, 2**63 - 1])
+def test_windows_past_32_bits(fp8idx, window):
+    """A window longer than every context is none."""
+    rng = np.random.default_rng(39)
+    x = setup(rng, [300, 40], [2, 40], 4, 2, 128, 32)
+    with_window, without = call(fp8idx, x, 0.1, window=window), call(fp8idx, x, 0.1)
+    assert all(torch.equal(a, b) for a, b in zip(with_window, without))

@@ -247,6 +247,21 @@ def test_binding_refuses_other_workspaces(monkeypatch):
             fp8idx.fp8_paged_block_attn(q, q, q, q, q, 1.0, q, workspace=ws)
 
 
+def test_binding_keeps_whole_numbers_whole(monkeypatch):
+    """Numbers past 32 bits are refused, not cut to their lower bits."""
+    x = torch.zeros((1, 1, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="window"):
+        fp8idx.fp8_paged_block_attn(x, x, x, x, x, 1.0, x, window=5 - 2**32, workspace=torch.zeros(9, dtype=torch.uint8))
+    monkeypatch.setattr(_native, "_descs", lambda *t: [None] * len(t))
+    with pytest.raises(ValueError, match="rot_start"):
+        fp8idx.head_norm_rope(x, None, x, x, x, rot_start=2**32)
+    for sizes in ((2**32 + 64, 128), (64, 2**32 + 128)):
+        with pytest.raises(ValueError, match="32 bits"):
+            fp8idx.kv_block_page_bytes(*sizes)
+    with pytest.raises(ValueError, match="head_dim"):
+        fp8idx.paged_block_attn_workspace(2**32 + 128)
+
+
 # --------------------------------------------------------------- definitions
 def test_definition_of_the_rotation_by_hand():
     x = np.arange(1.0, 9.0).reshape(1, 1, 8)
