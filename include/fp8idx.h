@@ -550,7 +550,7 @@ fp8idx_status fp8_mqa_sparse_attn_paged(const fp8idx_tensor* q,
  * and then, in its rotated part (rot = 2 * len(inv_freq) elements from
  * rot_start on), each pair (a, b) with index i becomes
  *   ((a cos - b sin) * rope_scale, (b cos + a sin) * rope_scale),
- * cos and sin of positions[token] * inv_freq[i], to within 1e-7 at every
+ * cos and sin of positions[token] * inv_freq[i], to within 2^-23 at every
  * position.  Pair i is elements (i, i + rot/2) of the rotated part, or with
  * `interleaved` (2i, 2i + 1).  Sums are f32, rounded once at the end (with a
  * norm, the mean square has to be an f32 number: values below 2^60 in size).  A
