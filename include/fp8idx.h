@@ -666,9 +666,9 @@ fp8idx_status fp8_paged_block_store(const fp8idx_tensor* k,
  *                matter.  Two calls in flight at once (two captured graphs,
  *                too) need two workspaces.
  *
- * Precision: a query element is exact, but for those below 2^-10 of its head's
- * largest one, which are off by up to 2^-17 of that.  Products and sums are
- * f32.  What is multiplied with a value's code is probability * value scale as
+ * Precision: a query element is exact, but for those below 2^-9 of its head's
+ * largest one, which are off by up to 2^-17 of that (of 2^-113 where that one is
+ * smaller).  Products and sums are f32.  What is multiplied with a value's code is probability * value scale as
  * f16 (2^-11 of itself, and 2^-24 of the row's largest one, where a scale of 0
  * counts as 2^-64 of the largest one); value scales other than 0 should lie
  * within 2^64 of one another (values far below that count as next to nothing,

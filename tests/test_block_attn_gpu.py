@@ -588,3 +588,32 @@ def test_windows_past_32_bits(fp8idx, window):
     x = setup(rng, [300, 40], [2, 40], 4, 2, 128, 32)
     with_window, without = call(fp8idx, x, 0.1, window=window), call(fp8idx, x, 0.1)
     assert all(torch.equal(a, b) for a, b in zip(with_window, without))
+
+
+def test_small_query_elements(fp8idx):
+    """Elements down to 2^-9 of their head's largest one are exact, smaller ones
+    off by 2^-17 of it at most: the score of a key that takes one element."""
+    bs, D = 16, 64
+    tops = np.array([1.0, 1.9921875, 0.75, 2.0**20, 1.9921875 * 2.0**-40], np.float32)  # (255 / 128 has all of bf16's bits)
+    down = np.arange(0, 24)
+    bits = np.array([1.0, 129 / 128, 171 / 128, 255 / 128])
+    small = (tops[:, None, None] * np.exp2(-down)[:, None] * bits).reshape(len(tops), -1)
+    small = bf16(np.minimum(small, tops[:, None]))
+    H = small.shape[1]
+    q = np.zeros((len(tops), H, D), np.float32)
+    q[:, :, 0] = tops[:, None]
+    q[:, :, 1] = small
+    cache = np.zeros((1, 1, ref.block_page_bytes(bs, D)), np.uint8)
+    cache[0, 0, 1] = 0x38  # key element 1 is 1
+    set_scales(cache, bs, D, np.ones((1, 1, 2)))
+    for r, top in enumerate(tops):
+        x = {"q": q[r: r + 1], "cache": cache, "tables": np.zeros((1, 1), np.int32), "ctx": np.array([1], np.int32),
+             "cu": np.array([0, 1], np.int32), "bs": bs}
+        scale = 2.0**8 / float(top)
+        _, lse = call(fp8idx, x, scale)
+        got, want = lse[0].double().cpu().numpy(), scale * small[r].astype(np.float64)
+        exact = small[r] >= top * 2.0**-9
+        assert exact.any() and not exact.all()
+        # (scores to 2^8 in f32, the exponential and the logarithm)
+        tol = 2.0**-21 * np.maximum(want, 1) + np.where(exact, 0, 2.0**-17 * 2.0**8)
+        assert (np.abs(got - want) <= tol).all(), (top, np.abs(got - want).max())
