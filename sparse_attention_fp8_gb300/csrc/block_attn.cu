@@ -105,7 +105,8 @@ struct Piece {
 
 // Scales of a tile: per 16 tokens the keys' (times the softmax's), log2 of the
 // values' over `ref` and its inverse; bits of groups of 16 tokens without
-// values (0-7), with values that are NaN (8-15), in the cache (16-23).
+// values (0-7), with values that are NaN (8-15), in the cache (16-23), with a
+// negative key scale (24-31).
 struct TileScales {
   float key[8], vlog[8], vinv[8];
   float ref;
@@ -276,25 +277,18 @@ struct ChunkScale {
     vinv = reinterpret_cast<const float2*>(sc.vinv)[k];
   }
 };
-// The largest log2 probability: of the largest score, or (a negative key scale) the smallest one.
 __device__ __forceinline__ float chunk_max(const uint32_t (&r)[32], const ChunkScale& cs) {
   float top = -INFINITY;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     const uint32_t* v = &r[16 * g];
-    const float c = g ? cs.c.y : cs.c.x;
     float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]);
 #pragma unroll
     for (int j = 2; j < 16; j += 4) {
       a = fmaxf(fmaxf(a, __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
       if (j + 2 < 16) b = fmaxf(fmaxf(b, __uint_as_float(v[j + 2])), __uint_as_float(v[j + 3]));
     }
-    a = fmaxf(a, b);
-    if (c < 0.f) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) a = fminf(a, __uint_as_float(v[j]));
-    }
-    top = fmaxf(top, fmaf(a, c, g ? cs.o.y : cs.o.x));
+    top = fmaxf(top, fmaf(fmaxf(a, b), g ? cs.c.y : cs.c.x, g ? cs.o.y : cs.o.x));
   }
   return top;
 }
@@ -323,8 +317,9 @@ __device__ __forceinline__ float chunk_exp(const uint32_t (&r)[32], const ChunkS
   return l;
 }
 
-// Of a tile that not every row sees in full: log2 probabilities, -inf where the
-// row sees nothing, in the scores' place.
+// Of a tile that not every row sees in full, or where a key scale is negative (the
+// largest score is not the largest probability's then): log2 probabilities, -inf
+// where the row sees nothing, in the scores' place.
 __device__ __noinline__ void mask_tile(uint32_t s_tm, const TileScales* sc, int chunk0, int end, int pos, int window, int len,
                                        int tile0, float row_scale) {
 #pragma unroll 1
@@ -883,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool zero = s0.y == 0.f, bad = !(s0.y >= 0.f && s0.y < INFINITY);
         const float own = here && !zero && !bad ? s0.y : 0.f;
         const uint32_t flags = __ballot_sync(kFull, here && zero) | __ballot_sync(kFull, here && bad) << 8 |
-                               __ballot_sync(kFull, here) << 16;
+                               __ballot_sync(kFull, here) << 16 | __ballot_sync(kFull, here && s0.x < 0.f) << 24;
         if (a0.first) ref = most = 0.f;
         most = fmaxf(most, own);
         if (ref == 0.f || (flags & 0xFFFFu) != 0u) {  // (a tile without scales of zero needs the largest one at first only)
@@ -1148,7 +1143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         {
           const TileScales& sc = tile_scales[j % kScaleSlots];
           ref = sc.ref;
-          const bool masked = tile0 + kTile > full_to || tile0 < full_from || (sc.flags >> 16) != 0xFFu;
+          const bool masked = tile0 + kTile > full_to || tile0 < full_from || (sc.flags >> 16) != 0xFFu;  // (a block outside, a negative key scale)
           softmax_tile<D>(s_tm, o_tm, sc, chunk0, copy_lanes / 32, masked, pos, p.window, len, tile0, row_scale, k == 0, st);
         }
         ptx::tmem_wait_st();
