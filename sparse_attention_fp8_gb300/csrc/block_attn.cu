@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         rest -= __shfl_sync(kFull, sum, 31);
       }
-      skip = static_cast<int32_t>(rest);
+      skip = static_cast<int32_t>(min(rest, static_cast<int64_t>(0x7fffffff)));
     }
   }
   __syncthreads();
@@ -753,6 +753,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     reg_dec<kOtherRegs>();
     if (warp == kPlanWarp) {
       // ============================ the plan ============================
+      // (Lengths are read again here.  If someone writes them meanwhile, they need not be the ones the sums
+      // were made of: every request, unit, step and piece stays in range all the same.)
       BlockAttnMeta meta = {};
       if (at < end) {
         Request r(p, req);
@@ -767,6 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (at < end) {
             const Unit u(p, r, unit);
             const int32_t all = u.steps + kUnitCost;
+            skip = min(skip, all);
             const int32_t stop = static_cast<int32_t>(min(static_cast<int64_t>(all), skip + (end - at)));
             // (the unit's cost stands before its steps)
             const int32_t from = max(skip - kUnitCost, 0), to = max(stop - kUnitCost, 0);
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               meta.row0 = out.row0;
               meta.positions = out.positions;
               meta.head = head;
-              meta.last = static_cast<int32_t>((at - skip + all - 1) / per_cta);
+              meta.last = static_cast<int32_t>(min((at - skip + all - 1) / per_cta, static_cast<int64_t>(gridDim.x - 1)));
               meta.shared = out.shared;
             }
             at += stop - skip;
@@ -802,14 +805,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++n;
           }
           if (out.row0 < 0) break;
-          if (at < end && ++unit == n_units) {
+          if (at < end && ++unit >= n_units) {
             unit = 0;
             if (++head == p.kv_heads) {
               head = 0;
-              do {  // (there is one: steps are left)
-                r = Request(p, ++req);
+              do {
+                if (++req == p.n_req) at = end;
+                r = Request(p, min(req, p.n_req - 1));
                 n_units = unit_count(p, r);
-              } while (n_units == 0 && req + 1 < p.n_req);
+              } while (n_units == 0 && at < end);
             }
           }
         }
@@ -1316,10 +1320,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) block_attn_join_kernel(const 
   const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), g = meta.shared ? r / kTile : 0;
   const int index = (r - g * kTile) / p.group, position = index + g * half;
   if ((meta.shared && index >= half) || position >= meta.positions) return;
+  // (a record that another call in flight wrote into the same workspace leads nowhere else)
+  const int last = min(meta.last, static_cast<int>(gridDim.x) - 1);
+  const int head = meta.head * p.group + (r - g * kTile) - index * p.group;
+  if (meta.row0 + position >= p.rows || head >= p.heads) return;
   // Outputs go by the power of two below the first value scale: their sums may be 2^15 times the mean.
   float top = kMinM, l = 0.f, over = 0.f, o[kPer] = {};
 #pragma unroll 4
-  for (int c = blockIdx.x; c <= meta.last; ++c) {
+  for (int c = blockIdx.x; c <= last; ++c) {
     const float* const ws =
         p.partial + (static_cast<int64_t>(c) * 2 + (c == static_cast<int>(blockIdx.x) ? 1 : 0)) * block_attn_piece_floats(D);
     const float4 ml = __ldcg(reinterpret_cast<const float4*>(ws + kBlockAttnLanes * D) + r);
@@ -1340,7 +1348,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) block_attn_join_kernel(const 
   }
   const float inv = l == 0.f ? 0.f : 1.f / l, under = over > 0.f ? 1.f / over : 0.f;
   const int64_t row = static_cast<int64_t>(meta.row0) + position;
-  const int head = meta.head * p.group + (r - g * kTile) - index * p.group;
   __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + row * p.out_row_stride + head * p.out_head_stride;
 #pragma unroll
   for (int i = 0; i < kPer; i += 2)
