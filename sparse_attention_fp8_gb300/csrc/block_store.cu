@@ -101,7 +101,8 @@ __global__ void __launch_bounds__(THREADS) block_store_kernel(const BlockStorePa
       }
       const int32_t t0 = t_base + i0;
       const int run = min(end, n) - i0;
-      const int32_t slot = __ldg(p.slots + t0);
+      // (read again: if someone writes it meanwhile, the block and its rows stay in range)
+      const int32_t slot = min(max(__ldg(p.slots + t0), 0), p.num_slots - 1);
       const int off0 = slot & (bs - 1);
       uint8_t* const page = p.cache + static_cast<int64_t>(slot >> p.block_shift) * p.block_stride + h * p.cache_head_stride;
       float* const scale_at = reinterpret_cast<float*>(page + (2 * D << p.block_shift)) + part;
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(THREADS) block_store_kernel(const BlockStorePa
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) {
         const int r = row + k * kRows;
-        if (r >= run) break;
+        if (r >= run || off0 + r >= bs) break;
         float v[8], y[8];
         raw[k].values(v);
         uint2 sign = make_uint2(0u, 0u);
