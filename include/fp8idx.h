@@ -553,8 +553,9 @@ fp8idx_status fp8_mqa_sparse_attn_paged(const fp8idx_tensor* q,
  * cos and sin of positions[token] * inv_freq[i], to within 2^-23 at every
  * position.  Pair i is elements (i, i + rot/2) of the rotated part, or with
  * `interleaved` (2i, 2i + 1).  Sums are f32, rounded once at the end (with a
- * norm, the mean square has to be an f32 number: values below 2^60 in size).  A
- * token with a negative position is not written.
+ * norm, the mean square has to be an f32 number: values below 2^60 in size; the
+ * mean that norm 2 takes off is good to 2^-20 of the row's largest |x|).  A token
+ * with a negative position is not written.
  *
  *  q, k          [tokens, heads, head_dim] and [tokens, kv_heads, head_dim]
  *                BF16, F16 or F32 (the same), unit inner stride, rows 16-byte
@@ -654,7 +655,7 @@ fp8idx_status fp8_paged_block_store(const fp8idx_tensor* k,
  *  kv_cache      as for fp8_paged_block_store; a value scale below zero, which
  *                no store writes, counts as NaN.
  *  block_tables  [batch, max_blocks] I32, rows contiguous, batch <= 4096,
- *                max_blocks*block_size < 2^31 - 256.
+ *                max_blocks at least 1, max_blocks*block_size < 2^31 - 256.
  *  context_lens  [batch] I32; cu_new_lens [batch + 1] I32, a prefix sum, at
  *                most `rows`: both as fp8idx_paged_step_tables makes them.
  *  out           shape and type of q, the same rules; rows that overlap
@@ -668,12 +669,13 @@ fp8idx_status fp8_paged_block_store(const fp8idx_tensor* k,
  *
  * Precision: a query element is exact, but for those below 2^-9 of its head's
  * largest one, which are off by up to 2^-17 of that (of 2^-113 where that one is
- * smaller).  Products and sums are f32.  What is multiplied with a value's code is probability * value scale as
- * f16 (2^-11 of itself, and 2^-24 of the row's largest one, where a scale of 0
- * counts as 2^-64 of the largest one); value scales other than 0 should lie
- * within 2^64 of one another (values far below that count as next to nothing,
- * their weights as they are), scores (times log2 e) below 10^7.  The sum of the
- * probabilities is not rounded to f16.  out is rounded once to BF16.
+ * smaller).  Products and sums are f32.  What is multiplied with a value's code
+ * is probability * value scale as f16 (2^-11 of itself, and 2^-23 of the row's
+ * largest one, where a scale of 0 counts as 2^-64 of the largest one); value
+ * scales other than 0 should lie within 2^64 of one another (values far below
+ * that count as next to nothing, their weights as they are), scores (times
+ * log2 e) below 10^7.  The sum of the probabilities is not rounded to f16.  out is
+ * rounded once to BF16.
  * NaN and infinities: in a query they make its head's out and lse NaN; a NaN
  * key code or key scale, the out and lse of the rows that see the key; a NaN
  * value code, or a value scale that is NaN, infinite or negative, every channel

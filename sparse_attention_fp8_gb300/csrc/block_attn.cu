@@ -39,12 +39,12 @@
 // then so do the others.
 //
 // What bounds it, measured with replayed graphs (the join included):
-//  * 32 requests of one row, 64 / 8 heads, 32768 positions: 338 us, 5.4 TB/s of
-//    cache, 81% of a copy's rate.  A tile's 32 KB take 1420 clocks of an SM's
+//  * 32 requests of one row, 64 / 8 heads, 32768 positions: 341 us, 5.4 TB/s of
+//    cache, 81% of a copy's rate (one cache over and over; 374 to 385 over several).  A tile's 32 KB take 1420 clocks of an SM's
 //    share of that rate, its products 1024 of the tensor pipe, for 8 rows as for
 //    128, and its softmax and conversion have to stay below as well.
 //  * 16 requests of 6 rows, 32 heads on one key head, 131072 positions: 198 us,
-//    895 TFLOP/s; 4 requests of 2048 prompt rows, 32 / 8 heads, 8192 positions:
+//    892 TFLOP/s; 4 requests of 2048 prompt rows, 32 / 8 heads, 8192 positions:
 //    577 us, 1135 TFLOP/s, 58% of a bf16 product's rate.  The 1024 clocks of a
 //    tile and 128 rows are half scores (e4m3, but twice: both parts of a query)
 //    and half outputs (f16); the tensor pipe is busy 47% and the issue slots 44%
@@ -53,7 +53,8 @@
 //    code of the roles' inner loops has to stay within the instruction cache:
 //    loops are rolled and what is rare is out of line (unrolled softmax 924 us
 //    where the rolled one took 861).
-//  * one row of 1024 positions: 15.2 us, 2.5 of it the join: launch, plan, table
+//  * the prompts with heads of 64: 500 us, 655 TFLOP/s.
+//  * one row of 1024 positions: 15.4 us, 2.5 of it the join: launch, plan, table
 //    entry, scales, tile, one step and the meeting are one chain.
 // Queries in tensor memory with scores in halves of a tile (887 us where this
 // took 802), all scores of a tile held in registers (1203 against 820) and both
@@ -1147,7 +1148,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         {
           const TileScales& sc = tile_scales[j % kScaleSlots];
           ref = sc.ref;
-          const bool masked = tile0 + kTile > full_to || tile0 < full_from || (sc.flags >> 16) != 0xFFu;  // (a block outside, a negative key scale)
+          // (the flags: a block that is not there, a negative key scale)
+          const bool masked = tile0 + kTile > full_to || tile0 < full_from || (sc.flags >> 16) != 0xFFu;
           softmax_tile<D>(s_tm, o_tm, sc, chunk0, copy_lanes / 32, masked, pos, p.window, len, tile0, row_scale, k == 0, st);
         }
         ptx::tmem_wait_st();

@@ -22,8 +22,8 @@
 // the arithmetic (with floating-point maxima and signs value by value, 92
 // registers, 19.2 us).  Fewer registers for f32 rows (4.4 us instead of 4.1 for
 // 3 heads of 64) and rows fetched into L2 before their slots are known (17.3) do
-// not pay.  A decode step of 96 rows
-// takes 3.5 us, a launch.
+// not pay.  The same
+// rows in f32 take 21.8 us, 5.8 TB/s; a decode step of 96 rows 3.5 us, a launch.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -16,11 +16,12 @@
 // around zero, where the Taylor series of sine and cosine to x^9 and x^10 are
 // good to 2e-9; with the f32 roundings of the angle and the series a cosine is off
 // by 1.02e-7 at most and a sine by 9.1e-8 (over all 2^30 reduced angles), and by
-// 1.5e-9 for the angle's last bit.  (In 32-bit floats the product alone would be off by 0.004 at
-// position 100000; 64-bit floats run at a sixty-fourth of the rate here.)
+// 1.5e-9 for the angle's last bit.  (In 32-bit floats the product alone would be
+// off by 0.004 at position 100000; 64-bit floats run at a sixty-fourth of the rate
+// here.)
 // DRAM bound: every value is read and written once.  16384 tokens of 32 + 8 bf16
-// heads of 128 take 55.3 us, 6.07 TB/s of the 6.68 that a copy reaches; one
-// token 3.3 us, a launch.
+// heads of 128 take 55.3 us, 6.07 TB/s of the 6.68 that a copy reaches, f32 heads
+// 100.5 us, 6.68 TB/s; one token 3.3 us, a launch.
 #include <cuda_runtime.h>
 
 #include <type_traits>
